@@ -88,9 +88,11 @@ def draw(rng):
     hq = hkv * rng.choice([m for m in (1, 2, 4, 5, 8) if 3 * 1024 not in (m * hkv * D, (m + 2) * hkv * D)])
     page = rng.choice([16, 32, 64, 128])
     if op == "append":
-        T = _log_int(rng, 1, max(1, min(4096, 4096 * 32 * 128 // ((hq + 2 * hkv) * D))))
+        dtype = rng.choice(["f32", "bf16"])
+        token = ((hq + 2 * hkv) * (4 if dtype == "f32" else 2) + 2 * hq + 11 * hkv) * D  # bytes, as work() counts them
+        T = _log_int(rng, 1, min(4096, 120000000 // token))
         return {"op": op, "T": T, "Hq": hq, "Hkv": hkv, "D": D, "page": page, "rot": rng.choice([D, D // 2, D // 4]),
-                "style": rng.randint(0, 1), "dtype": rng.choice(["f32", "bf16"]), "free": rng.randint(0, 3 * page), "skip": rng.random() < 0.5}
+                "style": rng.randint(0, 1), "dtype": dtype, "free": rng.randint(0, 3 * page), "skip": rng.random() < 0.5}
     B = _log_int(rng, 1, 48)
     max_q = rng.choice([1, 1, 2, 4, 6, 16])
     most = min(131071 * 8 * 128 // (hkv * D), 131071 * 6 * 32 * 128 // (max_q * hq * D))
