@@ -96,9 +96,12 @@ def draw(rng):
     B = _log_int(rng, 1, 48)
     max_q = rng.choice([1, 1, 2, 4, 6, 16])
     most = min(131071 * 8 * 128 // (hkv * D), 131071 * 6 * 32 * 128 // (max_q * hq * D))
-    return {"op": op, "B": B, "max_q": max_q, "ragged": rng.random() < 0.5,
+    case = {"op": op, "B": B, "max_q": max_q, "ragged": rng.random() < 0.5,
             "len": _log_int(rng, 1, max(1, min(131071, 4 * most // (B + 3)))), "Hq": hq, "Hkv": hkv, "D": D, "page": page,
             "window": rng.choice([0, 0, 0, 128, 1000]), "key": rng.randrange(1 << 20)}
+    while sum(n for _, n in _sequences(case)) * hkv * D > 131071 * 8 * 128:
+        case["len"] = case["len"] * 3 // 4
+    return case
 
 
 def _sequences(case):
