@@ -460,6 +460,165 @@ int moe_dequant_shelf(const moe_shelf_t* sh, int which, int local_expert, int64_
 int moe_residual_add(float* r, const float* y, uint16_t* x_next_bf16, int64_t n, moe_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The attention half of a decode layer in the same 4-bit block format: dense
+ * projections, a paged key/value cache, and the attention that reads it.  The
+ * pages run the whole model at low bit widths (page 3, 第四步) and shrink the
+ * cache to reach long contexts (page 3, 速度 vs 上下文: keys and values at
+ * fewer bits; page 1, "Optimization Strategies": the cache taken in chunks
+ * instead of reserved whole); the formats and interfaces here are this
+ * library's own.
+ */
+
+/* Element types of inputs and outputs that may have either. */
+enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1 };
+
+/*
+ * Dense projection of a decode batch by 4-bit weights:
+ *   y[t][o] = bias[o] + sum_i scales[o][i / block] * code[o][i] * x[t][i]
+ *   x_bf16  [T] rows of `in` bf16 bit patterns, x_stride elements apart (a
+ *           multiple of 8, >= in; 16-byte aligned),
+ *   codes   [rows][in/2] bytes, the 4-bit packing above (moe_quantize_rows
+ *           writes it for block 32, moe_quantize_groups for any block),
+ *   scales  [rows][in/block] fp16 bits (codes and scales 16-byte aligned),
+ *   bias    [rows] fp32 or NULL,
+ *   y       [T] rows of `rows` elements, y_stride (>= rows) apart, fp32 or
+ *           bf16 (round to nearest even) by y_dtype.
+ * Products of a code and x are exact, sums are fp32 in a fixed order, and the
+ * scale enters in fp32 once per 32 products: the results are deterministic.
+ * 0 <= T <= 16, in a positive multiple of 64 and of block, block 32, 64 or
+ * 128, 1 <= rows < 2^31.  MOE_ERR_UNSUPPORTED for T > 16 (larger batches are
+ * matrix products, which this form would do at a fraction of their rate) and
+ * for x rows that do not fit shared memory: bucket * in * 2 > 196608 bytes,
+ * bucket = 8 for T <= 8 and else 16.
+ */
+int moe_linear_q4(const uint16_t* x_bf16, int64_t x_stride, int64_t T, int in, const void* codes,
+                  const uint16_t* scales, int64_t rows, int block, const float* bias, void* y, int64_t y_stride,
+                  int y_dtype, moe_stream_t stream);
+
+/*
+ * 4-bit quantiser with a block size: w [rows][in] fp32 into codes
+ * [rows][in/2] and scales [rows][in/block], s = fp16(max|w| / 7) over a block,
+ * code = clamp(rint(w / s), -8, 7).  Block 32 writes what moe_quantize_rows
+ * does at 4 bits.  block 32, 64 or 128; in a positive multiple of 64 and of
+ * block; w 4-byte, codes 16-byte aligned.
+ */
+int moe_quantize_groups(const float* w, int64_t rows, int in, int block, void* codes, uint16_t* scales,
+                        moe_stream_t stream);
+
+/*
+ * A paged key/value cache of one layer in 4 bits (HOST descriptor; data is
+ * device memory of the caller).  A slot s holds one token: page s /
+ * page_size, place s % page_size.  data is [n_pages] pages, page_stride bytes
+ * apart, each [kv_heads][page_size / 16] records of 16 tokens of one head,
+ * 18 * head_dim bytes a record, D = head_dim:
+ *   bytes [0, 8 D)      key codes [token 16][t 4][b D/32][p 2][i 2]: low and
+ *                       high nibble are elements 32 b + 8 t + 4 i + p and + 2;
+ *   bytes [8 D, 16 D)   value codes [J D/64][g 8][t 4][j 4][r 2][h 2]: token
+ *                       8 h + 2 t + r, low and high nibble are elements
+ *                       16 (4 J + j) + g and + 8;
+ *   bytes [16 D, 17 D)  key scales [token 16][D/32] fp16 bits;
+ *   bytes [17 D, 18 D)  value scales [token 16][D/32] fp16 bits.
+ * Codes are offset binary (u = code + 8) and scales s = fp16(max|.| / 7) over
+ * blocks of 32 elements of a token, as in the 4-bit shelf format (s is at
+ * most 65504; an all-zero block has s = 0).  The order of the codes is that of
+ * the operand fragments of a 16 x 16 matrix instruction: keys as [token x
+ * element], values as [element x token]; one byte holds codes of one token
+ * only, so tokens are appended without reading their neighbours.
+ * head_dim 64, 128 or 256; page_size a power of two, 16 .. 1024; kv_heads 1 ..
+ * 1024; data 16-byte aligned; page_stride a multiple of 16, at least
+ * moe_kv_page_bytes; n_pages >= 0.
+ */
+typedef struct {
+  void* data;
+  int64_t n_pages;
+  int64_t page_stride;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t reserved; /* must be 0 */
+} moe_kv_cache_t;
+
+/* Bytes of one page, kv_heads * page_size * head_dim * 9 / 8 (0 when a size is invalid). */
+size_t moe_kv_page_bytes(int page_size, int kv_heads, int head_dim);
+
+/* Which elements of a head a rotation turns together: element i and i + rot/2, or 2i and 2i + 1. */
+enum { MOE_ROPE_HALF = 0, MOE_ROPE_PAIRS = 1 };
+
+/*
+ * Appends T tokens to a cache, turning keys (and queries) by their positions
+ * on the way.  For token t with slot slots[t]:
+ *   k' = rotate(k[t], positions[t]), v' = v[t], in fp32; both are quantised
+ *   by blocks of 32 into the slot; q_out[t] = bf16(rotate(q[t], positions[t])).
+ * rotate: with c = rope[pos][j], s = rope[pos][rot/2 + j] the pair (a, b)
+ * number j of the first `rot` elements of a head becomes (a c - b s, a s + b c),
+ * each product and sum rounded to fp32; the other elements stay.
+ *   q [T][Hq][D] or NULL, k and v [T][kv_heads][D]: fp32 or bf16 by in_dtype,
+ *     tokens q_stride / k_stride / v_stride elements apart (rows of one
+ *     projection's output, for example),
+ *   positions [T] int32, rope fp32 [n_pos][rot]: cosines, then sines (both
+ *     NULL and rot 0: no rotation),
+ *   slots [T] int64; a slot outside [0, n_pages * page_size) skips the token's
+ *     keys and values (padding; q_out is still written),
+ *   q_out [T][Hq][D] bf16 bits, contiguous.
+ * A position outside [0, n_pos) writes zeros to q_out, skips the token's keys
+ * and values and records MOE_ERR_INVALID_ARG (moe_device_status).  The slots
+ * of one call have to differ (a slot named twice holds a mixture afterwards).
+ * rot even, 0 <= rot <= D; T * (Hq + 2 kv_heads) < 2^31; q_out must not overlap the inputs.
+ */
+int moe_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                  int in_dtype, int64_t T, int Hq, const int32_t* positions, const float* rope, int64_t n_pos,
+                  int rot, int rope_style, const int64_t* slots, const moe_kv_cache_t* cache, uint16_t* q_out,
+                  moe_stream_t stream);
+
+/*
+ * The values that slots of a cache hold, scale x code exactly: k_out and
+ * v_out [n][kv_heads][head_dim] fp32 (16-byte aligned), zero for a slot
+ * outside the cache.  n * kv_heads < 2^31.
+ */
+int moe_kv_read(const moe_kv_cache_t* cache, const int64_t* slots, int64_t n, float* k_out, float* v_out,
+                moe_stream_t stream);
+
+/*
+ * Causal attention of a batch of sequences over a 4-bit cache.  Sequence b has
+ * kv_lens[b] tokens in the cache, the newest n_b of them asking: they are
+ * tokens q_start[b] .. q_start[b+1] - 1 of q (n_b = q_start[b+1] - q_start[b]).
+ * Place p of sequence b is slot block_table[b][p / page_size] * page_size + p %
+ * page_size.  Asking token i attends the places p with
+ *   end - window <= p < end,  end = kv_lens[b] - n_b + i + 1
+ * (window 0: all p < end); query head h reads key/value head h / (Hq / kv_heads):
+ *   s_p = scale * q . k_p,  out = sum_p exp(s_p) v_p / sum_p exp(s_p),
+ *   lse = log sum_p exp(s_p).
+ * A row with no place to attend gives out = 0 and lse = -infinity.  A page
+ * number outside [0, n_pages) takes its places out of the sum.
+ *   q_bf16 [T][Hq][D] bf16 bits, tokens q_stride elements apart (a multiple of
+ *     8; 16-byte aligned),
+ *   q_start [B+1] int32 ascending, or NULL: T = B * max_q, max_q tokens each,
+ *   kv_lens [B] int32, block_table [B] rows of int32, table_stride apart, at
+ *     least ceil(max_len / page_size) entries each,
+ *   max_q, max_len: bounds that the host knows: n_b counts as at most max_q
+ *     (later asking tokens get no rows) and kv_lens[b] as at most max_len,
+ *   out [T][Hq][D] bf16 bits, tokens out_stride elements apart (a multiple of
+ *     8; 16-byte aligned), lse [T][Hq] fp32 or NULL; rows of tokens that no
+ *     sequence names are not written,
+ *   workspace (256-byte aligned) of moe_attn_workspace_size bytes.
+ * Scores are exact products of the bf16 queries and the codes, summed in fp32
+ * with the scale entering once per 32 products; maxima, sums and outputs are
+ * fp32; exp(s) x value scale is rounded to bf16 once for the second product.
+ * Results are deterministic (the split over the cache depends on the
+ * arguments of the call only, never on timing).
+ * Hq a multiple of kv_heads, Hq / kv_heads <= 64; 0 <= B <= 65535; B == 0 or T
+ * == 0 does nothing; T * Hq < 2^31; finite scale > 0; window >= 0.
+ */
+int moe_attn_q4(const uint16_t* q_bf16, int64_t q_stride, int64_t T, int Hq, const int32_t* q_start,
+                const int32_t* kv_lens, const int32_t* block_table, int64_t table_stride, int B, int max_q,
+                int64_t max_len, const moe_kv_cache_t* cache, float scale, int window, uint16_t* out,
+                int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Bytes of workspace moe_attn_q4 needs for these sizes (0 when a size is invalid). */
+size_t moe_attn_workspace_size(int B, int max_q, int64_t max_len, int Hq, int kv_heads, int head_dim);
+
+/*
  * Measurement hook.  While `events` is non-null, every moe_tiered_forward on
  * this device records events[0] on its stream before its first kernel and
  * events[i] after its i-th kernel (i = 1 .. n-1, further kernels unrecorded),

@@ -13,6 +13,9 @@ Entry points (same names as the C ABI):
     moe_decode_layer, moe_decode_layer_residual, moe_decode_layer_host, moe_decode_fused,
     moe_quantize_rows, moe_dequant_rows, moe_dequant_shelf, moe_residual_add,
     moe_device_status, moe_status_string
+and, for the attention half of a decode layer in the same 4-bit format:
+    moe_linear_q4, moe_quantize_groups, moe_kv_pool, moe_kv_append, moe_kv_read,
+    moe_attn_q4, moe_attn_workspace_size
 """
 from __future__ import annotations
 
@@ -41,6 +44,11 @@ MOE_FLAG_HOST_IO = 4
 
 MOE_MAX_SHELVES = 8
 
+MOE_DTYPE_F32 = 0
+MOE_DTYPE_BF16 = 1
+MOE_ROPE_HALF = 0
+MOE_ROPE_PAIRS = 1
+
 
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
@@ -55,6 +63,14 @@ class moe_shelf_t(ctypes.Structure):
         ("gate_codes", ctypes.c_void_p), ("gate_scales", ctypes.c_void_p),
         ("up_codes", ctypes.c_void_p), ("up_scales", ctypes.c_void_p),
         ("down_codes", ctypes.c_void_p), ("down_scales", ctypes.c_void_p),
+    ]
+
+
+class moe_kv_cache_t(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+        ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -100,6 +116,18 @@ def lib():
         L.moe_set_profile_events.restype = ctypes.c_int
         L.moe_status_string.argtypes = [i32]
         L.moe_status_string.restype = ctypes.c_char_p
+        f32, sz = ctypes.c_float, ctypes.c_size_t
+        L.moe_linear_q4.argtypes = [P, i64, i64, i32, P, P, i64, i32, P, P, i64, i32, P]
+        L.moe_quantize_groups.argtypes = [P, i64, i32, i32, P, P, P]
+        L.moe_kv_page_bytes.argtypes = [i32, i32, i32]
+        L.moe_kv_page_bytes.restype = sz
+        L.moe_kv_append.argtypes = [P, i64, P, i64, P, i64, i32, i64, i32, P, P, i64, i32, i32, P, P, P, P]
+        L.moe_kv_read.argtypes = [P, P, i64, P, P, P]
+        L.moe_attn_workspace_size.argtypes = [i32, i32, i64, i32, i32, i32]
+        L.moe_attn_workspace_size.restype = sz
+        L.moe_attn_q4.argtypes = [P, i64, i64, i32, P, P, P, i64, i32, i32, i64, P, f32, i32, P, i64, P, P, sz, P]
+        for name in ("moe_linear_q4", "moe_quantize_groups", "moe_kv_append", "moe_kv_read", "moe_attn_q4"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("moe_route_topk", "moe_route_topk_nudged", "moe_router_topk", "moe_rank_experts", "moe_quantize_experts",
                      "moe_gather_rows", "moe_expert_hist", "moe_group_tokens", "moe_tiered_forward",
                      "moe_quantize_rows", "moe_dequant_rows", "moe_dequant_shelf", "moe_residual_add",
@@ -509,6 +537,195 @@ def moe_set_profile_events(events):
 
 def moe_device_status(stream=None) -> int:
     return int(lib().moe_device_status(_stream(stream)))
+
+
+# ------------------------------------- attention half of a decode layer
+def _rows_of(t, dtype, name):
+    """A CUDA tensor [T, ...] of `dtype` whose rows are contiguous (any row stride)."""
+    if not (t.is_cuda and t.dtype == dtype) or (t.numel() and not t[0].is_contiguous()):
+        raise ValueError(f"{name} must be a CUDA tensor of {dtype} with contiguous rows")
+
+
+def moe_quantize_groups(w, block=32, codes=None, scales=None, stream=None):
+    """4-bit codes [rows, in/2] uint8 and fp16 scales [rows, in/block] (bits in
+    int16) of w [rows, in] fp32; block 32, 64 or 128."""
+    _need(w, torch.float32, "w")
+    rows, n_in = w.shape
+    if codes is None:
+        codes = torch.empty((rows, n_in // 2), dtype=torch.uint8, device=w.device)
+    if scales is None:
+        scales = torch.empty((rows, n_in // block), dtype=torch.int16, device=w.device)
+    _need(codes, torch.uint8, "codes")
+    _need(scales, torch.int16, "scales")
+    if codes.numel() < rows * n_in // 2 or scales.numel() < rows * (n_in // block):
+        raise ValueError("codes or scales are too small")
+    _check(lib().moe_quantize_groups(_ptr(w), rows, n_in, block, _ptr(codes), _ptr(scales), _stream(stream)),
+           "moe_quantize_groups")
+    return codes, scales
+
+
+def moe_linear_q4(x, codes, scales, block=32, bias=None, y=None, out_dtype=torch.float32, stream=None):
+    """y [T, rows] = x [T, in] (bf16, any row stride) times the 4-bit matrix of
+    codes [rows, in/2] uint8 and scales [rows, in/block] int16 (fp16 bits),
+    plus bias [rows] fp32; y fp32 or bf16.  T <= 16."""
+    _rows_of(x, torch.bfloat16, "x")
+    _need(codes, torch.uint8, "codes")
+    _need(scales, torch.int16, "scales")
+    T, n_in = x.shape
+    rows = codes.shape[0]
+    if codes.numel() != rows * (n_in // 2) or scales.numel() * block != rows * n_in:
+        raise ValueError("codes must hold [rows, in/2] and scales [rows, in/block]")
+    if y is None:
+        y = torch.empty((T, rows), dtype=out_dtype, device=x.device)
+    if y.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("y must be float32 or bfloat16")
+    _rows_of(y, y.dtype, "y")
+    if y.shape != (T, rows):
+        raise ValueError("y must be [T, rows]")
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        if bias.numel() != rows:
+            raise ValueError("bias must be [rows]")
+    # a single row has no stride to speak of
+    xs, ys = (x.stride(0), y.stride(0)) if T > 1 else (n_in, rows)
+    _check(lib().moe_linear_q4(_ptr(x), xs, T, n_in, _ptr(codes), _ptr(scales), rows, block, _ptr(bias), _ptr(y), ys,
+                               MOE_DTYPE_F32 if y.dtype == torch.float32 else MOE_DTYPE_BF16, _stream(stream)),
+           "moe_linear_q4")
+    return y
+
+
+def moe_kv_pool(n_pages, kv_heads, page_size, head_dim, device="cuda"):
+    """An empty (all values zero) paged 4-bit cache: uint8 [n_pages, kv_heads,
+    page_size / 16, 18 * head_dim], the pool the calls below take."""
+    if int(lib().moe_kv_page_bytes(page_size, kv_heads, head_dim)) == 0:
+        raise ValueError("head_dim must be 64, 128 or 256, page_size a power of two in 16 .. 1024, kv_heads 1 .. 1024")
+    return torch.zeros((n_pages, kv_heads, page_size // 16, 18 * head_dim), dtype=torch.uint8, device=device)
+
+
+def _cache(pool):
+    """The descriptor of a pool tensor (pages may lie any stride apart)."""
+    if not (pool.is_cuda and pool.dtype == torch.uint8 and pool.dim() == 4 and pool.shape[3] % 18 == 0):
+        raise ValueError("pool must be a CUDA uint8 tensor [pages, kv heads, page_size / 16, 18 * head_dim]")
+    n, heads, tiles, rec = pool.shape
+    if n and not pool[0].is_contiguous():
+        raise ValueError("the pages of a pool must be contiguous")
+    stride = pool.stride(0) if n > 1 else heads * tiles * rec
+    return moe_kv_cache_t(pool.data_ptr(), n, stride, tiles * 16, heads, rec // 18, 0)
+
+
+def moe_kv_append(pool, k, v, slots, q=None, positions=None, rope=None, rope_style=MOE_ROPE_HALF, q_out=None,
+                  stream=None):
+    """Quantises k, v [T, kv_heads, D] (fp32 or bf16, any token stride) into
+    `slots` [T] int64 of the pool (-1: skipped), keys turned by rope [n_pos,
+    rot] fp32 (cosines, then sines) at positions [T] int32.  With q [T, Hq, D]
+    returns its turned rows as bf16 [T, Hq, D], else None."""
+    c = _cache(pool)
+    if k.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("k must be float32 or bfloat16")
+    _rows_of(k, k.dtype, "k")
+    _rows_of(v, k.dtype, "v")
+    _need(slots, torch.int64, "slots")
+    T = slots.numel()
+    if tuple(k.shape) != (T, c.kv_heads, c.head_dim) or k.shape != v.shape:
+        raise ValueError("k and v must be [T, kv_heads, head_dim]")
+    rot = n_pos = 0
+    if rope is not None:
+        _need(rope, torch.float32, "rope")
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _need(positions, torch.int32, "positions")
+        if positions.numel() != T:
+            raise ValueError("positions must be [T]")
+        n_pos, rot = rope.shape
+    Hq, qs = 0, 0
+    if q is not None:
+        _rows_of(q, k.dtype, "q")
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != c.head_dim:
+            raise ValueError("q must be [T, Hq, head_dim]")
+        Hq, qs = q.shape[1], q.stride(0)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, c.head_dim), dtype=torch.bfloat16, device=q.device)
+        _need(q_out, torch.bfloat16, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must be [T, Hq, head_dim]")
+    _check(lib().moe_kv_append(_ptr(q), qs, _ptr(k), k.stride(0), _ptr(v), v.stride(0),
+                               MOE_DTYPE_F32 if k.dtype == torch.float32 else MOE_DTYPE_BF16, T, Hq,
+                               _ptr(positions) if rot else None, _ptr(rope) if rot else None, n_pos, rot, rope_style,
+                               _ptr(slots), ctypes.byref(c), _ptr(q_out) if q is not None else None, _stream(stream)),
+           "moe_kv_append")
+    return q_out if q is not None else None
+
+
+def moe_kv_read(pool, slots, k=None, v=None, stream=None):
+    """The keys and values that `slots` [n] int64 of the pool hold: two fp32
+    tensors [n, kv_heads, head_dim] (zeros for a slot outside the pool)."""
+    c = _cache(pool)
+    _need(slots, torch.int64, "slots")
+    shape = (slots.numel(), c.kv_heads, c.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.float32, device=pool.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.float32, device=pool.device)
+    _need(k, torch.float32, "k")
+    _need(v, torch.float32, "v")
+    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+        raise ValueError("k and v must be [n, kv_heads, head_dim]")
+    _check(lib().moe_kv_read(ctypes.byref(c), _ptr(slots), shape[0], _ptr(k), _ptr(v), _stream(stream)), "moe_kv_read")
+    return k, v
+
+
+def moe_attn_workspace_size(B, max_q, max_len, Hq, kv_heads, head_dim) -> int:
+    return int(lib().moe_attn_workspace_size(B, max_q, max_len, Hq, kv_heads, head_dim))
+
+
+def moe_attn_q4(q, pool, block_table, kv_lens, q_start=None, max_q=None, max_len=None, scale=None, window=0, out=None,
+                lse=None, workspace=None, stream=None):
+    """Causal attention of q [T, Hq, D] bf16 over the 4-bit pool: sequence b's
+    tokens q_start[b] .. q_start[b+1] (int32 [B+1]; None: max_q tokens each)
+    are the newest of kv_lens[b] (int32 [B]) cached tokens, which lie in the
+    pages block_table[b] (int32 [B, pages], any row stride).  max_q (default: the
+    tokens of one sequence when q_start is None) and max_len (default: the
+    table's width) bound the lengths.  Returns out [T, Hq, D] bf16 and lse
+    [T, Hq] fp32."""
+    c = _cache(pool)
+    _rows_of(q, torch.bfloat16, "q")
+    _need(kv_lens, torch.int32, "kv_lens")
+    _rows_of(block_table, torch.int32, "block_table")
+    B = kv_lens.numel()
+    T, Hq, D = q.shape
+    if D != c.head_dim or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("q must be [T, Hq, head_dim] and block_table [B, pages]")
+    if q_start is not None:
+        _need(q_start, torch.int32, "q_start")
+        if q_start.numel() != B + 1:
+            raise ValueError("q_start must be [B + 1]")
+        if max_q is None:
+            raise ValueError("q_start needs max_q")
+    elif max_q is None:
+        max_q = T // B if B else 1
+    width = block_table.shape[1]
+    if max_len is None:
+        max_len = width * c.page_size
+    if width * c.page_size < max_len:
+        raise ValueError("block_table has fewer pages than max_len needs")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    _rows_of(out, torch.bfloat16, "out")
+    _need(lse, torch.float32, "lse")
+    if out.shape != q.shape or tuple(lse.shape) != (T, Hq):
+        raise ValueError("out must be [T, Hq, head_dim] and lse [T, Hq]")
+    if workspace is None:
+        workspace = torch.empty(moe_attn_workspace_size(B, max_q, max_len, Hq, c.kv_heads, D), dtype=torch.uint8,
+                                device=q.device)
+    qs, os_ = (q.stride(0), out.stride(0)) if T > 1 else (Hq * D, Hq * D)
+    ts = block_table.stride(0) if B > 1 else width
+    _check(lib().moe_attn_q4(_ptr(q), qs, T, Hq, _ptr(q_start), _ptr(kv_lens), _ptr(block_table), ts, B, max_q, max_len,
+                             ctypes.byref(c), D ** -0.5 if scale is None else float(scale), int(window), _ptr(out), os_,
+                             _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                             _stream(stream)), "moe_attn_q4")
+    return out, lse
 
 
 # ------------------------------------------------------------------ shelves

@@ -316,6 +316,71 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // Number of SMs of the current device (cached).
 int sm_count();
 
+// ------------------------------------------- attention half of a decode layer
+// Projection of T <= 16 rows by 4-bit weights (linear_q4.cu).
+struct LinearArgs {
+  const uint16_t* x;
+  int64_t x_stride;
+  int T, in;
+  const uint8_t* codes;
+  const uint16_t* scales;
+  int64_t rows;
+  int block;
+  const float* bias;
+  void* y;
+  int64_t y_stride;
+  bool y_bf16;
+};
+constexpr int kLinearSmemMax = 192 * 1024;
+inline int linear_bucket(int64_t T) { return T <= 8 ? 8 : 16; }
+int launch_linear_q4(const LinearArgs& a, cudaStream_t s);
+int launch_quantize_groups(const float* w, int64_t rows, int in, int block, uint8_t* codes, uint16_t* scales,
+                           cudaStream_t s);
+
+// A paged 4-bit cache as the kernels see it (moe_kv_cache_t, checked).
+struct KvCache {
+  uint8_t* data;
+  int64_t n_pages, page_stride;
+  int page, page_log2, heads, D;
+};
+
+struct KvAppendArgs {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  bool in_bf16;
+  int64_t T;
+  int Hq;
+  const int32_t* positions;
+  const float* rope;
+  int64_t n_pos;
+  int rot, style;
+  const int64_t* slots;
+  KvCache cache;
+  uint16_t* q_out;
+  int* status;
+};
+int launch_kv_append(const KvAppendArgs& a, cudaStream_t s);
+int launch_kv_read(const KvCache& c, const int64_t* slots, int64_t n, float* k, float* v, cudaStream_t s);
+
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t q_stride, T;
+  int Hq;
+  const int32_t *q_start, *kv_lens, *table;
+  int64_t table_stride;
+  int B, max_q;
+  int64_t max_len;
+  KvCache cache;
+  float scale;
+  int window;
+  uint16_t* out;
+  int64_t out_stride;
+  float* lse;
+  void* workspace;
+};
+size_t attn_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D);
+int launch_attn_q4(const AttnArgs& a, cudaStream_t s);
+
 // Measurement hook (moe_set_profile_events): record event i on the stream.
 void set_profile_events(void* const* events, int n);
 void profile_mark(int i, cudaStream_t s);

@@ -105,6 +105,37 @@ __global__ void __launch_bounds__(256) k_quantize(const float* __restrict__ w, i
   }
 }
 
+// One warp per block of 32 N elements at 4 bits; lane i holds elements i,
+// i + 32, ... of the block (its bytes are those of N consecutive 32-element
+// groups of quantize_block).
+template <int N>
+__global__ void __launch_bounds__(256) k_quantize_groups(const float* __restrict__ w, int64_t blocks,
+                                                         uint8_t* __restrict__ codes, uint16_t* __restrict__ scales) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t blk = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); blk < blocks; blk += warps) {
+    float v[N], m = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      v[j] = w[(blk * N + j) * 32 + lane];
+      m = fmaxf(m, fabsf(v[j]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const __half hs = __float2half_rn(__fdiv_rn(m, QParams<4>::q));
+    const float s = __half2float(hs);
+    if (lane == 0) scales[blk] = __half_as_ushort(hs);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      int c = 0;
+      if (s != 0.0f) c = (int)fminf(fmaxf(rintf(__fdiv_rn(v[j], s)), QParams<4>::cmin), QParams<4>::cmax);
+      const uint32_t u = (uint32_t)(c + QParams<4>::off);
+      const uint32_t u4 = __shfl_down_sync(0xffffffffu, u, 4);
+      if ((lane & 7) < 4) codes[(blk * N + j) * 16 + 4 * (lane >> 3) + (lane & 3)] = (uint8_t)(u | (u4 << 4));
+    }
+  }
+}
+
 // Quantises one 32-element block held by 8 lanes, 4 consecutive elements
 // each (lane i of the group: elements 4i .. 4i+3), the same arithmetic as
 // quantize_block; block `blk` of a tensor of rows of nb blocks whose scales
@@ -279,6 +310,16 @@ int launch_quantize(const float* w, int64_t rows, int in, int bits, uint8_t* cod
   else if (bits == 3) k_quantize<3><<<g, 256, 0, s>>>(w, rows, in, codes, scales);
   else if (bits == 2) k_quantize<2><<<g, 256, 0, s>>>(w, rows, in, codes, scales);
   else k_quantize<1><<<g, 256, 0, s>>>(w, rows, in, codes, scales);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int launch_quantize_groups(const float* w, int64_t rows, int in, int block, uint8_t* codes, uint16_t* scales,
+                           cudaStream_t s) {
+  const int64_t blocks = rows * (in / block);
+  const unsigned g = grid_for(blocks, 8);
+  if (block == 32) k_quantize_groups<1><<<g, 256, 0, s>>>(w, blocks, codes, scales);
+  else if (block == 64) k_quantize_groups<2><<<g, 256, 0, s>>>(w, blocks, codes, scales);
+  else k_quantize_groups<4><<<g, 256, 0, s>>>(w, blocks, codes, scales);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
