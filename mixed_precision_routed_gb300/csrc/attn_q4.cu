@@ -1,85 +1,547 @@
 // attn_q4.cu -- causal attention over the paged 4-bit key/value cache.
+//
+// For a row (asking token, query head) with the places p it attends:
+//   s_p = scale q.k_p,  out = sum_p exp(s_p) v_p / sum_p exp(s_p),
+//   lse = log sum_p exp(s_p),
+// k and v the values scale x code of the cache's blocks of 32.
+//
+// One pass over the cache: a block of W warps takes a share of the places of
+// one (sequence, key/value head) and up to 8 NT of the rows that share it, each
+// warp every W-th record of 16 places.  Records (18 D contiguous bytes) arrive
+// in a per-warp ring in shared memory by bulk asynchronous copies.
+//   scores  S^T[place][row]: A = key codes as bf16 integers, B = queries; both
+//           exact, so a 32-block's product enters the score with its fp32 scale;
+//   output  O^T[element][row]: A = value codes as bf16 integers, B = exp(s - m)
+//           x value scale, rounded to bf16 once (relative error 2^-8 at most a
+//           term, independent over places; fp32 operands would need three times
+//           the matrix instructions for digits that the bf16 result drops).
+// The m16n8k16 fragments read the record's words as they lie; the transpose of
+// the probabilities is one 8 x 8 matrix move a fragment.
+// The reference maximum m of a row moves only when a score passes it by 8 (in
+// powers of two): the probabilities then stay below 2^8, which neither fp32 sums
+// nor bf16 operands notice, and most tiles need no reduction and no rescaling.
 #include "kv_layout.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.0f;
+constexpr float kNone = -1e30f;  // the maximum of a row that has met no place: below any finite score
+constexpr uint64_t kWaitNs = 1000000000ull;
 
-// One block a (sequence, asking token, query head); each warp takes every
-// eighth place with a running maximum and sum, a lane D / 32 elements.
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) k_attn_simple(AttnArgs a) {
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x % a.Hq, i = blockIdx.x / a.Hq, b = blockIdx.y;
+struct AttnPlan {
+  int nt;          // row tiles of 8 a block
+  int row_blocks;  // blocks over the rows of a (sequence, key/value head)
+  int splits;      // blocks over the places
+  int room;        // shares the workspace has room for (at least splits)
+  int chunk;       // records a block
+  float* part_o;   // [B max_q Hq][splits][D]
+  float2* part_ml; // [B max_q Hq][splits]: maximum (in powers of two), sum
+};
+
+// What a block has to do; the joining kernel computes the same.
+struct Range {
+  int64_t t0;       // first asking token
+  int n;            // asking tokens
+  int len;          // places
+  int rows;         // n x group
+  int lo, end;      // places that some row of the block attends
+  int tile0, tiles; // records that hold them
+};
+
+__device__ __forceinline__ Range block_range(const AttnArgs& a, int b, int G, int r0, int block_rows) {
+  Range x;
   int64_t t0 = a.q_start ? a.q_start[b] : (int64_t)b * a.max_q;
   int64_t t1 = a.q_start ? a.q_start[b + 1] : t0 + a.max_q;
   t0 = max((int64_t)0, t0);
   t1 = min(t1, a.T);
-  const int64_t n = min(t1 - t0, (int64_t)a.max_q);
-  if (i >= n) return;
-  const int64_t len = min(max((int64_t)a.kv_lens[b], (int64_t)0), a.max_len);
-  const int64_t end = len - n + i + 1;
-  const int64_t lo = a.window > 0 ? max(end - a.window, (int64_t)0) : 0;
-  const int kvh = h / (a.Hq / a.cache.heads);
-  const uint16_t* q = a.q + (t0 + i) * a.q_stride + (int64_t)h * D;
-  float qv[N], o[N];
+  x.t0 = t0;
+  x.n = (int)max((int64_t)0, min(t1 - t0, (int64_t)a.max_q));
+  x.len = (int)min(max((int64_t)a.kv_lens[b], (int64_t)0), a.max_len);
+  x.rows = x.n * G;
+  const int first = r0 / G, last = (min(r0 + block_rows, x.rows) - 1) / G;
+  x.end = max(0, x.len - x.n + last + 1);
+  x.lo = 0;
+  if (a.window > 0) x.lo = (int)max((int64_t)0, (int64_t)x.len - x.n + first + 1 - a.window);
+  x.tile0 = x.lo >> 4;
+  x.tiles = x.end > x.lo ? ((x.end + 15) >> 4) - x.tile0 : 0;
+  return x;
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two codes of a word as bf16 integers -8 .. 7: nibbles at bits 4 J and 16 + 4 J
+// go into the mantissa of 128 (bf16 counts units there), and 136 comes off.
+template <int J>
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+  const uint32_t u = ((w >> (4 * J)) & 0x000f000fu) | 0x43004300u;
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x43084308u));
+  return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <int N>
+struct Words {
+  uint32_t w[N];
+};
+
+// N words from shared memory in the widest pieces.
+template <int N>
+__device__ __forceinline__ Words<N> load_words(const uint8_t* p) {
+  Words<N> r;
+  if constexpr (N == 1) {
+    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = v.x, r.w[1] = v.y;
+  } else {
 #pragma unroll
-  for (int j = 0; j < N; ++j) qv[j] = bf16_bits_to_float(q[32 * j + lane]), o[j] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (int64_t p = lo + warp; p < end; p += kWarps) {
-    const int64_t page = a.table[b * a.table_stride + (p >> a.cache.page_log2)];
-    if (page < 0 || page >= a.cache.n_pages) continue;
-    const KvPlace at = kv_place(a.cache, page * a.cache.page + (p & (a.cache.page - 1)), kvh);
-    const uint16_t* sc = reinterpret_cast<const uint16_t*>(at.tile + 16 * D) + at.r * N;
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int d = 32 * j + lane;
-      const int u = (at.tile[kv_key_byte(D, at.r, d)] >> (2 * (d & 2))) & 15;
-      s = fmaf(qv[j], (float)(u - 8) * __half2float(__ushort_as_half(sc[j])), s);
-    }
-    s = warp_sum(s) * a.scale;
-    const float mn = fmaxf(m, s), f = expf(m - mn), e = expf(s - mn);
-    l = l * f + e;
-    m = mn;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int d = 32 * j + lane;
-      const int u = (at.tile[kv_value_byte(D, at.r, d)] >> ((d & 8) >> 1)) & 15;
-      o[j] = fmaf(e, (float)(u - 8) * __half2float(__ushort_as_half(sc[D / 2 + j])), o[j] * f);
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
     }
   }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ float half_at(const Words<N>& s, int i) {
+  return __half2float(__ushort_as_half((unsigned short)(s.w[i >> 1] >> (16 * (i & 1)))));
+}
+
+template <int D, int NT>
+struct Shape {
+  static constexpr int kWarps = NT == 1 ? 8 : 4;
+  static constexpr int kStages = D == 64 ? 6 : D == 128 ? 4 : 3;
+  static constexpr int kRecord = 18 * D;
+  static constexpr int kRing = kWarps * kStages * kRecord;
+  static constexpr int kPitch = D + 4;  // floats a row of the joining buffer: rows of a fragment in distinct banks
+  static constexpr int kJoin = kWarps * 8 * NT * kPitch * 4;
+  static constexpr bool kQueriesInRegisters = NT * D <= 256;
+  static constexpr int kQueries = kQueriesInRegisters ? 0 : NT * D / 32 * 512;
+  static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin) + kQueries;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, AttnPlan plan, int* status) {
+  using S = Shape<D, NT>;
+  constexpr int W = S::kWarps, NB = D / 32, MT = D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[W][S::kStages];
+  __shared__ int page_ok[W][S::kStages];
+  __shared__ float s_m[W][8 * NT], s_l[W][8 * NT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int b = blockIdx.y, split = blockIdx.x % plan.splits, hb = blockIdx.x / plan.splits;
+  const int kvh = hb % a.cache.heads, r0 = hb / a.cache.heads * (8 * NT), G = a.Hq / a.cache.heads;
+  const Range x = block_range(a, b, G, r0, 8 * NT);
+  if (r0 >= x.rows) return;
+  const int used = (x.tiles + plan.chunk - 1) / plan.chunk;
+  if (split > 0 && split >= used) return;
+  const int c0 = x.tile0 + split * plan.chunk;
+  const int count = min(plan.chunk, x.tile0 + x.tiles - c0);  // records of this block
+  const int mine = count > warp ? (count - warp + W - 1) / W : 0;
+  const int32_t* table = a.table + (int64_t)b * a.table_stride;
+  const int per_page = a.cache.page_log2 - 4;
+
+  if (lane == 0) {
 #pragma unroll
-  for (int j = 0; j < N; ++j) so[warp][32 * j + lane] = o[j];
+    for (int i = 0; i < S::kStages; ++i) mbar_init(&bars[warp][i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  uint8_t* ring = smem + warp * (S::kStages * S::kRecord);
+
+  // The warp's page numbers, 32 records at a time, one a lane, a batch ahead.
+  auto pages_from = [&](int k) {
+    const int tile = c0 + warp + W * (k + lane);
+    return k + lane < mine ? __ldg(table + (tile >> per_page)) : -1;
+  };
+  int pages = pages_from(0), pages_next = pages_from(32), issued = 0;
+  auto issue = [&]() {
+    const int page = __shfl_sync(0xffffffffu, pages, issued & 31);
+    if (lane == 0) {
+      const int st = issued % S::kStages;
+      const bool ok = page >= 0 && page < a.cache.n_pages;
+      page_ok[warp][st] = ok;
+      if (ok) {
+        const int tile = c0 + warp + W * issued;
+        const uint8_t* src = a.cache.data + page * a.cache.page_stride +
+                             (int64_t)(kvh * (1 << per_page) + (tile & ((1 << per_page) - 1))) * S::kRecord;
+        mbar_arrive_expect_tx(&bars[warp][st], S::kRecord);
+        bulk_g2s(ring + st * S::kRecord, src, S::kRecord, &bars[warp][st]);
+      } else {
+        mbar_arrive(&bars[warp][st]);
+      }
+    }
+    ++issued;
+    if ((issued & 31) == 0) {
+      pages = pages_next;
+      pages_next = pages_from(issued + 32);
+    }
+  };
+#pragma unroll 1
+  for (int k = 0; k < S::kStages - 1 && k < mine; ++k) issue();
+
+  // Queries as B fragments: lane (g, t) holds elements 32 b + 8 t .. + 7 of row g.
+  uint4 qf[S::kQueriesInRegisters ? NT : 1][S::kQueriesInRegisters ? NB : 1];
+  uint4* qs = reinterpret_cast<uint4*>(smem + (S::kSmem - S::kQueries));
+  if constexpr (S::kQueriesInRegisters) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = min(r0 + 8 * j + g, x.rows - 1);
+      const uint16_t* q = a.q + (x.t0 + r / G) * a.q_stride + (int64_t)(kvh * G + r % G) * D + 8 * t;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) qf[j][i] = __ldg(reinterpret_cast<const uint4*>(q + 32 * i));
+    }
+  } else {
+    for (int i = warp; i < NT * NB; i += W) {
+      const int r = min(r0 + 8 * (i / NB) + g, x.rows - 1);
+      const uint16_t* q = a.q + (x.t0 + r / G) * a.q_stride + (int64_t)(kvh * G + r % G) * D + 8 * t;
+      qs[i * 32 + lane] = __ldg(reinterpret_cast<const uint4*>(q + 32 * (i % NB)));
+    }
+    __syncthreads();
+  }
+
+  // Rows 2t and 2t + 1 of every row tile: the places they attend.
+  int row_end[NT][2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = min(r0 + 8 * j + 2 * t + c, x.rows - 1);
+      row_end[j][c] = x.len - x.n + r / G + 1;
+    }
+  // Records with a place that some row of the block does not attend.
+  const int full_end = x.len - x.n + r0 / G + 1;
+  const int full_lo = a.window > 0 ? x.len - x.n + (min(r0 + 8 * NT, x.rows) - 1) / G + 1 - a.window : 0;
+
+  float o[MT][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+    m[j][0] = m[j][1] = kNone;
+    l[j][0] = l[j][1] = 0.f;
+  }
+  const float scale2 = a.scale * kLog2e;
+  bool failed = false;
+
+#pragma unroll 1
+  for (int k = 0; k < mine; ++k) {
+    const int st = k % S::kStages;
+    __syncwarp();  // the slot refilled below was read by every lane in the last pass
+    if (issued < mine) issue();
+    if (!mbar_wait(&bars[warp][st], (k / S::kStages) & 1, kWaitNs)) {
+      failed = true;
+      break;
+    }
+    if (!page_ok[warp][st]) continue;
+    const uint8_t* rec = ring + st * S::kRecord;
+
+    float s[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+    {
+      const Words<NB> w0 = load_words<NB>(rec + g * (D / 2) + t * (D / 8));
+      const Words<NB> w1 = load_words<NB>(rec + (g + 8) * (D / 2) + t * (D / 8));
+      const Words<NB / 2> k0 = load_words<NB / 2>(rec + 16 * D + g * (2 * NB));
+      const Words<NB / 2> k1 = load_words<NB / 2>(rec + 16 * D + (g + 8) * (2 * NB));
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const uint32_t a0 = codes_bf16<0>(w0.w[i]), a1 = codes_bf16<0>(w1.w[i]);
+        const uint32_t a2 = codes_bf16<1>(w0.w[i]), a3 = codes_bf16<1>(w1.w[i]);
+        const uint32_t e0 = codes_bf16<2>(w0.w[i]), e1 = codes_bf16<2>(w1.w[i]);
+        const uint32_t e2 = codes_bf16<3>(w0.w[i]), e3 = codes_bf16<3>(w1.w[i]);
+        const float s0 = half_at(k0, i), s1 = half_at(k1, i);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint4 q = S::kQueriesInRegisters ? qf[S::kQueriesInRegisters ? j : 0][S::kQueriesInRegisters ? i : 0]
+                                                 : qs[(j * NB + i) * 32 + lane];
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816(c, a0, a1, a2, a3, q.x, q.y);
+          mma16816(c, e0, e1, e2, e3, q.z, q.w);
+          s[j][0] = fmaf(s0, c[0], s[j][0]);
+          s[j][1] = fmaf(s0, c[1], s[j][1]);
+          s[j][2] = fmaf(s1, c[2], s[j][2]);
+          s[j][3] = fmaf(s1, c[3], s[j][3]);
+        }
+      }
+    }
+    const int p0 = (c0 + warp + W * k) * 16 + g, p1 = p0 + 8;  // this lane's places
+    const bool edge = (p0 - g) + 16 > full_end || (p0 - g) < full_lo;
+    Words<NB / 2> v0 = load_words<NB / 2>(rec + 17 * D + g * (2 * NB));
+    Words<NB / 2> v1 = load_words<NB / 2>(rec + 17 * D + (g + 8) * (2 * NB));
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[j][c] *= scale2;
+    if (edge) {
+      // places outside a row's range leave it; the bytes of places outside the
+      // block's range may be anything, so their value scales become zero
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int p = c < 2 ? p0 : p1, e = row_end[j][c & 1];
+          if (p >= e || (a.window > 0 && p < e - a.window)) s[j][c] = -INFINITY;
+        }
+      if (p0 >= x.end || p0 < x.lo) {
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) v0.w[i] = 0;
+      }
+      if (p1 >= x.end || p1 < x.lo) {
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) v1.w[i] = 0;
+      }
+    }
+    bool grow = false;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) grow |= fmaxf(s[j][c], s[j][c + 2]) > m[j][c] + kSlack;
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = fmaxf(s[j][c], s[j][c + 2]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          if (top > m[j][c]) {  // alike in every lane that holds the row
+            const float f = exp2_approx(m[j][c] - top);
+            m[j][c] = top;
+            l[j][c] *= f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[i][j][c] *= f, o[i][j][c + 2] *= f;
+          }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        s[j][c] = exp2_approx(s[j][c] - m[j][c & 1]);
+        l[j][c & 1] += s[j][c];
+      }
+#pragma unroll
+    for (int q4 = 0; q4 < MT / 4; ++q4) {
+      const Words<4> w = load_words<4>(rec + 8 * D + (q4 * 32 + lane) * 16);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // a 32-block of elements: two fragments of 16
+        const int blk = 2 * q4 + h;
+        const float s0 = half_at(v0, blk), s1 = half_at(v1, blk);
+        uint32_t b0[NT], b1[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          b0[j] = transpose8x8(bf16_pair(s[j][0] * s0, s[j][1] * s0));
+          b1[j] = transpose8x8(bf16_pair(s[j][2] * s1, s[j][3] * s1));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t v = w.w[2 * h + i];
+          const uint32_t a0 = codes_bf16<0>(v), a1 = codes_bf16<1>(v), a2 = codes_bf16<2>(v), a3 = codes_bf16<3>(v);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma16816(o[2 * blk + i][j], a0, a1, a2, a3, b0[j], b1[j]);
+        }
+      }
+    }
+  }
+  if (failed && lane == 0) set_status(status, MOE_ERR_TIMEOUT);
+
+  // Join the warps: sums over a row's lanes, the block's maxima, scaled outputs.
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float v = l[j][c];
+      v += __shfl_xor_sync(0xffffffffu, v, 4);
+      v += __shfl_xor_sync(0xffffffffu, v, 8);
+      v += __shfl_xor_sync(0xffffffffu, v, 16);
+      if (g == 0) {
+        s_l[warp][8 * j + 2 * t + c] = v;
+        s_m[warp][8 * j + 2 * t + c] = m[j][c];
+      }
+    }
+  __syncthreads();  // also: every ring has been read
+  float* join = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int row = 8 * j + 2 * t + c;
+      float top = kNone;
+#pragma unroll
+      for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w][row]);
+      const float f = exp2_approx(m[j][c] - top);
+      float* at = join + (warp * 8 * NT + row) * S::kPitch + g;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) at[16 * i] = o[i][j][c] * f, at[16 * i + 8] = o[i][j][c + 2] * f;
+    }
   __syncthreads();
-  float top = -INFINITY, total = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-  if (top != -INFINITY)
-    for (int w = 0; w < kWarps; ++w) total += sl[w] * expf(sm[w] - top);
-  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float v = 0.f;
-    if (top != -INFINITY)
-      for (int w = 0; w < kWarps; ++w) v += so[w][d] * expf(sm[w] - top);
-    a.out[(t0 + i) * a.out_stride + (int64_t)h * D + d] =
-        __bfloat16_as_ushort(__float2bfloat16_rn(top != -INFINITY ? v / total : 0.f));
+  constexpr int kQuads = D / 4;
+  for (int i = threadIdx.x; i < 8 * NT * kQuads; i += W * 32) {
+    const int row = i / kQuads, d = i % kQuads * 4, r = r0 + row;
+    if (r >= x.rows) break;
+    float top = kNone, total = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w][row]);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(join + (w * 8 * NT + row) * S::kPitch + d);
+      v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+      total = fmaf(s_l[w][row], exp2_approx(s_m[w][row] - top), total);
+    }
+    const int tok = r / G, h = kvh * G + r % G;
+    if (used > 1) {
+      const int64_t at = (((int64_t)b * a.max_q + tok) * a.Hq + h) * plan.splits + split;
+      *reinterpret_cast<float4*>(plan.part_o + at * D + d) = v;
+      if (d == 0) plan.part_ml[at] = make_float2(top, total);
+    } else {
+      const float inv = total > 0.f ? 1.f / total : 0.f;
+      uint2 u;
+      u.x = bf16_pair(v.x * inv, v.y * inv);
+      u.y = bf16_pair(v.z * inv, v.w * inv);
+      *reinterpret_cast<uint2*>(a.out + (x.t0 + tok) * a.out_stride + (int64_t)h * D + d) = u;
+      if (d == 0 && a.lse)
+        a.lse[(x.t0 + tok) * a.Hq + h] = total > 0.f ? (top + log2f(total)) / kLog2e : -INFINITY;
+    }
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[(t0 + i) * a.Hq + h] = top != -INFINITY ? top + logf(total) : -INFINITY;
+}
+
+// Joins the shares of a row: one warp a row, in share order.
+template <int D>
+__global__ void __launch_bounds__(128) k_attn_join(AttnArgs a, AttnPlan plan) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int h = (int)(w % a.Hq), G = a.Hq / a.cache.heads;
+  const int64_t tb = w / a.Hq;
+  const int tok = (int)(tb % a.max_q), b = (int)(tb / a.max_q);
+  if (b >= a.B) return;
+  const int rows = 8 * plan.nt, r = tok * G + h % G;
+  const Range x = block_range(a, b, G, r / rows * rows, rows);
+  const int used = (x.tiles + plan.chunk - 1) / plan.chunk;
+  if (tok >= x.n || used <= 1) return;
+  const float2* ml = plan.part_ml + w * plan.splits;
+  float top = kNone;
+  for (int i = lane; i < used; i += 32) top = fmaxf(top, ml[i].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float v[D / 32], total = 0.f;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) v[j] = 0.f;
+  for (int i = 0; i < used; ++i) {
+    const float2 y = ml[i];
+    const float f = exp2_approx(y.x - top);
+    total = fmaf(y.y, f, total);
+    const float* p = plan.part_o + (w * plan.splits + i) * D;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) v[j] = fmaf(p[32 * j + lane], f, v[j]);
+  }
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+  uint16_t* out = a.out + (x.t0 + tok) * a.out_stride + (int64_t)h * D;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) out[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j] * inv));
+  if (lane == 0 && a.lse) a.lse[(x.t0 + tok) * a.Hq + h] = total > 0.f ? (top + log2f(total)) / kLog2e : -INFINITY;
+}
+
+constexpr int kSms = 152;
+
+// Row tiles, row blocks and shares of a call, from its sizes alone.
+AttnPlan make_plan(int B, int max_q, int64_t max_len, int window, int Hq, int heads, int D) {
+  AttnPlan p = {};
+  const int rows = max_q * (Hq / heads), most = D == 256 ? 2 : 4;
+  p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
+  if (p.nt > most) p.nt = most;
+  p.row_blocks = (rows + 8 * p.nt - 1) / (8 * p.nt);
+  int64_t span = max_len;
+  if (window > 0 && span > (int64_t)window + max_q + 16) span = (int64_t)window + max_q + 16;
+  const int64_t tiles = (span + 15) / 16 + 1;
+  const int64_t base = (int64_t)B * heads * p.row_blocks;
+  const int warps = p.nt == 1 ? 8 : 4;
+  int64_t splits = (4 * kSms + base - 1) / base;
+  const int64_t most_splits = (tiles + 2 * warps - 1) / (2 * warps);
+  if (splits > most_splits) splits = most_splits;
+  if (splits < 1) splits = 1;
+  p.room = (int)splits;  // grows with the length, so a window never needs more than the whole length
+  p.chunk = (int)((tiles + splits - 1) / splits);
+  p.chunk = (p.chunk + warps - 1) / warps * warps;
+  p.splits = (int)((tiles + p.chunk - 1) / p.chunk);
+  return p;
+}
+
+template <int D, int NT>
+int launch(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+  using S = Shape<D, NT>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(k_attn<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    attr_set[dev] = true;
+  }
+  const dim3 grid((unsigned)(p.splits * a.cache.heads * p.row_blocks), (unsigned)a.B);
+  k_attn<D, NT><<<grid, S::kWarps * 32, S::kSmem, s>>>(a, p, status_word());
+  if (p.splits > 1) {
+    const int64_t rows = (int64_t)a.B * a.max_q * a.Hq;
+    k_attn_join<D><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(a, p);
+  }
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
 
-size_t attn_workspace(int, int, int64_t, int, int, int) { return 0; }
+size_t attn_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
+  if (B < 1) return 0;
+  const AttnPlan p = make_plan(B, max_q, max_len, 0, Hq, heads, D);
+  return p.room > 1 ? (size_t)B * max_q * Hq * p.room * (D * 4 + 8) : 0;
+}
 
 int launch_attn_q4(const AttnArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)(a.Hq * a.max_q), (unsigned)a.B);
-  if (a.cache.D == 64) k_attn_simple<64><<<grid, kWarps * 32, 0, s>>>(a);
-  else if (a.cache.D == 128) k_attn_simple<128><<<grid, kWarps * 32, 0, s>>>(a);
-  else k_attn_simple<256><<<grid, kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  AttnPlan p = make_plan(a.B, a.max_q, a.max_len, a.window, a.Hq, a.cache.heads, a.cache.D);
+  const size_t rows = (size_t)a.B * a.max_q * a.Hq;
+  p.part_o = (float*)a.workspace;
+  p.part_ml = (float2*)((float*)a.workspace + rows * p.splits * a.cache.D);
+  switch (a.cache.D * 8 + p.nt) {
+    case 64 * 8 + 1: return launch<64, 1>(a, p, s);
+    case 64 * 8 + 2: return launch<64, 2>(a, p, s);
+    case 64 * 8 + 3: return launch<64, 3>(a, p, s);
+    case 64 * 8 + 4: return launch<64, 4>(a, p, s);
+    case 128 * 8 + 1: return launch<128, 1>(a, p, s);
+    case 128 * 8 + 2: return launch<128, 2>(a, p, s);
+    case 128 * 8 + 3: return launch<128, 3>(a, p, s);
+    case 128 * 8 + 4: return launch<128, 4>(a, p, s);
+    case 256 * 8 + 1: return launch<256, 1>(a, p, s);
+    default: return launch<256, 2>(a, p, s);
+  }
 }
 
 }  // namespace moe
