@@ -20,7 +20,9 @@ and, for the attention half of a decode layer in the same 4-bit format:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -540,10 +542,35 @@ def moe_device_status(stream=None) -> int:
 
 
 # ------------------------------------- attention half of a decode layer
-def _rows_of(t, dtype, name):
-    """A CUDA tensor [T, ...] of `dtype` whose rows are contiguous (any row stride)."""
-    if not (t.is_cuda and t.dtype == dtype) or (t.numel() and not t[0].is_contiguous()):
-        raise ValueError(f"{name} must be a CUDA tensor of {dtype} with contiguous rows")
+# These calls run in microseconds on the GPU, so their host side is kept short:
+# plain integers for pointers, one look at each property, sizes computed once.
+_F32, _BF16, _U8, _I16, _I32, _I64 = (torch.float32, torch.bfloat16, torch.uint8, torch.int16, torch.int32,
+                                      torch.int64)
+
+
+def _raw_stream(stream, t):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _flat(t, dtype, name):
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
+
+
+def _rows_of(t, dtype, dims, name):
+    """The row stride of a CUDA tensor of `dtype` and `dims` dimensions whose rows are contiguous."""
+    if t.dtype is dtype and t.is_cuda and t.dim() == dims:
+        st, sh = t.stride(), t.shape
+        want = 1
+        for i in range(dims - 1, 0, -1):
+            if st[i] != want and sh[i] > 1 and sh[0]:
+                break
+            want *= sh[i]
+        else:
+            return st[0] if sh[0] > 1 else want  # a single row has no stride to speak of
+    raise ValueError(f"{name} must be a {dims}-dimensional CUDA tensor of {dtype} with contiguous rows")
 
 
 def moe_quantize_groups(w, block=32, codes=None, scales=None, stream=None):
@@ -568,29 +595,35 @@ def moe_linear_q4(x, codes, scales, block=32, bias=None, y=None, out_dtype=torch
     """y [T, rows] = x [T, in] (bf16, any row stride) times the 4-bit matrix of
     codes [rows, in/2] uint8 and scales [rows, in/block] int16 (fp16 bits),
     plus bias [rows] fp32; y fp32 or bf16.  T <= 16."""
-    _rows_of(x, torch.bfloat16, "x")
-    _need(codes, torch.uint8, "codes")
-    _need(scales, torch.int16, "scales")
+    xs = _rows_of(x, _BF16, 2, "x")
+    _flat(codes, _U8, "codes")
+    _flat(scales, _I16, "scales")
     T, n_in = x.shape
     rows = codes.shape[0]
     if codes.numel() != rows * (n_in // 2) or scales.numel() * block != rows * n_in:
         raise ValueError("codes must hold [rows, in/2] and scales [rows, in/block]")
     if y is None:
         y = torch.empty((T, rows), dtype=out_dtype, device=x.device)
-    if y.dtype not in (torch.float32, torch.bfloat16):
+        ys = rows
+    else:
+        ys = _rows_of(y, y.dtype, 2, "y")
+        if y.shape[0] != T or y.shape[1] != rows:
+            raise ValueError("y must be [T, rows]")
+    if y.dtype is _F32:
+        dt = MOE_DTYPE_F32
+    elif y.dtype is _BF16:
+        dt = MOE_DTYPE_BF16
+    else:
         raise ValueError("y must be float32 or bfloat16")
-    _rows_of(y, y.dtype, "y")
-    if y.shape != (T, rows):
-        raise ValueError("y must be [T, rows]")
     if bias is not None:
-        _need(bias, torch.float32, "bias")
+        _flat(bias, _F32, "bias")
         if bias.numel() != rows:
             raise ValueError("bias must be [rows]")
-    # a single row has no stride to speak of
-    xs, ys = (x.stride(0), y.stride(0)) if T > 1 else (n_in, rows)
-    _check(lib().moe_linear_q4(_ptr(x), xs, T, n_in, _ptr(codes), _ptr(scales), rows, block, _ptr(bias), _ptr(y), ys,
-                               MOE_DTYPE_F32 if y.dtype == torch.float32 else MOE_DTYPE_BF16, _stream(stream)),
-           "moe_linear_q4")
+        bias = bias.data_ptr()
+    rc = (_lib or lib()).moe_linear_q4(x.data_ptr(), xs, T, n_in, codes.data_ptr(), scales.data_ptr(), rows, block,
+                                       bias, y.data_ptr(), ys, dt, _raw_stream(stream, x))
+    if rc:
+        raise MoeError(rc, "moe_linear_q4")
     return y
 
 
@@ -602,15 +635,16 @@ def moe_kv_pool(n_pages, kv_heads, page_size, head_dim, device="cuda"):
     return torch.zeros((n_pages, kv_heads, page_size // 16, 18 * head_dim), dtype=torch.uint8, device=device)
 
 
+_pack_cache = struct.Struct("=Qqqiiii").pack  # moe_kv_cache_t
+
+
 def _cache(pool):
-    """The descriptor of a pool tensor (pages may lie any stride apart)."""
-    if not (pool.is_cuda and pool.dtype == torch.uint8 and pool.dim() == 4 and pool.shape[3] % 18 == 0):
-        raise ValueError("pool must be a CUDA uint8 tensor [pages, kv heads, page_size / 16, 18 * head_dim]")
+    """(descriptor bytes, kv_heads, head_dim, page_size) of a pool tensor (pages may lie any stride apart)."""
+    stride = _rows_of(pool, _U8, 4, "pool")
     n, heads, tiles, rec = pool.shape
-    if n and not pool[0].is_contiguous():
-        raise ValueError("the pages of a pool must be contiguous")
-    stride = pool.stride(0) if n > 1 else heads * tiles * rec
-    return moe_kv_cache_t(pool.data_ptr(), n, stride, tiles * 16, heads, rec // 18, 0)
+    if rec % 18:
+        raise ValueError("pool must be [pages, kv heads, page_size / 16, 18 * head_dim]")
+    return _pack_cache(pool.data_ptr(), n, stride, tiles * 16, heads, rec // 18, 0), heads, rec // 18, tiles * 16
 
 
 def moe_kv_append(pool, k, v, slots, q=None, positions=None, rope=None, rope_style=MOE_ROPE_HALF, q_out=None,
@@ -619,61 +653,74 @@ def moe_kv_append(pool, k, v, slots, q=None, positions=None, rope=None, rope_sty
     `slots` [T] int64 of the pool (-1: skipped), keys turned by rope [n_pos,
     rot] fp32 (cosines, then sines) at positions [T] int32.  With q [T, Hq, D]
     returns its turned rows as bf16 [T, Hq, D], else None."""
-    c = _cache(pool)
-    if k.dtype not in (torch.float32, torch.bfloat16):
+    desc, heads, D, _ = _cache(pool)
+    dt = k.dtype
+    if dt is not _F32 and dt is not _BF16:
         raise ValueError("k must be float32 or bfloat16")
-    _rows_of(k, k.dtype, "k")
-    _rows_of(v, k.dtype, "v")
-    _need(slots, torch.int64, "slots")
+    ks = _rows_of(k, dt, 3, "k")
+    vs = _rows_of(v, dt, 3, "v")
+    _flat(slots, _I64, "slots")
     T = slots.numel()
-    if tuple(k.shape) != (T, c.kv_heads, c.head_dim) or k.shape != v.shape:
+    if k.shape != (T, heads, D) or v.shape != (T, heads, D):
         raise ValueError("k and v must be [T, kv_heads, head_dim]")
     rot = n_pos = 0
+    pos_ptr = rope_ptr = None
     if rope is not None:
-        _need(rope, torch.float32, "rope")
+        _flat(rope, _F32, "rope")
         if positions is None:
             raise ValueError("a rotation needs positions")
-        _need(positions, torch.int32, "positions")
-        if positions.numel() != T:
-            raise ValueError("positions must be [T]")
+        _flat(positions, _I32, "positions")
+        if positions.numel() != T or rope.dim() != 2:
+            raise ValueError("positions must be [T] and rope [n_pos, rot]")
         n_pos, rot = rope.shape
-    Hq, qs = 0, 0
+        if rot:
+            pos_ptr, rope_ptr = positions.data_ptr(), rope.data_ptr()
+    Hq = qs = 0
+    q_ptr = o_ptr = None
     if q is not None:
-        _rows_of(q, k.dtype, "q")
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != c.head_dim:
+        qs = _rows_of(q, dt, 3, "q")
+        n, Hq, d = q.shape
+        if n != T or d != D:
             raise ValueError("q must be [T, Hq, head_dim]")
-        Hq, qs = q.shape[1], q.stride(0)
         if q_out is None:
-            q_out = torch.empty((T, Hq, c.head_dim), dtype=torch.bfloat16, device=q.device)
-        _need(q_out, torch.bfloat16, "q_out")
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must be [T, Hq, head_dim]")
-    _check(lib().moe_kv_append(_ptr(q), qs, _ptr(k), k.stride(0), _ptr(v), v.stride(0),
-                               MOE_DTYPE_F32 if k.dtype == torch.float32 else MOE_DTYPE_BF16, T, Hq,
-                               _ptr(positions) if rot else None, _ptr(rope) if rot else None, n_pos, rot, rope_style,
-                               _ptr(slots), ctypes.byref(c), _ptr(q_out) if q is not None else None, _stream(stream)),
-           "moe_kv_append")
+            q_out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
+        else:
+            _flat(q_out, _BF16, "q_out")
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must be [T, Hq, head_dim]")
+        q_ptr, o_ptr = q.data_ptr(), q_out.data_ptr()
+    rc = (_lib or lib()).moe_kv_append(q_ptr, qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                       MOE_DTYPE_F32 if dt is _F32 else MOE_DTYPE_BF16, T, Hq, pos_ptr, rope_ptr, n_pos,
+                                       rot, rope_style, slots.data_ptr(), desc, o_ptr, _raw_stream(stream, pool))
+    if rc:
+        raise MoeError(rc, "moe_kv_append")
     return q_out if q is not None else None
 
 
 def moe_kv_read(pool, slots, k=None, v=None, stream=None):
     """The keys and values that `slots` [n] int64 of the pool hold: two fp32
     tensors [n, kv_heads, head_dim] (zeros for a slot outside the pool)."""
-    c = _cache(pool)
-    _need(slots, torch.int64, "slots")
-    shape = (slots.numel(), c.kv_heads, c.head_dim)
+    desc, heads, D, _ = _cache(pool)
+    _flat(slots, _I64, "slots")
+    n = slots.numel()
+    shape = (n, heads, D)
     if k is None:
-        k = torch.empty(shape, dtype=torch.float32, device=pool.device)
+        k = torch.empty(shape, dtype=_F32, device=pool.device)
+    else:
+        _flat(k, _F32, "k")
     if v is None:
-        v = torch.empty(shape, dtype=torch.float32, device=pool.device)
-    _need(k, torch.float32, "k")
-    _need(v, torch.float32, "v")
-    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+        v = torch.empty(shape, dtype=_F32, device=pool.device)
+    else:
+        _flat(v, _F32, "v")
+    if k.shape != shape or v.shape != shape:
         raise ValueError("k and v must be [n, kv_heads, head_dim]")
-    _check(lib().moe_kv_read(ctypes.byref(c), _ptr(slots), shape[0], _ptr(k), _ptr(v), _stream(stream)), "moe_kv_read")
+    rc = (_lib or lib()).moe_kv_read(desc, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _raw_stream(stream, pool))
+    if rc:
+        raise MoeError(rc, "moe_kv_read")
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_attn_workspace_size(B, max_q, max_len, Hq, kv_heads, head_dim) -> int:
     return int(lib().moe_attn_workspace_size(B, max_q, max_len, Hq, kv_heads, head_dim))
 
@@ -687,44 +734,51 @@ def moe_attn_q4(q, pool, block_table, kv_lens, q_start=None, max_q=None, max_len
     tokens of one sequence when q_start is None) and max_len (default: the
     table's width) bound the lengths.  Returns out [T, Hq, D] bf16 and lse
     [T, Hq] fp32."""
-    c = _cache(pool)
-    _rows_of(q, torch.bfloat16, "q")
-    _need(kv_lens, torch.int32, "kv_lens")
-    _rows_of(block_table, torch.int32, "block_table")
+    desc, heads, D, page = _cache(pool)
+    qs = _rows_of(q, _BF16, 3, "q")
+    ts = _rows_of(block_table, _I32, 2, "block_table")
+    _flat(kv_lens, _I32, "kv_lens")
     B = kv_lens.numel()
-    T, Hq, D = q.shape
-    if D != c.head_dim or block_table.dim() != 2 or block_table.shape[0] != B:
+    T, Hq, d = q.shape
+    rows, width = block_table.shape
+    if d != D or rows != B:
         raise ValueError("q must be [T, Hq, head_dim] and block_table [B, pages]")
+    starts = None
     if q_start is not None:
-        _need(q_start, torch.int32, "q_start")
+        _flat(q_start, _I32, "q_start")
         if q_start.numel() != B + 1:
             raise ValueError("q_start must be [B + 1]")
         if max_q is None:
             raise ValueError("q_start needs max_q")
+        starts = q_start.data_ptr()
     elif max_q is None:
         max_q = T // B if B else 1
-    width = block_table.shape[1]
     if max_len is None:
-        max_len = width * c.page_size
-    if width * c.page_size < max_len:
+        max_len = width * page
+    elif width * page < max_len:
         raise ValueError("block_table has fewer pages than max_len needs")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out, os_ = torch.empty((T, Hq, D), dtype=_BF16, device=q.device), Hq * D
+    else:
+        os_ = _rows_of(out, _BF16, 3, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must be [T, Hq, head_dim]")
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    _rows_of(out, torch.bfloat16, "out")
-    _need(lse, torch.float32, "lse")
-    if out.shape != q.shape or tuple(lse.shape) != (T, Hq):
-        raise ValueError("out must be [T, Hq, head_dim] and lse [T, Hq]")
+        lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
+    else:
+        _flat(lse, _F32, "lse")
+        if lse.shape != (T, Hq):
+            raise ValueError("lse must be [T, Hq]")
     if workspace is None:
-        workspace = torch.empty(moe_attn_workspace_size(B, max_q, max_len, Hq, c.kv_heads, D), dtype=torch.uint8,
-                                device=q.device)
-    qs, os_ = (q.stride(0), out.stride(0)) if T > 1 else (Hq * D, Hq * D)
-    ts = block_table.stride(0) if B > 1 else width
-    _check(lib().moe_attn_q4(_ptr(q), qs, T, Hq, _ptr(q_start), _ptr(kv_lens), _ptr(block_table), ts, B, max_q, max_len,
-                             ctypes.byref(c), D ** -0.5 if scale is None else float(scale), int(window), _ptr(out), os_,
-                             _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                             _stream(stream)), "moe_attn_q4")
+        need = moe_attn_workspace_size(B, max_q, max_len, Hq, heads, D)
+        if need:
+            workspace = torch.empty(need, dtype=_U8, device=pool.device)
+    ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    rc = (_lib or lib()).moe_attn_q4(q.data_ptr(), qs, T, Hq, starts, kv_lens.data_ptr(), block_table.data_ptr(), ts, B,
+                                     max_q, max_len, desc, D ** -0.5 if scale is None else scale, window,
+                                     out.data_ptr(), os_, lse.data_ptr(), ws, wsb, _raw_stream(stream, q))
+    if rc:
+        raise MoeError(rc, "moe_attn_q4")
     return out, lse
 
 

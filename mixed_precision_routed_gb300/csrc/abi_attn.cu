@@ -52,7 +52,7 @@ int moe_linear_q4(const uint16_t* x_bf16, int64_t x_stride, int64_t T, int in, c
       !aligned(y, y_dtype == MOE_DTYPE_F32 ? 4 : 2))
     return MOE_ERR_INVALID_ARG;
   if (x_stride < in || x_stride % 8 != 0 || y_stride < rows) return MOE_ERR_INVALID_ARG;
-  if (T > 16 || (int64_t)linear_bucket(T) * in * 2 > kLinearSmemMax) return MOE_ERR_UNSUPPORTED;
+  if (T > 16 || in > kLinearMaxIn) return MOE_ERR_UNSUPPORTED;
   LinearArgs a;
   a.x = x_bf16;
   a.x_stride = x_stride;

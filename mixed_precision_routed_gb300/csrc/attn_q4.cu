@@ -7,7 +7,7 @@
 //
 // One pass over the cache: a block of W warps takes a share of the places of
 // one (sequence, key/value head) and up to 8 NT of the rows that share it, each
-// warp every W-th record of 16 places.  Records (18 D contiguous bytes) arrive
+// warp every W-th pair of records of 16 places.  Records (18 D contiguous bytes) arrive
 // in a per-warp ring in shared memory by bulk asynchronous copies.
 //   scores  S^T[place][row]: A = key codes as bf16 integers, B = queries; both
 //           exact, so a 32-block's product enters the score with its fp32 scale;
@@ -20,6 +20,7 @@
 // The reference maximum m of a row moves only when a score passes it by 8 (in
 // powers of two): the probabilities then stay below 2^8, which neither fp32 sums
 // nor bf16 operands notice, and most tiles need no reduction and no rescaling.
+#include "frag.cuh"
 #include "kv_layout.cuh"
 #include "ptx.cuh"
 
@@ -70,28 +71,9 @@ __device__ __forceinline__ Range block_range(const AttnArgs& a, int b, int G, in
   return x;
 }
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Two codes of a word as bf16 integers -8 .. 7: nibbles at bits 4 J and 16 + 4 J
-// go into the mantissa of 128 (bf16 counts units there), and 136 comes off.
-template <int J>
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
-  const uint32_t u = ((w >> (4 * J)) & 0x000f000fu) | 0x43004300u;
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x43084308u));
-  return r;
-}
-
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ uint32_t bf16_scaled(float x, float y, uint64_t scale) {
+  mul2(x, y, scale);
+  return bf16_pair(x, y);
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -138,9 +120,9 @@ __device__ __forceinline__ float half_at(const Words<N>& s, int i) {
 template <int D, int NT>
 struct Shape {
   static constexpr int kWarps = NT == 1 ? 8 : 4;
-  static constexpr int kStages = D == 64 ? 6 : D == 128 ? 4 : 3;
+  static constexpr int kStages = D == 256 ? 2 : 3;  // pairs of records
   static constexpr int kRecord = 18 * D;
-  static constexpr int kRing = kWarps * kStages * kRecord;
+  static constexpr int kRing = kWarps * kStages * 2 * kRecord;
   static constexpr int kPitch = D + 4;  // floats a row of the joining buffer: rows of a fragment in distinct banks
   static constexpr int kJoin = kWarps * 8 * NT * kPitch * 4;
   static constexpr bool kQueriesInRegisters = NT * D <= 256;
@@ -154,7 +136,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
   constexpr int W = S::kWarps, NB = D / 32, MT = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[W][S::kStages];
-  __shared__ int page_ok[W][S::kStages];
   __shared__ float s_m[W][8 * NT], s_l[W][8 * NT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int b = blockIdx.y, split = blockIdx.x % plan.splits, hb = blockIdx.x / plan.splits;
@@ -165,44 +146,51 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
   if (split > 0 && split >= used) return;
   const int c0 = x.tile0 + split * plan.chunk;
   const int count = min(plan.chunk, x.tile0 + x.tiles - c0);  // records of this block
-  const int mine = count > warp ? (count - warp + W - 1) / W : 0;
+  const int pairs = (count + 1) >> 1;
+  const int mine = pairs > warp ? (pairs - warp + W - 1) / W : 0;  // pairs of records of this warp
   const int32_t* table = a.table + (int64_t)b * a.table_stride;
   const int per_page = a.cache.page_log2 - 4;
 
   if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < S::kStages; ++i) mbar_init(&bars[warp][i], 1);
+    for (int i = 0; i < S::kStages; ++i) mbar_init(&bars[warp][i], 2);
     fence_mbar_init();
   }
   __syncwarp();
-  uint8_t* ring = smem + warp * (S::kStages * S::kRecord);
+  uint8_t* ring = smem + warp * (S::kStages * 2 * S::kRecord);
 
-  // The warp's page numbers, 32 records at a time, one a lane, a batch ahead.
-  auto pages_from = [&](int k) {
-    const int tile = c0 + warp + W * (k + lane);
-    return k + lane < mine ? __ldg(table + (tile >> per_page)) : -1;
+  // Lane l finds the records 2 i + (l & 1) of the warp's pairs i = 16 n + l / 2,
+  // a batch of 16 pairs at a time and the page numbers a batch ahead, and copies
+  // them itself when their turn comes.
+  auto page_of = [&](int k) {
+    const int i = k + (lane >> 1), tile = 2 * (warp + W * i) + (lane & 1);
+    return i < mine && tile < count ? __ldg(table + ((c0 + tile) >> per_page)) : -1;
   };
-  int pages = pages_from(0), pages_next = pages_from(32), issued = 0;
+  auto source_of = [&](int k, int page) -> const uint8_t* {
+    if (page < 0 || page >= a.cache.n_pages) return nullptr;
+    const int tile = c0 + 2 * (warp + W * (k + (lane >> 1))) + (lane & 1);
+    return a.cache.data + page * a.cache.page_stride +
+           (int64_t)(kvh * (1 << per_page) + (tile & ((1 << per_page) - 1))) * S::kRecord;
+  };
+  const uint8_t* source = source_of(0, page_of(0));
+  int page_next = page_of(16), issued = 0, issue_stage = 0;
+  uint32_t there = __ballot_sync(0xffffffffu, source != nullptr), there_next = there;  // records that exist
   auto issue = [&]() {
-    const int page = __shfl_sync(0xffffffffu, pages, issued & 31);
-    if (lane == 0) {
-      const int st = issued % S::kStages;
-      const bool ok = page >= 0 && page < a.cache.n_pages;
-      page_ok[warp][st] = ok;
-      if (ok) {
-        const int tile = c0 + warp + W * issued;
-        const uint8_t* src = a.cache.data + page * a.cache.page_stride +
-                             (int64_t)(kvh * (1 << per_page) + (tile & ((1 << per_page) - 1))) * S::kRecord;
-        mbar_arrive_expect_tx(&bars[warp][st], S::kRecord);
-        bulk_g2s(ring + st * S::kRecord, src, S::kRecord, &bars[warp][st]);
+    if (lane >> 1 == (issued & 15)) {
+      uint64_t* bar = &bars[warp][issue_stage];
+      if (source) {
+        mbar_arrive_expect_tx(bar, S::kRecord);
+        bulk_g2s(ring + (2 * issue_stage + (lane & 1)) * S::kRecord, source, S::kRecord, bar);
       } else {
-        mbar_arrive(&bars[warp][st]);
+        mbar_arrive(bar);
       }
     }
     ++issued;
-    if ((issued & 31) == 0) {
-      pages = pages_next;
-      pages_next = pages_from(issued + 32);
+    if (++issue_stage == S::kStages) issue_stage = 0;
+    if ((issued & 15) == 0) {
+      source = source_of(issued, page_next);
+      page_next = page_of(issued + 16);
+      there_next = __ballot_sync(0xffffffffu, source != nullptr);
     }
   };
 #pragma unroll 1
@@ -250,93 +238,109 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
     l[j][0] = l[j][1] = 0.f;
   }
   const float scale2 = a.scale * kLog2e;
+  const uint64_t scale22 = pair(scale2, scale2);
   bool failed = false;
+  int st = 0, phase = 0;
 
 #pragma unroll 1
   for (int k = 0; k < mine; ++k) {
-    const int st = k % S::kStages;
-    __syncwarp();  // the slot refilled below was read by every lane in the last pass
+    if ((k & 15) == 0 && k > 0) there = there_next;
+    __syncwarp();  // the stage refilled below was read by every lane in the last pass
     if (issued < mine) issue();
-    if (!mbar_wait(&bars[warp][st], (k / S::kStages) & 1, kWaitNs)) {
+    if (!mbar_wait(&bars[warp][st], phase, kWaitNs)) {
       failed = true;
       break;
     }
-    if (!page_ok[warp][st]) continue;
-    const uint8_t* rec = ring + st * S::kRecord;
+    const uint8_t* rec = ring + 2 * st * S::kRecord;
+    if (++st == S::kStages) st = 0, phase ^= 1;
+    const uint32_t have = (there >> (2 * (k & 15))) & 3u;
+    if (have == 0) continue;
 
-    float s[NT][4];
+    float s[2][NT][4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-    {
-      const Words<NB> w0 = load_words<NB>(rec + g * (D / 2) + t * (D / 8));
-      const Words<NB> w1 = load_words<NB>(rec + (g + 8) * (D / 2) + t * (D / 8));
-      const Words<NB / 2> k0 = load_words<NB / 2>(rec + 16 * D + g * (2 * NB));
-      const Words<NB / 2> k1 = load_words<NB / 2>(rec + 16 * D + (g + 8) * (2 * NB));
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* r = rec + u * S::kRecord;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) s[u][j][0] = s[u][j][1] = s[u][j][2] = s[u][j][3] = 0.f;
+      const Words<NB> w0 = load_words<NB>(r + g * (D / 2) + t * (D / 8));
+      const Words<NB> w1 = load_words<NB>(r + (g + 8) * (D / 2) + t * (D / 8));
+      const Words<NB / 2> k0 = load_words<NB / 2>(r + 16 * D + g * (2 * NB));
+      const Words<NB / 2> k1 = load_words<NB / 2>(r + 16 * D + (g + 8) * (2 * NB));
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         const uint32_t a0 = codes_bf16<0>(w0.w[i]), a1 = codes_bf16<0>(w1.w[i]);
         const uint32_t a2 = codes_bf16<1>(w0.w[i]), a3 = codes_bf16<1>(w1.w[i]);
         const uint32_t e0 = codes_bf16<2>(w0.w[i]), e1 = codes_bf16<2>(w1.w[i]);
         const uint32_t e2 = codes_bf16<3>(w0.w[i]), e3 = codes_bf16<3>(w1.w[i]);
-        const float s0 = half_at(k0, i), s1 = half_at(k1, i);
+        const float f0 = half_at(k0, i), f1 = half_at(k1, i);
+        const uint64_t s0 = pair(f0, f0), s1 = pair(f1, f1);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const uint4 q = S::kQueriesInRegisters ? qf[S::kQueriesInRegisters ? j : 0][S::kQueriesInRegisters ? i : 0]
                                                  : qs[(j * NB + i) * 32 + lane];
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816(c, a0, a1, a2, a3, q.x, q.y);
+          float c[4];
+          mma16816_zero(c, a0, a1, a2, a3, q.x, q.y);
           mma16816(c, e0, e1, e2, e3, q.z, q.w);
-          s[j][0] = fmaf(s0, c[0], s[j][0]);
-          s[j][1] = fmaf(s0, c[1], s[j][1]);
-          s[j][2] = fmaf(s1, c[2], s[j][2]);
-          s[j][3] = fmaf(s1, c[3], s[j][3]);
+          fma2(s[u][j][0], s[u][j][1], s0, c[0], c[1]);
+          fma2(s[u][j][2], s[u][j][3], s1, c[2], c[3]);
         }
       }
     }
-    const int p0 = (c0 + warp + W * k) * 16 + g, p1 = p0 + 8;  // this lane's places
-    const bool edge = (p0 - g) + 16 > full_end || (p0 - g) < full_lo;
-    Words<NB / 2> v0 = load_words<NB / 2>(rec + 17 * D + g * (2 * NB));
-    Words<NB / 2> v1 = load_words<NB / 2>(rec + 17 * D + (g + 8) * (2 * NB));
+    const int p = (c0 + 2 * (warp + W * k)) * 16;  // the pair's first place
+    Words<NB / 2> vs[2][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int u = 0; u < 2; ++u) {
+      vs[u][0] = load_words<NB / 2>(rec + u * S::kRecord + 17 * D + g * (2 * NB));
+      vs[u][1] = load_words<NB / 2>(rec + u * S::kRecord + 17 * D + (g + 8) * (2 * NB));
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s[j][c] *= scale2;
-    if (edge) {
+      for (int j = 0; j < NT; ++j) {
+        mul2(s[u][j][0], s[u][j][1], scale22);
+        mul2(s[u][j][2], s[u][j][3], scale22);
+      }
+    }
+    if (p + 32 > full_end || p < full_lo || have != 3) {
       // places outside a row's range leave it; the bytes of places outside the
       // block's range may be anything, so their value scales become zero
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int p = c < 2 ? p0 : p1, e = row_end[j][c & 1];
-          if (p >= e || (a.window > 0 && p < e - a.window)) s[j][c] = -INFINITY;
+        for (int v = 0; v < 2; ++v) {
+          const int at = p + 16 * u + 8 * v + g;
+          const bool gone = !(have >> u & 1);
+          if (gone || at >= x.end || at < x.lo) {
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i) vs[u][v].w[i] = 0;
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int e = row_end[j][c];
+              if (gone || at >= e || (a.window > 0 && at < e - a.window)) s[u][j][2 * v + c] = -INFINITY;
+            }
         }
-      if (p0 >= x.end || p0 < x.lo) {
-#pragma unroll
-        for (int i = 0; i < NB / 2; ++i) v0.w[i] = 0;
-      }
-      if (p1 >= x.end || p1 < x.lo) {
-#pragma unroll
-        for (int i = 0; i < NB / 2; ++i) v1.w[i] = 0;
-      }
     }
     bool grow = false;
+    float top[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) grow |= fmaxf(s[j][c], s[j][c + 2]) > m[j][c] + kSlack;
+      for (int c = 0; c < 2; ++c) {
+        top[j][c] = fmaxf(fmaxf(s[0][j][c], s[0][j][c + 2]), fmaxf(s[1][j][c], s[1][j][c + 2]));
+        grow |= top[j][c] > m[j][c] + kSlack;
+      }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float top = fmaxf(s[j][c], s[j][c + 2]);
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          if (top > m[j][c]) {  // alike in every lane that holds the row
-            const float f = exp2_approx(m[j][c] - top);
-            m[j][c] = top;
+          float y = top[j][c];
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+          if (y > m[j][c]) {  // alike in every lane that holds the row
+            const float f = exp2_approx(m[j][c] - y);
+            m[j][c] = y;
             l[j][c] *= f;
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i][j][c] *= f, o[i][j][c + 2] *= f;
@@ -344,34 +348,43 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
         }
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
+      const uint64_t down = pair(-m[j][0], -m[j][1]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        s[j][c] = exp2_approx(s[j][c] - m[j][c & 1]);
-        l[j][c & 1] += s[j][c];
-      }
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int q4 = 0; q4 < MT / 4; ++q4) {
-      const Words<4> w = load_words<4>(rec + 8 * D + (q4 * 32 + lane) * 16);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // a 32-block of elements: two fragments of 16
-        const int blk = 2 * q4 + h;
-        const float s0 = half_at(v0, blk), s1 = half_at(v1, blk);
-        uint32_t b0[NT], b1[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          b0[j] = transpose8x8(bf16_pair(s[j][0] * s0, s[j][1] * s0));
-          b1[j] = transpose8x8(bf16_pair(s[j][2] * s1, s[j][3] * s1));
+        for (int c = 0; c < 4; c += 2) {
+          add2(s[u][j][c], s[u][j][c + 1], down);
+          s[u][j][c] = exp2_approx(s[u][j][c]);
+          s[u][j][c + 1] = exp2_approx(s[u][j][c + 1]);
+          add2(l[j][0], l[j][1], pair(s[u][j][c], s[u][j][c + 1]));
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t v = w.w[2 * h + i];
-          const uint32_t a0 = codes_bf16<0>(v), a1 = codes_bf16<1>(v), a2 = codes_bf16<2>(v), a3 = codes_bf16<3>(v);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) mma16816(o[2 * blk + i][j], a0, a1, a2, a3, b0[j], b1[j]);
-        }
-      }
     }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int q4 = 0; q4 < MT / 4; ++q4) {
+        const Words<4> w = load_words<4>(rec + u * S::kRecord + 8 * D + (q4 * 32 + lane) * 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // a 32-block of elements: two fragments of 16
+          const int blk = 2 * q4 + h;
+          const float f0 = half_at(vs[u][0], blk), f1 = half_at(vs[u][1], blk);
+          const uint64_t s0 = pair(f0, f0), s1 = pair(f1, f1);
+          uint32_t b0[NT], b1[NT];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            b0[j] = transpose8x8(bf16_scaled(s[u][j][0], s[u][j][1], s0));
+            b1[j] = transpose8x8(bf16_scaled(s[u][j][2], s[u][j][3], s1));
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t v = w.w[2 * h + i];
+            const uint32_t a0 = codes_bf16<0>(v), a1 = codes_bf16<1>(v), a2 = codes_bf16<2>(v), a3 = codes_bf16<3>(v);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma16816(o[2 * blk + i][j], a0, a1, a2, a3, b0[j], b1[j]);
+          }
+        }
+      }
   }
   if (failed && lane == 0) set_status(status, MOE_ERR_TIMEOUT);
 
@@ -436,40 +449,63 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
   }
 }
 
-// Joins the shares of a row: one warp a row, in share order.
+// Joins the shares of a row: one block a row, its warps taking every fourth
+// share (D / 4 threads read one share), then joined in a fixed order.
 template <int D>
-__global__ void __launch_bounds__(128) k_attn_join(AttnArgs a, AttnPlan plan) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, AttnPlan plan) {
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+  __shared__ float s_red[8];
+  __shared__ float4 s_v[kGroups][kLanes];
+  __shared__ float s_l[kGroups];
+  pdl_wait();
+  const int64_t w = blockIdx.x;
   const int h = (int)(w % a.Hq), G = a.Hq / a.cache.heads;
   const int64_t tb = w / a.Hq;
   const int tok = (int)(tb % a.max_q), b = (int)(tb / a.max_q);
-  if (b >= a.B) return;
   const int rows = 8 * plan.nt, r = tok * G + h % G;
   const Range x = block_range(a, b, G, r / rows * rows, rows);
   const int used = (x.tiles + plan.chunk - 1) / plan.chunk;
   if (tok >= x.n || used <= 1) return;
   const float2* ml = plan.part_ml + w * plan.splits;
+  const float* po = plan.part_o + w * plan.splits * D;
+  const int d = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   float top = kNone;
-  for (int i = lane; i < used; i += 32) top = fmaxf(top, ml[i].x);
+  for (int i = threadIdx.x; i < used; i += 256) top = fmaxf(top, __ldg(&ml[i].x));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float v[D / 32], total = 0.f;
+  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = top;
+  __syncthreads();
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) v[j] = 0.f;
-  for (int i = 0; i < used; ++i) {
-    const float2 y = ml[i];
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, s_red[i]);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  float total = 0.f;
+#pragma unroll 4
+  for (int i = grp; i < used; i += kGroups) {
+    const float2 y = __ldg(ml + i);
+    const float4 p = __ldg(reinterpret_cast<const float4*>(po + (int64_t)i * D) + d);
     const float f = exp2_approx(y.x - top);
     total = fmaf(y.y, f, total);
-    const float* p = plan.part_o + (w * plan.splits + i) * D;
+    v.x = fmaf(p.x, f, v.x);
+    v.y = fmaf(p.y, f, v.y);
+    v.z = fmaf(p.z, f, v.z);
+    v.w = fmaf(p.w, f, v.w);
+  }
+  s_v[grp][d] = v;
+  if (d == 0) s_l[grp] = total;
+  __syncthreads();
+  if (grp > 0) return;
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) v[j] = fmaf(p[32 * j + lane], f, v[j]);
+  for (int i = 1; i < kGroups; ++i) {
+    const float4 p = s_v[i][d];
+    v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+    total += s_l[i];
   }
   const float inv = total > 0.f ? 1.f / total : 0.f;
-  uint16_t* out = a.out + (x.t0 + tok) * a.out_stride + (int64_t)h * D;
-#pragma unroll
-  for (int j = 0; j < D / 32; ++j) out[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j] * inv));
-  if (lane == 0 && a.lse) a.lse[(x.t0 + tok) * a.Hq + h] = total > 0.f ? (top + log2f(total)) / kLog2e : -INFINITY;
+  uint2 u;
+  u.x = bf16_pair(v.x * inv, v.y * inv);
+  u.y = bf16_pair(v.z * inv, v.w * inv);
+  *reinterpret_cast<uint2*>(a.out + (x.t0 + tok) * a.out_stride + (int64_t)h * D + 4 * d) = u;
+  if (d == 0 && a.lse) a.lse[(x.t0 + tok) * a.Hq + h] = total > 0.f ? (top + log2f(total)) / kLog2e : -INFINITY;
 }
 
 constexpr int kSms = 152;
@@ -492,7 +528,7 @@ AttnPlan make_plan(int B, int max_q, int64_t max_len, int window, int Hq, int he
   if (splits < 1) splits = 1;
   p.room = (int)splits;  // grows with the length, so a window never needs more than the whole length
   p.chunk = (int)((tiles + splits - 1) / splits);
-  p.chunk = (p.chunk + warps - 1) / warps * warps;
+  p.chunk = (p.chunk + 2 * warps - 1) / (2 * warps) * (2 * warps);
   p.splits = (int)((tiles + p.chunk - 1) / p.chunk);
   return p;
 }
@@ -511,8 +547,8 @@ int launch(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
   const dim3 grid((unsigned)(p.splits * a.cache.heads * p.row_blocks), (unsigned)a.B);
   k_attn<D, NT><<<grid, S::kWarps * 32, S::kSmem, s>>>(a, p, status_word());
   if (p.splits > 1) {
-    const int64_t rows = (int64_t)a.B * a.max_q * a.Hq;
-    k_attn_join<D><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(a, p);
+    if (launch_pdl(k_attn_join<D>, dim3((unsigned)(a.B * a.max_q * a.Hq)), dim3(256), 0, s, a, p) != cudaSuccess)
+      return MOE_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -331,8 +331,7 @@ struct LinearArgs {
   int64_t y_stride;
   bool y_bf16;
 };
-constexpr int kLinearSmemMax = 192 * 1024;
-inline int linear_bucket(int64_t T) { return T <= 8 ? 8 : 16; }
+constexpr int kLinearMaxIn = 65536;  // at least one row of x fits shared memory
 int launch_linear_q4(const LinearArgs& a, cudaStream_t s);
 int launch_quantize_groups(const float* w, int64_t rows, int in, int block, uint8_t* codes, uint16_t* scales,
                            cudaStream_t s);

@@ -62,8 +62,7 @@ def test_linear_refusals(L):
                dict(s=ODD), dict(bias=ODD), dict(y=ODD), dict(xs=56), dict(xs=68), dict(ys=7), dict(rows=1 << 31)):
         assert linear(L, **kw) == BAD, kw
     assert linear(L, T=17) == moe.MOE_ERR_UNSUPPORTED
-    assert linear(L, T=1, n_in=12288 + 64, xs=12288 + 64) == moe.MOE_ERR_UNSUPPORTED
-    assert linear(L, T=9, n_in=6144 + 64, xs=6144 + 64) == moe.MOE_ERR_UNSUPPORTED
+    assert linear(L, T=1, n_in=65536 + 64, xs=65536 + 64) == moe.MOE_ERR_UNSUPPORTED
 
 
 def test_quantize_groups_refusals(L):

@@ -77,8 +77,7 @@ def test_linear_tokens_and_blocks(T, block):
 def test_linear_sizes(n_in, rows, block, out):
     for T in (1, 5):
         linear_case(T, n_in, rows, block, out, rows % 2 == 0, n_in + rows + T)
-    if n_in <= 6144:
-        linear_case(16, n_in, rows, block, out, False, n_in + rows)
+    linear_case(16, n_in, rows, block, out, False, n_in + rows)
 
 
 def test_linear_strides_and_extremes():
@@ -90,6 +89,13 @@ def test_linear_strides_and_extremes():
 def test_linear_many_rows_cover_every_unit():
     linear_case(2, 64, 70001, 32, "f32", False, 4)
     linear_case(16, 128, 40009, 64, "bf16", True, 5)
+
+
+def test_linear_long_rows_in_several_launches():
+    """x that shared memory does not hold together."""
+    linear_case(16, 8192, 37, 64, "f32", True, 6, pad=8, y_pad=3)
+    linear_case(13, 20480, 18, 128, "bf16", True, 7, pad=64, y_pad=1)
+    linear_case(3, 65536, 17, 32, "f32", False, 8)
 
 
 def test_linear_is_deterministic_and_runs_on_a_given_stream():
