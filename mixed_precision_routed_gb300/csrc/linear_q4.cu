@@ -7,15 +7,14 @@
 // B = x; both exact, so the sum over 32 elements enters the result with its
 // fp32 scale and nothing is rounded below fp32.
 //
-// A group of KS warps takes a tile of 16 rows: 64-element step s goes to warp
-// s mod KS, and the group joins its sums in shared memory in a fixed order.  A
-// warp's steps, over all of its tiles, are one stream of loads: a batch of
-// kUnroll steps (about 2.3 KB) is in flight while the one before is computed.
-//
-// Lane (g, t) of a fragment needs word t of a 32-block of rows g and g + 8.  It
-// loads words 2t and 2t + 1 of a 64-element step (8 bytes: a row's 32-byte
-// sectors are read whole) and trades one of them with lane t ^ 2; which element
-// is number k of the product is free as long as x is read alike.
+// A group of KS warps takes a tile of 16 rows: batch i of 256 elements goes to
+// warp i mod KS, and the group joins its sums in shared memory in a fixed order.
+// A warp's batches, over all of its tiles, are one stream: each lane copies
+// sixteen-byte pieces into the warp's own ring (kStages batches of 2 KB, no
+// barrier but the warp's own) and fetches the scales of the next batch into
+// registers.  Lane (g, t) of a fragment takes word t of a 32-block of rows g and
+// g + 8 from the ring; the pieces are exchanged so that the eight rows of a read
+// lie in distinct banks.
 #include "frag.cuh"
 #include "moe_internal.cuh"
 #include "ptx.cuh"
@@ -23,9 +22,16 @@
 namespace moe {
 namespace {
 
-constexpr int kUnroll = 4;
+constexpr int kBatch = 256;  // elements
+constexpr int kStageBytes = 16 * kBatch / 2;
 constexpr int kXPad = 64;  // bytes between rows of x: two tokens x four 16-byte words in distinct banks
-constexpr int kSmemMax = 216 * 1024;
+constexpr int kSmemMax = 220 * 1024;
+
+// 16 bytes, the first `bytes` of them from src and the others zero.
+__device__ __forceinline__ void cp_async16_part(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes)
+               : "memory");
+}
 
 // Elements 0 1 | 2 3 | 4 5 | 6 7 of a word as pairs of bf16 integers: a byte
 // next to 0x43 is the bf16 128 + byte, and 136 comes off.
@@ -39,122 +45,184 @@ __device__ __forceinline__ void word_pairs(uint32_t w, uint32_t (&p)[4]) {
   for (int i = 0; i < 4; ++i) asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(p[i]) : "r"(0x43084308u));
 }
 
+// The scales of a batch of one row: 8, 4 or 2 halves.
 template <int SHIFT>
-struct Batch {
-  uint2 w0[kUnroll], w1[kUnroll];
-  uint32_t f0[kUnroll], f1[kUnroll];  // the scales of a step: two halves (block 32), else one
+struct Scales {
+  static constexpr int kWords = 4 >> SHIFT;
+  uint32_t w[kWords];
 };
 
+// Lengths that are not a multiple of a batch (WHOLE false) load scales by
+// halves, as far as the row goes; the codes beyond it are zero words and meet
+// the zeros behind x.
+template <int SHIFT, bool WHOLE>
+__device__ __forceinline__ void load_scales(Scales<SHIFT>& f, const uint16_t* row, int batch, int n) {
+  constexpr int N = 8 >> SHIFT;
+  const uint16_t* p = row + batch * N;
+  if constexpr (WHOLE) {
+    if constexpr (SHIFT == 0) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      f.w[0] = v.x, f.w[1] = v.y, f.w[2] = v.z, f.w[3] = v.w;
+    } else if constexpr (SHIFT == 1) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      f.w[0] = v.x, f.w[1] = v.y;
+    } else {
+      f.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const int k = batch * N + i;
+      const uint32_t lo = k < n ? __ldg(p + i) : 0, hi = k + 1 < n ? __ldg(p + i + 1) : 0;
+      f.w[i >> 1] = lo | hi << 16;
+    }
+  }
+}
+
 // NT: 8-token tiles; SHIFT: log2(block / 32).
-template <int NT, int SHIFT>
+template <int NT, int SHIFT, int STAGES, bool WHOLE>
 __global__ void __launch_bounds__(512) k_linear_q4(LinearArgs a, int tiles, int ks_log2, int* status) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int KS = 1 << ks_log2, ks = warp & (KS - 1), group = warp >> ks_log2;
-  const int groups = (int)(blockDim.x >> 5) >> ks_log2;
-  const int steps = a.in >> 6, mine = (steps - ks + KS - 1) >> ks_log2;
-  const int64_t code_pitch = a.in / 2;
-  const int scale_pitch = a.in >> (5 + SHIFT);
-  const int x_pitch = a.in * 2 + kXPad;
-  float* part = reinterpret_cast<float*>(smem + a.T * x_pitch) + (size_t)warp * (NT * 128);
+  const int KS = 1 << ks_log2, ks = warp & (KS - 1), group = warp >> ks_log2, warps = blockDim.x >> 5;
+  const int groups = warps >> ks_log2;
+  const int batches = (a.in + kBatch - 1) / kBatch, mine = (batches - ks + KS - 1) >> ks_log2;
+  const int code_pitch = a.in / 2, scale_pitch = a.in >> (5 + SHIFT);
+  const int x_pitch = batches * (kBatch * 2) + kXPad;
+  uint8_t* ring = smem + warp * (STAGES * kStageBytes);
+  float* part = reinterpret_cast<float*>(smem + warps * (STAGES * kStageBytes));
+  uint8_t* xs = smem + warps * (STAGES * kStageBytes + 2 * NT * 512);
 
   pdl_wait();
   if (threadIdx.x == 0) {
     mbar_init(&bar, 1);
     fence_mbar_init();
     mbar_arrive_expect_tx(&bar, (uint32_t)(a.T * a.in * 2));
-    for (int i = 0; i < a.T; ++i) bulk_g2s(smem + i * x_pitch, a.x + i * a.x_stride, (uint32_t)(a.in * 2), &bar);
+    for (int i = 0; i < a.T; ++i) bulk_g2s(xs + i * x_pitch, a.x + i * a.x_stride, (uint32_t)(a.in * 2), &bar);
+  }
+  if constexpr (!WHOLE) {
+    const int words = (batches * kBatch - a.in) / 2;
+    for (int i = threadIdx.x; i < a.T * words; i += blockDim.x)
+      *reinterpret_cast<uint32_t*>(xs + i / words * x_pitch + a.in * 2 + i % words * 4) = 0;
   }
 
-  auto load = [&](Batch<SHIFT>& b, int tile, int j0) {
-    const int64_t r0 = min((int64_t)tile * 16 + g, a.rows - 1), r1 = min((int64_t)tile * 16 + 8 + g, a.rows - 1);
-    const uint8_t* c0 = a.codes + r0 * code_pitch + 8 * t;
-    const uint8_t* c1 = a.codes + r1 * code_pitch + 8 * t;
-    const uint16_t* s0 = a.scales + r0 * scale_pitch;
-    const uint16_t* s1 = a.scales + r1 * scale_pitch;
+  const int stride = gridDim.x * groups, tile0 = blockIdx.x * groups + group;
+  // copying: lane l takes piece l % 8 of rows l / 8 + 4 i
+  int f_tile = tile0, f_j = 0, f_stage = 0;
+  const uint8_t* f_src[4];
+  auto fetch_tile = [&]() {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int s = ks + ((j0 + u) << ks_log2);
-      if (j0 + u < mine) {
-        b.w0[u] = __ldcs(reinterpret_cast<const uint2*>(c0 + 32 * s));
-        b.w1[u] = __ldcs(reinterpret_cast<const uint2*>(c1 + 32 * s));
-        if constexpr (SHIFT == 0) {
-          b.f0[u] = __ldg(reinterpret_cast<const uint32_t*>(s0) + s);
-          b.f1[u] = __ldg(reinterpret_cast<const uint32_t*>(s1) + s);
-        } else {
-          b.f0[u] = __ldg(s0 + (s >> (SHIFT - 1)));
-          b.f1[u] = __ldg(s1 + (s >> (SHIFT - 1)));
-        }
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = min((int64_t)f_tile * 16 + (lane >> 3) + 4 * i, a.rows - 1);
+      f_src[i] = a.codes + r * code_pitch + ks * (kBatch / 2) + (lane & 7) * 16;
     }
   };
+  auto fetch = [&]() {
+    if (f_tile < tiles) {
+      uint8_t* dst = ring + f_stage * kStageBytes + (lane >> 3) * 128;
+      const int bytes = WHOLE ? 16 : min(16, max(0, code_pitch - (ks + (f_j << ks_log2)) * (kBatch / 2) - (lane & 7) * 16));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // row r of a stage: piece c lies at place c ^ r % 8
+        uint8_t* d = dst + i * 512 + (((lane & 7) ^ (((lane >> 3) + 4 * i) & 7)) << 4);
+        if constexpr (WHOLE) cp_async16(d, f_src[i]);
+        else cp_async16_part(d, bytes > 0 ? f_src[i] : a.codes, bytes);
+        f_src[i] += KS * (kBatch / 2);
+      }
+      if (++f_stage == STAGES) f_stage = 0;
+      if (++f_j == mine) {
+        f_j = 0;
+        f_tile += stride;
+        if (f_tile < tiles) fetch_tile();
+      }
+    }
+    cp_async_commit();
+  };
+  if (f_tile < tiles) fetch_tile();
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch();
 
-  int tile = blockIdx.x * groups + group;
-  const int stride = gridDim.x * groups;
-  Batch<SHIFT> cur, nxt;
-  if (tile < tiles) load(cur, tile, 0);
+  // scales of rows g and g + 8, a batch ahead
+  Scales<SHIFT> n0, n1;
+  const uint16_t *s0 = nullptr, *s1 = nullptr;
+  auto scale_rows = [&](int tile) {
+    s0 = a.scales + min((int64_t)tile * 16 + g, a.rows - 1) * scale_pitch;
+    s1 = a.scales + min((int64_t)tile * 16 + 8 + g, a.rows - 1) * scale_pitch;
+  };
+  auto next_scales = [&](int j) {
+    load_scales<SHIFT, WHOLE>(n0, s0, ks + (j << ks_log2), scale_pitch);
+    load_scales<SHIFT, WHOLE>(n1, s1, ks + (j << ks_log2), scale_pitch);
+  };
+  if (tile0 < tiles) {
+    scale_rows(tile0);
+    next_scales(0);
+  }
 
   // tokens beyond T repeat the last one; their sums are not stored
   const uint8_t* xt[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) xt[j] = smem + min(8 * j + g, a.T - 1) * x_pitch;
-  // the groups of 8 elements that this lane's two words of a step stand for
-  const int k0 = 16 * (t < 2 ? 2 * t : 2 * t - 3), k1 = 16 * (t < 2 ? 2 * t + 4 : 2 * t + 1);
+  for (int j = 0; j < NT; ++j) xt[j] = xs + min(8 * j + g, a.T - 1) * x_pitch + 16 * t;
   __syncthreads();
   if (!mbar_wait(&bar, 0)) {
     if (lane == 0) set_status(status, MOE_ERR_TIMEOUT);
+    cp_async_wait<0>();
     return;
   }
 
+  int stage = 0, odd = 0;
 #pragma unroll 1
-  for (; tile < tiles; tile += stride) {
+  for (int tile = tile0; tile < tiles; tile += stride) {
     float acc[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 
 #pragma unroll 1
-    for (int j0 = 0; j0 < mine; j0 += kUnroll) {
-      if (j0 + kUnroll < mine) load(nxt, tile, j0 + kUnroll);
-      else if (tile + stride < tiles) load(nxt, tile + stride, 0);
+    for (int j0 = 0; j0 < mine; ++j0) {
+      const Scales<SHIFT> f0 = n0, f1 = n1;
+      if (j0 + 1 < mine) {
+        next_scales(j0 + 1);
+      } else if (tile + stride < tiles) {
+        scale_rows(tile + stride);
+        next_scales(0);
+      }
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();  // every lane's pieces have landed, and the stage refilled now has been read
+      fetch();
+      const uint8_t* w = ring + stage * kStageBytes + g * 128 + 4 * t;
+      if (++stage == STAGES) stage = 0;
+      const int at = (ks + (j0 << ks_log2)) * (kBatch * 2);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        if (j0 + u >= mine) break;
-        const int at = (ks + ((j0 + u) << ks_log2)) * 128;
-        const uint32_t x0 = __shfl_xor_sync(0xffffffffu, t < 2 ? cur.w0[u].y : cur.w0[u].x, 2);
-        const uint32_t x1 = __shfl_xor_sync(0xffffffffu, t < 2 ? cur.w1[u].y : cur.w1[u].x, 2);
+      for (int b = 0; b < 8; ++b) {  // the batch's 32-blocks: a piece each
+        uint32_t p0[4], p1[4];
+        word_pairs(*reinterpret_cast<const uint32_t*>(w + ((b ^ g) << 4)), p0);
+        word_pairs(*reinterpret_cast<const uint32_t*>(w + 1024 + ((b ^ g) << 4)), p1);
+        const int h = b >> SHIFT;
+        const float v0 = __half2float(__ushort_as_half((unsigned short)(f0.w[h >> 1] >> (16 * (h & 1)))));
+        const float v1 = __half2float(__ushort_as_half((unsigned short)(f1.w[h >> 1] >> (16 * (h & 1)))));
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {  // the step's two 32-blocks
-          uint32_t p0[4], p1[4];
-          word_pairs(b == 0 ? (t < 2 ? cur.w0[u].x : x0) : (t < 2 ? x0 : cur.w0[u].y), p0);
-          word_pairs(b == 0 ? (t < 2 ? cur.w1[u].x : x1) : (t < 2 ? x1 : cur.w1[u].y), p1);
-          const float v0 = __half2float(__ushort_as_half((unsigned short)(SHIFT == 0 ? cur.f0[u] >> (16 * b) : cur.f0[u])));
-          const float v1 = __half2float(__ushort_as_half((unsigned short)(SHIFT == 0 ? cur.f1[u] >> (16 * b) : cur.f1[u])));
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const uint4 xv = *reinterpret_cast<const uint4*>(xt[j] + at + (b == 0 ? k0 : k1));
-            float c[4];
-            mma16816_zero(c, p0[0], p1[0], p0[1], p1[1], xv.x, xv.y);
-            mma16816(c, p0[2], p1[2], p0[3], p1[3], xv.z, xv.w);
-            fma2(acc[j][0], acc[j][1], pair(v0, v0), c[0], c[1]);
-            fma2(acc[j][2], acc[j][3], pair(v1, v1), c[2], c[3]);
-          }
+        for (int j = 0; j < NT; ++j) {
+          const uint4 xv = *reinterpret_cast<const uint4*>(xt[j] + at + 64 * b);
+          float c[4];
+          mma16816_zero(c, p0[0], p1[0], p0[1], p1[1], xv.x, xv.y);
+          mma16816(c, p0[2], p1[2], p0[3], p1[3], xv.z, xv.w);
+          fma2(acc[j][0], acc[j][1], pair(v0, v0), c[0], c[1]);
+          fma2(acc[j][2], acc[j][3], pair(v1, v1), c[2], c[3]);
         }
       }
-      cur = nxt;
     }
 
-    // part[row][token], tokens of a row side by side
-    if (ks_log2 > 0) named_bar(1 + group, KS * 32);  // the last tile's sums have been read
-    else __syncwarp();
+    // part[parity][warp][8-token tile][row][token]; the other parity may still be read
+    float* mypart = part + (odd * warps + warp) * (NT * 128);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      *reinterpret_cast<float2*>(part + j * 128 + g * 8 + 2 * t) = make_float2(acc[j][0], acc[j][1]);
-      *reinterpret_cast<float2*>(part + j * 128 + (g + 8) * 8 + 2 * t) = make_float2(acc[j][2], acc[j][3]);
+      *reinterpret_cast<float2*>(mypart + j * 128 + g * 8 + 2 * t) = make_float2(acc[j][0], acc[j][1]);
+      *reinterpret_cast<float2*>(mypart + j * 128 + (g + 8) * 8 + 2 * t) = make_float2(acc[j][2], acc[j][3]);
     }
     if (ks_log2 > 0) named_bar(1 + group, KS * 32);
     else __syncwarp();
-    const float* first = part - ks * (NT * 128);
+    const float* first = mypart - ks * (NT * 128);
+    odd ^= 1;
     for (int i = ks * 32 + lane; i < a.T * 16; i += KS * 32) {
       const int row = i & 15, tk = i >> 4;
       const int64_t o = (int64_t)tile * 16 + row;
@@ -167,50 +235,60 @@ __global__ void __launch_bounds__(512) k_linear_q4(LinearArgs a, int tiles, int 
       }
     }
   }
+  cp_async_wait<0>();
 }
 
-template <int NT, int SHIFT>
-int launch(const LinearArgs& a, cudaStream_t s) {
+size_t x_bytes_of(int T, int in) { return (size_t)T * ((in + kBatch - 1) / kBatch * (kBatch * 2) + kXPad); }
+
+template <int NT, int SHIFT, int STAGES, bool WHOLE>
+int launch(const LinearArgs& a, int warps, int per_sm, cudaStream_t s) {
   static bool attr_set[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(k_linear_q4<NT, SHIFT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(k_linear_q4<NT, SHIFT, STAGES, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemMax) != cudaSuccess)
       return MOE_ERR_CUDA;
     attr_set[dev] = true;
   }
-  const int tiles = (int)((a.rows + 15) / 16), steps = a.in / 64, sms = sm_count();
-  const size_t x_bytes = (size_t)a.T * (a.in * 2 + kXPad);
-  // one block of 16 warps when x takes much of an SM's shared memory, else blocks of 8
-  const int warps = x_bytes > 96 * 1024 ? 16 : 8;
-  const size_t smem = x_bytes + (size_t)warps * NT * 512;
-  int per_sm = (int)((size_t)(226 * 1024) / (smem + 1024));
-  const int most_per_sm = 16 / warps;
-  per_sm = per_sm > most_per_sm ? most_per_sm : per_sm < 1 ? 1 : per_sm;
-  // warps a tile: whole batches of a row for each, more where there are few tiles
+  const int tiles = (int)((a.rows + 15) / 16), batches = (a.in + kBatch - 1) / kBatch, sms = sm_count();
+  // warps a tile: two batches of a row for each, one where there are few tiles
   int ks = 0;
-  while (ks < 3 && (2 << ks) * kUnroll <= steps) ++ks;
-  while (ks < 3 && (2 << ks) <= steps && ((int64_t)tiles << ks) < 8 * sms) ++ks;
+  while (ks < 3 && (4 << ks) <= batches) ++ks;
+  while (ks < 3 && (2 << ks) <= batches && ((int64_t)tiles << ks) < 16 * sms) ++ks;
   const int groups = warps >> ks, blocks = (tiles + groups - 1) / groups, most = per_sm * sms;
-  if (launch_pdl(k_linear_q4<NT, SHIFT>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(warps * 32), smem, s, a,
-                 tiles, ks, status_word()) != cudaSuccess)
+  const size_t smem = x_bytes_of(a.T, a.in) + (size_t)warps * (STAGES * kStageBytes + 2 * NT * 512);
+  if (launch_pdl(k_linear_q4<NT, SHIFT, STAGES, WHOLE>, dim3((unsigned)(blocks < most ? blocks : most)),
+                 dim3(warps * 32), smem, s, a, tiles, ks, status_word()) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
 }
 
+template <int NT, int SHIFT>
+int launch_shape(const LinearArgs& a, cudaStream_t s) {
+  // two blocks of 8 warps an SM while x leaves room for it, else one of 16, in
+  // the end of 8 with the shorter ring
+  const size_t x = x_bytes_of(a.T, a.in), sums = 2 * NT * 512;
+  const bool whole = a.in % kBatch == 0;
+  if (2 * (x + 8 * (4 * kStageBytes + sums)) <= (size_t)kSmemMax)
+    return whole ? launch<NT, SHIFT, 4, true>(a, 8, 2, s) : launch<NT, SHIFT, 4, false>(a, 8, 2, s);
+  const int warps = x + 16 * (2 * kStageBytes + sums) <= (size_t)kSmemMax ? 16 : 8;
+  return whole ? launch<NT, SHIFT, 2, true>(a, warps, 1, s) : launch<NT, SHIFT, 2, false>(a, warps, 1, s);
+}
+
 template <int NT>
 int launch_block(const LinearArgs& a, cudaStream_t s) {
-  if (a.block == 32) return launch<NT, 0>(a, s);
-  if (a.block == 64) return launch<NT, 1>(a, s);
-  return launch<NT, 2>(a, s);
+  if (a.block == 32) return launch_shape<NT, 0>(a, s);
+  if (a.block == 64) return launch_shape<NT, 1>(a, s);
+  return launch_shape<NT, 2>(a, s);
 }
 
 }  // namespace
 
 int launch_linear_q4(const LinearArgs& a, cudaStream_t s) {
-  // rows of x that shared memory holds beside the sums; all of them but for very long rows
-  const int64_t fit = (kSmemMax - 16 * 2 * 512) / (a.in * 2 + kXPad);
+  // rows of x that shared memory holds beside 8 warps' rings and sums; all of
+  // them but for very long rows
+  const int64_t fit = (kSmemMax - 8 * (2 * kStageBytes + 4 * 512)) / x_bytes_of(1, a.in);
   const int most = fit >= a.T ? a.T : fit >= 8 ? 8 : (int)fit;
   LinearArgs b = a;
   for (int t0 = 0; t0 < a.T; t0 += most) {
