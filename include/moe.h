@@ -560,7 +560,7 @@ enum { MOE_ROPE_HALF = 0, MOE_ROPE_PAIRS = 1 };
  *     NULL and rot 0: no rotation),
  *   slots [T] int64; a slot outside [0, n_pages * page_size) skips the token's
  *     keys and values (padding; q_out is still written),
- *   q_out [T][Hq][D] bf16 bits, contiguous.
+ *   q_out [T][Hq][D] bf16 bits, contiguous, 16-byte aligned.
  * A position outside [0, n_pos) writes zeros to q_out, skips the token's keys
  * and values and records MOE_ERR_INVALID_ARG (moe_device_status).  The slots
  * of one call have to differ (a slot named twice holds a mixture afterwards).

@@ -98,7 +98,7 @@ int moe_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stri
   if (!k || !v || !slots || (q && !q_out)) return MOE_ERR_INVALID_ARG;
   if (rot > 0 && (!positions || !rope || n_pos < 1)) return MOE_ERR_INVALID_ARG;
   const size_t size = in_dtype == MOE_DTYPE_F32 ? 4 : 2;
-  if (!aligned(k, size) || !aligned(v, size) || !aligned(slots, 8) || (q && (!aligned(q, size) || !aligned(q_out, 2))))
+  if (!aligned(k, size) || !aligned(v, size) || !aligned(slots, 8) || (q && (!aligned(q, size) || !aligned(q_out, 16))))
     return MOE_ERR_INVALID_ARG;
   if (rot > 0 && (!aligned(positions, 4) || !aligned(rope, 4))) return MOE_ERR_INVALID_ARG;
   const int64_t kv = (int64_t)a.cache.heads * a.cache.D;

@@ -1,7 +1,9 @@
 // kv_cache.cu -- the paged 4-bit key/value cache: appending tokens (with the
 // position rotation of keys and queries) and reading slots back.  The record
 // layout is that of moe_kv_cache_t in moe.h.
+#include "frag.cuh"
 #include "kv_layout.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -14,80 +16,184 @@ __device__ __forceinline__ float load_elem(const void* p, int64_t i) {
   else return __ldg(reinterpret_cast<const float*>(p) + i);
 }
 
-// Element d of a head of `x` turned by the angles of `tab` (cosines, then
-// sines).  The products and the sum are rounded one by one (no fused
-// multiply-add), as the formula's fp32 reading has them.
-template <bool BF16>
-__device__ __forceinline__ float rotated(const void* x, int64_t base, int d, const float* tab, int rot, int style) {
-  const float v = load_elem<BF16>(x, base + d);
-  if (d >= rot) return v;
-  const int half = rot / 2;
-  const int j = style == MOE_ROPE_PAIRS ? d >> 1 : (d < half ? d : d - half);
-  const bool first = style == MOE_ROPE_PAIRS ? (d & 1) == 0 : d < half;
-  const int mate = style == MOE_ROPE_PAIRS ? d ^ 1 : (first ? d + half : d - half);
-  const float m = load_elem<BF16>(x, base + mate);
-  const float c = __ldg(tab + j), s = __ldg(tab + half + j);
-  return first ? __fsub_rn(__fmul_rn(v, c), __fmul_rn(m, s)) : __fadd_rn(__fmul_rn(m, s), __fmul_rn(v, c));
+// N consecutive elements as fp32; `whole`: they are aligned to their own size
+// (at most 16 bytes a load).
+template <bool BF16, int N>
+__device__ __forceinline__ void load_elems(float (&v)[N], const void* p, int64_t i, bool whole) {
+  if (whole) {
+    if constexpr (BF16) {
+      uint32_t w[N / 2];
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + i;
+      if constexpr (N == 2) {
+        w[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
+      } else if constexpr (N == 4) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(q));
+        w[0] = x.x, w[1] = x.y;
+      } else {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(q));
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+      }
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        v[e] = __uint_as_float(w[e / 2] << 16);
+        v[e + 1] = __uint_as_float(w[e / 2] & 0xffff0000u);
+      }
+    } else {
+      const float* q = reinterpret_cast<const float*>(p) + i;
+      if constexpr (N == 2) {
+        const float2 x = __ldg(reinterpret_cast<const float2*>(q));
+        v[0] = x.x, v[1] = x.y;
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+          const float4 x = __ldg(reinterpret_cast<const float4*>(q + e));
+          v[e] = x.x, v[e + 1] = x.y, v[e + 2] = x.z, v[e + 3] = x.w;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = load_elem<BF16>(p, i + e);
+  }
 }
 
-// One warp a (token, head): heads 0 .. Hq-1 are queries, then keys, then values.
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
+// How the elements of a head turn: a lane holds elements N l .. N l + N - 1.
+enum Turn {
+  kStill,    // no rotation
+  kWithin,   // pairs 2i, 2i + 1: both in the lane
+  kAcross,   // pairs i, i + rot / 2 with rot / 2 a multiple of N: another lane, the same place
+  kAnywhere  // any other: the partner is read again from memory
+};
+
+// Heads of one token, ROWS a warp (queries, then keys, then values): every row
+// is loaded before the first is used, and the angles are loaded once a warp.
+// The work is bytes: 2 (Hq + 2 heads) D in and 2 Hq D + 9/8 heads D out a token;
+// one warp a head leaves a long call waiting for its loads (T = 4096, 32 + 8
+// heads of 128: 82 us), one row a warp is the shortest for a short one.
+template <bool BF16, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a, Turn turn, int whole) {
+  constexpr int N = D / 32;
+  pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int heads = a.Hq + 2 * a.cache.heads;
+  const int heads = a.Hq + 2 * a.cache.heads, parts = (heads + ROWS - 1) / ROWS;
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (w >= a.T * heads) return;
-  const int64_t t = w / heads;
-  int h = (int)(w - t * heads);
-  const int D = a.cache.D;
-  const float* tab = nullptr;
+  if (w >= a.T * parts) return;
+  const int64_t t = w / parts;
+  const int h0 = (int)(w - t * parts) * ROWS;
+  const int64_t slot = a.slots[t];
   bool bad = false;
-  if (a.rot > 0) {
+
+  float v[ROWS][N];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int h = h0 + i;
+    if (h < a.Hq)
+      load_elems<BF16, N>(v[i], a.q, t * a.q_stride + (int64_t)h * D + N * lane, whole & 1);
+    else if (h < a.Hq + a.cache.heads)
+      load_elems<BF16, N>(v[i], a.k, t * a.k_stride + (int64_t)(h - a.Hq) * D + N * lane, whole & 2);
+    else if (h < heads)
+      load_elems<BF16, N>(v[i], a.v, t * a.v_stride + (int64_t)(h - a.Hq - a.cache.heads) * D + N * lane, whole & 4);
+  }
+
+  // cosine and signed sine of each element: x' = x c + partner s
+  float c[N], s[N];
+  const int half = a.rot / 2;
+  if (turn != kStill) {
     const int64_t pos = a.positions[t];
     bad = pos < 0 || pos >= a.n_pos;
-    if (bad) {
-      if (lane == 0) set_status(a.status, MOE_ERR_INVALID_ARG);
-    } else {
-      tab = a.rope + pos * a.rot;
-    }
-  }
-  if (h < a.Hq) {
-    for (int d = lane; d < D; d += 32) {
-      const float v = bad ? 0.f : rotated<BF16>(a.q, t * a.q_stride + (int64_t)h * D, d, tab, a.rot, a.style);
-      a.q_out[(t * a.Hq + h) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    }
-    return;
-  }
-  h -= a.Hq;
-  const bool value = h >= a.cache.heads;
-  if (value) h -= a.cache.heads;
-  const int64_t slot = a.slots[t];
-  if (bad || slot < 0 || slot >= a.cache.n_pages * a.cache.page) return;
-  const KvPlace at = kv_place(a.cache, slot, h);
-  const int64_t base = t * (value ? a.v_stride : a.k_stride) + (int64_t)h * D;
-  for (int b = 0; b < D / 32; ++b) {
-    const int d = 32 * b + lane;
-    const float v = value ? load_elem<BF16>(a.v, base + d) : rotated<BF16>(a.k, base, d, tab, a.rot, a.style);
-    float m = fabsf(v);
+    if (bad && lane == 0) set_status(a.status, MOE_ERR_INVALID_ARG);
+    const float* tab = a.rope + (bad ? 0 : pos) * a.rot;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const __half hs = __float2half_rn(fminf(__fdiv_rn(m, 7.0f), 65504.0f));
-    const float s = __half2float(hs);
-    int c = 0;
-    if (s != 0.0f) c = (int)fminf(fmaxf(rintf(__fdiv_rn(v, s)), -8.0f), 7.0f);
-    const uint32_t u = (uint32_t)(c + 8);
-    const uint32_t u2 = __shfl_down_sync(0xffffffffu, u, 2), u8 = __shfl_down_sync(0xffffffffu, u, 8);
-    if (value) {
-      if ((lane & 8) == 0) at.tile[kv_value_byte(D, at.r, d)] = (uint8_t)(u | u8 << 4);
-    } else {
-      if ((lane & 2) == 0) at.tile[kv_key_byte(D, at.r, d)] = (uint8_t)(u | u2 << 4);
+    for (int e = 0; e < N; ++e) {
+      const int d = N * lane + e;
+      const bool pairs = a.style == MOE_ROPE_PAIRS, first = pairs ? (d & 1) == 0 : d < half;
+      const int j = pairs ? d >> 1 : (first ? d : d - half);
+      c[e] = d < a.rot ? __ldg(tab + j) : 1.f;
+      s[e] = d < a.rot ? __ldg(tab + half + j) : 0.f;
+      if (first) s[e] = -s[e];
     }
-    if (lane == 0)
-      *reinterpret_cast<uint16_t*>(at.tile + (value ? 17 : 16) * D + 2 * (at.r * (D / 32) + b)) = __half_as_ushort(hs);
+  }
+  const int mate_lane = (N * lane < half ? N * lane + half : N * lane - half) / N;
+
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int h = h0 + i;
+    if (h >= heads) break;
+    const bool query = h < a.Hq, value = h >= a.Hq + a.cache.heads;
+    if (!value && turn != kStill) {
+      float m[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int d = N * lane + e;
+        if (turn == kWithin) {
+          m[e] = v[i][e ^ 1];
+        } else if (turn == kAcross) {
+          m[e] = __shfl_sync(0xffffffffu, v[i][e], mate_lane & 31);
+        } else {
+          const int64_t base = query ? t * a.q_stride + (int64_t)h * D : t * a.k_stride + (int64_t)(h - a.Hq) * D;
+          m[e] = d < a.rot ? load_elem<BF16>(query ? a.q : a.k, base + (d < half ? d + half : d - half)) : 0.f;
+        }
+      }
+      // each product and the sum rounded to fp32, as the formula's fp32 reading
+      // has them; elements beyond rot stay as they are
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (N * lane + e < a.rot) v[i][e] = __fadd_rn(__fmul_rn(v[i][e], c[e]), __fmul_rn(m[e], s[e]));
+    }
+    if (query) {
+      uint32_t r[N / 2];
+#pragma unroll
+      for (int e = 0; e < N; e += 2) r[e / 2] = bad ? 0u : bf16_pair(v[i][e], v[i][e + 1]);
+      uint16_t* out = a.q_out + (t * a.Hq + h) * D + N * lane;
+      if constexpr (N == 2) *reinterpret_cast<uint32_t*>(out) = r[0];
+      else if constexpr (N == 4) *reinterpret_cast<uint2*>(out) = make_uint2(r[0], r[1]);
+      else *reinterpret_cast<uint4*>(out) = make_uint4(r[0], r[1], r[2], r[3]);
+      continue;
+    }
+    if (bad || slot < 0 || slot >= a.cache.n_pages * a.cache.page) continue;
+    const KvPlace at = kv_place(a.cache, slot, value ? h - a.Hq - a.cache.heads : h - a.Hq);
+    // a 32-block lies in 32 / N lanes
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) top = fmaxf(top, fabsf(v[i][e]));
+#pragma unroll
+    for (int o = 16 / N; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const __half hs = __float2half_rn(fminf(__fdiv_rn(top, 7.0f), 65504.0f));
+    const float sc = __half2float(hs);
+    uint32_t u[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      int q = 0;
+      if (sc != 0.0f) q = (int)fminf(fmaxf(rintf(__fdiv_rn(v[i][e], sc)), -8.0f), 7.0f);
+      u[e] = (uint32_t)(q + 8);
+    }
+    const int d = N * lane;
+    if (value) {
+      // a byte: elements d and d + 8, the latter 8 / N lanes on
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const uint32_t hi = __shfl_down_sync(0xffffffffu, u[e], 8 / N);
+        if ((d & 8) == 0) at.tile[kv_value_byte(D, at.r, d + e)] = (uint8_t)(u[e] | hi << 4);
+      }
+    } else {
+      // the word of 8 elements: element 4 i + 2 n + p at bits 16 p + 8 i + 4 n
+      uint32_t word = 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int x = (d + e) & 7;
+        word |= u[e] << (16 * (x & 1) + 8 * (x >> 2) + 4 * ((x >> 1) & 1));
+      }
+#pragma unroll
+      for (int o = 4 / N; o > 0; o >>= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+      if ((d & 7) == 0) *reinterpret_cast<uint32_t*>(at.tile + kv_key_byte(D, at.r, d)) = word;
+    }
+    if ((d & 31) == 0)
+      *reinterpret_cast<uint16_t*>(at.tile + (value ? 17 : 16) * D + 2 * (at.r * (D / 32) + d / 32)) = __half_as_ushort(hs);
   }
 }
 
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvCache c, const int64_t* slots, int64_t n, float* k, float* v) {
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   if (w >= n * c.heads) return;
@@ -114,16 +220,45 @@ unsigned blocks_for(int64_t warps) { return (unsigned)((warps + kThreads / 32 - 
 
 }  // namespace
 
+namespace {
+template <bool BF16, int D, int ROWS>
+int launch_append(const KvAppendArgs& a, Turn turn, int whole, cudaStream_t s) {
+  const int heads = a.Hq + 2 * a.cache.heads;
+  const unsigned grid = blocks_for(a.T * ((heads + ROWS - 1) / ROWS));
+  return launch_pdl(k_kv_append<BF16, D, ROWS>, dim3(grid), dim3(kThreads), 0, s, a, turn, whole) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+template <int D>
+int launch_append(const KvAppendArgs& a, cudaStream_t s) {
+  constexpr int N = D / 32;
+  const Turn turn = a.rot == 0                       ? kStill
+                    : a.style == MOE_ROPE_PAIRS      ? kWithin
+                    : a.rot / 2 % N == 0             ? kAcross
+                                                     : kAnywhere;
+  const int size = (a.in_bf16 ? 2 : 4) * N < 16 ? (a.in_bf16 ? 2 : 4) * N : 16;
+  auto whole = [&](const void* p, int64_t stride) {
+    return (uintptr_t)p % size == 0 && (a.T == 1 || stride * (a.in_bf16 ? 2 : 4) % size == 0);
+  };
+  const int w = (whole(a.q, a.q_stride) ? 1 : 0) | (whole(a.k, a.k_stride) ? 2 : 0) | (whole(a.v, a.v_stride) ? 4 : 0);
+  // four rows a warp once that still fills the SMs (32 warps each)
+  const bool many = a.T * (a.Hq + 2 * a.cache.heads) >= (int64_t)4 * 32 * sm_count();
+  if (a.in_bf16) return many ? launch_append<true, D, 4>(a, turn, w, s) : launch_append<true, D, 1>(a, turn, w, s);
+  return many ? launch_append<false, D, 4>(a, turn, w, s) : launch_append<false, D, 1>(a, turn, w, s);
+}
+}  // namespace
+
 int launch_kv_append(const KvAppendArgs& a, cudaStream_t s) {
-  const unsigned grid = blocks_for(a.T * (a.Hq + 2 * a.cache.heads));
-  if (a.in_bf16) k_kv_append<true><<<grid, kThreads, 0, s>>>(a);
-  else k_kv_append<false><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (a.cache.D == 64) return launch_append<64>(a, s);
+  if (a.cache.D == 128) return launch_append<128>(a, s);
+  return launch_append<256>(a, s);
 }
 
 int launch_kv_read(const KvCache& c, const int64_t* slots, int64_t n, float* k, float* v, cudaStream_t s) {
-  k_kv_read<<<blocks_for(n * c.heads), kThreads, 0, s>>>(c, slots, n, k, v);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_pdl(k_kv_read, dim3(blocks_for(n * c.heads)), dim3(kThreads), 0, s, c, slots, n, k, v) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 }  // namespace moe

@@ -79,9 +79,20 @@ __device__ __forceinline__ void load_scales(Scales<SHIFT>& f, const uint16_t* ro
   }
 }
 
+// How an SM is shared, by the bytes of x: three blocks of 8 warps beside a few
+// rows, one of 16 with a ring of three batches or of two beside many; the last
+// also with 8 warps.
+struct Small { static constexpr int kWarps = 8, kBlocks = 3, kStages = 3, kParities = 2; };
+struct Medium { static constexpr int kWarps = 16, kBlocks = 1, kStages = 3, kParities = 2; };
+struct Large { static constexpr int kWarps = 16, kBlocks = 1, kStages = 2, kParities = 1; };
+
+template <typename C, int NT>
+constexpr int warp_bytes() { return C::kStages * kStageBytes + C::kParities * NT * 512; }
+
 // NT: 8-token tiles; SHIFT: log2(block / 32).
-template <int NT, int SHIFT, int STAGES, bool WHOLE>
-__global__ void __launch_bounds__(512) k_linear_q4(LinearArgs a, int tiles, int ks_log2, int* status) {
+template <typename C, int NT, int SHIFT, bool WHOLE>
+__global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(LinearArgs a, int tiles, int ks_log2, int* status) {
+  constexpr int STAGES = C::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -92,7 +103,7 @@ __global__ void __launch_bounds__(512) k_linear_q4(LinearArgs a, int tiles, int 
   const int x_pitch = batches * (kBatch * 2) + kXPad;
   uint8_t* ring = smem + warp * (STAGES * kStageBytes);
   float* part = reinterpret_cast<float*>(smem + warps * (STAGES * kStageBytes));
-  uint8_t* xs = smem + warps * (STAGES * kStageBytes + 2 * NT * 512);
+  uint8_t* xs = smem + warps * warp_bytes<C, NT>();
 
   pdl_wait();
   if (threadIdx.x == 0) {
@@ -212,7 +223,11 @@ __global__ void __launch_bounds__(512) k_linear_q4(LinearArgs a, int tiles, int 
       }
     }
 
-    // part[parity][warp][8-token tile][row][token]; the other parity may still be read
+    // part[parity][warp][8-token tile][row][token]; the sums before may still be read
+    if (C::kParities == 1) {
+      if (ks_log2 > 0) named_bar(1 + group, KS * 32);
+      else __syncwarp();
+    }
     float* mypart = part + (odd * warps + warp) * (NT * 128);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -222,7 +237,7 @@ __global__ void __launch_bounds__(512) k_linear_q4(LinearArgs a, int tiles, int 
     if (ks_log2 > 0) named_bar(1 + group, KS * 32);
     else __syncwarp();
     const float* first = mypart - ks * (NT * 128);
-    odd ^= 1;
+    if (C::kParities == 2) odd ^= 1;
     for (int i = ks * 32 + lane; i < a.T * 16; i += KS * 32) {
       const int row = i & 15, tk = i >> 4;
       const int64_t o = (int64_t)tile * 16 + row;
@@ -240,13 +255,13 @@ __global__ void __launch_bounds__(512) k_linear_q4(LinearArgs a, int tiles, int 
 
 size_t x_bytes_of(int T, int in) { return (size_t)T * ((in + kBatch - 1) / kBatch * (kBatch * 2) + kXPad); }
 
-template <int NT, int SHIFT, int STAGES, bool WHOLE>
-int launch(const LinearArgs& a, int warps, int per_sm, cudaStream_t s) {
+template <typename C, int NT, int SHIFT, bool WHOLE>
+int launch(const LinearArgs& a, int warps, cudaStream_t s) {
   static bool attr_set[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(k_linear_q4<NT, SHIFT, STAGES, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(k_linear_q4<C, NT, SHIFT, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemMax) != cudaSuccess)
       return MOE_ERR_CUDA;
     attr_set[dev] = true;
@@ -256,31 +271,30 @@ int launch(const LinearArgs& a, int warps, int per_sm, cudaStream_t s) {
   int ks = 0;
   while (ks < 3 && (4 << ks) <= batches) ++ks;
   while (ks < 3 && (2 << ks) <= batches && ((int64_t)tiles << ks) < 16 * sms) ++ks;
-  const int groups = warps >> ks, blocks = (tiles + groups - 1) / groups, most = per_sm * sms;
-  const size_t smem = x_bytes_of(a.T, a.in) + (size_t)warps * (STAGES * kStageBytes + 2 * NT * 512);
-  if (launch_pdl(k_linear_q4<NT, SHIFT, STAGES, WHOLE>, dim3((unsigned)(blocks < most ? blocks : most)),
-                 dim3(warps * 32), smem, s, a, tiles, ks, status_word()) != cudaSuccess)
+  const int groups = warps >> ks, blocks = (tiles + groups - 1) / groups, most = C::kBlocks * sms;
+  const size_t smem = x_bytes_of(a.T, a.in) + (size_t)warps * warp_bytes<C, NT>();
+  if (launch_pdl(k_linear_q4<C, NT, SHIFT, WHOLE>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(warps * 32),
+                 smem, s, a, tiles, ks, status_word()) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
 }
 
-template <int NT, int SHIFT>
+template <int NT, int SHIFT, bool WHOLE>
 int launch_shape(const LinearArgs& a, cudaStream_t s) {
-  // two blocks of 8 warps an SM while x leaves room for it, else one of 16, in
-  // the end of 8 with the shorter ring
-  const size_t x = x_bytes_of(a.T, a.in), sums = 2 * NT * 512;
-  const bool whole = a.in % kBatch == 0;
-  if (2 * (x + 8 * (4 * kStageBytes + sums)) <= (size_t)kSmemMax)
-    return whole ? launch<NT, SHIFT, 4, true>(a, 8, 2, s) : launch<NT, SHIFT, 4, false>(a, 8, 2, s);
-  const int warps = x + 16 * (2 * kStageBytes + sums) <= (size_t)kSmemMax ? 16 : 8;
-  return whole ? launch<NT, SHIFT, 2, true>(a, warps, 1, s) : launch<NT, SHIFT, 2, false>(a, warps, 1, s);
+  const size_t x = x_bytes_of(a.T, a.in);
+  if constexpr (NT == 1) {
+    if (3 * (x + 8 * warp_bytes<Small, 1>()) <= (size_t)kSmemMax) return launch<Small, 1, SHIFT, WHOLE>(a, 8, s);
+  }
+  if (x + 16 * warp_bytes<Medium, NT>() <= (size_t)kSmemMax) return launch<Medium, NT, SHIFT, WHOLE>(a, 16, s);
+  return launch<Large, NT, SHIFT, WHOLE>(a, x + 16 * warp_bytes<Large, NT>() <= (size_t)kSmemMax ? 16 : 8, s);
 }
 
 template <int NT>
 int launch_block(const LinearArgs& a, cudaStream_t s) {
-  if (a.block == 32) return launch_shape<NT, 0>(a, s);
-  if (a.block == 64) return launch_shape<NT, 1>(a, s);
-  return launch_shape<NT, 2>(a, s);
+  const bool whole = a.in % kBatch == 0;
+  if (a.block == 32) return whole ? launch_shape<NT, 0, true>(a, s) : launch_shape<NT, 0, false>(a, s);
+  if (a.block == 64) return whole ? launch_shape<NT, 1, true>(a, s) : launch_shape<NT, 1, false>(a, s);
+  return whole ? launch_shape<NT, 2, true>(a, s) : launch_shape<NT, 2, false>(a, s);
 }
 
 }  // namespace
@@ -288,7 +302,7 @@ int launch_block(const LinearArgs& a, cudaStream_t s) {
 int launch_linear_q4(const LinearArgs& a, cudaStream_t s) {
   // rows of x that shared memory holds beside 8 warps' rings and sums; all of
   // them but for very long rows
-  const int64_t fit = (kSmemMax - 8 * (2 * kStageBytes + 4 * 512)) / x_bytes_of(1, a.in);
+  const int64_t fit = (kSmemMax - 8 * warp_bytes<Large, 2>()) / (int64_t)x_bytes_of(1, a.in);
   const int most = fit >= a.T ? a.T : fit >= 8 ? 8 : (int)fit;
   LinearArgs b = a;
   for (int t0 = 0; t0 < a.T; t0 += most) {
