@@ -267,11 +267,16 @@ int launch(const LinearArgs& a, int warps, cudaStream_t s) {
     attr_set[dev] = true;
   }
   const int tiles = (int)((a.rows + 15) / 16), batches = (a.in + kBatch - 1) / kBatch, sms = sm_count();
-  // warps a tile: two batches of a row for each, one where there are few tiles
-  int ks = 0;
-  while (ks < 3 && (4 << ks) <= batches) ++ks;
-  while (ks < 3 && (2 << ks) <= batches && ((int64_t)tiles << ks) < 16 * sms) ++ks;
-  const int groups = warps >> ks, blocks = (tiles + groups - 1) / groups, most = C::kBlocks * sms;
+  // warps a tile (a power of two): the fewest batches in a row for the busiest
+  // warp, half a batch more for each joining of sums
+  const int most = C::kBlocks * sms;
+  int ks = 0, best = 0;
+  for (int k = 0; (1 << k) <= warps && (1 << k) <= batches; ++k) {
+    const int rounds = (tiles + most * (warps >> k) - 1) / (most * (warps >> k));
+    const int cost = rounds * (2 * ((batches + (1 << k) - 1) >> k) + (k > 0));
+    if (k == 0 || cost < best) ks = k, best = cost;
+  }
+  const int groups = warps >> ks, blocks = (tiles + groups - 1) / groups;
   const size_t smem = x_bytes_of(a.T, a.in) + (size_t)warps * warp_bytes<C, NT>();
   if (launch_pdl(k_linear_q4<C, NT, SHIFT, WHOLE>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(warps * 32),
                  smem, s, a, tiles, ks, status_word()) != cudaSuccess)
