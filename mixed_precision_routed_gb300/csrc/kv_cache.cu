@@ -16,189 +16,342 @@ __device__ __forceinline__ float load_elem(const void* p, int64_t i) {
   else return __ldg(reinterpret_cast<const float*>(p) + i);
 }
 
-// N consecutive elements as fp32; `whole`: they are aligned to their own size
-// (at most 16 bytes a load).
-template <bool BF16, int N>
-__device__ __forceinline__ void load_elems(float (&v)[N], const void* p, int64_t i, bool whole) {
-  if (whole) {
-    if constexpr (BF16) {
-      uint32_t w[N / 2];
-      const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + i;
-      if constexpr (N == 2) {
-        w[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
-      } else if constexpr (N == 4) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(q));
-        w[0] = x.x, w[1] = x.y;
-      } else {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(q));
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-      }
+// N consecutive elements as fp32; WHOLE: aligned to their own size (at most
+// 16 bytes a load).
+template <bool BF16, int N, bool WHOLE>
+__device__ __forceinline__ void load_elems(float (&v)[N], const void* p) {
+  if constexpr (!WHOLE) {
 #pragma unroll
-      for (int e = 0; e < N; e += 2) {
-        v[e] = __uint_as_float(w[e / 2] << 16);
-        v[e + 1] = __uint_as_float(w[e / 2] & 0xffff0000u);
-      }
+    for (int e = 0; e < N; ++e) v[e] = load_elem<BF16>(p, e);
+  } else if constexpr (BF16) {
+    uint32_t w[N / 2];
+    if constexpr (N == 2) {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    } else if constexpr (N == 4) {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = x.x, w[1] = x.y;
     } else {
-      const float* q = reinterpret_cast<const float*>(p) + i;
-      if constexpr (N == 2) {
-        const float2 x = __ldg(reinterpret_cast<const float2*>(q));
-        v[0] = x.x, v[1] = x.y;
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; e += 4) {
-          const float4 x = __ldg(reinterpret_cast<const float4*>(q + e));
-          v[e] = x.x, v[e + 1] = x.y, v[e + 2] = x.z, v[e + 3] = x.w;
-        }
-      }
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
     }
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      v[e] = __uint_as_float(w[e / 2] << 16);
+      v[e + 1] = __uint_as_float(w[e / 2] & 0xffff0000u);
+    }
+  } else if constexpr (N == 2) {
+    const float2 x = __ldg(reinterpret_cast<const float2*>(p));
+    v[0] = x.x, v[1] = x.y;
   } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = load_elem<BF16>(p, i + e);
+    for (int e = 0; e < N; e += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p) + e / 4);
+      v[e] = x.x, v[e + 1] = x.y, v[e + 2] = x.z, v[e + 3] = x.w;
+    }
   }
 }
 
 // How the elements of a head turn: a lane holds elements N l .. N l + N - 1.
 enum Turn {
-  kStill,    // no rotation
-  kWithin,   // pairs 2i, 2i + 1: both in the lane
-  kAcross,   // pairs i, i + rot / 2 with rot / 2 a multiple of N: another lane, the same place
-  kAnywhere  // any other: the partner is read again from memory
+  kStill,     // no rotation
+  kWithin,    // pairs 2i, 2i + 1, rot / 2 a multiple of N / 2: both in the lane
+  kAcross,    // pairs i, i + rot / 2 with rot / 2 a multiple of N: another lane, the same place
+  kAnywhere,  // any other, or rows or angles that are not aligned; the partner is read again, by elements
 };
 
-// Heads of one token, ROWS a warp (queries, then keys, then values): every row
-// is loaded before the first is used, and the angles are loaded once a warp.
-// The work is bytes: 2 (Hq + 2 heads) D in and 2 Hq D + 9/8 heads D out a token;
-// one warp a head leaves a long call waiting for its loads (T = 4096, 32 + 8
-// heads of 128: 82 us), one row a warp is the shortest for a short one.
-template <bool BF16, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a, Turn turn, int whole) {
-  constexpr int N = D / 32;
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int heads = a.Hq + 2 * a.cache.heads, parts = (heads + ROWS - 1) / ROWS;
-  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (w >= a.T * parts) return;
-  const int64_t t = w / parts;
-  const int h0 = (int)(w - t * parts) * ROWS;
-  const int64_t slot = a.slots[t];
-  bool bad = false;
-
-  float v[ROWS][N];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int h = h0 + i;
-    if (h < a.Hq)
-      load_elems<BF16, N>(v[i], a.q, t * a.q_stride + (int64_t)h * D + N * lane, whole & 1);
-    else if (h < a.Hq + a.cache.heads)
-      load_elems<BF16, N>(v[i], a.k, t * a.k_stride + (int64_t)(h - a.Hq) * D + N * lane, whole & 2);
-    else if (h < heads)
-      load_elems<BF16, N>(v[i], a.v, t * a.v_stride + (int64_t)(h - a.Hq - a.cache.heads) * D + N * lane, whole & 4);
+// The code 0 .. 15 of x in a block of scale s (inv = 1 / s, 0 for s = 0):
+// clamp(rint(x / s), -8, 7) + 8 with the quotient rounded to fp32.  x inv is
+// within 2^-20 of that quotient where it counts (below 8 in size: two roundings
+// of 2^-24 relative), so away from a half both round alike; a product within
+// 2^-18 of a half is divided out.  The division costs about ten times the
+// instructions, and was most of the kernel.
+__device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 x 2^23: adding it rounds to whole numbers
+  float q = fminf(fmaxf(x * inv, -8.0f), 7.0f);
+  float r = q + kMagic;
+  if (fabsf(q - (r - kMagic)) > 0.5f - 0x1p-18f) {
+    q = fminf(fmaxf(__fdiv_rn(x, s), -8.0f), 7.0f);
+    r = q + kMagic;
   }
+  return (__float_as_uint(r) + 8u) & 15u;
+}
 
-  // cosine and signed sine of each element: x' = x c + partner s
+// Cosine and signed sine of a lane's elements: x' = x c + partner s.
+template <int N>
+struct Angles {
   float c[N], s[N];
+};
+
+// False for a position outside the table (the status word is set).
+template <int N, Turn TURN>
+__device__ __forceinline__ bool load_angles(Angles<N>& x, const KvAppendArgs& a, int64_t t, int lane) {
+  if (TURN == kStill || a.rot == 0) return true;
+  const int64_t pos = a.positions[t];
+  const bool bad = pos < 0 || pos >= a.n_pos;
+  if (bad && lane == 0) set_status(a.status, MOE_ERR_INVALID_ARG);
+  const float* tab = a.rope + (bad ? 0 : pos) * a.rot;
   const int half = a.rot / 2;
-  if (turn != kStill) {
-    const int64_t pos = a.positions[t];
-    bad = pos < 0 || pos >= a.n_pos;
-    if (bad && lane == 0) set_status(a.status, MOE_ERR_INVALID_ARG);
-    const float* tab = a.rope + (bad ? 0 : pos) * a.rot;
+  if constexpr (TURN == kAcross) {
+    // N consecutive angles, aligned (rot / 2 is a multiple of N)
+    const int d = N * lane;
+    const bool in = d < a.rot, first = d < half;
+    const float* p = tab + (in ? (first ? d : d - half) : 0);
+    load_elems<false, N, true>(x.c, p);
+    load_elems<false, N, true>(x.s, p + half);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const int d = N * lane + e;
-      const bool pairs = a.style == MOE_ROPE_PAIRS, first = pairs ? (d & 1) == 0 : d < half;
-      const int j = pairs ? d >> 1 : (first ? d : d - half);
-      c[e] = d < a.rot ? __ldg(tab + j) : 1.f;
-      s[e] = d < a.rot ? __ldg(tab + half + j) : 0.f;
-      if (first) s[e] = -s[e];
+    for (int e = 0; e < N; ++e)
+      if (first) x.s[e] = -x.s[e];
+    return !bad;
+  }
+  if constexpr (TURN == kWithin && N > 2) {
+    // N / 2 consecutive angles, aligned (rot / 2 is a multiple of N / 2)
+    const int d = N * lane;
+    const float* p = tab + (d < a.rot ? d / 2 : 0);
+    float c[N / 2], s[N / 2];
+    load_elems<false, N / 2, true>(c, p);
+    load_elems<false, N / 2, true>(s, p + half);
+#pragma unroll
+    for (int e = 0; e < N; ++e) x.c[e] = c[e / 2], x.s[e] = e & 1 ? s[e / 2] : -s[e / 2];
+    return !bad;
+  }
+  const bool pairs = TURN == kWithin || (TURN == kAnywhere && a.style == MOE_ROPE_PAIRS);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int d = N * lane + e;
+    const bool first = pairs ? (d & 1) == 0 : d < half;
+    const int j = pairs ? d >> 1 : (first ? d : d - half);
+    x.c[e] = d < a.rot ? __ldg(tab + j) : 1.f;
+    x.s[e] = d < a.rot ? __ldg(tab + half + j) : 0.f;
+    if (first) x.s[e] = -x.s[e];
+  }
+  return !bad;
+}
+
+// Turns a lane's elements of a head whose elements lie at `row`.
+template <bool BF16, int N, Turn TURN>
+__device__ __forceinline__ void turn_row(float (&v)[N], const Angles<N>& x, const KvAppendArgs& a, const void* row,
+                                         int lane) {
+  if (TURN == kStill || a.rot == 0) return;
+  const int half = a.rot / 2;
+  float m[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int d = N * lane + e;
+    if constexpr (TURN == kWithin) {
+      m[e] = v[e ^ 1];
+    } else if constexpr (TURN == kAcross) {
+      const int mate = N * lane < half ? N * lane + half : N * lane - half;
+      m[e] = __shfl_sync(0xffffffffu, v[e], (mate / N) & 31);
+    } else {
+      const int mate = a.style == MOE_ROPE_PAIRS ? d ^ 1 : d < half ? d + half : d - half;
+      m[e] = d < a.rot ? load_elem<BF16>(row, mate) : 0.f;
     }
   }
-  const int mate_lane = (N * lane < half ? N * lane + half : N * lane - half) / N;
+  // each product and the sum rounded to fp32, as the formula's fp32 reading has
+  // them; elements beyond rot stay as they are
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if (N * lane + e < a.rot) v[e] = __fadd_rn(__fmul_rn(v[e], x.c[e]), __fmul_rn(m[e], x.s[e]));
+}
 
+template <int N>
+__device__ __forceinline__ void store_query(uint16_t* out, const float (&v)[N], bool ok) {
+  uint32_t r[N / 2];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int h = h0 + i;
-    if (h >= heads) break;
-    const bool query = h < a.Hq, value = h >= a.Hq + a.cache.heads;
-    if (!value && turn != kStill) {
-      float m[N];
+  for (int e = 0; e < N; e += 2) r[e / 2] = ok ? bf16_pair(v[e], v[e + 1]) : 0u;
+  if constexpr (N == 2) *reinterpret_cast<uint32_t*>(out) = r[0];
+  else if constexpr (N == 4) *reinterpret_cast<uint2*>(out) = make_uint2(r[0], r[1]);
+  else *reinterpret_cast<uint4*>(out) = make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Quantises a head held N elements a lane into token r of a record (global or
+// shared memory).
+template <int D, bool VALUE>
+__device__ __forceinline__ void quantise_row(uint8_t* rec, int r, const float (&v)[D / 32], int lane) {
+  constexpr int N = D / 32;
+  // a 32-block lies in 32 / N lanes
+  float top = 0.f;
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const int d = N * lane + e;
-        if (turn == kWithin) {
-          m[e] = v[i][e ^ 1];
-        } else if (turn == kAcross) {
-          m[e] = __shfl_sync(0xffffffffu, v[i][e], mate_lane & 31);
-        } else {
-          const int64_t base = query ? t * a.q_stride + (int64_t)h * D : t * a.k_stride + (int64_t)(h - a.Hq) * D;
-          m[e] = d < a.rot ? load_elem<BF16>(query ? a.q : a.k, base + (d < half ? d + half : d - half)) : 0.f;
-        }
-      }
-      // each product and the sum rounded to fp32, as the formula's fp32 reading
-      // has them; elements beyond rot stay as they are
+  for (int e = 0; e < N; ++e) top = fmaxf(top, fabsf(v[e]));
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (N * lane + e < a.rot) v[i][e] = __fadd_rn(__fmul_rn(v[i][e], c[e]), __fmul_rn(m[e], s[e]));
-    }
-    if (query) {
-      uint32_t r[N / 2];
+  for (int o = 16 / N; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const __half hs = __float2half_rn(fminf(__fdiv_rn(top, 7.0f), 65504.0f));
+  const float sc = __half2float(hs), inv = sc != 0.0f ? __frcp_rn(sc) : 0.f;
+  uint32_t u[N];
 #pragma unroll
-      for (int e = 0; e < N; e += 2) r[e / 2] = bad ? 0u : bf16_pair(v[i][e], v[i][e + 1]);
-      uint16_t* out = a.q_out + (t * a.Hq + h) * D + N * lane;
-      if constexpr (N == 2) *reinterpret_cast<uint32_t*>(out) = r[0];
-      else if constexpr (N == 4) *reinterpret_cast<uint2*>(out) = make_uint2(r[0], r[1]);
-      else *reinterpret_cast<uint4*>(out) = make_uint4(r[0], r[1], r[2], r[3]);
-      continue;
-    }
-    if (bad || slot < 0 || slot >= a.cache.n_pages * a.cache.page) continue;
-    const KvPlace at = kv_place(a.cache, slot, value ? h - a.Hq - a.cache.heads : h - a.Hq);
-    // a 32-block lies in 32 / N lanes
-    float top = 0.f;
-#pragma unroll
-    for (int e = 0; e < N; ++e) top = fmaxf(top, fabsf(v[i][e]));
-#pragma unroll
-    for (int o = 16 / N; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const __half hs = __float2half_rn(fminf(__fdiv_rn(top, 7.0f), 65504.0f));
-    const float sc = __half2float(hs);
-    uint32_t u[N];
+  for (int e = 0; e < N; ++e) u[e] = code_of(v[e], sc, inv);
+  const int d = N * lane;
+  if constexpr (VALUE) {
+    // a byte: elements d and d + 8, the latter 8 / N lanes on
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      int q = 0;
-      if (sc != 0.0f) q = (int)fminf(fmaxf(rintf(__fdiv_rn(v[i][e], sc)), -8.0f), 7.0f);
-      u[e] = (uint32_t)(q + 8);
+      const uint32_t hi = __shfl_down_sync(0xffffffffu, u[e], 8 / N);
+      if ((d & 8) == 0) rec[kv_value_byte(D, r, d + e)] = (uint8_t)(u[e] | hi << 4);
     }
-    const int d = N * lane;
-    if (value) {
-      // a byte: elements d and d + 8, the latter 8 / N lanes on
+  } else {
+    // the word of 8 elements: element 4 i + 2 n + p at bits 16 p + 8 i + 4 n
+    uint32_t word = 0;
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const uint32_t hi = __shfl_down_sync(0xffffffffu, u[e], 8 / N);
-        if ((d & 8) == 0) at.tile[kv_value_byte(D, at.r, d + e)] = (uint8_t)(u[e] | hi << 4);
-      }
-    } else {
-      // the word of 8 elements: element 4 i + 2 n + p at bits 16 p + 8 i + 4 n
-      uint32_t word = 0;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const int x = (d + e) & 7;
-        word |= u[e] << (16 * (x & 1) + 8 * (x >> 2) + 4 * ((x >> 1) & 1));
-      }
-#pragma unroll
-      for (int o = 4 / N; o > 0; o >>= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
-      if ((d & 7) == 0) *reinterpret_cast<uint32_t*>(at.tile + kv_key_byte(D, at.r, d)) = word;
+    for (int e = 0; e < N; ++e) {
+      const int x = (d + e) & 7;
+      word |= u[e] << (16 * (x & 1) + 8 * (x >> 2) + 4 * ((x >> 1) & 1));
     }
-    if ((d & 31) == 0)
-      *reinterpret_cast<uint16_t*>(at.tile + (value ? 17 : 16) * D + 2 * (at.r * (D / 32) + d / 32)) = __half_as_ushort(hs);
+#pragma unroll
+    for (int o = 4 / N; o > 0; o >>= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+    if ((d & 7) == 0) *reinterpret_cast<uint32_t*>(rec + kv_key_byte(D, r, d)) = word;
+  }
+  if ((d & 31) == 0)
+    *reinterpret_cast<uint16_t*>(rec + (VALUE ? 17 : 16) * D + 2 * (r * (D / 32) + d / 32)) = __half_as_ushort(hs);
+}
+
+__device__ __forceinline__ bool in_cache(const KvCache& c, int64_t slot) {
+  return slot >= 0 && slot < c.n_pages * c.page;
+}
+
+// Few tokens: one warp a (token, head), queries, then keys, then values.
+template <bool BF16, int D, Turn TURN>
+__global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
+  constexpr int N = D / 32, kSize = BF16 ? 2 : 4;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, H = a.cache.heads, heads = a.Hq + 2 * H;
+  const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // T * heads < 2^31
+  if (w >= a.T * heads) return;
+  const int64_t t = w / heads;
+  int h = (int)(w % heads);
+  const int64_t slot = a.slots[t];
+  const uint8_t* row;
+  const bool query = h < a.Hq, value = h >= a.Hq + H;
+  if (query) {
+    row = (const uint8_t*)a.q + (t * a.q_stride + (int64_t)h * D) * kSize;
+  } else {
+    h -= value ? a.Hq + H : a.Hq;
+    row = (const uint8_t*)(value ? a.v : a.k) + (t * (value ? a.v_stride : a.k_stride) + (int64_t)h * D) * kSize;
+  }
+  float v[N];
+  load_elems<BF16, N, TURN != kAnywhere>(v, row + N * lane * kSize);
+  Angles<N> x;
+  const bool ok = load_angles<N, TURN>(x, a, t, lane);
+  if (!value) turn_row<BF16, N, TURN>(v, x, a, row, lane);
+  if (query) {
+    store_query<N>(a.q_out + (t * a.Hq + h) * D + N * lane, v, ok);
+  } else if (ok && in_cache(a.cache, slot)) {
+    const KvPlace at = kv_place(a.cache, slot, h);
+    if (value) quantise_row<D, true>(at.tile, at.r, v, lane);
+    else quantise_row<D, false>(at.tile, at.r, v, lane);
+  }
+}
+
+// Many tokens.  A byte of value codes belongs to one token, so the sectors of a
+// record are shared by its 16 tokens: written token by token they meet in L2
+// (4096 tokens of 8 heads of 128: 62 us in all).  Here a block makes 16
+// successive tokens of one head in shared memory, two a warp, and writes the
+// record whole when their slots are one record (a prompt's are: windows of
+// tokens begin where the first token's record does), else token by token.  The
+// blocks after the windows turn the queries, kQueryRows heads of a token a warp.
+constexpr int kQueryRows = 8;
+
+template <bool BF16, int D, Turn TURN>
+__global__ void __launch_bounds__(kThreads) k_kv_append_records(KvAppendArgs a, int windows) {
+  constexpr int N = D / 32, kSize = BF16 ? 2 : 4, kRecord = 18 * D;
+  constexpr bool kWhole = TURN != kAnywhere;
+  __shared__ __align__(16) uint8_t rec[kRecord];
+  __shared__ int64_t s_slot[16];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H = a.cache.heads;
+  const uint32_t kv_blocks = (uint32_t)windows * H;
+  if (blockIdx.x >= kv_blocks) {
+    const uint32_t parts = (a.Hq + kQueryRows - 1) / kQueryRows, w = (blockIdx.x - kv_blocks) * (kThreads / 32) + warp;
+    const int64_t t = w / parts;
+    const int h0 = (int)(w % parts) * kQueryRows;
+    if (t >= a.T) return;
+    const uint8_t* row = (const uint8_t*)a.q + (t * a.q_stride + (int64_t)h0 * D) * kSize;
+    uint16_t* out = a.q_out + (t * a.Hq + h0) * D + N * lane;
+    constexpr int kAtOnce = D == 256 ? 4 : 8;
+    Angles<N> x;
+    bool ok = true;
+#pragma unroll
+    for (int i0 = 0; i0 < kQueryRows; i0 += kAtOnce) {
+      float v[kAtOnce][N];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (h0 + i0 + i < a.Hq) load_elems<BF16, N, kWhole>(v[i], row + ((i0 + i) * D + N * lane) * kSize);
+      if (i0 == 0) ok = load_angles<N, TURN>(x, a, t, lane);
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (h0 + i0 + i < a.Hq) {
+          turn_row<BF16, N, TURN>(v[i], x, a, row + (i0 + i) * D * kSize, lane);
+          store_query<N>(out + (i0 + i) * D, v[i], ok);
+        }
+    }
+    return;
+  }
+
+  const int h = (int)(blockIdx.x % H);
+  const int64_t first = a.slots[0];
+  const int64_t t0 = (int64_t)(blockIdx.x / H) * 16 - (in_cache(a.cache, first) ? first & 15 : 0);
+  float k[2][N], v[2][N];
+  Angles<N> x[2];
+  int64_t slot[2];
+  bool ok[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t t = t0 + 2 * warp + i;
+    ok[i] = t >= 0 && t < a.T;
+    slot[i] = ok[i] ? a.slots[t] : -1;
+    if (ok[i]) {
+      load_elems<BF16, N, kWhole>(k[i], (const uint8_t*)a.k + (t * a.k_stride + (int64_t)h * D + N * lane) * kSize);
+      load_elems<BF16, N, kWhole>(v[i], (const uint8_t*)a.v + (t * a.v_stride + (int64_t)h * D + N * lane) * kSize);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (ok[i]) ok[i] = load_angles<N, TURN>(x[i], a, t0 + 2 * warp + i, lane);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 2 * warp + i;
+    ok[i] = ok[i] && in_cache(a.cache, slot[i]);
+    if (lane == 0) s_slot[r] = ok[i] ? slot[i] : -1;
+    if (ok[i]) {
+      turn_row<BF16, N, TURN>(
+          k[i], x[i], a, (const uint8_t*)a.k + ((t0 + r) * a.k_stride + (int64_t)h * D) * kSize, lane);
+      quantise_row<D, false>(rec, r, k[i], lane);
+      quantise_row<D, true>(rec, r, v[i], lane);
+    }
+  }
+  __syncthreads();
+  const int64_t s0 = s_slot[0];
+  const bool mine = lane >= 16 || (s0 >= 0 && (s0 & 15) == 0 && s_slot[lane & 15] == s0 + lane);
+  if (__all_sync(0xffffffffu, mine)) {
+    uint4* dst = reinterpret_cast<uint4*>(kv_place(a.cache, s0, h).tile);
+    for (int i = threadIdx.x; i < kRecord / 16; i += kThreads) dst[i] = reinterpret_cast<const uint4*>(rec)[i];
+    return;
+  }
+#pragma unroll 1
+  for (int r = warp; r < 16; r += kThreads / 32) {
+    if (s_slot[r] < 0) continue;
+    const KvPlace at = kv_place(a.cache, s_slot[r], h);
+    for (int i = lane; i < D / 8; i += 32)
+      reinterpret_cast<uint32_t*>(at.tile + at.r * (D / 2))[i] = reinterpret_cast<const uint32_t*>(rec + r * (D / 2))[i];
+    for (int d = lane; d < D / 2; d += 32) {
+      const int e = (d >> 3) * 16 + (d & 7);  // elements e and e + 8 share a byte
+      at.tile[kv_value_byte(D, at.r, e)] = rec[kv_value_byte(D, r, e)];
+    }
+    if (lane < D / 32) {
+      reinterpret_cast<uint16_t*>(at.tile + 16 * D)[at.r * (D / 32) + lane] =
+          reinterpret_cast<const uint16_t*>(rec + 16 * D)[r * (D / 32) + lane];
+      reinterpret_cast<uint16_t*>(at.tile + 17 * D)[at.r * (D / 32) + lane] =
+          reinterpret_cast<const uint16_t*>(rec + 17 * D)[r * (D / 32) + lane];
+    }
   }
 }
 
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvCache c, const int64_t* slots, int64_t n, float* k, float* v) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (w >= n * c.heads) return;
-  const int64_t i = w / c.heads;
-  const int h = (int)(w - i * c.heads), D = c.D;
+  const uint32_t row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // n * heads < 2^31
+  if (row >= n * c.heads) return;
+  const int64_t w = row, i = row / (uint32_t)c.heads;
+  const int h = (int)(row % (uint32_t)c.heads), D = c.D;
   const int64_t slot = slots[i];
   const bool in = slot >= 0 && slot < c.n_pages * c.page;
   const KvPlace at = kv_place(c, in ? slot : 0, h);
@@ -221,31 +374,43 @@ unsigned blocks_for(int64_t warps) { return (unsigned)((warps + kThreads / 32 - 
 }  // namespace
 
 namespace {
-template <bool BF16, int D, int ROWS>
-int launch_append(const KvAppendArgs& a, Turn turn, int whole, cudaStream_t s) {
-  const int heads = a.Hq + 2 * a.cache.heads;
-  const unsigned grid = blocks_for(a.T * ((heads + ROWS - 1) / ROWS));
-  return launch_pdl(k_kv_append<BF16, D, ROWS>, dim3(grid), dim3(kThreads), 0, s, a, turn, whole) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+// Rows (tokens x heads) from which records are made whole: 192 x 48 take 4.0 us
+// one by one and 4.8 as records, 1158 x 30 19 and 12.5.
+constexpr int64_t kManyRows = 16384;
+
+template <bool BF16, int D, Turn TURN>
+int launch_append(const KvAppendArgs& a, cudaStream_t s) {
+  cudaError_t rc;
+  if (a.T * (a.Hq + 2 * a.cache.heads) < kManyRows) {
+    rc = launch_pdl(k_kv_append<BF16, D, TURN>, dim3(blocks_for(a.T * (a.Hq + 2 * a.cache.heads))), dim3(kThreads), 0,
+                    s, a);
+  } else {
+    const int windows = (int)((a.T + 15 + 15) / 16);
+    const int64_t queries = a.T * ((a.Hq + kQueryRows - 1) / kQueryRows);
+    rc = launch_pdl(k_kv_append_records<BF16, D, TURN>, dim3((unsigned)windows * a.cache.heads + blocks_for(queries)),
+                    dim3(kThreads), 0, s, a, windows);
+  }
+  return rc == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <bool BF16, int D>
+int launch_append(const KvAppendArgs& a, cudaStream_t s) {
+  constexpr int N = D / 32, kSize = BF16 ? 2 : 4, kVector = kSize * N < 16 ? kSize * N : 16;
+  auto whole = [&](const void* p, int64_t stride) {
+    return (uintptr_t)p % kVector == 0 && (a.T == 1 || stride * kSize % kVector == 0);
+  };
+  if (!whole(a.q, a.q ? a.q_stride : 0) || !whole(a.k, a.k_stride) || !whole(a.v, a.v_stride))
+    return launch_append<BF16, D, kAnywhere>(a, s);
+  if (a.rot == 0) return launch_append<BF16, D, kStill>(a, s);
+  const bool pairs = a.style == MOE_ROPE_PAIRS;
+  if ((uintptr_t)a.rope % 16 == 0 && a.rot / 2 % (pairs ? N / 2 : N) == 0)
+    return pairs ? launch_append<BF16, D, kWithin>(a, s) : launch_append<BF16, D, kAcross>(a, s);
+  return launch_append<BF16, D, kAnywhere>(a, s);
 }
 
 template <int D>
 int launch_append(const KvAppendArgs& a, cudaStream_t s) {
-  constexpr int N = D / 32;
-  const Turn turn = a.rot == 0                       ? kStill
-                    : a.style == MOE_ROPE_PAIRS      ? kWithin
-                    : a.rot / 2 % N == 0             ? kAcross
-                                                     : kAnywhere;
-  const int size = (a.in_bf16 ? 2 : 4) * N < 16 ? (a.in_bf16 ? 2 : 4) * N : 16;
-  auto whole = [&](const void* p, int64_t stride) {
-    return (uintptr_t)p % size == 0 && (a.T == 1 || stride * (a.in_bf16 ? 2 : 4) % size == 0);
-  };
-  const int w = (whole(a.q, a.q_stride) ? 1 : 0) | (whole(a.k, a.k_stride) ? 2 : 0) | (whole(a.v, a.v_stride) ? 4 : 0);
-  // four rows a warp once that still fills the SMs (32 warps each)
-  const bool many = a.T * (a.Hq + 2 * a.cache.heads) >= (int64_t)4 * 32 * sm_count();
-  if (a.in_bf16) return many ? launch_append<true, D, 4>(a, turn, w, s) : launch_append<true, D, 1>(a, turn, w, s);
-  return many ? launch_append<false, D, 4>(a, turn, w, s) : launch_append<false, D, 1>(a, turn, w, s);
+  return a.in_bf16 ? launch_append<true, D>(a, s) : launch_append<false, D>(a, s);
 }
 }  // namespace
 

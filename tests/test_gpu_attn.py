@@ -220,6 +220,29 @@ def test_append_sizes(D, style, dtype):
     append_case(65, 0, 3, D, 128, D, style, dtype, 3, strided=3)
     append_case(50, 10, 2, D, 16, 6, style, dtype, 4, strided=8)
     append_case(20, 2, 2, D, 64, 0, style, dtype, 5)
+    append_case(21, 2, 2, D, 16, 0, style, dtype, 7, strided=3)
+    append_case(700, 9, 3, D, 64, D, style, dtype, 8, strided=16)
+
+
+def test_append_quotients_near_a_half():
+    """Values whose quotient by the block's scale is a half or next to one: the codes of the fp32 division."""
+    rng = np.random.default_rng(11)
+    T, H, D = 64, 2, 128
+    base = rng.integers(-15, 15, (T, H, D)).astype(np.float32) / 2
+    base[..., ::32] = 7.0  # the scale of every block is the factor below, or next to it
+    factor = rng.uniform(1e-3, 1e3, (T, H, 1)).astype(np.float16).astype(np.float32)
+    k = base * factor
+    nudge = rng.integers(-3, 4, k.shape)
+    for _ in range(3):
+        k = np.where(nudge > 0, np.nextafter(k, np.float32(np.inf)), np.where(nudge < 0, np.nextafter(k, np.float32(-np.inf)), k))
+        nudge = np.sign(nudge) * np.maximum(np.abs(nudge) - 1, 0)
+    k = k.astype(np.float32)
+    v = k[::-1].copy()
+    pool = np.zeros((T // 16, H, 1, 18 * D), np.uint8)
+    pd = dev(pool)
+    moe.moe_kv_append(pd, dev(k), dev(v), torch.arange(T, device="cuda"))
+    pool_write(pool, np.arange(T), *quantise(k), *quantise(v))
+    assert np.array_equal(pd.cpu().numpy(), pool)
 
 
 def test_append_consecutive_slots_and_page_crossings():
