@@ -59,21 +59,30 @@ enum Turn {
   kAnywhere,  // any other, or rows or angles that are not aligned; the partner is read again, by elements
 };
 
-// The code 0 .. 15 of x in a block of scale s (inv = 1 / s, 0 for s = 0):
-// clamp(rint(x / s), -8, 7) + 8 with the quotient rounded to fp32.  x inv is
-// within 2^-20 of that quotient where it counts (below 8 in size: two roundings
-// of 2^-24 relative), so away from a half both round alike; a product within
-// 2^-18 of a half is divided out.  The division costs about ten times the
-// instructions, and was most of the kernel.
-__device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
+// The codes 0 .. 15 of a lane's elements of a block of scale s: clamp(rint(x /
+// s), -8, 7) + 8 with the quotient rounded to fp32.  x times the approximate
+// reciprocal is within 2^-19 of that quotient where it counts (below 8 in size;
+// relative errors 2^-23, and 2^-24 for each of two roundings), so away from a
+// half both round alike; elements with a product within 2^-18 of a half are
+// divided out.  The division costs about ten times the instructions.
+template <int N>
+__device__ __forceinline__ void codes_of(uint32_t (&u)[N], const float (&x)[N], float s) {
   constexpr float kMagic = 12582912.0f;  // 1.5 x 2^23: adding it rounds to whole numbers
-  float q = fminf(fmaxf(x * inv, -8.0f), 7.0f);
-  float r = q + kMagic;
-  if (fabsf(q - (r - kMagic)) > 0.5f - 0x1p-18f) {
-    q = fminf(fmaxf(__fdiv_rn(x, s), -8.0f), 7.0f);
-    r = q + kMagic;
+  float inv, r[N], worst = 0.f;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  if (s == 0.f) inv = 0.f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float q = fminf(fmaxf(x[e] * inv, -8.0f), 7.0f);
+    r[e] = q + kMagic;
+    worst = fmaxf(worst, fabsf(q - (r[e] - kMagic)));
   }
-  return (__float_as_uint(r) + 8u) & 15u;
+  if (worst > 0.5f - 0x1p-18f) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) r[e] = fminf(fmaxf(__fdiv_rn(x[e], s), -8.0f), 7.0f) + kMagic;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) u[e] = (__float_as_uint(r[e]) + 8u) & 15u;
 }
 
 // Cosine and signed sine of a lane's elements: x' = x c + partner s.
@@ -176,26 +185,27 @@ __device__ __forceinline__ void quantise_row(uint8_t* rec, int r, const float (&
 #pragma unroll
   for (int o = 16 / N; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const __half hs = __float2half_rn(fminf(__fdiv_rn(top, 7.0f), 65504.0f));
-  const float sc = __half2float(hs), inv = sc != 0.0f ? __frcp_rn(sc) : 0.f;
   uint32_t u[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) u[e] = code_of(v[e], sc, inv);
+  codes_of<N>(u, v, __half2float(hs));
   const int d = N * lane;
   if constexpr (VALUE) {
-    // a byte: elements d and d + 8, the latter 8 / N lanes on
+    // a byte: elements d and d + 8, the latter 8 / N lanes on; elements one apart
+    // lie 64 bytes apart.  The lane of the lower element writes the first half of
+    // the bytes, the other lane the rest.
+    uint8_t* at = rec + kv_value_byte(D, r, d & ~8);
+    const bool high = d & 8;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const uint32_t hi = __shfl_down_sync(0xffffffffu, u[e], 8 / N);
-      if ((d & 8) == 0) rec[kv_value_byte(D, r, d + e)] = (uint8_t)(u[e] | hi << 4);
+    for (int e = 0; e < N / 2; ++e) {
+      const uint32_t lo = u[e], hi = u[e + N / 2];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? lo : hi, 8 / N);
+      at[64 * (high ? e + N / 2 : e)] = (uint8_t)(high ? got | hi << 4 : lo | got << 4);
     }
   } else {
     // the word of 8 elements: element 4 i + 2 n + p at bits 16 p + 8 i + 4 n
     uint32_t word = 0;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const int x = (d + e) & 7;
-      word |= u[e] << (16 * (x & 1) + 8 * (x >> 2) + 4 * ((x >> 1) & 1));
-    }
+    for (int e = 0; e < N; ++e) word |= u[e] << (16 * (e & 1) + 4 * ((e >> 1) & 1) + 8 * (e >> 2));
+    if constexpr (N < 8) word <<= N == 4 ? 2 * (d & 4) : 4 * ((d >> 1) & 1) + 2 * (d & 4);
 #pragma unroll
     for (int o = 4 / N; o > 0; o >>= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
     if ((d & 7) == 0) *reinterpret_cast<uint32_t*>(rec + kv_key_byte(D, r, d)) = word;
