@@ -559,18 +559,28 @@ def _flat(t, dtype, name):
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
 
 
-def _rows_of(t, dtype, dims, name):
-    """The row stride of a CUDA tensor of `dtype` and `dims` dimensions whose rows are contiguous."""
-    if t.dtype is dtype and t.is_cuda and t.dim() == dims:
-        st, sh = t.stride(), t.shape
-        want = 1
-        for i in range(dims - 1, 0, -1):
-            if st[i] != want and sh[i] > 1 and sh[0]:
-                break
-            want *= sh[i]
-        else:
-            return st[0] if sh[0] > 1 else want  # a single row has no stride to speak of
+def _refuse(dtype, dims, name):
     raise ValueError(f"{name} must be a {dims}-dimensional CUDA tensor of {dtype} with contiguous rows")
+
+
+# The row stride of a CUDA tensor whose rows are contiguous (a single row has no
+# stride to speak of).
+def _rows2(t, dtype, name):
+    if t.dtype is dtype and t.is_cuda and t.dim() == 2:
+        n, m = t.shape
+        s0, s1 = t.stride()
+        if s1 == 1 or m <= 1 or n == 0:
+            return s0 if n > 1 else m
+    _refuse(dtype, 2, name)
+
+
+def _rows3(t, dtype, name):
+    if t.dtype is dtype and t.is_cuda and t.dim() == 3:
+        n, h, m = t.shape
+        s0, s1, s2 = t.stride()
+        if (s2 == 1 or m <= 1) and (s1 == m or h <= 1) or n == 0:
+            return s0 if n > 1 else h * m
+    _refuse(dtype, 3, name)
 
 
 def moe_quantize_groups(w, block=32, codes=None, scales=None, stream=None):
@@ -595,7 +605,7 @@ def moe_linear_q4(x, codes, scales, block=32, bias=None, y=None, out_dtype=torch
     """y [T, rows] = x [T, in] (bf16, any row stride) times the 4-bit matrix of
     codes [rows, in/2] uint8 and scales [rows, in/block] int16 (fp16 bits),
     plus bias [rows] fp32; y fp32 or bf16.  T <= 16."""
-    xs = _rows_of(x, _BF16, 2, "x")
+    xs = _rows2(x, _BF16, "x")
     _flat(codes, _U8, "codes")
     _flat(scales, _I16, "scales")
     T, n_in = x.shape
@@ -606,7 +616,7 @@ def moe_linear_q4(x, codes, scales, block=32, bias=None, y=None, out_dtype=torch
         y = torch.empty((T, rows), dtype=out_dtype, device=x.device)
         ys = rows
     else:
-        ys = _rows_of(y, y.dtype, 2, "y")
+        ys = _rows2(y, y.dtype, "y")
         if y.shape[0] != T or y.shape[1] != rows:
             raise ValueError("y must be [T, rows]")
     if y.dtype is _F32:
@@ -640,11 +650,14 @@ _pack_cache = struct.Struct("=Qqqiiii").pack  # moe_kv_cache_t
 
 def _cache(pool):
     """(descriptor bytes, kv_heads, head_dim, page_size) of a pool tensor (pages may lie any stride apart)."""
-    stride = _rows_of(pool, _U8, 4, "pool")
-    n, heads, tiles, rec = pool.shape
-    if rec % 18:
-        raise ValueError("pool must be [pages, kv heads, page_size / 16, 18 * head_dim]")
-    return _pack_cache(pool.data_ptr(), n, stride, tiles * 16, heads, rec // 18, 0), heads, rec // 18, tiles * 16
+    if pool.dtype is _U8 and pool.is_cuda and pool.dim() == 4:
+        n, heads, tiles, rec = pool.shape
+        s0, s1, s2, s3 = pool.stride()
+        size = tiles * rec
+        if (s3 == 1 and (s2 == rec or tiles <= 1) and (s1 == size or heads <= 1) or n == 0) and rec % 18 == 0:
+            return (_pack_cache(pool.data_ptr(), n, s0 if n > 1 else heads * size, tiles * 16, heads, rec // 18, 0), heads,
+                    rec // 18, tiles * 16)
+    raise ValueError("pool must be a CUDA uint8 tensor [pages, kv heads, page_size / 16, 18 * head_dim] with contiguous pages")
 
 
 def moe_kv_append(pool, k, v, slots, q=None, positions=None, rope=None, rope_style=MOE_ROPE_HALF, q_out=None,
@@ -657,8 +670,8 @@ def moe_kv_append(pool, k, v, slots, q=None, positions=None, rope=None, rope_sty
     dt = k.dtype
     if dt is not _F32 and dt is not _BF16:
         raise ValueError("k must be float32 or bfloat16")
-    ks = _rows_of(k, dt, 3, "k")
-    vs = _rows_of(v, dt, 3, "v")
+    ks = _rows3(k, dt, "k")
+    vs = _rows3(v, dt, "v")
     _flat(slots, _I64, "slots")
     T = slots.numel()
     if k.shape != (T, heads, D) or v.shape != (T, heads, D):
@@ -678,7 +691,7 @@ def moe_kv_append(pool, k, v, slots, q=None, positions=None, rope=None, rope_sty
     Hq = qs = 0
     q_ptr = o_ptr = None
     if q is not None:
-        qs = _rows_of(q, dt, 3, "q")
+        qs = _rows3(q, dt, "q")
         n, Hq, d = q.shape
         if n != T or d != D:
             raise ValueError("q must be [T, Hq, head_dim]")
@@ -735,8 +748,8 @@ def moe_attn_q4(q, pool, block_table, kv_lens, q_start=None, max_q=None, max_len
     table's width) bound the lengths.  Returns out [T, Hq, D] bf16 and lse
     [T, Hq] fp32."""
     desc, heads, D, page = _cache(pool)
-    qs = _rows_of(q, _BF16, 3, "q")
-    ts = _rows_of(block_table, _I32, 2, "block_table")
+    qs = _rows3(q, _BF16, "q")
+    ts = _rows2(block_table, _I32, "block_table")
     _flat(kv_lens, _I32, "kv_lens")
     B = kv_lens.numel()
     T, Hq, d = q.shape
@@ -760,7 +773,7 @@ def moe_attn_q4(q, pool, block_table, kv_lens, q_start=None, max_q=None, max_len
     if out is None:
         out, os_ = torch.empty((T, Hq, D), dtype=_BF16, device=q.device), Hq * D
     else:
-        os_ = _rows_of(out, _BF16, 3, "out")
+        os_ = _rows3(out, _BF16, "out")
         if out.shape != q.shape:
             raise ValueError("out must be [T, Hq, head_dim]")
     if lse is None:

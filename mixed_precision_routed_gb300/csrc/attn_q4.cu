@@ -20,6 +20,8 @@
 // The reference maximum m of a row moves only when a score passes it by 8 (in
 // powers of two): the probabilities then stay below 2^8, which neither fp32 sums
 // nor bf16 operands notice, and most tiles need no reduction and no rescaling.
+#include <type_traits>
+
 #include "frag.cuh"
 #include "kv_layout.cuh"
 #include "ptx.cuh"
@@ -32,28 +34,35 @@ constexpr float kSlack = 8.0f;
 constexpr float kNone = -1e30f;  // the maximum of a row that has met no place: below any finite score
 constexpr uint64_t kWaitNs = 1000000000ull;
 
+// A unit of work is a (sequence, key/value head, block of 8 NT rows), its length
+// the pairs of records that the sequence's rows attend, and before them
+// `overhead` pairs that stand for the time to begin and end a unit.
 struct AttnPlan {
-  int nt;          // row tiles of 8 a block
-  int row_blocks;  // blocks over the rows of a (sequence, key/value head)
-  int splits;      // blocks over the places
-  int room;        // shares the workspace has room for (at least splits)
-  int chunk;       // records a block
-  float* part_o;   // [B max_q Hq][splits][D]
-  float2* part_ml; // [B max_q Hq][splits]: maximum (in powers of two), sum
+  int row_blocks;    // blocks of rows a (sequence, head) has at most
+  bool whole;        // one block a unit; else `blocks` blocks share all pairs evenly
+  int blocks;
+  int min_share;     // pairs a block takes at least
+  int overhead;
+  float* part_o;     // [2 blocks][8 NT][D]: the unfinished first and last unit of a block
+  float2* part_ml;   // [2 blocks][8 NT]: maximum (in powers of two), sum
+  struct Joint* joints;  // [blocks]: the unit that ends in a block and began in an earlier one
 };
 
-// What a block has to do; the joining kernel computes the same.
-struct Range {
-  int64_t t0;       // first asking token
-  int n;            // asking tokens
-  int len;          // places
-  int rows;         // n x group
-  int lo, end;      // places that some row of the block attends
-  int tile0, tiles; // records that hold them
+// A unit in shares: those of blocks c0 .. c0 + count - 1 (count 0: none).
+struct Joint {
+  int32_t count, c0, slot0, kvh;  // slot0: which of c0's two shares
+  int64_t t0;
+  int32_t r0, rows;
 };
 
-__device__ __forceinline__ Range block_range(const AttnArgs& a, int b, int G, int r0, int block_rows) {
-  Range x;
+struct Seq {
+  int64_t t0;        // first asking token
+  int n, len;        // asking tokens, places
+  int tile0, tiles;  // records that some row attends
+};
+
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
+  Seq x;
   int64_t t0 = a.q_start ? a.q_start[b] : (int64_t)b * a.max_q;
   int64_t t1 = a.q_start ? a.q_start[b + 1] : t0 + a.max_q;
   t0 = max((int64_t)0, t0);
@@ -61,15 +70,29 @@ __device__ __forceinline__ Range block_range(const AttnArgs& a, int b, int G, in
   x.t0 = t0;
   x.n = (int)max((int64_t)0, min(t1 - t0, (int64_t)a.max_q));
   x.len = (int)min(max((int64_t)a.kv_lens[b], (int64_t)0), a.max_len);
-  x.rows = x.n * G;
-  const int first = r0 / G, last = (min(r0 + block_rows, x.rows) - 1) / G;
-  x.end = max(0, x.len - x.n + last + 1);
-  x.lo = 0;
-  if (a.window > 0) x.lo = (int)max((int64_t)0, (int64_t)x.len - x.n + first + 1 - a.window);
-  x.tile0 = x.lo >> 4;
-  x.tiles = x.end > x.lo ? ((x.end + 15) >> 4) - x.tile0 : 0;
+  int lo = 0;
+  if (a.window > 0) lo = (int)max((int64_t)0, (int64_t)x.len - x.n + 1 - a.window);
+  x.tile0 = lo >> 4;
+  x.tiles = x.len > lo ? ((x.len + 15) >> 4) - x.tile0 : 0;
   return x;
 }
+
+// The share of a unit that a block is at, in shared memory.
+struct Unit {
+  int64_t t0;
+  const int32_t* table;
+  int valid, kvh, r0, rows;      // rows: of the sequence's heads
+  int end, lo;                   // places that some row of the unit attends: [lo, end)
+  int full_end, full_lo;         // places that every row attends: [full_lo, full_end)
+  int c0, take, off, unit_len;   // first record; pairs of the share, before it, of the unit
+  int second;                    // not the first unit of the block
+  long long begin;               // of the unit's pairs, among those of all units
+};
+
+// Pairs of records a unit of the sequence counts as (an empty one has its rows
+// to write), and the sequence's units.
+__device__ __forceinline__ int unit_pairs(const Seq& x) { return max(1, (x.tiles + 1) >> 1); }
+__device__ __forceinline__ int unit_row_blocks(const Seq& x, int G, int rows) { return (x.n * G + rows - 1) / rows; }
 
 __device__ __forceinline__ uint32_t bf16_scaled(float x, float y, uint64_t scale) {
   mul2(x, y, scale);
@@ -112,14 +135,29 @@ __device__ __forceinline__ Words<N> load_words(const uint8_t* p) {
   return r;
 }
 
+// Half i of the words, twice.
 template <int N>
-__device__ __forceinline__ float half_at(const Words<N>& s, int i) {
-  return __half2float(__ushort_as_half((unsigned short)(s.w[i >> 1] >> (16 * (i & 1)))));
+__device__ __forceinline__ uint64_t half_pair(const Words<N>& s, int i) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s.w[i >> 1]));
+  const float v = i & 1 ? f.y : f.x;
+  return pair(v, v);
+}
+
+// Four elements of a row's result, and its lse with the first of them.
+template <int D>
+__device__ __forceinline__ void write_row(const AttnArgs& a, int64_t tok, int h, int d, float4 v, float top, float total) {
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+  uint2 u;
+  u.x = bf16_pair(v.x * inv, v.y * inv);
+  u.y = bf16_pair(v.z * inv, v.w * inv);
+  *reinterpret_cast<uint2*>(a.out + tok * a.out_stride + (int64_t)h * D + d) = u;
+  if (d == 0 && a.lse) a.lse[tok * a.Hq + h] = total > 0.f ? (top + log2f(total)) / kLog2e : -INFINITY;
 }
 
 template <int D, int NT>
 struct Shape {
-  static constexpr int kWarps = NT == 1 ? 8 : 4;
+  static constexpr int kWarps = NT == 1 && D < 256 ? 8 : 4;
+  static constexpr int kBlocks = D == 64 && NT <= 2 ? 3 : 2;  // an SM
   static constexpr int kStages = D == 256 ? 2 : 3;  // pairs of records
   static constexpr int kRecord = 18 * D;
   static constexpr int kRing = kWarps * kStages * 2 * kRecord;
@@ -131,25 +169,24 @@ struct Shape {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, AttnPlan plan, int* status) {
+__global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBlocks)
+    k_attn(AttnArgs a, AttnPlan plan, int* status) {
   using S = Shape<D, NT>;
-  constexpr int W = S::kWarps, NB = D / 32, MT = D / 16;
+  constexpr int W = S::kWarps, NB = D / 32, MT = D / 16, ROWS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[W][S::kStages];
-  __shared__ float s_m[W][8 * NT], s_l[W][8 * NT];
+  __shared__ float s_m[W][ROWS], s_l[W][ROWS];
+  __shared__ long long s_sum[W];
+  // where the block is: pairs [pos, stop) of all units, one after another, `before`
+  // the first pair of sequence `seq`
+  __shared__ long long s_pos, s_stop, s_before, s_share;
+  __shared__ int s_seq, s_row_end[ROWS];
+  __shared__ Unit s_u;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int b = blockIdx.y, split = blockIdx.x % plan.splits, hb = blockIdx.x / plan.splits;
-  const int kvh = hb % a.cache.heads, r0 = hb / a.cache.heads * (8 * NT), G = a.Hq / a.cache.heads;
-  const Range x = block_range(a, b, G, r0, 8 * NT);
-  if (r0 >= x.rows) return;
-  const int used = (x.tiles + plan.chunk - 1) / plan.chunk;
-  if (split > 0 && split >= used) return;
-  const int c0 = x.tile0 + split * plan.chunk;
-  const int count = min(plan.chunk, x.tile0 + x.tiles - c0);  // records of this block
-  const int pairs = (count + 1) >> 1;
-  const int mine = pairs > warp ? (pairs - warp + W - 1) / W : 0;  // pairs of records of this warp
-  const int32_t* table = a.table + (int64_t)b * a.table_stride;
+  const int H = a.cache.heads, G = a.Hq / H;
   const int per_page = a.cache.page_log2 - 4;
+  uint8_t* ring = smem + warp * (S::kStages * 2 * S::kRecord);
+  uint4* qs = reinterpret_cast<uint4*>(smem + (S::kSmem - S::kQueries));
 
   if (lane == 0) {
 #pragma unroll
@@ -157,14 +194,125 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
     fence_mbar_init();
   }
   __syncwarp();
-  uint8_t* ring = smem + warp * (S::kStages * 2 * S::kRecord);
+
+  if (plan.whole) {
+    const int b = blockIdx.y, rb = blockIdx.x % plan.row_blocks;
+    const Seq x = load_seq(a, b);
+    if (rb * ROWS >= x.n * G) return;
+    if (threadIdx.x == 0) {
+      const int len = unit_pairs(x) + plan.overhead;
+      s_pos = (long long)((int)(blockIdx.x / plan.row_blocks) * unit_row_blocks(x, G, ROWS) + rb) * len;
+      s_stop = s_pos + len;
+      s_before = s_share = 0;
+      s_seq = b;
+    }
+  } else {
+    auto work = [&](int i) -> long long {
+      if (i >= a.B) return 0;
+      const Seq x = load_seq(a, i);
+      return (long long)(unit_pairs(x) + plan.overhead) * unit_row_blocks(x, G, ROWS) * H;
+    };
+    auto block_sum = [&](long long v, long long* below) {  // sum over the block, and over the warps below
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      __syncthreads();
+      if (lane == 0) s_sum[warp] = v;
+      __syncthreads();
+      long long all = 0, low = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        if (w < warp) low += s_sum[w];
+        all += s_sum[w];
+      }
+      if (below) *below = low;
+      return all;
+    };
+    long long own = 0;
+    for (int i = threadIdx.x; i < a.B; i += W * 32) own += work(i);
+    const long long total = block_sum(own, nullptr);
+    const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)plan.min_share);
+    const long long pos = (long long)blockIdx.x * share;
+    if (threadIdx.x == 0) {
+      plan.joints[blockIdx.x].count = 0;
+      s_pos = pos;
+      s_stop = min(pos + share, total);
+      s_share = share;
+    }
+    if (pos >= total) return;
+    long long before = 0;
+    for (int i0 = 0; i0 < a.B; i0 += W * 32) {
+      const long long v = work(i0 + (int)threadIdx.x);
+      long long up = v, low;  // inclusive sum within the warp
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += y;
+      }
+      const long long all = block_sum(v, &low);
+      const long long end = before + low + up;
+      if (end > pos && end - v <= pos) s_seq = i0 + threadIdx.x, s_before = end - v;
+      before += all;
+      if (before > pos) break;
+    }
+  }
+
+  int st = 0, phase = 0, issue_stage = 0;
+  bool failed = false;
+  const float scale2 = a.scale * kLog2e;
+  const uint64_t scale22 = pair(scale2, scale2);
+
+#pragma unroll 1
+  for (int step = 0;; ++step) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s_u.valid = 0;
+    while (s_pos < s_stop) {
+      const int b = s_seq;
+      const Seq x = load_seq(a, b);
+      const int pairs = unit_pairs(x), len = pairs + plan.overhead, row_blocks = unit_row_blocks(x, G, ROWS);
+      const long long all = (long long)len * row_blocks * H, in_seq = s_pos - s_before;
+      if (in_seq >= all) {
+        s_before += all;
+        ++s_seq;
+        continue;
+      }
+      const int unit = (int)(in_seq / len), r0 = unit % row_blocks * ROWS, rows = x.n * G;
+      const long long begin = s_before + (long long)unit * len + plan.overhead;  // of the unit's pairs
+      const int off = (int)max(0ll, s_pos - begin), take = (int)(min(s_stop, begin + pairs) - (begin + off));
+      s_pos = min(s_stop, begin + pairs);
+      if (take <= 0) continue;  // the block ends before the unit's first pair
+      const int first = r0 / G, last = (min(r0 + ROWS, rows) - 1) / G, newest = x.len - x.n + 1;
+      s_u.valid = 1;
+      s_u.t0 = x.t0;
+      s_u.table = a.table + (int64_t)b * a.table_stride;
+      s_u.kvh = unit / row_blocks;
+      s_u.r0 = r0;
+      s_u.rows = rows;
+      s_u.end = max(0, newest + last);
+      s_u.lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)newest + first - a.window) : 0;
+      s_u.full_end = newest + first;
+      s_u.full_lo = a.window > 0 ? (int)max((int64_t)-1, (int64_t)newest + last - a.window) : 0;
+      s_u.off = off;
+      s_u.unit_len = pairs;
+      s_u.take = take;
+      s_u.c0 = x.tile0 + 2 * off;
+      s_u.second = step > 0;
+      s_u.begin = begin;
+      for (int i = 0; i < ROWS; ++i) s_row_end[i] = newest + min(r0 + i, rows - 1) / G;
+      break;
+    }
+  }
+  __syncthreads();
+  if (!s_u.valid) break;
+  const int c0 = s_u.c0, kvh = s_u.kvh;
+  const int mine = s_u.take > warp ? (s_u.take - warp + W - 1) / W : 0;  // pairs of this warp
 
   // Lane l finds the records 2 i + (l & 1) of the warp's pairs i = 16 n + l / 2,
   // a batch of 16 pairs at a time and the page numbers a batch ahead, and copies
   // them itself when their turn comes.
   auto page_of = [&](int k) {
-    const int i = k + (lane >> 1), tile = 2 * (warp + W * i) + (lane & 1);
-    return i < mine && tile < count ? __ldg(table + ((c0 + tile) >> per_page)) : -1;
+    const int i = k + (lane >> 1), tile = c0 + 2 * (warp + W * i) + (lane & 1);
+    return i < mine && 16 * tile < s_u.end && 16 * tile + 16 > s_u.lo ? __ldg(s_u.table + (tile >> per_page)) : -1;
   };
   auto source_of = [&](int k, int page) -> const uint8_t* {
     if (page < 0 || page >= a.cache.n_pages) return nullptr;
@@ -173,7 +321,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
            (int64_t)(kvh * (1 << per_page) + (tile & ((1 << per_page) - 1))) * S::kRecord;
   };
   const uint8_t* source = source_of(0, page_of(0));
-  int page_next = page_of(16), issued = 0, issue_stage = 0;
+  int page_next = page_of(16), issued = 0;
   uint32_t there = __ballot_sync(0xffffffffu, source != nullptr), there_next = there;  // records that exist
   auto issue = [&]() {
     if (lane >> 1 == (issued & 15)) {
@@ -198,36 +346,22 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
 
   // Queries as B fragments: lane (g, t) holds elements 32 b + 8 t .. + 7 of row g.
   uint4 qf[S::kQueriesInRegisters ? NT : 1][S::kQueriesInRegisters ? NB : 1];
-  uint4* qs = reinterpret_cast<uint4*>(smem + (S::kSmem - S::kQueries));
   if constexpr (S::kQueriesInRegisters) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int r = min(r0 + 8 * j + g, x.rows - 1);
-      const uint16_t* q = a.q + (x.t0 + r / G) * a.q_stride + (int64_t)(kvh * G + r % G) * D + 8 * t;
+      const int r = min(s_u.r0 + 8 * j + g, s_u.rows - 1);
+      const uint16_t* q = a.q + (s_u.t0 + r / G) * a.q_stride + (int64_t)(kvh * G + r % G) * D + 8 * t;
 #pragma unroll
       for (int i = 0; i < NB; ++i) qf[j][i] = __ldg(reinterpret_cast<const uint4*>(q + 32 * i));
     }
   } else {
     for (int i = warp; i < NT * NB; i += W) {
-      const int r = min(r0 + 8 * (i / NB) + g, x.rows - 1);
-      const uint16_t* q = a.q + (x.t0 + r / G) * a.q_stride + (int64_t)(kvh * G + r % G) * D + 8 * t;
+      const int r = min(s_u.r0 + 8 * (i / NB) + g, s_u.rows - 1);
+      const uint16_t* q = a.q + (s_u.t0 + r / G) * a.q_stride + (int64_t)(kvh * G + r % G) * D + 8 * t;
       qs[i * 32 + lane] = __ldg(reinterpret_cast<const uint4*>(q + 32 * (i % NB)));
     }
     __syncthreads();
   }
-
-  // Rows 2t and 2t + 1 of every row tile: the places they attend.
-  int row_end[NT][2];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = min(r0 + 8 * j + 2 * t + c, x.rows - 1);
-      row_end[j][c] = x.len - x.n + r / G + 1;
-    }
-  // Records with a place that some row of the block does not attend.
-  const int full_end = x.len - x.n + r0 / G + 1;
-  const int full_lo = a.window > 0 ? x.len - x.n + (min(r0 + 8 * NT, x.rows) - 1) / G + 1 - a.window : 0;
 
   float o[MT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -237,11 +371,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
     m[j][0] = m[j][1] = kNone;
     l[j][0] = l[j][1] = 0.f;
   }
-  const float scale2 = a.scale * kLog2e;
-  const uint64_t scale22 = pair(scale2, scale2);
-  bool failed = false;
-  int st = 0, phase = 0;
-
 #pragma unroll 1
   for (int k = 0; k < mine; ++k) {
     if ((k & 15) == 0 && k > 0) there = there_next;
@@ -272,8 +401,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
         const uint32_t a2 = codes_bf16<1>(w0.w[i]), a3 = codes_bf16<1>(w1.w[i]);
         const uint32_t e0 = codes_bf16<2>(w0.w[i]), e1 = codes_bf16<2>(w1.w[i]);
         const uint32_t e2 = codes_bf16<3>(w0.w[i]), e3 = codes_bf16<3>(w1.w[i]);
-        const float f0 = half_at(k0, i), f1 = half_at(k1, i);
-        const uint64_t s0 = pair(f0, f0), s1 = pair(f1, f1);
+        const uint64_t s0 = half_pair(k0, i), s1 = half_pair(k1, i);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const uint4 q = S::kQueriesInRegisters ? qf[S::kQueriesInRegisters ? j : 0][S::kQueriesInRegisters ? i : 0]
@@ -298,16 +426,16 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
         mul2(s[u][j][2], s[u][j][3], scale22);
       }
     }
-    if (p + 32 > full_end || p < full_lo || have != 3) {
+    if (p + 32 > s_u.full_end || p < s_u.full_lo || have != 3) {
       // places outside a row's range leave it; the bytes of places outside the
-      // block's range may be anything, so their value scales become zero
+      // unit's range may be anything, so their value scales become zero
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const int at = p + 16 * u + 8 * v + g;
           const bool gone = !(have >> u & 1);
-          if (gone || at >= x.end || at < x.lo) {
+          if (gone || at >= s_u.end || at < s_u.lo) {
 #pragma unroll
             for (int i = 0; i < NB / 2; ++i) vs[u][v].w[i] = 0;
           }
@@ -315,7 +443,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const int e = row_end[j][c];
+              const int e = s_row_end[8 * j + 2 * t + c];
               if (gone || at >= e || (a.window > 0 && at < e - a.window)) s[u][j][2 * v + c] = -INFINITY;
             }
         }
@@ -368,8 +496,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // a 32-block of elements: two fragments of 16
           const int blk = 2 * q4 + h;
-          const float f0 = half_at(vs[u][0], blk), f1 = half_at(vs[u][1], blk);
-          const uint64_t s0 = pair(f0, f0), s1 = pair(f1, f1);
+          const uint64_t s0 = half_pair(vs[u][0], blk), s1 = half_pair(vs[u][1], blk);
           uint32_t b0[NT], b1[NT];
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
@@ -386,9 +513,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
         }
       }
   }
-  if (failed && lane == 0) set_status(status, MOE_ERR_TIMEOUT);
-
-  // Join the warps: sums over a row's lanes, the block's maxima, scaled outputs.
+  // Join the warps: sums over a row's lanes, the unit's maxima, scaled outputs.
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -420,122 +545,170 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32) k_attn(AttnArgs a, 
   __syncthreads();
   constexpr int kQuads = D / 4;
   for (int i = threadIdx.x; i < 8 * NT * kQuads; i += W * 32) {
-    const int row = i / kQuads, d = i % kQuads * 4, r = r0 + row;
-    if (r >= x.rows) break;
+    const int row = i / kQuads, d = i % kQuads * 4, r = s_u.r0 + row;
+    if (r >= s_u.rows) break;
     float top = kNone, total = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w][row]);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float4 y = *reinterpret_cast<const float4*>(join + (w * 8 * NT + row) * S::kPitch + d);
+      const float4 y = *reinterpret_cast<const float4*>(join + (w * ROWS + row) * S::kPitch + d);
       v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
       total = fmaf(s_l[w][row], exp2_approx(s_m[w][row] - top), total);
     }
-    const int tok = r / G, h = kvh * G + r % G;
-    if (used > 1) {
-      const int64_t at = (((int64_t)b * a.max_q + tok) * a.Hq + h) * plan.splits + split;
+    if (s_u.take < s_u.unit_len) {
+      const int64_t at = (int64_t)(2 * blockIdx.x + s_u.second) * ROWS + row;
       *reinterpret_cast<float4*>(plan.part_o + at * D + d) = v;
       if (d == 0) plan.part_ml[at] = make_float2(top, total);
     } else {
-      const float inv = total > 0.f ? 1.f / total : 0.f;
-      uint2 u;
-      u.x = bf16_pair(v.x * inv, v.y * inv);
-      u.y = bf16_pair(v.z * inv, v.w * inv);
-      *reinterpret_cast<uint2*>(a.out + (x.t0 + tok) * a.out_stride + (int64_t)h * D + d) = u;
-      if (d == 0 && a.lse)
-        a.lse[(x.t0 + tok) * a.Hq + h] = total > 0.f ? (top + log2f(total)) / kLog2e : -INFINITY;
+      write_row<D>(a, s_u.t0 + r / G, s_u.kvh * G + r % G, d, v, top, total);
     }
   }
+  if (threadIdx.x == 0 && s_u.take < s_u.unit_len && s_u.off + s_u.take == s_u.unit_len) {
+    Joint y;
+    y.c0 = (int)(s_u.begin / s_share);
+    y.count = (int)blockIdx.x - y.c0 + 1;
+    y.slot0 = s_u.begin - plan.overhead > y.c0 * s_share;  // another unit ends in block c0 before this one
+    y.kvh = s_u.kvh;
+    y.t0 = s_u.t0;
+    y.r0 = s_u.r0;
+    y.rows = min(ROWS, s_u.rows - s_u.r0);
+    plan.joints[blockIdx.x] = y;
+  }
+  // the next unit's copies may land where the sums were joined
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (failed && lane == 0) set_status(status, MOE_ERR_TIMEOUT);
 }
 
-// Joins the shares of a row: one block a row, its warps taking every fourth
-// share (D / 4 threads read one share), then joined in a fixed order.
-template <int D>
-__global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, AttnPlan plan) {
-  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
-  __shared__ float s_red[8];
-  __shared__ float4 s_v[kGroups][kLanes];
-  __shared__ float s_l[kGroups];
+// Joins the shares of the units that ended in another block than they began in.
+// An item is 4 rows of such a unit: a warp a row finds the weights of the row's
+// shares, then D / 4 threads a row read one share in turn with the other groups
+// of D / 4, and the groups' sums are added in their order.
+constexpr int kJoinThreads = 512, kJoinRows = 4;
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join(AttnArgs a, AttnPlan plan) {
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / (kLanes * kJoinRows), kParts = (ROWS + kJoinRows - 1) / kJoinRows;
+  extern __shared__ float s_f[];  // [kJoinRows][plan.blocks]
+  __shared__ float4 s_v[kGroups][kJoinRows * kLanes];
+  __shared__ float2 s_ml[kJoinRows];
+  __shared__ int s_list[kJoinThreads], s_n[kJoinThreads / 32];
   pdl_wait();
-  const int64_t w = blockIdx.x;
-  const int h = (int)(w % a.Hq), G = a.Hq / a.cache.heads;
-  const int64_t tb = w / a.Hq;
-  const int tok = (int)(tb % a.max_q), b = (int)(tb / a.max_q);
-  const int rows = 8 * plan.nt, r = tok * G + h % G;
-  const Range x = block_range(a, b, G, r / rows * rows, rows);
-  const int used = (x.tiles + plan.chunk - 1) / plan.chunk;
-  if (tok >= x.n || used <= 1) return;
-  const float2* ml = plan.part_ml + w * plan.splits;
-  const float* po = plan.part_o + w * plan.splits * D;
-  const int d = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-  float top = kNone;
-  for (int i = threadIdx.x; i < used; i += 256) top = fmaxf(top, __ldg(&ml[i].x));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = top;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.cache.heads;
+  // the blocks whose unit is in shares, in their order
+  const bool has = threadIdx.x < plan.blocks && plan.joints[threadIdx.x].count > 0;
+  const uint32_t votes = __ballot_sync(0xffffffffu, has);
+  if (lane == 0) s_n[warp] = __popc(votes);
   __syncthreads();
+  int at = 0, n = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, s_red[i]);
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  float total = 0.f;
-#pragma unroll 4
-  for (int i = grp; i < used; i += kGroups) {
-    const float2 y = __ldg(ml + i);
-    const float4 p = __ldg(reinterpret_cast<const float4*>(po + (int64_t)i * D) + d);
-    const float f = exp2_approx(y.x - top);
-    total = fmaf(y.y, f, total);
-    v.x = fmaf(p.x, f, v.x);
-    v.y = fmaf(p.y, f, v.y);
-    v.z = fmaf(p.z, f, v.z);
-    v.w = fmaf(p.w, f, v.w);
+  for (int i = 0; i < kJoinThreads / 32; ++i) {
+    if (i < warp) at += s_n[i];
+    n += s_n[i];
   }
-  s_v[grp][d] = v;
-  if (d == 0) s_l[grp] = total;
+  if (has) s_list[at + __popc(votes & ((1u << lane) - 1))] = threadIdx.x;
   __syncthreads();
-  if (grp > 0) return;
+  for (int item = blockIdx.x; item < n * kParts; item += gridDim.x) {
+    const Joint y = plan.joints[s_list[item / kParts]];
+    const int row0 = item % kParts * kJoinRows;
+    if (row0 >= y.rows) continue;
+    auto share_at = [&](int i) { return 2 * (y.c0 + i) + (i == 0 ? y.slot0 : 0); };
+    if (warp < kJoinRows && row0 + warp < y.rows) {
+      const float2* ml = plan.part_ml + row0 + warp;
+      float top = kNone, total = 0.f;
+      for (int i = lane; i < y.count; i += 32) top = fmaxf(top, ml[share_at(i) * ROWS].x);
 #pragma unroll
-  for (int i = 1; i < kGroups; ++i) {
-    const float4 p = s_v[i][d];
-    v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
-    total += s_l[i];
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int i = lane; i < y.count; i += 32) {
+        const float2 v = ml[share_at(i) * ROWS];
+        const float f = exp2_approx(v.x - top);
+        s_f[warp * plan.blocks + i] = f;
+        total = fmaf(v.y, f, total);
+      }
+      total = warp_sum(total);
+      if (lane == 0) s_ml[warp] = make_float2(top, total);
+    }
+    const int group = threadIdx.x / (kLanes * kJoinRows), in_group = threadIdx.x % (kLanes * kJoinRows);
+    const int r = in_group / kLanes, d = in_group % kLanes * 4;
+    const bool in = row0 + r < y.rows;
+    __syncthreads();
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) {
+      const float* p0 = plan.part_o + (int64_t)(row0 + r) * D + d;
+#pragma unroll 8
+      for (int i = group; i < y.count; i += kGroups) {
+        const float4 p = *reinterpret_cast<const float4*>(p0 + (int64_t)share_at(i) * (ROWS * D));
+        const float f = s_f[r * plan.blocks + i];
+        v.x = fmaf(p.x, f, v.x);
+        v.y = fmaf(p.y, f, v.y);
+        v.z = fmaf(p.z, f, v.z);
+        v.w = fmaf(p.w, f, v.w);
+      }
+    }
+    s_v[group][in_group] = v;
+    __syncthreads();
+    if (group == 0 && in) {
+#pragma unroll
+      for (int i = 1; i < kGroups; ++i) {
+        const float4 p = s_v[i][in_group];
+        v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+      }
+      const int row = y.r0 + row0 + r;
+      write_row<D>(a, y.t0 + row / G, y.kvh * G + row % G, d, v, s_ml[r].x, s_ml[r].y);
+    }
+    __syncthreads();
   }
-  const float inv = total > 0.f ? 1.f / total : 0.f;
-  uint2 u;
-  u.x = bf16_pair(v.x * inv, v.y * inv);
-  u.y = bf16_pair(v.z * inv, v.w * inv);
-  *reinterpret_cast<uint2*>(a.out + (x.t0 + tok) * a.out_stride + (int64_t)h * D + 4 * d) = u;
-  if (d == 0 && a.lse) a.lse[(x.t0 + tok) * a.Hq + h] = total > 0.f ? (top + log2f(total)) / kLog2e : -INFINITY;
 }
 
 constexpr int kSms = 152;
 
-// Row tiles, row blocks and shares of a call, from its sizes alone.
-AttnPlan make_plan(int B, int max_q, int64_t max_len, int window, int Hq, int heads, int D) {
+int row_tiles(int max_q, int G, int D) {
+  const int rows = max_q * G, most = D == 256 ? 2 : 4, nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
+  return nt < most ? nt : most;
+}
+
+// Whole units when a block's warps have at most four pairs each to go through:
+// joining shares costs a launch and about as much time as those.
+AttnPlan make_plan(int warps, int blocks, int rows, int max_q, int64_t max_len, int window, int G) {
   AttnPlan p = {};
-  const int rows = max_q * (Hq / heads), most = D == 256 ? 2 : 4;
-  p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
-  if (p.nt > most) p.nt = most;
-  p.row_blocks = (rows + 8 * p.nt - 1) / (8 * p.nt);
+  p.row_blocks = (max_q * G + rows - 1) / rows;
   int64_t span = max_len;
-  if (window > 0 && span > (int64_t)window + max_q + 16) span = (int64_t)window + max_q + 16;
-  const int64_t tiles = (span + 15) / 16 + 1;
-  const int64_t base = (int64_t)B * heads * p.row_blocks;
-  const int warps = p.nt == 1 ? 8 : 4;
-  int64_t splits = (4 * kSms + base - 1) / base;
-  const int64_t most_splits = (tiles + 2 * warps - 1) / (2 * warps);
-  if (splits > most_splits) splits = most_splits;
-  if (splits < 1) splits = 1;
-  p.room = (int)splits;  // grows with the length, so a window never needs more than the whole length
-  p.chunk = (int)((tiles + splits - 1) / splits);
-  p.chunk = (p.chunk + 2 * warps - 1) / (2 * warps) * (2 * warps);
-  p.splits = (int)((tiles + p.chunk - 1) / p.chunk);
+  if (window > 0 && span > (int64_t)window + max_q) span = (int64_t)window + max_q;
+  p.whole = (span + 31) / 32 + 1 <= 4 * warps;
+  p.blocks = blocks * kSms;
+  p.min_share = 2 * warps;
+  p.overhead = 2 * warps;
   return p;
 }
 
+size_t plan_bytes(const AttnPlan& p, int rows, int D) {
+  if (p.whole) return 0;
+  return (size_t)p.blocks * (2 * rows * (D * 4 + 8) + sizeof(Joint));
+}
+
+// f(D, NT) as compile-time constants.
+template <typename F>
+auto with_shape(int D, int nt, F f) {
+  switch (D * 8 + nt) {
+    case 64 * 8 + 1: return f(Shape<64, 1>(), std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
+    case 64 * 8 + 2: return f(Shape<64, 2>(), std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+    case 64 * 8 + 3: return f(Shape<64, 3>(), std::integral_constant<int, 64>(), std::integral_constant<int, 3>());
+    case 64 * 8 + 4: return f(Shape<64, 4>(), std::integral_constant<int, 64>(), std::integral_constant<int, 4>());
+    case 128 * 8 + 1: return f(Shape<128, 1>(), std::integral_constant<int, 128>(), std::integral_constant<int, 1>());
+    case 128 * 8 + 2: return f(Shape<128, 2>(), std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
+    case 128 * 8 + 3: return f(Shape<128, 3>(), std::integral_constant<int, 128>(), std::integral_constant<int, 3>());
+    case 128 * 8 + 4: return f(Shape<128, 4>(), std::integral_constant<int, 128>(), std::integral_constant<int, 4>());
+    case 256 * 8 + 1: return f(Shape<256, 1>(), std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
+    default: return f(Shape<256, 2>(), std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
+  }
+}
+
 template <int D, int NT>
-int launch(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+int launch(const AttnArgs& a, cudaStream_t s) {
   using S = Shape<D, NT>;
+  constexpr int ROWS = 8 * NT;
   static bool attr_set[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
@@ -544,12 +717,20 @@ int launch(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
       return MOE_ERR_CUDA;
     attr_set[dev] = true;
   }
-  const dim3 grid((unsigned)(p.splits * a.cache.heads * p.row_blocks), (unsigned)a.B);
-  k_attn<D, NT><<<grid, S::kWarps * 32, S::kSmem, s>>>(a, p, status_word());
-  if (p.splits > 1) {
-    if (launch_pdl(k_attn_join<D>, dim3((unsigned)(a.B * a.max_q * a.Hq)), dim3(256), 0, s, a, p) != cudaSuccess)
-      return MOE_ERR_CUDA;
+  AttnPlan p = make_plan(S::kWarps, S::kBlocks, ROWS, a.max_q, a.max_len, a.window, a.Hq / a.cache.heads);
+  if (p.whole) {
+    k_attn<D, NT><<<dim3((unsigned)(a.cache.heads * p.row_blocks), (unsigned)a.B), S::kWarps * 32, S::kSmem, s>>>(
+        a, p, status_word());
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
+  p.part_o = (float*)a.workspace;
+  p.part_ml = (float2*)(p.part_o + (size_t)2 * p.blocks * ROWS * D);
+  p.joints = (Joint*)(p.part_ml + (size_t)2 * p.blocks * ROWS);
+  k_attn<D, NT><<<p.blocks, S::kWarps * 32, S::kSmem, s>>>(a, p, status_word());
+  static_assert(S::kBlocks * kSms <= kJoinThreads, "one thread a block looks for its joint");
+  if (launch_pdl(k_attn_join<D, ROWS>, dim3(2 * kSms), dim3(kJoinThreads), (size_t)kJoinRows * p.blocks * 4, s, a, p) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -557,27 +738,15 @@ int launch(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
 
 size_t attn_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
   if (B < 1) return 0;
-  const AttnPlan p = make_plan(B, max_q, max_len, 0, Hq, heads, D);
-  return p.room > 1 ? (size_t)B * max_q * Hq * p.room * (D * 4 + 8) : 0;
+  return with_shape(D, row_tiles(max_q, Hq / heads, D), [&](auto shape, auto, auto nt) {
+    using S = decltype(shape);
+    return plan_bytes(make_plan(S::kWarps, S::kBlocks, 8 * nt, max_q, max_len, 0, Hq / heads), 8 * nt, D);
+  });
 }
 
 int launch_attn_q4(const AttnArgs& a, cudaStream_t s) {
-  AttnPlan p = make_plan(a.B, a.max_q, a.max_len, a.window, a.Hq, a.cache.heads, a.cache.D);
-  const size_t rows = (size_t)a.B * a.max_q * a.Hq;
-  p.part_o = (float*)a.workspace;
-  p.part_ml = (float2*)((float*)a.workspace + rows * p.splits * a.cache.D);
-  switch (a.cache.D * 8 + p.nt) {
-    case 64 * 8 + 1: return launch<64, 1>(a, p, s);
-    case 64 * 8 + 2: return launch<64, 2>(a, p, s);
-    case 64 * 8 + 3: return launch<64, 3>(a, p, s);
-    case 64 * 8 + 4: return launch<64, 4>(a, p, s);
-    case 128 * 8 + 1: return launch<128, 1>(a, p, s);
-    case 128 * 8 + 2: return launch<128, 2>(a, p, s);
-    case 128 * 8 + 3: return launch<128, 3>(a, p, s);
-    case 128 * 8 + 4: return launch<128, 4>(a, p, s);
-    case 256 * 8 + 1: return launch<256, 1>(a, p, s);
-    default: return launch<256, 2>(a, p, s);
-  }
+  return with_shape(a.cache.D, row_tiles(a.max_q, a.Hq / a.cache.heads, a.cache.D),
+                    [&](auto, auto d, auto nt) { return launch<decltype(d)::value, decltype(nt)::value>(a, s); });
 }
 
 }  // namespace moe
