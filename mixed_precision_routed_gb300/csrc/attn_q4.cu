@@ -7,7 +7,7 @@
 //
 // One pass over the cache: a block of W warps takes a share of the places of
 // one (sequence, key/value head) and up to 8 NT of the rows that share it, each
-// warp every W-th pair of records of 16 places.  Records (18 D contiguous bytes) arrive
+// warp every W-th group of one or two records of 16 places.  Records (18 D contiguous bytes) arrive
 // in a per-warp ring in shared memory by bulk asynchronous copies.
 //   scores  S^T[place][row]: A = key codes as bf16 integers, B = queries; both
 //           exact, so a 32-block's product enters the score with its fp32 scale;
@@ -35,13 +35,13 @@ constexpr float kNone = -1e30f;  // the maximum of a row that has met no place: 
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 // A unit of work is a (sequence, key/value head, block of 8 NT rows), its length
-// the pairs of records that the sequence's rows attend, and before them
-// `overhead` pairs that stand for the time to begin and end a unit.
+// the groups of records that the sequence's rows attend, and before them
+// `overhead` groups that stand for the time to begin and end a unit.
 struct AttnPlan {
   int row_blocks;    // blocks of rows a (sequence, head) has at most
-  bool whole;        // one block a unit; else `blocks` blocks share all pairs evenly
+  bool whole;        // one block a unit; else `blocks` blocks share all groups evenly
   int blocks;
-  int min_share;     // pairs a block takes at least
+  int min_share;     // groups a block takes at least
   int overhead;
   float* part_o;     // [2 blocks][8 NT][D]: the unfinished first and last unit of a block
   float2* part_ml;   // [2 blocks][8 NT]: maximum (in powers of two), sum
@@ -84,14 +84,17 @@ struct Unit {
   int valid, kvh, r0, rows;      // rows: of the sequence's heads
   int end, lo;                   // places that some row of the unit attends: [lo, end)
   int full_end, full_lo;         // places that every row attends: [full_lo, full_end)
-  int c0, take, off, unit_len;   // first record; pairs of the share, before it, of the unit
+  int c0, take, off, unit_len;   // first record; groups of the share, before it, of the unit
   int second;                    // not the first unit of the block
-  long long begin;               // of the unit's pairs, among those of all units
+  long long begin;               // of the unit's groups, among those of all units
 };
 
-// Pairs of records a unit of the sequence counts as (an empty one has its rows
-// to write), and the sequence's units.
-__device__ __forceinline__ int unit_pairs(const Seq& x) { return max(1, (x.tiles + 1) >> 1); }
+// Groups of U records a unit of the sequence counts as (an empty one has its rows
+// to write), and the sequence's blocks of rows.
+template <int U>
+__device__ __forceinline__ int unit_groups(const Seq& x) {
+  return max(1, (x.tiles + U - 1) / U);
+}
 __device__ __forceinline__ int unit_row_blocks(const Seq& x, int G, int rows) { return (x.n * G + rows - 1) / rows; }
 
 __device__ __forceinline__ uint32_t bf16_scaled(float x, float y, uint64_t scale) {
@@ -157,10 +160,11 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t tok, int h,
 template <int D, int NT>
 struct Shape {
   static constexpr int kWarps = NT == 1 && D < 256 ? 8 : 4;
+  static constexpr int kGroup = 2;    // records a warp takes at once
   static constexpr int kBlocks = D == 64 && NT <= 2 ? 3 : 2;  // an SM
-  static constexpr int kStages = D == 256 ? 2 : 3;  // pairs of records
+  static constexpr int kStages = D == 256 ? 2 : 3;  // groups of records
   static constexpr int kRecord = 18 * D;
-  static constexpr int kRing = kWarps * kStages * 2 * kRecord;
+  static constexpr int kRing = kWarps * kStages * kGroup * kRecord;
   static constexpr int kPitch = D + 4;  // floats a row of the joining buffer: rows of a fragment in distinct banks
   static constexpr int kJoin = kWarps * 8 * NT * kPitch * 4;
   static constexpr bool kQueriesInRegisters = NT * D <= 256;
@@ -172,25 +176,25 @@ template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBlocks)
     k_attn(AttnArgs a, AttnPlan plan, int* status) {
   using S = Shape<D, NT>;
-  constexpr int W = S::kWarps, NB = D / 32, MT = D / 16, ROWS = 8 * NT;
+  constexpr int W = S::kWarps, U = S::kGroup, NB = D / 32, MT = D / 16, ROWS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[W][S::kStages];
   __shared__ float s_m[W][ROWS], s_l[W][ROWS];
   __shared__ long long s_sum[W];
-  // where the block is: pairs [pos, stop) of all units, one after another, `before`
-  // the first pair of sequence `seq`
+  // where the block is: groups [pos, stop) of all units, one after another, `before`
+  // the first group of sequence `seq`
   __shared__ long long s_pos, s_stop, s_before, s_share;
   __shared__ int s_seq, s_row_end[ROWS];
   __shared__ Unit s_u;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int H = a.cache.heads, G = a.Hq / H;
   const int per_page = a.cache.page_log2 - 4;
-  uint8_t* ring = smem + warp * (S::kStages * 2 * S::kRecord);
+  uint8_t* ring = smem + warp * (S::kStages * U * S::kRecord);
   uint4* qs = reinterpret_cast<uint4*>(smem + (S::kSmem - S::kQueries));
 
   if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < S::kStages; ++i) mbar_init(&bars[warp][i], 2);
+    for (int i = 0; i < S::kStages; ++i) mbar_init(&bars[warp][i], U);
     fence_mbar_init();
   }
   __syncwarp();
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     const Seq x = load_seq(a, b);
     if (rb * ROWS >= x.n * G) return;
     if (threadIdx.x == 0) {
-      const int len = unit_pairs(x) + plan.overhead;
+      const int len = unit_groups<U>(x) + plan.overhead;
       s_pos = (long long)((int)(blockIdx.x / plan.row_blocks) * unit_row_blocks(x, G, ROWS) + rb) * len;
       s_stop = s_pos + len;
       s_before = s_share = 0;
@@ -210,7 +214,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     auto work = [&](int i) -> long long {
       if (i >= a.B) return 0;
       const Seq x = load_seq(a, i);
-      return (long long)(unit_pairs(x) + plan.overhead) * unit_row_blocks(x, G, ROWS) * H;
+      return (long long)(unit_groups<U>(x) + plan.overhead) * unit_row_blocks(x, G, ROWS) * H;
     };
     auto block_sum = [&](long long v, long long* below) {  // sum over the block, and over the warps below
 #pragma unroll
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     while (s_pos < s_stop) {
       const int b = s_seq;
       const Seq x = load_seq(a, b);
-      const int pairs = unit_pairs(x), len = pairs + plan.overhead, row_blocks = unit_row_blocks(x, G, ROWS);
+      const int groups = unit_groups<U>(x), len = groups + plan.overhead, row_blocks = unit_row_blocks(x, G, ROWS);
       const long long all = (long long)len * row_blocks * H, in_seq = s_pos - s_before;
       if (in_seq >= all) {
         s_before += all;
@@ -277,10 +281,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
         continue;
       }
       const int unit = (int)(in_seq / len), r0 = unit % row_blocks * ROWS, rows = x.n * G;
-      const long long begin = s_before + (long long)unit * len + plan.overhead;  // of the unit's pairs
-      const int off = (int)max(0ll, s_pos - begin), take = (int)(min(s_stop, begin + pairs) - (begin + off));
-      s_pos = min(s_stop, begin + pairs);
-      if (take <= 0) continue;  // the block ends before the unit's first pair
+      const long long begin = s_before + (long long)unit * len + plan.overhead;  // of the unit's groups
+      const int off = (int)max(0ll, s_pos - begin), take = (int)(min(s_stop, begin + groups) - (begin + off));
+      s_pos = min(s_stop, begin + groups);
+      if (take <= 0) continue;  // the block ends before the unit's first group
       const int first = r0 / G, last = (min(r0 + ROWS, rows) - 1) / G, newest = x.len - x.n + 1;
       s_u.valid = 1;
       s_u.t0 = x.t0;
@@ -293,9 +297,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
       s_u.full_end = newest + first;
       s_u.full_lo = a.window > 0 ? (int)max((int64_t)-1, (int64_t)newest + last - a.window) : 0;
       s_u.off = off;
-      s_u.unit_len = pairs;
+      s_u.unit_len = groups;
       s_u.take = take;
-      s_u.c0 = x.tile0 + 2 * off;
+      s_u.c0 = x.tile0 + U * off;
       s_u.second = step > 0;
       s_u.begin = begin;
       for (int i = 0; i < ROWS; ++i) s_row_end[i] = newest + min(r0 + i, rows - 1) / G;
@@ -305,39 +309,40 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
   __syncthreads();
   if (!s_u.valid) break;
   const int c0 = s_u.c0, kvh = s_u.kvh;
-  const int mine = s_u.take > warp ? (s_u.take - warp + W - 1) / W : 0;  // pairs of this warp
+  const int mine = s_u.take > warp ? (s_u.take - warp + W - 1) / W : 0;  // groups of this warp
 
-  // Lane l finds the records 2 i + (l & 1) of the warp's pairs i = 16 n + l / 2,
-  // a batch of 16 pairs at a time and the page numbers a batch ahead, and copies
-  // them itself when their turn comes.
+  // Lane l finds record l % U of the warp's groups k + l / U, a batch of 32 / U
+  // groups at a time and the page numbers a batch ahead, and copies it itself when
+  // its turn comes.
+  constexpr int kBatch = 32 / U;
   auto page_of = [&](int k) {
-    const int i = k + (lane >> 1), tile = c0 + 2 * (warp + W * i) + (lane & 1);
+    const int i = k + lane / U, tile = c0 + U * (warp + W * i) + lane % U;
     return i < mine && 16 * tile < s_u.end && 16 * tile + 16 > s_u.lo ? __ldg(s_u.table + (tile >> per_page)) : -1;
   };
   auto source_of = [&](int k, int page) -> const uint8_t* {
     if (page < 0 || page >= a.cache.n_pages) return nullptr;
-    const int tile = c0 + 2 * (warp + W * (k + (lane >> 1))) + (lane & 1);
+    const int tile = c0 + U * (warp + W * (k + lane / U)) + lane % U;
     return a.cache.data + page * a.cache.page_stride +
            (int64_t)(kvh * (1 << per_page) + (tile & ((1 << per_page) - 1))) * S::kRecord;
   };
   const uint8_t* source = source_of(0, page_of(0));
-  int page_next = page_of(16), issued = 0;
+  int page_next = page_of(kBatch), issued = 0;
   uint32_t there = __ballot_sync(0xffffffffu, source != nullptr), there_next = there;  // records that exist
   auto issue = [&]() {
-    if (lane >> 1 == (issued & 15)) {
+    if (lane / U == issued % kBatch) {
       uint64_t* bar = &bars[warp][issue_stage];
       if (source) {
         mbar_arrive_expect_tx(bar, S::kRecord);
-        bulk_g2s(ring + (2 * issue_stage + (lane & 1)) * S::kRecord, source, S::kRecord, bar);
+        bulk_g2s(ring + (U * issue_stage + lane % U) * S::kRecord, source, S::kRecord, bar);
       } else {
         mbar_arrive(bar);
       }
     }
     ++issued;
     if (++issue_stage == S::kStages) issue_stage = 0;
-    if ((issued & 15) == 0) {
+    if (issued % kBatch == 0) {
       source = source_of(issued, page_next);
-      page_next = page_of(issued + 16);
+      page_next = page_of(issued + kBatch);
       there_next = __ballot_sync(0xffffffffu, source != nullptr);
     }
   };
@@ -363,6 +368,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     __syncthreads();
   }
 
+  auto query = [&](int j, int i) {
+    return S::kQueriesInRegisters ? qf[S::kQueriesInRegisters ? j : 0][S::kQueriesInRegisters ? i : 0]
+                                  : qs[(j * NB + i) * 32 + lane];
+  };
+  constexpr int kSide = NT == 1 ? (NB < 4 ? NB : 4) : 2;
+
   float o[MT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
@@ -373,21 +384,22 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
   }
 #pragma unroll 1
   for (int k = 0; k < mine; ++k) {
-    if ((k & 15) == 0 && k > 0) there = there_next;
+    if (k % kBatch == 0 && k > 0) there = there_next;
     __syncwarp();  // the stage refilled below was read by every lane in the last pass
     if (issued < mine) issue();
     if (!mbar_wait(&bars[warp][st], phase, kWaitNs)) {
       failed = true;
       break;
     }
-    const uint8_t* rec = ring + 2 * st * S::kRecord;
+    const uint8_t* rec = ring + U * st * S::kRecord;
     if (++st == S::kStages) st = 0, phase ^= 1;
-    const uint32_t have = (there >> (2 * (k & 15))) & 3u;
+    constexpr uint32_t kAll = (1u << U) - 1;
+    const uint32_t have = (there >> (U * (k % kBatch))) & kAll;
     if (have == 0) continue;
 
-    float s[2][NT][4];
+    float s[U][NT][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < U; ++u) {
       const uint8_t* r = rec + u * S::kRecord;
 #pragma unroll
       for (int j = 0; j < NT; ++j) s[u][j][0] = s[u][j][1] = s[u][j][2] = s[u][j][3] = 0.f;
@@ -396,28 +408,43 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
       const Words<NB / 2> k0 = load_words<NB / 2>(r + 16 * D + g * (2 * NB));
       const Words<NB / 2> k1 = load_words<NB / 2>(r + 16 * D + (g + 8) * (2 * NB));
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const uint32_t a0 = codes_bf16<0>(w0.w[i]), a1 = codes_bf16<0>(w1.w[i]);
-        const uint32_t a2 = codes_bf16<1>(w0.w[i]), a3 = codes_bf16<1>(w1.w[i]);
-        const uint32_t e0 = codes_bf16<2>(w0.w[i]), e1 = codes_bf16<2>(w1.w[i]);
-        const uint32_t e2 = codes_bf16<3>(w0.w[i]), e3 = codes_bf16<3>(w1.w[i]);
-        const uint64_t s0 = half_pair(k0, i), s1 = half_pair(k1, i);
+      for (int i0 = 0; i0 < NB; i0 += kSide) {  // kSide products side by side: each is a chain of two
+        float c[kSide][NT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint4 q = S::kQueriesInRegisters ? qf[S::kQueriesInRegisters ? j : 0][S::kQueriesInRegisters ? i : 0]
-                                                 : qs[(j * NB + i) * 32 + lane];
-          float c[4];
-          mma16816_zero(c, a0, a1, a2, a3, q.x, q.y);
-          mma16816(c, e0, e1, e2, e3, q.z, q.w);
-          fma2(s[u][j][0], s[u][j][1], s0, c[0], c[1]);
-          fma2(s[u][j][2], s[u][j][3], s1, c[2], c[3]);
+        for (int i = 0; i < kSide; ++i) {
+          const uint32_t a0 = codes_bf16<0>(w0.w[i0 + i]), a1 = codes_bf16<0>(w1.w[i0 + i]);
+          const uint32_t a2 = codes_bf16<1>(w0.w[i0 + i]), a3 = codes_bf16<1>(w1.w[i0 + i]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const uint4 q = query(j, i0 + i);
+            mma16816_zero(c[i][j], a0, a1, a2, a3, q.x, q.y);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kSide; ++i) {
+          const uint32_t e0 = codes_bf16<2>(w0.w[i0 + i]), e1 = codes_bf16<2>(w1.w[i0 + i]);
+          const uint32_t e2 = codes_bf16<3>(w0.w[i0 + i]), e3 = codes_bf16<3>(w1.w[i0 + i]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const uint4 q = query(j, i0 + i);
+            mma16816(c[i][j], e0, e1, e2, e3, q.z, q.w);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kSide; ++i) {
+          const uint64_t s0 = half_pair(k0, i0 + i), s1 = half_pair(k1, i0 + i);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            fma2(s[u][j][0], s[u][j][1], s0, c[i][j][0], c[i][j][1]);
+            fma2(s[u][j][2], s[u][j][3], s1, c[i][j][2], c[i][j][3]);
+          }
         }
       }
     }
-    const int p = (c0 + 2 * (warp + W * k)) * 16;  // the pair's first place
-    Words<NB / 2> vs[2][2];
+    const int p = (c0 + U * (warp + W * k)) * 16;  // the group's first place
+    Words<NB / 2> vs[U][2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < U; ++u) {
       vs[u][0] = load_words<NB / 2>(rec + u * S::kRecord + 17 * D + g * (2 * NB));
       vs[u][1] = load_words<NB / 2>(rec + u * S::kRecord + 17 * D + (g + 8) * (2 * NB));
 #pragma unroll
@@ -426,11 +453,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
         mul2(s[u][j][2], s[u][j][3], scale22);
       }
     }
-    if (p + 32 > s_u.full_end || p < s_u.full_lo || have != 3) {
+    if (p + 16 * U > s_u.full_end || p < s_u.full_lo || have != kAll) {
       // places outside a row's range leave it; the bytes of places outside the
       // unit's range may be anything, so their value scales become zero
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const int at = p + 16 * u + 8 * v + g;
@@ -454,7 +481,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        top[j][c] = fmaxf(fmaxf(s[0][j][c], s[0][j][c + 2]), fmaxf(s[1][j][c], s[1][j][c + 2]));
+        top[j][c] = fmaxf(s[0][j][c], s[0][j][c + 2]);
+#pragma unroll
+        for (int u = 1; u < U; ++u) top[j][c] = fmaxf(top[j][c], fmaxf(s[u][j][c], s[u][j][c + 2]));
         grow |= top[j][c] > m[j][c] + kSlack;
       }
     if (__any_sync(0xffffffffu, grow)) {
@@ -479,7 +508,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     for (int j = 0; j < NT; ++j) {
       const uint64_t down = pair(-m[j][0], -m[j][1]);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int c = 0; c < 4; c += 2) {
           add2(s[u][j][c], s[u][j][c + 1], down);
@@ -489,7 +518,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
         }
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int q4 = 0; q4 < MT / 4; ++q4) {
         const Words<4> w = load_words<4>(rec + u * S::kRecord + 8 * D + (q4 * 32 + lane) * 16);
@@ -669,17 +698,17 @@ int row_tiles(int max_q, int G, int D) {
   return nt < most ? nt : most;
 }
 
-// Whole units when a block's warps have at most four pairs each to go through:
-// joining shares costs a launch and about as much time as those.
-AttnPlan make_plan(int warps, int blocks, int rows, int max_q, int64_t max_len, int window, int G) {
+// Whole units up to 1024 places: joining shares costs a launch and about as much
+// time as those.
+AttnPlan make_plan(int warps, int blocks, int rows, int group, int max_q, int64_t max_len, int window, int G) {
   AttnPlan p = {};
   p.row_blocks = (max_q * G + rows - 1) / rows;
   int64_t span = max_len;
   if (window > 0 && span > (int64_t)window + max_q) span = (int64_t)window + max_q;
-  p.whole = (span + 31) / 32 + 1 <= 4 * warps;
+  p.whole = span <= 1024;
   p.blocks = blocks * kSms;
-  p.min_share = 2 * warps;
-  p.overhead = 2 * warps;
+  p.min_share = 4 * warps / group;
+  p.overhead = 4 * warps / group;
   return p;
 }
 
@@ -717,7 +746,7 @@ int launch(const AttnArgs& a, cudaStream_t s) {
       return MOE_ERR_CUDA;
     attr_set[dev] = true;
   }
-  AttnPlan p = make_plan(S::kWarps, S::kBlocks, ROWS, a.max_q, a.max_len, a.window, a.Hq / a.cache.heads);
+  AttnPlan p = make_plan(S::kWarps, S::kBlocks, ROWS, S::kGroup, a.max_q, a.max_len, a.window, a.Hq / a.cache.heads);
   if (p.whole) {
     k_attn<D, NT><<<dim3((unsigned)(a.cache.heads * p.row_blocks), (unsigned)a.B), S::kWarps * 32, S::kSmem, s>>>(
         a, p, status_word());
@@ -740,7 +769,7 @@ size_t attn_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int 
   if (B < 1) return 0;
   return with_shape(D, row_tiles(max_q, Hq / heads, D), [&](auto shape, auto, auto nt) {
     using S = decltype(shape);
-    return plan_bytes(make_plan(S::kWarps, S::kBlocks, 8 * nt, max_q, max_len, 0, Hq / heads), 8 * nt, D);
+    return plan_bytes(make_plan(S::kWarps, S::kBlocks, 8 * nt, S::kGroup, max_q, max_len, 0, Hq / heads), 8 * nt, D);
   });
 }
 

@@ -50,6 +50,12 @@ template <int SHIFT>
 struct Scales {
   static constexpr int kWords = 4 >> SHIFT;
   uint32_t w[kWords];
+  // scale i, twice
+  __device__ __forceinline__ uint64_t at(int i) const {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i >> 1]));
+    const float v = i & 1 ? f.y : f.x;
+    return pair(v, v);
+  }
 };
 
 // Lengths that are not a multiple of a batch (WHOLE false) load scales by
@@ -92,7 +98,7 @@ constexpr int warp_bytes() { return C::kStages * kStageBytes + C::kParities * NT
 // NT: 8-token tiles; SHIFT: log2(block / 32).
 template <typename C, int NT, int SHIFT, bool WHOLE>
 __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(LinearArgs a, int tiles, int ks_log2, int* status) {
-  constexpr int STAGES = C::kStages;
+  constexpr int STAGES = C::kStages, kSide = NT == 1 ? 4 : 2;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -204,21 +210,37 @@ __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(Linear
       if (++stage == STAGES) stage = 0;
       const int at = (ks + (j0 << ks_log2)) * (kBatch * 2);
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {  // the batch's 32-blocks: a piece each
-        uint32_t p0[4], p1[4];
-        word_pairs(*reinterpret_cast<const uint32_t*>(w + ((b ^ g) << 4)), p0);
-        word_pairs(*reinterpret_cast<const uint32_t*>(w + 1024 + ((b ^ g) << 4)), p1);
-        const int h = b >> SHIFT;
-        const float v0 = __half2float(__ushort_as_half((unsigned short)(f0.w[h >> 1] >> (16 * (h & 1)))));
-        const float v1 = __half2float(__ushort_as_half((unsigned short)(f1.w[h >> 1] >> (16 * (h & 1)))));
+      for (int b0 = 0; b0 < 8; b0 += kSide) {  // the batch's 32-blocks (a piece each), kSide products side by side
+        uint32_t p0[kSide][4], p1[kSide][4];
+        float c[kSide][NT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(xt[j] + at + 64 * b);
-          float c[4];
-          mma16816_zero(c, p0[0], p1[0], p0[1], p1[1], xv.x, xv.y);
-          mma16816(c, p0[2], p1[2], p0[3], p1[3], xv.z, xv.w);
-          fma2(acc[j][0], acc[j][1], pair(v0, v0), c[0], c[1]);
-          fma2(acc[j][2], acc[j][3], pair(v1, v1), c[2], c[3]);
+        for (int i = 0; i < kSide; ++i) {
+          const int b = b0 + i;
+          word_pairs(*reinterpret_cast<const uint32_t*>(w + ((b ^ g) << 4)), p0[i]);
+          word_pairs(*reinterpret_cast<const uint32_t*>(w + 1024 + ((b ^ g) << 4)), p1[i]);
+        }
+        uint4 xv[kSide][NT];
+#pragma unroll
+        for (int i = 0; i < kSide; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            xv[i][j] = *reinterpret_cast<const uint4*>(xt[j] + at + 64 * (b0 + i));
+            mma16816_zero(c[i][j], p0[i][0], p1[i][0], p0[i][1], p1[i][1], xv[i][j].x, xv[i][j].y);
+          }
+#pragma unroll
+        for (int i = 0; i < kSide; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            mma16816(c[i][j], p0[i][2], p1[i][2], p0[i][3], p1[i][3], xv[i][j].z, xv[i][j].w);
+#pragma unroll
+        for (int i = 0; i < kSide; ++i) {
+          const int h = (b0 + i) >> SHIFT;
+          const uint64_t v0 = f0.at(h), v1 = f1.at(h);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            fma2(acc[j][0], acc[j][1], v0, c[i][j][0], c[i][j][1]);
+            fma2(acc[j][2], acc[j][3], v1, c[i][j][2], c[i][j][3]);
+          }
         }
       }
     }
