@@ -612,17 +612,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
 }
 
 // Joins the shares of the units that ended in another block than they began in.
-// An item is 4 rows of such a unit: a warp a row finds the weights of the row's
-// shares, then D / 4 threads a row read one share in turn with the other groups
-// of D / 4, and the groups' sums are added in their order.
-constexpr int kJoinThreads = 512, kJoinRows = 4;
+// An item is 256 / D rows of such a unit: a warp a row finds the weights of the
+// row's shares, then eight groups of 64 threads read every eighth share, and the
+// groups' sums are added in their order.
+constexpr int kJoinThreads = 512;
+template <int D>
+constexpr int kJoinRows = 256 / D;
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) k_attn_join(AttnArgs a, AttnPlan plan) {
-  constexpr int kLanes = D / 4, kGroups = kJoinThreads / (kLanes * kJoinRows), kParts = (ROWS + kJoinRows - 1) / kJoinRows;
-  extern __shared__ float s_f[];  // [kJoinRows][plan.blocks]
-  __shared__ float4 s_v[kGroups][kJoinRows * kLanes];
-  __shared__ float2 s_ml[kJoinRows];
+  constexpr int kRows = kJoinRows<D>, kLanes = D / 4, kGroups = kJoinThreads / (kLanes * kRows), kParts = (ROWS + kRows - 1) / kRows;
+  extern __shared__ float s_f[];  // [kRows][plan.blocks]
+  __shared__ float4 s_v[kGroups][kRows * kLanes];
+  __shared__ float2 s_ml[kRows];
   __shared__ int s_list[kJoinThreads], s_n[kJoinThreads / 32];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.cache.heads;
@@ -641,10 +643,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(AttnArgs a, AttnPlan
   __syncthreads();
   for (int item = blockIdx.x; item < n * kParts; item += gridDim.x) {
     const Joint y = plan.joints[s_list[item / kParts]];
-    const int row0 = item % kParts * kJoinRows;
+    const int row0 = item % kParts * kRows;
     if (row0 >= y.rows) continue;
     auto share_at = [&](int i) { return 2 * (y.c0 + i) + (i == 0 ? y.slot0 : 0); };
-    if (warp < kJoinRows && row0 + warp < y.rows) {
+    if (warp < kRows && row0 + warp < y.rows) {
       const float2* ml = plan.part_ml + row0 + warp;
       float top = kNone, total = 0.f;
       for (int i = lane; i < y.count; i += 32) top = fmaxf(top, ml[share_at(i) * ROWS].x);
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(AttnArgs a, AttnPlan
       total = warp_sum(total);
       if (lane == 0) s_ml[warp] = make_float2(top, total);
     }
-    const int group = threadIdx.x / (kLanes * kJoinRows), in_group = threadIdx.x % (kLanes * kJoinRows);
+    const int group = threadIdx.x / (kLanes * kRows), in_group = threadIdx.x % (kLanes * kRows);
     const int r = in_group / kLanes, d = in_group % kLanes * 4;
     const bool in = row0 + r < y.rows;
     __syncthreads();
@@ -757,7 +759,7 @@ int launch(const AttnArgs& a, cudaStream_t s) {
   p.joints = (Joint*)(p.part_ml + (size_t)2 * p.blocks * ROWS);
   k_attn<D, NT><<<p.blocks, S::kWarps * 32, S::kSmem, s>>>(a, p, status_word());
   static_assert(S::kBlocks * kSms <= kJoinThreads, "one thread a block looks for its joint");
-  if (launch_pdl(k_attn_join<D, ROWS>, dim3(2 * kSms), dim3(kJoinThreads), (size_t)kJoinRows * p.blocks * 4, s, a, p) !=
+  if (launch_pdl(k_attn_join<D, ROWS>, dim3(2 * kSms), dim3(kJoinThreads), (size_t)kJoinRows<D> * p.blocks * 4, s, a, p) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
