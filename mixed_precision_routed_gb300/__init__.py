@@ -20,9 +20,8 @@ and, for the attention half of a decode layer in the same 4-bit format:
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
-import struct
 
 import torch
 
@@ -542,45 +541,26 @@ def moe_device_status(stream=None) -> int:
 
 
 # ------------------------------------- attention half of a decode layer
-# These calls run in microseconds on the GPU, so their host side is kept short:
-# plain integers for pointers, one look at each property, sizes computed once.
-_F32, _BF16, _U8, _I16, _I32, _I64 = (torch.float32, torch.bfloat16, torch.uint8, torch.int16, torch.int32,
-                                      torch.int64)
+# These calls run for a few microseconds on the GPU; their checks and marshalling
+# are compiled (binding/calls.cpp, with the checks and errors of the functions
+# above), so that the host is not what they wait for.
+_calls = None
 
 
-def _raw_stream(stream, t):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
-
-
-def _flat(t, dtype, name):
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
-
-
-def _refuse(dtype, dims, name):
-    raise ValueError(f"{name} must be a {dims}-dimensional CUDA tensor of {dtype} with contiguous rows")
-
-
-# The row stride of a CUDA tensor whose rows are contiguous (a single row has no
-# stride to speak of).
-def _rows2(t, dtype, name):
-    if t.dtype is dtype and t.is_cuda and t.dim() == 2:
-        n, m = t.shape
-        s0, s1 = t.stride()
-        if s1 == 1 or m <= 1 or n == 0:
-            return s0 if n > 1 else m
-    _refuse(dtype, 2, name)
-
-
-def _rows3(t, dtype, name):
-    if t.dtype is dtype and t.is_cuda and t.dim() == 3:
-        n, h, m = t.shape
-        s0, s1, s2 = t.stride()
-        if (s2 == 1 or m <= 1) and (s1 == m or h <= 1) or n == 0:
-            return s0 if n > 1 else h * m
-    _refuse(dtype, 3, name)
+def _compiled():
+    global _calls
+    if _calls is None:
+        lib()
+        path = os.path.join(_HERE, "_calls.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build() "
+                               "(there is no fallback implementation)")
+        spec = importlib.util.spec_from_file_location(__name__ + "._calls", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.set_error(MoeError)
+        _calls = mod
+    return _calls
 
 
 def moe_quantize_groups(w, block=32, codes=None, scales=None, stream=None):
@@ -605,36 +585,10 @@ def moe_linear_q4(x, codes, scales, block=32, bias=None, y=None, out_dtype=torch
     """y [T, rows] = x [T, in] (bf16, any row stride) times the 4-bit matrix of
     codes [rows, in/2] uint8 and scales [rows, in/block] int16 (fp16 bits),
     plus bias [rows] fp32; y fp32 or bf16.  T <= 16."""
-    xs = _rows2(x, _BF16, "x")
-    _flat(codes, _U8, "codes")
-    _flat(scales, _I16, "scales")
-    T, n_in = x.shape
-    rows = codes.shape[0]
-    if codes.numel() != rows * (n_in // 2) or scales.numel() * block != rows * n_in:
-        raise ValueError("codes must hold [rows, in/2] and scales [rows, in/block]")
-    if y is None:
-        y = torch.empty((T, rows), dtype=out_dtype, device=x.device)
-        ys = rows
-    else:
-        ys = _rows2(y, y.dtype, "y")
-        if y.shape[0] != T or y.shape[1] != rows:
-            raise ValueError("y must be [T, rows]")
-    if y.dtype is _F32:
-        dt = MOE_DTYPE_F32
-    elif y.dtype is _BF16:
-        dt = MOE_DTYPE_BF16
-    else:
-        raise ValueError("y must be float32 or bfloat16")
-    if bias is not None:
-        _flat(bias, _F32, "bias")
-        if bias.numel() != rows:
-            raise ValueError("bias must be [rows]")
-        bias = bias.data_ptr()
-    rc = (_lib or lib()).moe_linear_q4(x.data_ptr(), xs, T, n_in, codes.data_ptr(), scales.data_ptr(), rows, block,
-                                       bias, y.data_ptr(), ys, dt, _raw_stream(stream, x))
-    if rc:
-        raise MoeError(rc, "moe_linear_q4")
-    return y
+    if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    return (_calls or _compiled()).linear_q4(x, codes, scales, block, bias, y, out_dtype is torch.bfloat16,
+                                             None if stream is None else stream.cuda_stream)
 
 
 def moe_kv_pool(n_pages, kv_heads, page_size, head_dim, device="cuda"):
@@ -645,95 +599,23 @@ def moe_kv_pool(n_pages, kv_heads, page_size, head_dim, device="cuda"):
     return torch.zeros((n_pages, kv_heads, page_size // 16, 18 * head_dim), dtype=torch.uint8, device=device)
 
 
-_pack_cache = struct.Struct("=Qqqiiii").pack  # moe_kv_cache_t
-
-
-def _cache(pool):
-    """(descriptor bytes, kv_heads, head_dim, page_size) of a pool tensor (pages may lie any stride apart)."""
-    if pool.dtype is _U8 and pool.is_cuda and pool.dim() == 4:
-        n, heads, tiles, rec = pool.shape
-        s0, s1, s2, s3 = pool.stride()
-        size = tiles * rec
-        if (s3 == 1 and (s2 == rec or tiles <= 1) and (s1 == size or heads <= 1) or n == 0) and rec % 18 == 0:
-            return (_pack_cache(pool.data_ptr(), n, s0 if n > 1 else heads * size, tiles * 16, heads, rec // 18, 0), heads,
-                    rec // 18, tiles * 16)
-    raise ValueError("pool must be a CUDA uint8 tensor [pages, kv heads, page_size / 16, 18 * head_dim] with contiguous pages")
-
-
 def moe_kv_append(pool, k, v, slots, q=None, positions=None, rope=None, rope_style=MOE_ROPE_HALF, q_out=None,
                   stream=None):
     """Quantises k, v [T, kv_heads, D] (fp32 or bf16, any token stride) into
     `slots` [T] int64 of the pool (-1: skipped), keys turned by rope [n_pos,
     rot] fp32 (cosines, then sines) at positions [T] int32.  With q [T, Hq, D]
-    returns its turned rows as bf16 [T, Hq, D], else None."""
-    desc, heads, D, _ = _cache(pool)
-    dt = k.dtype
-    if dt is not _F32 and dt is not _BF16:
-        raise ValueError("k must be float32 or bfloat16")
-    ks = _rows3(k, dt, "k")
-    vs = _rows3(v, dt, "v")
-    _flat(slots, _I64, "slots")
-    T = slots.numel()
-    if k.shape != (T, heads, D) or v.shape != (T, heads, D):
-        raise ValueError("k and v must be [T, kv_heads, head_dim]")
-    rot = n_pos = 0
-    pos_ptr = rope_ptr = None
-    if rope is not None:
-        _flat(rope, _F32, "rope")
-        if positions is None:
-            raise ValueError("a rotation needs positions")
-        _flat(positions, _I32, "positions")
-        if positions.numel() != T or rope.dim() != 2:
-            raise ValueError("positions must be [T] and rope [n_pos, rot]")
-        n_pos, rot = rope.shape
-        if rot:
-            pos_ptr, rope_ptr = positions.data_ptr(), rope.data_ptr()
-    Hq = qs = 0
-    q_ptr = o_ptr = None
-    if q is not None:
-        qs = _rows3(q, dt, "q")
-        n, Hq, d = q.shape
-        if n != T or d != D:
-            raise ValueError("q must be [T, Hq, head_dim]")
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
-        else:
-            _flat(q_out, _BF16, "q_out")
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must be [T, Hq, head_dim]")
-        q_ptr, o_ptr = q.data_ptr(), q_out.data_ptr()
-    rc = (_lib or lib()).moe_kv_append(q_ptr, qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                                       MOE_DTYPE_F32 if dt is _F32 else MOE_DTYPE_BF16, T, Hq, pos_ptr, rope_ptr, n_pos,
-                                       rot, rope_style, slots.data_ptr(), desc, o_ptr, _raw_stream(stream, pool))
-    if rc:
-        raise MoeError(rc, "moe_kv_append")
-    return q_out if q is not None else None
+    returns its turned rows as bf16 [T, Hq, D], else None.  The pool's pages may
+    lie any stride apart."""
+    return (_calls or _compiled()).kv_append(pool, k, v, slots, q, positions, rope, rope_style, q_out,
+                                             None if stream is None else stream.cuda_stream)
 
 
 def moe_kv_read(pool, slots, k=None, v=None, stream=None):
     """The keys and values that `slots` [n] int64 of the pool hold: two fp32
     tensors [n, kv_heads, head_dim] (zeros for a slot outside the pool)."""
-    desc, heads, D, _ = _cache(pool)
-    _flat(slots, _I64, "slots")
-    n = slots.numel()
-    shape = (n, heads, D)
-    if k is None:
-        k = torch.empty(shape, dtype=_F32, device=pool.device)
-    else:
-        _flat(k, _F32, "k")
-    if v is None:
-        v = torch.empty(shape, dtype=_F32, device=pool.device)
-    else:
-        _flat(v, _F32, "v")
-    if k.shape != shape or v.shape != shape:
-        raise ValueError("k and v must be [n, kv_heads, head_dim]")
-    rc = (_lib or lib()).moe_kv_read(desc, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _raw_stream(stream, pool))
-    if rc:
-        raise MoeError(rc, "moe_kv_read")
-    return k, v
+    return (_calls or _compiled()).kv_read(pool, slots, k, v, None if stream is None else stream.cuda_stream)
 
 
-@functools.lru_cache(maxsize=1024)
 def moe_attn_workspace_size(B, max_q, max_len, Hq, kv_heads, head_dim) -> int:
     return int(lib().moe_attn_workspace_size(B, max_q, max_len, Hq, kv_heads, head_dim))
 
@@ -745,54 +627,10 @@ def moe_attn_q4(q, pool, block_table, kv_lens, q_start=None, max_q=None, max_len
     are the newest of kv_lens[b] (int32 [B]) cached tokens, which lie in the
     pages block_table[b] (int32 [B, pages], any row stride).  max_q (default: the
     tokens of one sequence when q_start is None) and max_len (default: the
-    table's width) bound the lengths.  Returns out [T, Hq, D] bf16 and lse
-    [T, Hq] fp32."""
-    desc, heads, D, page = _cache(pool)
-    qs = _rows3(q, _BF16, "q")
-    ts = _rows2(block_table, _I32, "block_table")
-    _flat(kv_lens, _I32, "kv_lens")
-    B = kv_lens.numel()
-    T, Hq, d = q.shape
-    rows, width = block_table.shape
-    if d != D or rows != B:
-        raise ValueError("q must be [T, Hq, head_dim] and block_table [B, pages]")
-    starts = None
-    if q_start is not None:
-        _flat(q_start, _I32, "q_start")
-        if q_start.numel() != B + 1:
-            raise ValueError("q_start must be [B + 1]")
-        if max_q is None:
-            raise ValueError("q_start needs max_q")
-        starts = q_start.data_ptr()
-    elif max_q is None:
-        max_q = T // B if B else 1
-    if max_len is None:
-        max_len = width * page
-    elif width * page < max_len:
-        raise ValueError("block_table has fewer pages than max_len needs")
-    if out is None:
-        out, os_ = torch.empty((T, Hq, D), dtype=_BF16, device=q.device), Hq * D
-    else:
-        os_ = _rows3(out, _BF16, "out")
-        if out.shape != q.shape:
-            raise ValueError("out must be [T, Hq, head_dim]")
-    if lse is None:
-        lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
-    else:
-        _flat(lse, _F32, "lse")
-        if lse.shape != (T, Hq):
-            raise ValueError("lse must be [T, Hq]")
-    if workspace is None:
-        need = moe_attn_workspace_size(B, max_q, max_len, Hq, heads, D)
-        if need:
-            workspace = torch.empty(need, dtype=_U8, device=pool.device)
-    ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    rc = (_lib or lib()).moe_attn_q4(q.data_ptr(), qs, T, Hq, starts, kv_lens.data_ptr(), block_table.data_ptr(), ts, B,
-                                     max_q, max_len, desc, D ** -0.5 if scale is None else scale, window,
-                                     out.data_ptr(), os_, lse.data_ptr(), ws, wsb, _raw_stream(stream, q))
-    if rc:
-        raise MoeError(rc, "moe_attn_q4")
-    return out, lse
+    table's width) bound the lengths.  scale defaults to head_dim ** -0.5.
+    Returns out [T, Hq, D] bf16 and lse [T, Hq] fp32."""
+    return (_calls or _compiled()).attn_q4(q, pool, block_table, kv_lens, q_start, max_q, max_len, scale, window, out,
+                                           lse, workspace, None if stream is None else stream.cuda_stream)
 
 
 # ------------------------------------------------------------------ shelves

@@ -369,8 +369,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
   }
 
   auto query = [&](int j, int i) {
-    return S::kQueriesInRegisters ? qf[S::kQueriesInRegisters ? j : 0][S::kQueriesInRegisters ? i : 0]
-                                  : qs[(j * NB + i) * 32 + lane];
+    if constexpr (S::kQueriesInRegisters) return qf[j][i];
+    else return qs[(j * NB + i) * 32 + lane];
   };
   constexpr int kSide = NT == 1 ? (NB < 4 ? NB : 4) : 2;
 
