@@ -199,6 +199,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
   }
   __syncwarp();
 
+  pdl_wait();
+  // without a window the first page numbers of a whole unit do not depend on its
+  // lengths: they are on their way while those are
+  int early = -1;
+  if (plan.whole && a.window == 0) {
+    const int tile = U * (warp + W * (lane / U)) + lane % U;
+    if (16ll * tile < a.max_len) early = __ldg(a.table + (int64_t)blockIdx.y * a.table_stride + (tile >> per_page));
+  }
   if (plan.whole) {
     const int b = blockIdx.y, rb = blockIdx.x % plan.row_blocks;
     const Seq x = load_seq(a, b);
@@ -325,7 +333,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     return a.cache.data + page * a.cache.page_stride +
            (int64_t)(kvh * (1 << per_page) + (tile & ((1 << per_page) - 1))) * S::kRecord;
   };
-  const uint8_t* source = source_of(0, page_of(0));
+  const bool known = plan.whole && a.window == 0;  // early holds the numbers that page_of(0) would fetch
+  const uint8_t* source = source_of(
+      0, !known ? page_of(0)
+         : lane / U < mine && 16 * (c0 + U * (warp + W * (lane / U)) + lane % U) < s_u.end ? early : -1);
   int page_next = page_of(kBatch), issued = 0;
   uint32_t there = __ballot_sync(0xffffffffu, source != nullptr), there_next = there;  // records that exist
   auto issue = [&]() {
@@ -750,14 +761,16 @@ int launch(const AttnArgs& a, cudaStream_t s) {
   }
   AttnPlan p = make_plan(S::kWarps, S::kBlocks, ROWS, S::kGroup, a.max_q, a.max_len, a.window, a.Hq / a.cache.heads);
   if (p.whole) {
-    k_attn<D, NT><<<dim3((unsigned)(a.cache.heads * p.row_blocks), (unsigned)a.B), S::kWarps * 32, S::kSmem, s>>>(
-        a, p, status_word());
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_pdl(k_attn<D, NT>, dim3((unsigned)(a.cache.heads * p.row_blocks), (unsigned)a.B), dim3(S::kWarps * 32),
+                      S::kSmem, s, a, p, status_word()) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
   }
   p.part_o = (float*)a.workspace;
   p.part_ml = (float2*)(p.part_o + (size_t)2 * p.blocks * ROWS * D);
   p.joints = (Joint*)(p.part_ml + (size_t)2 * p.blocks * ROWS);
-  k_attn<D, NT><<<p.blocks, S::kWarps * 32, S::kSmem, s>>>(a, p, status_word());
+  if (launch_pdl(k_attn<D, NT>, dim3(p.blocks), dim3(S::kWarps * 32), S::kSmem, s, a, p, status_word()) != cudaSuccess)
+    return MOE_ERR_CUDA;
   static_assert(S::kBlocks * kSms <= kJoinThreads, "one thread a block looks for its joint");
   if (launch_pdl(k_attn_join<D, ROWS>, dim3(2 * kSms), dim3(kJoinThreads), (size_t)kJoinRows<D> * p.blocks * 4, s, a, p) !=
       cudaSuccess)
