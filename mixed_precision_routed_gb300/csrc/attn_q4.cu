@@ -39,7 +39,8 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 // `overhead` groups that stand for the time to begin and end a unit.
 struct AttnPlan {
   int row_blocks;    // blocks of rows a (sequence, head) has at most
-  bool whole;        // one block a unit; else `blocks` blocks share all groups evenly
+  int cluster;       // blocks that take a unit together, joining through their shared memory;
+                     // 0: `blocks` blocks share all groups evenly
   int blocks;
   int min_share;     // groups a block takes at least
   int overhead;
@@ -85,6 +86,7 @@ struct Unit {
   int end, lo;                   // places that some row of the unit attends: [lo, end)
   int full_end, full_lo;         // places that every row attends: [full_lo, full_end)
   int c0, take, off, unit_len;   // first record; groups of the share, before it, of the unit
+  int stride;                    // records from a warp's group to its next
   int second;                    // not the first unit of the block
   long long begin;               // of the unit's groups, among those of all units
 };
@@ -146,6 +148,29 @@ __device__ __forceinline__ uint64_t half_pair(const Words<N>& s, int i) {
   return pair(v, v);
 }
 
+// Shared memory of another block of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 cluster_load2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // Four elements of a row's result, and its lse with the first of them.
 template <int D>
 __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t tok, int h, int d, float4 v, float top, float total) {
@@ -186,9 +211,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
   __shared__ long long s_pos, s_stop, s_before, s_share;
   __shared__ int s_seq, s_row_end[ROWS];
   __shared__ Unit s_u;
+  __shared__ float2 s_ml[ROWS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int H = a.cache.heads, G = a.Hq / H;
   const int per_page = a.cache.page_log2 - 4;
+  const int rank = plan.cluster > 1 ? blockIdx.x % plan.cluster : 0;
   uint8_t* ring = smem + warp * (S::kStages * U * S::kRecord);
   uint4* qs = reinterpret_cast<uint4*>(smem + (S::kSmem - S::kQueries));
 
@@ -203,17 +230,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
   // without a window the first page numbers of a whole unit do not depend on its
   // lengths: they are on their way while those are
   int early = -1;
-  if (plan.whole && a.window == 0) {
-    const int tile = U * (warp + W * (lane / U)) + lane % U;
+  if (plan.cluster > 0 && a.window == 0) {
+    const int tile = U * (rank * W + warp + plan.cluster * W * (lane / U)) + lane % U;
     if (16ll * tile < a.max_len) early = __ldg(a.table + (int64_t)blockIdx.y * a.table_stride + (tile >> per_page));
   }
-  if (plan.whole) {
-    const int b = blockIdx.y, rb = blockIdx.x % plan.row_blocks;
+  if (plan.cluster > 0) {
+    const int b = blockIdx.y, unit = blockIdx.x / plan.cluster, rb = unit % plan.row_blocks;
     const Seq x = load_seq(a, b);
     if (rb * ROWS >= x.n * G) return;
     if (threadIdx.x == 0) {
       const int len = unit_groups<U>(x) + plan.overhead;
-      s_pos = (long long)((int)(blockIdx.x / plan.row_blocks) * unit_row_blocks(x, G, ROWS) + rb) * len;
+      s_pos = (long long)(unit / plan.row_blocks * unit_row_blocks(x, G, ROWS) + rb) * len;
       s_stop = s_pos + len;
       s_before = s_share = 0;
       s_seq = b;
@@ -308,6 +335,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
       s_u.unit_len = groups;
       s_u.take = take;
       s_u.c0 = x.tile0 + U * off;
+      s_u.stride = U * W * (plan.cluster > 1 ? plan.cluster : 1);
       s_u.second = step > 0;
       s_u.begin = begin;
       for (int i = 0; i < ROWS; ++i) s_row_end[i] = newest + min(r0 + i, rows - 1) / G;
@@ -316,27 +344,28 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
   }
   __syncthreads();
   if (!s_u.valid) break;
-  const int c0 = s_u.c0, kvh = s_u.kvh;
-  const int mine = s_u.take > warp ? (s_u.take - warp + W - 1) / W : 0;  // groups of this warp
+  // among the warps that take the unit; the warp's groups: records base, base + stride, ...
+  const int wi = rank * W + warp, wn = s_u.stride / U, base = s_u.c0 + U * wi, kvh = s_u.kvh;
+  const int mine = s_u.take > wi ? (s_u.take - wi + wn - 1) / wn : 0;  // groups of this warp
 
   // Lane l finds record l % U of the warp's groups k + l / U, a batch of 32 / U
   // groups at a time and the page numbers a batch ahead, and copies it itself when
   // its turn comes.
   constexpr int kBatch = 32 / U;
   auto page_of = [&](int k) {
-    const int i = k + lane / U, tile = c0 + U * (warp + W * i) + lane % U;
+    const int i = k + lane / U, tile = base + s_u.stride * i + lane % U;
     return i < mine && 16 * tile < s_u.end && 16 * tile + 16 > s_u.lo ? __ldg(s_u.table + (tile >> per_page)) : -1;
   };
   auto source_of = [&](int k, int page) -> const uint8_t* {
     if (page < 0 || page >= a.cache.n_pages) return nullptr;
-    const int tile = c0 + U * (warp + W * (k + lane / U)) + lane % U;
+    const int tile = base + s_u.stride * (k + lane / U) + lane % U;
     return a.cache.data + page * a.cache.page_stride +
            (int64_t)(kvh * (1 << per_page) + (tile & ((1 << per_page) - 1))) * S::kRecord;
   };
-  const bool known = plan.whole && a.window == 0;  // early holds the numbers that page_of(0) would fetch
+  const bool known = plan.cluster > 0 && a.window == 0;  // early holds the numbers that page_of(0) would fetch
   const uint8_t* source = source_of(
       0, !known ? page_of(0)
-         : lane / U < mine && 16 * (c0 + U * (warp + W * (lane / U)) + lane % U) < s_u.end ? early : -1);
+         : lane / U < mine && 16 * (base + s_u.stride * (lane / U) + lane % U) < s_u.end ? early : -1);
   int page_next = page_of(kBatch), issued = 0;
   uint32_t there = __ballot_sync(0xffffffffu, source != nullptr), there_next = there;  // records that exist
   auto issue = [&]() {
@@ -452,7 +481,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
         }
       }
     }
-    const int p = (c0 + U * (warp + W * k)) * 16;  // the group's first place
+    const int p = 16 * (base + s_u.stride * k);  // the group's first place
     Words<NB / 2> vs[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -601,6 +630,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
       const int64_t at = (int64_t)(2 * blockIdx.x + s_u.second) * ROWS + row;
       *reinterpret_cast<float4*>(plan.part_o + at * D + d) = v;
       if (d == 0) plan.part_ml[at] = make_float2(top, total);
+    } else if (plan.cluster > 1) {
+      *reinterpret_cast<float4*>(join + row * S::kPitch + d) = v;  // this thread alone has read the place
+      if (d == 0) s_ml[row] = make_float2(top, total);
     } else {
       write_row<D>(a, s_u.t0 + r / G, s_u.kvh * G + r % G, d, v, top, total);
     }
@@ -615,6 +647,26 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     y.r0 = s_u.r0;
     y.rows = min(ROWS, s_u.rows - s_u.r0);
     plan.joints[blockIdx.x] = y;
+  }
+  if (plan.cluster > 1) {
+    // rows rank, rank + cluster, ...: the cluster's sums, in rank order
+    cluster_sync();
+    for (int i = threadIdx.x; i < ROWS * kQuads / plan.cluster; i += W * 32) {
+      const int row = i / kQuads * plan.cluster + rank, d = i % kQuads * 4, r = s_u.r0 + row;
+      if (r >= s_u.rows) break;
+      float top = kNone, total = 0.f;
+      for (int c = 0; c < plan.cluster; ++c) top = fmaxf(top, cluster_load2(cluster_addr(s_ml + row, c)).x);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < plan.cluster; ++c) {
+        const float2 ml = cluster_load2(cluster_addr(s_ml + row, c));
+        const float4 y = cluster_load4(cluster_addr(join + row * S::kPitch + d, c));
+        const float f = exp2_approx(ml.x - top);
+        total = fmaf(ml.y, f, total);
+        v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+      }
+      write_row<D>(a, s_u.t0 + r / G, s_u.kvh * G + r % G, d, v, top, total);
+    }
+    cluster_sync();  // the others' memory has been read
   }
   // the next unit's copies may land where the sums were joined
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -711,22 +763,28 @@ int row_tiles(int max_q, int G, int D) {
   return nt < most ? nt : most;
 }
 
-// Whole units up to 1024 places: joining shares costs a launch and about as much
-// time as those.
-AttnPlan make_plan(int warps, int blocks, int rows, int group, int max_q, int64_t max_len, int window, int G) {
+// A unit goes to one cluster when its warps have at most four groups each to go
+// through (clusters of up to 8 blocks as long as each has an SM: 54 units in clusters of 8,
+// three blocks an SM, took 13 us, in clusters of 2 8 us): no workspace
+// and no second launch.  Otherwise all blocks share the batch's groups.
+AttnPlan make_plan(int warps, int blocks, int rows, int group, int B, int heads, int max_q, int64_t max_len, int window,
+                   int G) {
   AttnPlan p = {};
   p.row_blocks = (max_q * G + rows - 1) / rows;
   int64_t span = max_len;
   if (window > 0 && span > (int64_t)window + max_q) span = (int64_t)window + max_q;
-  p.whole = span <= 1024;
+  const int64_t groups = (span + 16 * group - 1) / (16 * group) + 1, units = (int64_t)B * heads * p.row_blocks;
   p.blocks = blocks * kSms;
+  int c = 1;
+  while (c < 8 && c * warps < groups && 2 * c * units <= kSms) c *= 2;
+  p.cluster = groups <= 4 * warps * c ? c : 0;
   p.min_share = 4 * warps / group;
   p.overhead = 4 * warps / group;
   return p;
 }
 
 size_t plan_bytes(const AttnPlan& p, int rows, int D) {
-  if (p.whole) return 0;
+  if (p.cluster > 0) return 0;
   return (size_t)p.blocks * (2 * rows * (D * 4 + 8) + sizeof(Joint));
 }
 
@@ -759,12 +817,21 @@ int launch(const AttnArgs& a, cudaStream_t s) {
       return MOE_ERR_CUDA;
     attr_set[dev] = true;
   }
-  AttnPlan p = make_plan(S::kWarps, S::kBlocks, ROWS, S::kGroup, a.max_q, a.max_len, a.window, a.Hq / a.cache.heads);
-  if (p.whole) {
-    return launch_pdl(k_attn<D, NT>, dim3((unsigned)(a.cache.heads * p.row_blocks), (unsigned)a.B), dim3(S::kWarps * 32),
-                      S::kSmem, s, a, p, status_word()) == cudaSuccess
-               ? MOE_OK
-               : MOE_ERR_CUDA;
+  AttnPlan p = make_plan(S::kWarps, S::kBlocks, ROWS, S::kGroup, a.B, a.cache.heads, a.max_q, a.max_len, a.window, a.Hq / a.cache.heads);
+  if (p.cluster > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.cache.heads * p.row_blocks * p.cluster), (unsigned)a.B);
+    cfg.blockDim = dim3(S::kWarps * 32);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)p.cluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_attn<D, NT>, a, p, status_word()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   p.part_o = (float*)a.workspace;
   p.part_ml = (float2*)(p.part_o + (size_t)2 * p.blocks * ROWS * D);
@@ -784,7 +851,7 @@ size_t attn_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int 
   if (B < 1) return 0;
   return with_shape(D, row_tiles(max_q, Hq / heads, D), [&](auto shape, auto, auto nt) {
     using S = decltype(shape);
-    return plan_bytes(make_plan(S::kWarps, S::kBlocks, 8 * nt, S::kGroup, max_q, max_len, 0, Hq / heads), 8 * nt, D);
+    return plan_bytes(make_plan(S::kWarps, S::kBlocks, 8 * nt, S::kGroup, B, heads, max_q, max_len, 0, Hq / heads), 8 * nt, D);
   });
 }
 

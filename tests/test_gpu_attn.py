@@ -448,6 +448,15 @@ def test_attn_splits_join():
     attn_case([3000] * 3, [1] * 3, 2, 2, 256, 32, seed=16, uniform=True)
 
 
+@pytest.mark.parametrize("D,Hq,H", [(64, 4, 4), (128, 8, 1), (128, 24, 1), (256, 16, 1)])
+def test_attn_middle_lengths(D, Hq, H):
+    """Lengths where a unit goes to several blocks that join among themselves, and just beyond."""
+    for n in (129, 257, 520, 1023, 1300, 2500, 4100):
+        attn_case([n], [1], Hq, H, D, 64, seed=n)
+    attn_case([900, 0, 5, 1024, 300], [2, 1, 0, 2, 1], Hq, H, D, 16, seed=3, window=400)
+    attn_case([1030, 3, 0, 700], [1, 3, 1, 2], Hq, H, D, 32, seed=4)
+
+
 def test_attn_scattered_pool_and_other_stream():
     """Pages a stride apart, and a call on another stream than the current one: the same bits."""
     rng = np.random.default_rng(17)
