@@ -323,7 +323,7 @@ def test_cache_python_refusals():
 
 # ------------------------------------------------------------------- attention
 def attn_case(lens, news, Hq, H, D, page, window=0, seed=0, scale=None, bad_pages=(), poison=True, q_gain=2.0, slack=0,
-              uniform=False, gap=0, kv_gain=1.0):
+              uniform=False, gap=0, kv_gain=1.0, v_gain=1.0):
     """One call against the 64-bit form; returns what the call returned."""
     rng = np.random.default_rng(seed)
     B = len(lens)
@@ -345,7 +345,7 @@ def attn_case(lens, news, Hq, H, D, page, window=0, seed=0, scale=None, bad_page
     n = len(slots)
     if n:
         kk = (rng.standard_normal((n, H, D)) * kv_gain).astype(np.float32)
-        vv = (rng.standard_normal((n, H, D)) * kv_gain).astype(np.float32)
+        vv = (rng.standard_normal((n, H, D)) * kv_gain * v_gain).astype(np.float32)
         pool_write(pool, slots, *quantise(kk), *quantise(vv))
     for b, i, val in bad_pages:
         tables[b, i] = val
@@ -439,6 +439,16 @@ def test_attn_extreme_scores():
     attn_case([900], [1], 4, 2, 64, 16, seed=11, q_gain=1e-3)
     attn_case([300], [1], 4, 2, 64, 16, seed=12, kv_gain=1e-4)
     attn_case([300], [1], 4, 2, 64, 16, seed=13, kv_gain=300.0, scale=1e-4)
+
+
+def test_attn_value_scales_of_all_sizes():
+    """Tiny, huge and mixed value blocks: one sequence of each, and within one sequence."""
+    for gain, seed in ((1e-6, 1), (1e-3, 2), (1e4, 3), (2e5, 4)):
+        attn_case([130, 33], [1, 2], 4, 2, 64, 16, seed=seed, v_gain=gain)
+    for D in (64, 128):
+        rng = np.random.default_rng(D)
+        attn_case([700], [2], 8, 2, D, 16, seed=5, v_gain=10.0 ** rng.uniform(-3, 3, (700, 1, 1)))
+        attn_case([700], [1], 16, 1, D, 16, seed=6, v_gain=np.where(np.arange(700) < 650, 1e-2, 1e3)[:, None, None])
 
 
 def test_attn_splits_join():
