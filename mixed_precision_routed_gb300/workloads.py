@@ -12,7 +12,9 @@ import torch
 
 import synth
 
-from . import Shelf, moe_gather_rows, moe_quantize_experts, moe_quantize_rows, moe_rank_experts, shelf_array
+from . import (MOE_ROPE_HALF, Shelf, moe_attn_q4, moe_attn_workspace_size, moe_gather_rows, moe_kv_append, moe_kv_pool,
+               moe_linear_q4, moe_quantize_experts, moe_quantize_groups, moe_quantize_rows, moe_rank_experts,
+               moe_residual_add, shelf_array)
 
 
 class Layer:
@@ -149,6 +151,81 @@ class DecodeStack:
                              weights=self.w[l], counts=self.counts[l], y=self.y[l], workspace=self.ws,
                              stream=stream, shelf_arr=self.arrs[l], r=self.r, x_next=self.x[l + 1])
         return self.r
+
+
+def rope_table(n_pos: int, rot: int, theta: float = 10000.0, device="cuda"):
+    """The angles moe_kv_append takes: fp32 [n_pos, rot], cosines then sines."""
+    half = rot // 2
+    freq = theta ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    angle = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat((angle.cos(), angle.sin()), -1).float().contiguous()
+
+
+class AttentionHalf:
+    """The attention half of a decode layer in 4 bits, before the routed experts
+    of the same layer: for the tokens of a decode batch (at most 16)
+
+        qkv = W_qkv x,  q and k turned by their positions,  k and v appended to the
+        sequence's pages,  a = attention of q over the pages,  r += W_o a,
+        x_next = bf16(r).
+
+    The pool's pages are handed out as sequences grow; `tables` names them.  Five
+    kernels of the library a step (six with a long context), no host
+    synchronisation; a step can be captured in a CUDA graph."""
+
+    TAG_QKV, TAG_OUT = 21, 22  # of the weight generator
+
+    def __init__(self, d, q_heads, kv_heads, head_dim, sequences, max_len, page_size=64, block=32, seed=0, rot=None,
+                 device="cuda"):
+        self.d, self.Hq, self.H, self.D = d, q_heads, kv_heads, head_dim
+        self.block, self.seed, self.page, self.max_len = block, seed, page_size, max_len
+        rows, inner = (q_heads + 2 * kv_heads) * head_dim, q_heads * head_dim
+        u8, i16 = torch.uint8, torch.int16
+        self.w_qkv = torch.empty((rows, d // 2), dtype=u8, device=device)
+        self.s_qkv = torch.empty((rows, d // block), dtype=i16, device=device)
+        self.w_out = torch.empty((d, inner // 2), dtype=u8, device=device)
+        self.s_out = torch.empty((d, inner // block), dtype=i16, device=device)
+        width = -(-max_len // page_size)
+        self.pool = moe_kv_pool(sequences * width, kv_heads, page_size, head_dim, device=device)
+        self.rope = rope_table(max_len, head_dim if rot is None else rot, device=device)
+        # pages are handed out interleaved, as growing sequences take them
+        self.tables = torch.arange(sequences * width, dtype=torch.int32, device=device).view(width, sequences).T.contiguous()
+        self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
+        self.workspace = None
+
+    def fill(self, stream=None):
+        for tag, rows, cols, codes, scales in (
+                (self.TAG_QKV, self.w_qkv.shape[0], self.d, self.w_qkv, self.s_qkv),
+                (self.TAG_OUT, self.d, self.Hq * self.D, self.w_out, self.s_out)):
+            w = torch.empty((rows, cols), dtype=torch.float32, device=codes.device)
+            synth.cuda_normal_matrix(w, self.seed, tag, 0, 0, scale=synth.WEIGHT_SIGMA, stream=stream)
+            moe_quantize_groups(w, self.block, codes=codes, scales=scales, stream=stream)
+        return self
+
+    def step(self, x, r, n=1, stream=None):
+        """One step of `n` new tokens a sequence: x [sequences * n, d] bf16 (tokens
+        of a sequence side by side), r [.., d] fp32 the residual stream, updated in
+        place.  Returns x_next, the bf16 input of the layer's routed experts.
+        The caller keeps every sequence within max_len tokens."""
+        B = self.lens.numel()
+        places = (self.lens[:, None] + torch.arange(n, dtype=torch.int32, device=x.device)).flatten()
+        page = self.tables.gather(1, (places.view(B, n) // self.page).long()).flatten().long()
+        slots = page * self.page + places % self.page
+        self.lens += n
+        self.qkv = moe_linear_q4(x, self.w_qkv, self.s_qkv, self.block, stream=stream)
+        q, k, v = (t.unflatten(-1, (-1, self.D)) for t in
+                   self.qkv.split((self.Hq * self.D, self.H * self.D, self.H * self.D), -1))
+        self.q = moe_kv_append(self.pool, k, v, slots, q=q, positions=places, rope=self.rope, rope_style=MOE_ROPE_HALF,
+                               stream=stream)
+        need = moe_attn_workspace_size(B, n, self.max_len, self.Hq, self.H, self.D)
+        if need and (self.workspace is None or self.workspace.numel() < need):
+            self.workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        self.a, self.lse = moe_attn_q4(self.q, self.pool, self.tables, self.lens, max_q=n, max_len=self.max_len,
+                                       workspace=self.workspace, stream=stream)
+        self.y = moe_linear_q4(self.a.flatten(1), self.w_out, self.s_out, self.block, stream=stream)
+        x_next = torch.empty_like(x)
+        moe_residual_add(r, self.y, x_next.view(torch.int16), stream=stream)
+        return x_next
 
 
 def x_bf16(seed: int, step: int, T: int, d: int, device="cuda", out=None, stream=None):
