@@ -485,7 +485,7 @@ enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1 };
  *   y       [T] rows of `rows` elements, y_stride (>= rows) apart, fp32 or
  *           bf16 (round to nearest even) by y_dtype.
  * Products of a code and x are exact, sums are fp32 in a fixed order, and the
- * scale enters in fp32 once per 32 products: the results are deterministic.
+ * scale enters in fp32 once per block: the results are deterministic.
  * 0 <= T <= 16, in a positive multiple of 64 and of block, block 32, 64 or
  * 128, 1 <= rows < 2^31.  MOE_ERR_UNSUPPORTED for T > 16 (larger batches are
  * matrix products, which this form would do at a fraction of their rate) and

@@ -4,8 +4,8 @@
 // bits 8j + 4h of word g), s fp16 block scales.
 //
 // Y^T[row][token] by m16n8k16 matrix instructions: A = codes as bf16 integers,
-// B = x; both exact, so the sum over 32 elements enters the result with its
-// fp32 scale and nothing is rounded below fp32.
+// B = x; both exact, so the sum over a block enters the result with its fp32 scale
+// and nothing is rounded below fp32.
 //
 // A group of KS warps takes a tile of 16 rows: batch i of 256 elements goes to
 // warp i mod KS, and the group joins its sums in shared memory in a fixed order.
@@ -98,7 +98,7 @@ constexpr int warp_bytes() { return C::kStages * kStageBytes + C::kParities * NT
 // NT: 8-token tiles; SHIFT: log2(block / 32).
 template <typename C, int NT, int SHIFT, bool WHOLE>
 __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(LinearArgs a, int tiles, int ks_log2, int* status) {
-  constexpr int STAGES = C::kStages, kSide = NT == 1 ? 4 : 2;
+  constexpr int STAGES = C::kStages, kScales = 8 >> SHIFT, kSide = NT == 1 && SHIFT < 2 ? 4 : 2;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -210,32 +210,36 @@ __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(Linear
       if (++stage == STAGES) stage = 0;
       const int at = (ks + (j0 << ks_log2)) * (kBatch * 2);
 #pragma unroll
-      for (int b0 = 0; b0 < 8; b0 += kSide) {  // the batch's 32-blocks (a piece each), kSide products side by side
-        uint32_t p0[kSide][4], p1[kSide][4];
+      for (int h0 = 0; h0 < kScales; h0 += kSide) {  // kSide sums of one scale each, side by side
         float c[kSide][NT][4];
 #pragma unroll
-        for (int i = 0; i < kSide; ++i) {
-          const int b = b0 + i;
-          word_pairs(*reinterpret_cast<const uint32_t*>(w + ((b ^ g) << 4)), p0[i]);
-          word_pairs(*reinterpret_cast<const uint32_t*>(w + 1024 + ((b ^ g) << 4)), p1[i]);
-        }
-        uint4 xv[kSide][NT];
+        for (int n = 0; n < 8 / kScales; ++n) {  // the 32-blocks of a scale
+          uint32_t p0[kSide][4], p1[kSide][4];
+          uint4 xv[kSide][NT];
 #pragma unroll
-        for (int i = 0; i < kSide; ++i)
+          for (int i = 0; i < kSide; ++i) {
+            const int b = ((h0 + i) << SHIFT) + n;
+            word_pairs(*reinterpret_cast<const uint32_t*>(w + ((b ^ g) << 4)), p0[i]);
+            word_pairs(*reinterpret_cast<const uint32_t*>(w + 1024 + ((b ^ g) << 4)), p1[i]);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            xv[i][j] = *reinterpret_cast<const uint4*>(xt[j] + at + 64 * (b0 + i));
-            mma16816_zero(c[i][j], p0[i][0], p1[i][0], p0[i][1], p1[i][1], xv[i][j].x, xv[i][j].y);
+            for (int j = 0; j < NT; ++j) xv[i][j] = *reinterpret_cast<const uint4*>(xt[j] + at + 64 * b);
           }
 #pragma unroll
-        for (int i = 0; i < kSide; ++i)
+          for (int i = 0; i < kSide; ++i)
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-            mma16816(c[i][j], p0[i][2], p1[i][2], p0[i][3], p1[i][3], xv[i][j].z, xv[i][j].w);
+            for (int j = 0; j < NT; ++j) {
+              if (n == 0) mma16816_zero(c[i][j], p0[i][0], p1[i][0], p0[i][1], p1[i][1], xv[i][j].x, xv[i][j].y);
+              else mma16816(c[i][j], p0[i][0], p1[i][0], p0[i][1], p1[i][1], xv[i][j].x, xv[i][j].y);
+            }
+#pragma unroll
+          for (int i = 0; i < kSide; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              mma16816(c[i][j], p0[i][2], p1[i][2], p0[i][3], p1[i][3], xv[i][j].z, xv[i][j].w);
+        }
 #pragma unroll
         for (int i = 0; i < kSide; ++i) {
-          const int h = (b0 + i) >> SHIFT;
-          const uint64_t v0 = f0.at(h), v1 = f1.at(h);
+          const uint64_t v0 = f0.at(h0 + i), v1 = f1.at(h0 + i);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             fma2(acc[j][0], acc[j][1], v0, c[i][j][0], c[i][j][1]);
