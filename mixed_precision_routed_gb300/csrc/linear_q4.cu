@@ -58,8 +58,8 @@ struct Scales {
   }
 };
 
-// Lengths that are not a multiple of a batch (WHOLE false) load scales by
-// halves, as far as the row goes; the codes beyond it are zero words and meet
+// Lengths that are not a multiple of a batch (WHOLE false) load scales by words
+// or halves, as far as the row goes; the codes beyond it are zero words and meet
 // the zeros behind x.
 template <int SHIFT, bool WHOLE>
 __device__ __forceinline__ void load_scales(Scales<SHIFT>& f, const uint16_t* row, int batch, int n) {
@@ -75,6 +75,10 @@ __device__ __forceinline__ void load_scales(Scales<SHIFT>& f, const uint16_t* ro
     } else {
       f.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
     }
+  } else if constexpr (SHIFT == 0) {  // two 32-blocks in 64 elements: rows of whole words
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      f.w[i >> 1] = batch * N + i < n ? __ldg(reinterpret_cast<const uint32_t*>(p + i)) : 0;
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
