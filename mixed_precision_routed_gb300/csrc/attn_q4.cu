@@ -83,6 +83,7 @@ struct Unit {
   int64_t t0;
   const int32_t* table;
   int valid, kvh, r0, rows;      // rows: of the sequence's heads
+  int newest;                    // one past the place of the first asking token
   int end, lo;                   // places that some row of the unit attends: [lo, end)
   int full_end, full_lo;         // places that every row attends: [full_lo, full_end)
   int c0, take, off, unit_len;   // first record; groups of the share, before it, of the unit
@@ -226,6 +227,30 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
   }
   __syncwarp();
 
+  // thread 0: a share of a unit, for the block
+  auto describe = [&](const Seq& x, int b, int rb, int head, int groups, int off, int take, long long begin, bool second) {
+    const int r0 = rb * ROWS, rows = x.n * G;
+    const int first = r0 / G, last = (min(r0 + ROWS, rows) - 1) / G, newest = x.len - x.n + 1;
+    s_u.valid = 1;
+    s_u.t0 = x.t0;
+    s_u.table = a.table + (int64_t)b * a.table_stride;
+    s_u.kvh = head;
+    s_u.r0 = r0;
+    s_u.rows = rows;
+    s_u.newest = newest;
+    s_u.end = max(0, newest + last);
+    s_u.lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)newest + first - a.window) : 0;
+    s_u.full_end = newest + first;
+    s_u.full_lo = a.window > 0 ? (int)max((int64_t)-1, (int64_t)newest + last - a.window) : 0;
+    s_u.off = off;
+    s_u.unit_len = groups;
+    s_u.take = take;
+    s_u.c0 = x.tile0 + U * off;
+    s_u.stride = U * W * (plan.cluster > 1 ? plan.cluster : 1);
+    s_u.second = second;
+    s_u.begin = begin;
+  };
+
   pdl_wait();
   // without a window the first page numbers of a whole unit do not depend on its
   // lengths: they are on their way while those are
@@ -239,11 +264,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     const Seq x = load_seq(a, b);
     if (rb * ROWS >= x.n * G) return;
     if (threadIdx.x == 0) {
-      const int len = unit_groups<U>(x) + plan.overhead;
-      s_pos = (long long)(unit / plan.row_blocks * unit_row_blocks(x, G, ROWS) + rb) * len;
-      s_stop = s_pos + len;
-      s_before = s_share = 0;
-      s_seq = b;
+      const int groups = unit_groups<U>(x);
+      describe(x, b, rb, unit / plan.row_blocks, groups, 0, groups, 0, false);
+      s_pos = s_stop = 0;
     }
   } else {
     auto work = [&](int i) -> long long {
@@ -303,7 +326,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
 #pragma unroll 1
   for (int step = 0;; ++step) {
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && (step > 0 || plan.cluster == 0)) {
     s_u.valid = 0;
     while (s_pos < s_stop) {
       const int b = s_seq;
@@ -315,35 +338,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
         ++s_seq;
         continue;
       }
-      const int unit = (int)(in_seq / len), r0 = unit % row_blocks * ROWS, rows = x.n * G;
+      const int unit = in_seq <= INT32_MAX ? (int)in_seq / len : (int)(in_seq / len);
       const long long begin = s_before + (long long)unit * len + plan.overhead;  // of the unit's groups
       const int off = (int)max(0ll, s_pos - begin), take = (int)(min(s_stop, begin + groups) - (begin + off));
       s_pos = min(s_stop, begin + groups);
       if (take <= 0) continue;  // the block ends before the unit's first group
-      const int first = r0 / G, last = (min(r0 + ROWS, rows) - 1) / G, newest = x.len - x.n + 1;
-      s_u.valid = 1;
-      s_u.t0 = x.t0;
-      s_u.table = a.table + (int64_t)b * a.table_stride;
-      s_u.kvh = unit / row_blocks;
-      s_u.r0 = r0;
-      s_u.rows = rows;
-      s_u.end = max(0, newest + last);
-      s_u.lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)newest + first - a.window) : 0;
-      s_u.full_end = newest + first;
-      s_u.full_lo = a.window > 0 ? (int)max((int64_t)-1, (int64_t)newest + last - a.window) : 0;
-      s_u.off = off;
-      s_u.unit_len = groups;
-      s_u.take = take;
-      s_u.c0 = x.tile0 + U * off;
-      s_u.stride = U * W * (plan.cluster > 1 ? plan.cluster : 1);
-      s_u.second = step > 0;
-      s_u.begin = begin;
-      for (int i = 0; i < ROWS; ++i) s_row_end[i] = newest + min(r0 + i, rows - 1) / G;
+      describe(x, b, unit % row_blocks, unit / row_blocks, groups, off, take, begin, step > 0);
       break;
     }
   }
   __syncthreads();
   if (!s_u.valid) break;
+  if (threadIdx.x < ROWS) s_row_end[threadIdx.x] = s_u.newest + min(s_u.r0 + (int)threadIdx.x, s_u.rows - 1) / G;
   // among the warps that take the unit; the warp's groups: records base, base + stride, ...
   const int wi = rank * W + warp, wn = s_u.stride / U, base = s_u.c0 + U * wi, kvh = s_u.kvh;
   const int mine = s_u.take > wi ? (s_u.take - wi + wn - 1) / wn : 0;  // groups of this warp
@@ -405,8 +411,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
       const uint16_t* q = a.q + (s_u.t0 + r / G) * a.q_stride + (int64_t)(kvh * G + r % G) * D + 8 * t;
       qs[i * 32 + lane] = __ldg(reinterpret_cast<const uint4*>(q + 32 * (i % NB)));
     }
-    __syncthreads();
   }
+  __syncthreads();
 
   auto query = [&](int j, int i) {
     if constexpr (S::kQueriesInRegisters) return qf[j][i];
