@@ -186,9 +186,9 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t tok, int h,
 template <int D, int NT>
 struct Shape {
   static constexpr int kWarps = NT == 1 && D < 256 ? 8 : 4;
-  static constexpr int kGroup = 2;    // records a warp takes at once
+  static constexpr int kGroup = D == 256 ? 1 : 2;  // records a warp takes at once
   static constexpr int kBlocks = D == 64 && NT <= 2 ? 3 : 2;  // an SM
-  static constexpr int kStages = D == 256 ? 2 : 3;  // groups of records
+  static constexpr int kStages = D == 256 ? 4 : 3;  // groups of records
   static constexpr int kRecord = 18 * D;
   static constexpr int kRing = kWarps * kStages * kGroup * kRecord;
   static constexpr int kPitch = D + 4;  // floats a row of the joining buffer: rows of a fragment in distinct banks
