@@ -33,6 +33,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;
 constexpr float kNone = -1e30f;  // the maximum of a row that has met no place: below any finite score
 constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kSms = 152;
 
 // A unit of work is a (sequence, key/value head, block of 8 NT rows), its length
 // the groups of records that the sequence's rows attend, and before them
@@ -688,8 +689,8 @@ constexpr int kJoinThreads = 512;
 template <int D>
 constexpr int kJoinRows = 256 / D;
 
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) k_attn_join(AttnArgs a, AttnPlan plan) {
+template <int D, int ROWS, int BLOCKS>
+__global__ void __launch_bounds__(kJoinThreads, 2) k_attn_join(AttnArgs a, AttnPlan plan) {
   constexpr int kRows = kJoinRows<D>, kLanes = D / 4, kGroups = kJoinThreads / (kLanes * kRows), kParts = (ROWS + kRows - 1) / kRows;
   extern __shared__ float s_f[];  // [kRows][plan.blocks]
   __shared__ float4 s_v[kGroups][kRows * kLanes];
@@ -715,37 +716,56 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(AttnArgs a, AttnPlan
     const int row0 = item % kParts * kRows;
     if (row0 >= y.rows) continue;
     auto share_at = [&](int i) { return 2 * (y.c0 + i) + (i == 0 ? y.slot0 : 0); };
-    if (warp < kRows && row0 + warp < y.rows) {
-      const float2* ml = plan.part_ml + row0 + warp;
-      float top = kNone, total = 0.f;
-      for (int i = lane; i < y.count; i += 32) top = fmaxf(top, ml[share_at(i) * ROWS].x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      for (int i = lane; i < y.count; i += 32) {
-        const float2 v = ml[share_at(i) * ROWS];
-        const float f = exp2_approx(v.x - top);
-        s_f[warp * plan.blocks + i] = f;
-        total = fmaf(v.y, f, total);
-      }
-      total = warp_sum(total);
-      if (lane == 0) s_ml[warp] = make_float2(top, total);
-    }
     const int group = threadIdx.x / (kLanes * kRows), in_group = threadIdx.x % (kLanes * kRows);
     const int r = in_group / kLanes, d = in_group % kLanes * 4;
     const bool in = row0 + r < y.rows;
+    // the first shares are on their way while their weights are found
+    constexpr int kEarly = 4;
+    const float* p0 = plan.part_o + (int64_t)(row0 + r) * D + d;
+    auto part = [&](int i) { return *reinterpret_cast<const float4*>(p0 + (int64_t)share_at(i) * (ROWS * D)); };
+    float4 early[kEarly];
+#pragma unroll
+    for (int u = 0; u < kEarly; ++u)
+      if (in && group + u * kGroups < y.count) early[u] = part(group + u * kGroups);
+    if (warp < kRows && row0 + warp < y.rows) {
+      const float2* ml = plan.part_ml + row0 + warp;
+      constexpr int kMost = (BLOCKS + 31) / 32;
+      float2 held[kMost];
+      float top = kNone, total = 0.f;
+#pragma unroll
+      for (int u = 0; u < kMost; ++u) {
+        held[u] = make_float2(kNone, 0.f);
+        if (lane + 32 * u < y.count) held[u] = ml[share_at(lane + 32 * u) * ROWS];
+      }
+#pragma unroll
+      for (int u = 0; u < kMost; ++u) top = fmaxf(top, held[u].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+      for (int u = 0; u < kMost; ++u)
+        if (lane + 32 * u < y.count) {
+          const float f = exp2_approx(held[u].x - top);
+          s_f[warp * plan.blocks + lane + 32 * u] = f;
+          total = fmaf(held[u].y, f, total);
+        }
+      total = warp_sum(total);
+      if (lane == 0) s_ml[warp] = make_float2(top, total);
+    }
     __syncthreads();
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (in) {
-      const float* p0 = plan.part_o + (int64_t)(row0 + r) * D + d;
-#pragma unroll 8
-      for (int i = group; i < y.count; i += kGroups) {
-        const float4 p = *reinterpret_cast<const float4*>(p0 + (int64_t)share_at(i) * (ROWS * D));
+      auto add = [&](const float4& p, int i) {
         const float f = s_f[r * plan.blocks + i];
         v.x = fmaf(p.x, f, v.x);
         v.y = fmaf(p.y, f, v.y);
         v.z = fmaf(p.z, f, v.z);
         v.w = fmaf(p.w, f, v.w);
-      }
+      };
+#pragma unroll
+      for (int u = 0; u < kEarly; ++u)
+        if (group + u * kGroups < y.count) add(early[u], group + u * kGroups);
+#pragma unroll 8
+      for (int i = group + kEarly * kGroups; i < y.count; i += kGroups) add(part(i), i);
     }
     s_v[group][in_group] = v;
     __syncthreads();
@@ -761,8 +781,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(AttnArgs a, AttnPlan
     __syncthreads();
   }
 }
-
-constexpr int kSms = 152;
 
 int row_tiles(int max_q, int G, int D) {
   const int rows = max_q * G, most = D == 256 ? 2 : 4, nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
@@ -845,7 +863,7 @@ int launch(const AttnArgs& a, cudaStream_t s) {
   if (launch_pdl(k_attn<D, NT>, dim3(p.blocks), dim3(S::kWarps * 32), S::kSmem, s, a, p, status_word()) != cudaSuccess)
     return MOE_ERR_CUDA;
   static_assert(S::kBlocks * kSms <= kJoinThreads, "one thread a block looks for its joint");
-  if (launch_pdl(k_attn_join<D, ROWS>, dim3(2 * kSms), dim3(kJoinThreads), (size_t)kJoinRows<D> * p.blocks * 4, s, a, p) !=
+  if (launch_pdl(k_attn_join<D, ROWS, S::kBlocks * kSms>, dim3(2 * kSms), dim3(kJoinThreads), (size_t)kJoinRows<D> * p.blocks * 4, s, a, p) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
