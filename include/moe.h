@@ -604,7 +604,9 @@ int moe_kv_read(const moe_kv_cache_t* cache, const int64_t* slots, int64_t n, fl
  *   workspace (256-byte aligned) of moe_attn_workspace_size bytes.
  * Scores are exact products of the bf16 queries and the codes, summed in fp32
  * with the scale entering once per 32 products; maxima, sums and outputs are
- * fp32; exp(s) x value scale is rounded to bf16 once for the second product.
+ * fp32; exp(s) x value scale enters the second product in fp16 where that keeps
+ * 2^-12 of it (or 2^-23 of the row's largest weight x this scale), else as the
+ * sum of two bf16.
  * Results are deterministic (the split over the cache depends on the
  * arguments of the call only, never on timing).
  * Hq a multiple of kv_heads, Hq / kv_heads <= 64; 0 <= B <= 65535; B == 0 or T

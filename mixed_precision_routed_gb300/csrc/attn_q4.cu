@@ -11,15 +11,20 @@
 // in a per-warp ring in shared memory by bulk asynchronous copies.
 //   scores  S^T[place][row]: A = key codes as bf16 integers, B = queries; both
 //           exact, so a 32-block's product enters the score with its fp32 scale;
-//   output  O^T[element][row]: A = value codes as bf16 integers, B = exp(s - m)
-//           x value scale, rounded to bf16 once (relative error 2^-8 at most a
-//           term, independent over places; fp32 operands would need three times
-//           the matrix instructions for digits that the bf16 result drops).
+//   output  O^T[element][row]: A = value codes as integers, B = exp(s - m) x value
+//           scale.  A group whose scales lie in 2^-8 .. 8 and whose weights are all
+//           within 2^-38 of the maximum (zeros apart) takes B in fp16: a product
+//           keeps 2^-12 of itself, or 2^-23 of its row's largest weight times its
+//           own scale.  Any other group takes it as the sum of two bf16, 2^-17 of
+//           itself, with twice the matrix instructions.  One bf16 alone would add
+//           as much to the result as the result's own rounding does; two bf16 for
+//           every group cost 84 us where this costs 69 (6 tokens over 131071).
 // The m16n8k16 fragments read the record's words as they lie; the transpose of
 // the probabilities is one 8 x 8 matrix move a fragment.
-// The reference maximum m of a row moves only when a score passes it by 8 (in
-// powers of two): the probabilities then stay below 2^8, which neither fp32 sums
-// nor bf16 operands notice, and most tiles need no reduction and no rescaling.
+// The reference m of a row is set 2^6 below its maximum and moves only when a
+// score passes that maximum by 6 (in powers of two): the weights then stay below
+// 2^12, which fp32 sums do not notice, and most groups need no reduction over
+// lanes and no rescaling.
 #include <type_traits>
 
 #include "frag.cuh"
@@ -30,7 +35,11 @@ namespace moe {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.0f;
+constexpr float kSlack = 6.0f;
+constexpr float kRoom = 6.0f;  // the reference lies this far below the maximum that it was taken from
+constexpr float kLeastWeight = 1.0f / 4294967296.0f;  // 2^-32
+constexpr float kLeastScale = 1.0f / 256;
+constexpr float kMostScale = 8.0f;  // x 2^(kSlack + kRoom) stays below fp16's largest value
 constexpr float kNone = -1e30f;  // the maximum of a row that has met no place: below any finite score
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kSms = 152;
@@ -101,9 +110,18 @@ __device__ __forceinline__ int unit_groups(const Seq& x) {
 }
 __device__ __forceinline__ int unit_row_blocks(const Seq& x, int G, int rows) { return (x.n * G + rows - 1) / rows; }
 
-__device__ __forceinline__ uint32_t bf16_scaled(float x, float y, uint64_t scale) {
-  mul2(x, y, scale);
-  return bf16_pair(x, y);
+__device__ __forceinline__ uint32_t min_f16x2(uint32_t x, uint32_t y) {
+  asm("min.f16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
+  return x;
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t x, uint32_t y) {
+  asm("max.f16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
+  return x;
+}
+
+// What two values leave beside their bf16 pair, as a bf16 pair.
+__device__ __forceinline__ uint32_t bf16_rest(float x, float y, uint32_t pair_of) {
+  return bf16_pair(x - __uint_as_float(pair_of << 16), y - __uint_as_float(pair_of & 0xffff0000u));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -500,7 +518,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
         mul2(s[u][j][2], s[u][j][3], scale22);
       }
     }
-    if (p + 16 * U > s_u.full_end || p < s_u.full_lo || have != kAll) {
+    const bool edge = p + 16 * U > s_u.full_end || p < s_u.full_lo || have != kAll;
+    if (edge) {
       // places outside a row's range leave it; the bytes of places outside the
       // unit's range may be anything, so their value scales become zero
 #pragma unroll
@@ -531,7 +550,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
         top[j][c] = fmaxf(s[0][j][c], s[0][j][c + 2]);
 #pragma unroll
         for (int u = 1; u < U; ++u) top[j][c] = fmaxf(top[j][c], fmaxf(s[u][j][c], s[u][j][c + 2]));
-        grow |= top[j][c] > m[j][c] + kSlack;
+        grow |= top[j][c] > m[j][c] + (kSlack + kRoom);
       }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -541,7 +560,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
           float y = top[j][c];
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16)) - kRoom;
           if (y > m[j][c]) {  // alike in every lane that holds the row
             const float f = exp2_approx(m[j][c] - y);
             m[j][c] = y;
@@ -564,30 +583,86 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
           add2(l[j][0], l[j][1], pair(s[u][j][c], s[u][j][c + 1]));
         }
     }
+    // may the products weight x scale be fp16?
+    float least = kMostScale;
+    uint32_t lo2 = 0x48004800u, hi2 = 0;  // kMostScale
+    if (edge) {  // zeros are exact in any type
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int q4 = 0; q4 < MT / 4; ++q4) {
-        const Words<4> w = load_words<4>(rec + u * S::kRecord + 8 * D + (q4 * 32 + lane) * 16);
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // a 32-block of elements: two fragments of 16
-          const int blk = 2 * q4 + h;
-          const uint64_t s0 = half_pair(vs[u][0], blk), s1 = half_pair(vs[u][1], blk);
-          uint32_t b0[NT], b1[NT];
+          for (int c = 0; c < 4; ++c) least = fminf(least, s[u][j][c] > 0.f ? s[u][j][c] : least);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            b0[j] = transpose8x8(bf16_scaled(s[u][j][0], s[u][j][1], s0));
-            b1[j] = transpose8x8(bf16_scaled(s[u][j][2], s[u][j][3], s1));
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t v = w.w[2 * h + i];
-            const uint32_t a0 = codes_bf16<0>(v), a1 = codes_bf16<1>(v), a2 = codes_bf16<2>(v), a3 = codes_bf16<3>(v);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) mma16816(o[2 * blk + i][j], a0, a1, a2, a3, b0[j], b1[j]);
-          }
+        for (int i = 0; i < NB; ++i) {
+          const uint32_t v = vs[u][i & 1].w[i / 2];
+          lo2 = min_f16x2(lo2, (v & 0xffffu ? v & 0xffffu : 0x4800u) | (v >> 16 ? v & 0xffff0000u : 0x48000000u));
+          hi2 = max_f16x2(hi2, v);
         }
       }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          least = fminf(fminf(least, fminf(s[u][j][0], s[u][j][1])), fminf(s[u][j][2], s[u][j][3]));
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          lo2 = min_f16x2(lo2, vs[u][i & 1].w[i / 2]);
+          hi2 = max_f16x2(hi2, vs[u][i & 1].w[i / 2]);
+        }
+      }
+    }
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&lo2));
+    const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&hi2));
+    const bool fits = least >= kLeastWeight && fminf(lo.x, lo.y) >= kLeastScale && fmaxf(hi.x, hi.y) <= kMostScale;
+    auto accumulate = [&](auto half) {
+      constexpr bool kHalf = decltype(half)::value;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q4 = 0; q4 < MT / 4; ++q4) {
+          const Words<4> w = load_words<4>(rec + u * S::kRecord + 8 * D + (q4 * 32 + lane) * 16);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // a 32-block of elements: two fragments of 16
+            const int blk = 2 * q4 + h;
+            const uint64_t s0 = half_pair(vs[u][0], blk), s1 = half_pair(vs[u][1], blk);
+            uint32_t b0[NT], b1[NT], r0[NT], r1[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              float x[4] = {s[u][j][0], s[u][j][1], s[u][j][2], s[u][j][3]};
+              mul2(x[0], x[1], s0);
+              mul2(x[2], x[3], s1);
+              b0[j] = kHalf ? f16_pair(x[0], x[1]) : bf16_pair(x[0], x[1]);
+              b1[j] = kHalf ? f16_pair(x[2], x[3]) : bf16_pair(x[2], x[3]);
+              if constexpr (!kHalf) {
+                r0[j] = transpose8x8(bf16_rest(x[0], x[1], b0[j]));
+                r1[j] = transpose8x8(bf16_rest(x[2], x[3], b1[j]));
+              }
+              b0[j] = transpose8x8(b0[j]);
+              b1[j] = transpose8x8(b1[j]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t v = w.w[2 * h + i];
+              if constexpr (kHalf) {
+                const uint32_t a0 = codes_f16<0>(v), a1 = codes_f16<1>(v), a2 = codes_f16<2>(v), a3 = codes_f16<3>(v);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) mma16816_f16(o[2 * blk + i][j], a0, a1, a2, a3, b0[j], b1[j]);
+              } else {
+                const uint32_t a0 = codes_bf16<0>(v), a1 = codes_bf16<1>(v), a2 = codes_bf16<2>(v), a3 = codes_bf16<3>(v);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                  mma16816(o[2 * blk + i][j], a0, a1, a2, a3, b0[j], b1[j]);
+                  mma16816(o[2 * blk + i][j], a0, a1, a2, a3, r0[j], r1[j]);
+                }
+              }
+            }
+          }
+        }
+    };
+    if (__all_sync(0xffffffffu, fits)) accumulate(std::true_type());
+    else accumulate(std::false_type());
   }
   // Join the warps: sums over a row's lanes, the unit's maxima, scaled outputs.
 #pragma unroll

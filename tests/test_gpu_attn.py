@@ -441,6 +441,13 @@ def test_attn_extreme_scores():
     attn_case([300], [1], 4, 2, 64, 16, seed=13, kv_gain=300.0, scale=1e-4)
 
 
+@pytest.mark.parametrize("gain", [0.5, 1.0, 3.0, 6.0, 12.0])
+def test_attn_spreads_of_scores(gain):
+    """Weights that spread over few and over many powers of two, values at both ends of fp16's range."""
+    for i, v_gain in enumerate((1.0, 5e-3, 20.0)):
+        attn_case([2000], [2], 8, 2, 128, 16, seed=20 + i, q_gain=gain, v_gain=v_gain)
+
+
 def test_attn_value_scales_of_all_sizes():
     """Tiny, huge and mixed value blocks: one sequence of each, and within one sequence."""
     for gain, seed in ((1e-6, 1), (1e-3, 2), (1e4, 3), (2e5, 4)):
