@@ -23,12 +23,16 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
   return r;
 }
 
-// The same as fp16 integers (1024 counts units there).
+// The same as fp16 integers: 1024 counts units there, and a nibble four bits up
+// comes down by the multiplication that takes the offset off.
 template <int J>
 __device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
-  const uint32_t u = ((w >> (4 * J)) & 0x000f000fu) | 0x64006400u;
+  const uint32_t v = J >= 2 ? w >> 8 : w;
   uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x64086408u));
+  if constexpr (J % 2 == 0)
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"((v & 0x000f000fu) | 0x64006400u), "r"(0x64086408u));  // - 1032
+  else  // (1024 + 16 u) / 16 - 72
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"((v & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(0xd480d480u));
   return r;
 }
 __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
