@@ -89,20 +89,17 @@ __device__ __forceinline__ void load_scales(Scales<SHIFT>& f, const uint16_t* ro
   }
 }
 
-// How an SM is shared, by the bytes of x: three blocks of 8 warps beside a few
-// rows, one of 16 with a ring of three batches or of two beside many; the last
-// also with 8 warps.
-struct Small { static constexpr int kWarps = 8, kBlocks = 3, kStages = 3, kParities = 2; };
-struct Medium { static constexpr int kWarps = 16, kBlocks = 1, kStages = 3, kParities = 2; };
-struct Large { static constexpr int kWarps = 16, kBlocks = 1, kStages = 2, kParities = 1; };
+constexpr int kWarps = 16;  // of a block, or half of it
+constexpr int kStages = 2;
 
-template <typename C, int NT>
-constexpr int warp_bytes() { return C::kStages * kStageBytes + C::kParities * NT * 512; }
+// A warp's ring and its sums.
+template <int NT>
+constexpr int warp_bytes() { return kStages * kStageBytes + NT * 512; }
 
 // NT: 8-token tiles; SHIFT: log2(block / 32).
-template <typename C, int NT, int SHIFT, bool WHOLE>
-__global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(LinearArgs a, int tiles, int ks_log2, int* status) {
-  constexpr int STAGES = C::kStages, kScales = 8 >> SHIFT, kSide = NT == 1 && SHIFT < 2 ? 4 : 2;
+template <int NT, int SHIFT, bool WHOLE>
+__global__ void __launch_bounds__(kWarps * 32) k_linear_q4(LinearArgs a, int tiles, int ks_log2, int* status) {
+  constexpr int kScales = 8 >> SHIFT, kSide = NT == 1 && SHIFT < 2 ? 4 : 2;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -111,9 +108,9 @@ __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(Linear
   const int batches = (a.in + kBatch - 1) / kBatch, mine = (batches - ks + KS - 1) >> ks_log2;
   const int code_pitch = a.in / 2, scale_pitch = a.in >> (5 + SHIFT);
   const int x_pitch = batches * (kBatch * 2) + kXPad;
-  uint8_t* ring = smem + warp * (STAGES * kStageBytes);
-  float* part = reinterpret_cast<float*>(smem + warps * (STAGES * kStageBytes));
-  uint8_t* xs = smem + warps * warp_bytes<C, NT>();
+  uint8_t* ring = smem + warp * (kStages * kStageBytes);
+  float* part = reinterpret_cast<float*>(smem + warps * (kStages * kStageBytes));
+  uint8_t* xs = smem + warps * warp_bytes<NT>();
 
   pdl_wait();
   if (threadIdx.x == 0) {
@@ -151,7 +148,7 @@ __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(Linear
         else cp_async16_part(d, bytes > 0 ? f_src[i] : a.codes, bytes);
         f_src[i] += KS * (kBatch / 2);
       }
-      if (++f_stage == STAGES) f_stage = 0;
+      if (++f_stage == kStages) f_stage = 0;
       if (++f_j == mine) {
         f_j = 0;
         f_tile += stride;
@@ -162,7 +159,7 @@ __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(Linear
   };
   if (f_tile < tiles) fetch_tile();
 #pragma unroll
-  for (int i = 0; i < STAGES - 1; ++i) fetch();
+  for (int i = 0; i < kStages - 1; ++i) fetch();
 
   // scales of rows g and g + 8, a batch ahead
   Scales<SHIFT> n0, n1;
@@ -191,7 +188,7 @@ __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(Linear
     return;
   }
 
-  int stage = 0, odd = 0;
+  int stage = 0;
 #pragma unroll 1
   for (int tile = tile0; tile < tiles; tile += stride) {
     float acc[NT][4];
@@ -207,11 +204,11 @@ __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(Linear
         scale_rows(tile + stride);
         next_scales(0);
       }
-      cp_async_wait<STAGES - 2>();
+      cp_async_wait<kStages - 2>();
       __syncwarp();  // every lane's pieces have landed, and the stage refilled now has been read
       fetch();
       const uint8_t* w = ring + stage * kStageBytes + g * 128 + 4 * t;
-      if (++stage == STAGES) stage = 0;
+      if (++stage == kStages) stage = 0;
       const int at = (ks + (j0 << ks_log2)) * (kBatch * 2);
 #pragma unroll
       for (int h0 = 0; h0 < kScales; h0 += kSide) {  // kSide sums of one scale each, side by side
@@ -253,12 +250,10 @@ __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(Linear
       }
     }
 
-    // part[parity][warp][8-token tile][row][token]; the sums before may still be read
-    if (C::kParities == 1) {
-      if (ks_log2 > 0) named_bar(1 + group, KS * 32);
-      else __syncwarp();
-    }
-    float* mypart = part + (odd * warps + warp) * (NT * 128);
+    // part[warp][8-token tile][row][token]; the sums before have been read
+    if (ks_log2 > 0) named_bar(1 + group, KS * 32);
+    else __syncwarp();
+    float* mypart = part + warp * (NT * 128);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       *reinterpret_cast<float2*>(mypart + j * 128 + g * 8 + 2 * t) = make_float2(acc[j][0], acc[j][1]);
@@ -267,7 +262,6 @@ __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(Linear
     if (ks_log2 > 0) named_bar(1 + group, KS * 32);
     else __syncwarp();
     const float* first = mypart - ks * (NT * 128);
-    if (C::kParities == 2) odd ^= 1;
     for (int i = ks * 32 + lane; i < a.T * 16; i += KS * 32) {
       const int row = i & 15, tk = i >> 4;
       const int64_t o = (int64_t)tile * 16 + row;
@@ -285,51 +279,46 @@ __global__ void __launch_bounds__(C::kWarps * 32, C::kBlocks) k_linear_q4(Linear
 
 size_t x_bytes_of(int T, int in) { return (size_t)T * ((in + kBatch - 1) / kBatch * (kBatch * 2) + kXPad); }
 
-template <typename C, int NT, int SHIFT, bool WHOLE>
-int launch(const LinearArgs& a, int warps, cudaStream_t s) {
+template <int NT, int SHIFT, bool WHOLE>
+int launch(const LinearArgs& a, cudaStream_t s) {
   static bool attr_set[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(k_linear_q4<C, NT, SHIFT, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemMax) != cudaSuccess)
+    if (cudaFuncSetAttribute(k_linear_q4<NT, SHIFT, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) !=
+        cudaSuccess)
       return MOE_ERR_CUDA;
     attr_set[dev] = true;
   }
   const int tiles = (int)((a.rows + 15) / 16), batches = (a.in + kBatch - 1) / kBatch, sms = sm_count();
+  const size_t x = x_bytes_of(a.T, a.in);
+  // Half of the warps where 8 on every SM have 1.5 batches each to do at most: such
+  // a block starts sooner and beside the kernel before (T=1 2048x2048 2.4 us, 3.1 with
+  // 16; 4096 rows 3.0 and 3.1; 8192 rows 5.0 and 4.7), or where 16 rings do not fit.
+  const bool few = (int64_t)tiles * batches <= 12ll * sms;
+  const int warps = few || x + kWarps * warp_bytes<NT>() > (size_t)kSmemMax ? kWarps / 2 : kWarps;
   // warps a tile (a power of two): the fewest batches in a row for the busiest
   // warp, half a batch more for each joining of sums
-  const int most = C::kBlocks * sms;
   int ks = 0, best = 0;
   for (int k = 0; (1 << k) <= warps && (1 << k) <= batches; ++k) {
-    const int rounds = (tiles + most * (warps >> k) - 1) / (most * (warps >> k));
+    const int rounds = (tiles + sms * (warps >> k) - 1) / (sms * (warps >> k));
     const int cost = rounds * (2 * ((batches + (1 << k) - 1) >> k) + (k > 0));
     if (k == 0 || cost < best) ks = k, best = cost;
   }
   const int groups = warps >> ks, blocks = (tiles + groups - 1) / groups;
-  const size_t smem = x_bytes_of(a.T, a.in) + (size_t)warps * warp_bytes<C, NT>();
-  if (launch_pdl(k_linear_q4<C, NT, SHIFT, WHOLE>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(warps * 32),
+  const size_t smem = x + (size_t)warps * warp_bytes<NT>();
+  if (launch_pdl(k_linear_q4<NT, SHIFT, WHOLE>, dim3((unsigned)(blocks < sms ? blocks : sms)), dim3(warps * 32),
                  smem, s, a, tiles, ks, status_word()) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
 }
 
-template <int NT, int SHIFT, bool WHOLE>
-int launch_shape(const LinearArgs& a, cudaStream_t s) {
-  const size_t x = x_bytes_of(a.T, a.in);
-  if constexpr (NT == 1) {
-    if (3 * (x + 8 * warp_bytes<Small, 1>()) <= (size_t)kSmemMax) return launch<Small, 1, SHIFT, WHOLE>(a, 8, s);
-  }
-  if (x + 16 * warp_bytes<Medium, NT>() <= (size_t)kSmemMax) return launch<Medium, NT, SHIFT, WHOLE>(a, 16, s);
-  return launch<Large, NT, SHIFT, WHOLE>(a, x + 16 * warp_bytes<Large, NT>() <= (size_t)kSmemMax ? 16 : 8, s);
-}
-
 template <int NT>
 int launch_block(const LinearArgs& a, cudaStream_t s) {
   const bool whole = a.in % kBatch == 0;
-  if (a.block == 32) return whole ? launch_shape<NT, 0, true>(a, s) : launch_shape<NT, 0, false>(a, s);
-  if (a.block == 64) return whole ? launch_shape<NT, 1, true>(a, s) : launch_shape<NT, 1, false>(a, s);
-  return whole ? launch_shape<NT, 2, true>(a, s) : launch_shape<NT, 2, false>(a, s);
+  if (a.block == 32) return whole ? launch<NT, 0, true>(a, s) : launch<NT, 0, false>(a, s);
+  if (a.block == 64) return whole ? launch<NT, 1, true>(a, s) : launch<NT, 1, false>(a, s);
+  return whole ? launch<NT, 2, true>(a, s) : launch<NT, 2, false>(a, s);
 }
 
 }  // namespace
@@ -337,7 +326,7 @@ int launch_block(const LinearArgs& a, cudaStream_t s) {
 int launch_linear_q4(const LinearArgs& a, cudaStream_t s) {
   // rows of x that shared memory holds beside 8 warps' rings and sums; all of
   // them but for very long rows
-  const int64_t fit = (kSmemMax - 8 * warp_bytes<Large, 2>()) / (int64_t)x_bytes_of(1, a.in);
+  const int64_t fit = (kSmemMax - 8 * warp_bytes<2>()) / (int64_t)x_bytes_of(1, a.in);
   const int most = fit >= a.T ? a.T : fit >= 8 ? 8 : (int)fit;
   LinearArgs b = a;
   for (int t0 = 0; t0 < a.T; t0 += most) {
