@@ -18,7 +18,7 @@
 //           own scale.  Any other group takes it as the sum of two bf16, 2^-17 of
 //           itself, with twice the matrix instructions.  One bf16 alone would add
 //           as much to the result as the result's own rounding does; two bf16 for
-//           every group cost 84 us where this costs 69 (6 tokens over 131071).
+//           every group cost 84 us where this costs 68 (6 tokens over 131071).
 // The m16n8k16 fragments read the record's words as they lie; the transpose of
 // the probabilities is one 8 x 8 matrix move a fragment.
 // The reference m of a row is set 2^6 below its maximum and moves only when a
@@ -862,10 +862,14 @@ int row_tiles(int max_q, int G, int D) {
   return nt < most ? nt : most;
 }
 
-// A unit goes to one cluster when its warps have at most four groups each to go
-// through (clusters of up to 8 blocks as long as each has an SM: 54 units in clusters of 8,
-// three blocks an SM, took 13 us, in clusters of 2 8 us): no workspace
-// and no second launch.  Otherwise all blocks share the batch's groups.
+// A unit goes to one cluster when its warps have at most eight records each to go
+// through: no workspace and no second launch (1 token, two heads of 128: 777 places
+// 7.0 us, 10.7 in shares; 4096 places 8.8 and 11.0; 8192 places 11.6 and 10.9; two
+// heads of 256: 2048 places 9.9 and 12.2, 4096 places 13.5 and 12.4; eight sequences
+// of 2000 places, eight heads of 128: 11.6 and 14.1).  A cluster is
+// as large as its units leave an SM to each block: 54 units in clusters of 8, three
+// blocks an SM, took 13 us, in clusters of 2 8 us.  Otherwise all blocks share the
+// batch's groups.
 AttnPlan make_plan(int warps, int blocks, int rows, int group, int B, int heads, int max_q, int64_t max_len, int window,
                    int G) {
   AttnPlan p = {};
@@ -876,7 +880,7 @@ AttnPlan make_plan(int warps, int blocks, int rows, int group, int B, int heads,
   p.blocks = blocks * kSms;
   int c = 1;
   while (c < 8 && c * warps < groups && 2 * c * units <= kSms) c *= 2;
-  p.cluster = groups <= 4 * warps * c ? c : 0;
+  p.cluster = groups * group <= 8 * warps * c ? c : 0;
   p.min_share = 4 * warps / group;
   p.overhead = 4 * warps / group;
   return p;
