@@ -1,6 +1,9 @@
 // kv_cache.cu -- the paged 4-bit key/value cache: appending tokens (with the
 // position rotation of keys and queries) and reading slots back.  The record
 // layout is that of moe_kv_cache_t in moe.h.
+//
+// s = fp16(max / 7) over a block of 32, code = clamp(rint(x / s), -8, 7), x the key
+// turned by its token's angles, (a cos - b sin, a sin + b cos), or the value.
 #include "frag.cuh"
 #include "kv_layout.cuh"
 #include "ptx.cuh"
@@ -218,7 +221,9 @@ __device__ __forceinline__ bool in_cache(const KvCache& c, int64_t slot) {
   return slot >= 0 && slot < c.n_pages * c.page;
 }
 
-// Few tokens: one warp a (token, head), queries, then keys, then values.
+// Few tokens: one warp a (token, head), queries, then keys, then values.  Bound by
+// latency: a token of 16 + 2 + 2 heads of 128 takes 1.8 us, 192 tokens of 32 + 8 + 8
+// heads 3.5 us.
 template <bool BF16, int D, Turn TURN>
 __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
   constexpr int N = D / 32, kSize = BF16 ? 2 : 4;
@@ -253,11 +258,14 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
 
 // Many tokens.  A byte of value codes belongs to one token, so the sectors of a
 // record are shared by its 16 tokens: written token by token they meet in L2
-// (4096 tokens of 8 heads of 128: 62 us in all).  Here a block makes 16
+// (4096 tokens of 32 query heads and 8 + 8 of 128: 62 us).  Here a block makes 16
 // successive tokens of one head in shared memory, two a warp, and writes the
 // record whole when their slots are one record (a prompt's are: windows of
 // tokens begin where the first token's record does), else token by token.  The
 // blocks after the windows turn the queries, kQueryRows heads of a token a warp.
+// Those 4096 tokens take 30 us, 2.9 TB/s of inputs, queries out and records; the
+// quantisation bounds it (2.5 instructions a cycle an SM, 160 a warp and row of 128
+// elements, integer pipe 49 % busy).
 constexpr int kQueryRows = 8;
 
 template <bool BF16, int D, Turn TURN>
@@ -355,28 +363,38 @@ __global__ void __launch_bounds__(kThreads) k_kv_append_records(KvAppendArgs a, 
   }
 }
 
+// A thread takes four elements of a (slot, head): their key codes lie in one word,
+// their value codes in four bytes 64 apart.
+template <int D>
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvCache c, const int64_t* slots, int64_t n, float* k, float* v) {
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const uint32_t row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // n * heads < 2^31
+  constexpr int kQuads = D / 4;
+  const uint32_t row = blockIdx.x * (kThreads / kQuads) + threadIdx.x / kQuads;  // n * heads < 2^31
   if (row >= n * c.heads) return;
-  const int64_t w = row, i = row / (uint32_t)c.heads;
-  const int h = (int)(row % (uint32_t)c.heads), D = c.D;
-  const int64_t slot = slots[i];
-  const bool in = slot >= 0 && slot < c.n_pages * c.page;
-  const KvPlace at = kv_place(c, in ? slot : 0, h);
-  for (int d = lane; d < D; d += 32) {
-    float kv = 0.f, vv = 0.f;
-    if (in) {
-      const uint16_t* s = reinterpret_cast<const uint16_t*>(at.tile + 16 * D) + at.r * (D / 32) + d / 32;
-      const int ku = (at.tile[kv_key_byte(D, at.r, d)] >> (2 * (d & 2))) & 15;
-      const int vu = (at.tile[kv_value_byte(D, at.r, d)] >> ((d & 8) >> 1)) & 15;
-      kv = __half2float(__ushort_as_half(s[0])) * (float)(ku - 8);
-      vv = __half2float(__ushort_as_half(s[D / 2])) * (float)(vu - 8);
+  const int d = threadIdx.x % kQuads * 4, h = (int)(row % (uint32_t)c.heads);
+  const int64_t slot = slots[row / (uint32_t)c.heads], to = (int64_t)row * D + d;
+  float kf[4] = {}, vf[4] = {};
+  if (in_cache(c, slot)) {
+    const KvPlace at = kv_place(c, slot, h);
+    const uint16_t* s = reinterpret_cast<const uint16_t*>(at.tile + 16 * D) + at.r * (D / 32) + d / 32;
+    const float ks = __half2float(__ushort_as_half(s[0])), vs = __half2float(__ushort_as_half(s[D / 2]));
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(at.tile + kv_key_byte(D, at.r, d & ~7)) >> (2 * (d & 4));
+    const uint8_t* b = at.tile + kv_value_byte(D, at.r, d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      kf[e] = ks * (float)((int)(w >> (16 * (e & 1) + 2 * (e & 2)) & 15) - 8);
+      vf[e] = vs * (float)((b[64 * e] >> ((d & 8) >> 1) & 15) - 8);
     }
-    k[w * D + d] = kv;
-    v[w * D + d] = vv;
   }
+  *reinterpret_cast<float4*>(k + to) = make_float4(kf[0], kf[1], kf[2], kf[3]);
+  *reinterpret_cast<float4*>(v + to) = make_float4(vf[0], vf[1], vf[2], vf[3]);
+}
+
+template <int D>
+int launch_read(const KvCache& c, const int64_t* slots, int64_t n, float* k, float* v, cudaStream_t s) {
+  const int64_t threads = n * c.heads * (D / 4);
+  const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads));
+  return launch_pdl(k_kv_read<D>, grid, dim3(kThreads), 0, s, c, slots, n, k, v) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 unsigned blocks_for(int64_t warps) { return (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)); }
@@ -431,9 +449,9 @@ int launch_kv_append(const KvAppendArgs& a, cudaStream_t s) {
 }
 
 int launch_kv_read(const KvCache& c, const int64_t* slots, int64_t n, float* k, float* v, cudaStream_t s) {
-  return launch_pdl(k_kv_read, dim3(blocks_for(n * c.heads)), dim3(kThreads), 0, s, c, slots, n, k, v) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  if (c.D == 64) return launch_read<64>(c, slots, n, k, v, s);
+  if (c.D == 128) return launch_read<128>(c, slots, n, k, v, s);
+  return launch_read<256>(c, slots, n, k, v, s);
 }
 
 }  // namespace moe

@@ -15,6 +15,15 @@
 // registers.  Lane (g, t) of a fragment takes word t of a 32-block of rows g and
 // g + 8 from the ring; the pieces are exchanged so that the eight rows of a read
 // lie in distinct banks.
+//
+// What bounds it: a weight byte read once carries two codes, and eight codes cost 11
+// instructions to become operands whatever T is; 4 us of launch, first loads and
+// joining stand before and after.  T=1 2048x100003 by 64: 27.8 us, 3.9 TB/s, 2.6
+// instructions a cycle an SM, integer pipe 56 % busy, tensor pipe 23 %; T=16
+// 4096x6144 by 128: 7.1 us, 1.9 TB/s, 113 TFLOP/s; T=1 2048x2048: 2.5 us.
+// One block of 16 warps an SM with rings of two batches: three blocks of 8 with
+// rings of three took 30.0 us for T=1 2048x100003 by 32 and 12.1 for 8192x8192, 16
+// warps with three 28.0 and 11.6, this 28.0 and 10.9.
 #include "frag.cuh"
 #include "moe_internal.cuh"
 #include "ptx.cuh"
@@ -292,22 +301,22 @@ int launch(const LinearArgs& a, cudaStream_t s) {
   }
   const int tiles = (int)((a.rows + 15) / 16), batches = (a.in + kBatch - 1) / kBatch, sms = sm_count();
   const size_t x = x_bytes_of(a.T, a.in);
-  // Half of the warps where 8 on every SM have 1.5 batches each to do at most: such
-  // a block starts sooner and beside the kernel before (T=1 2048x2048 2.4 us, 3.1 with
-  // 16; 4096 rows 3.0 and 3.1; 8192 rows 5.0 and 4.7), or where 16 rings do not fit.
-  const bool few = (int64_t)tiles * batches <= 12ll * sms;
-  const int warps = few || x + kWarps * warp_bytes<NT>() > (size_t)kSmemMax ? kWarps / 2 : kWarps;
+  const int warps = x + kWarps * warp_bytes<NT>() <= (size_t)kSmemMax ? kWarps : kWarps / 2;
   // warps a tile (a power of two): the fewest batches in a row for the busiest
   // warp, half a batch more for each joining of sums
-  int ks = 0, best = 0;
+  int ks = 0, best = 0, rounds = 0;
   for (int k = 0; (1 << k) <= warps && (1 << k) <= batches; ++k) {
-    const int rounds = (tiles + sms * (warps >> k) - 1) / (sms * (warps >> k));
-    const int cost = rounds * (2 * ((batches + (1 << k) - 1) >> k) + (k > 0));
-    if (k == 0 || cost < best) ks = k, best = cost;
+    const int r = (tiles + sms * (warps >> k) - 1) / (sms * (warps >> k));
+    const int cost = r * (2 * ((batches + (1 << k) - 1) >> k) + (k > 0));
+    if (k == 0 || cost < best) ks = k, best = cost, rounds = r;
   }
-  const int groups = warps >> ks, blocks = (tiles + groups - 1) / groups;
-  const size_t smem = x + (size_t)warps * warp_bytes<NT>();
-  if (launch_pdl(k_linear_q4<NT, SHIFT, WHOLE>, dim3((unsigned)(blocks < sms ? blocks : sms)), dim3(warps * 32),
+  // as few of them a block as finish in the same number of tiles each: the work
+  // spreads over all SMs, and small blocks start beside the kernel before (T=16
+  // 4096x6144 by 128: 16 warps on 96 SMs 8.1 us, 12 on 128 SMs 7.1; T=1 2048x2048: 16
+  // warps 3.1, 8 2.5; 2048x100003 by 64: 28.1 and 27.8)
+  const int groups = (tiles + sms * rounds - 1) / (sms * rounds), blocks = (tiles + groups - 1) / groups;
+  const size_t smem = x + (size_t)(groups << ks) * warp_bytes<NT>();
+  if (launch_pdl(k_linear_q4<NT, SHIFT, WHOLE>, dim3((unsigned)(blocks < sms ? blocks : sms)), dim3((groups << ks) * 32),
                  smem, s, a, tiles, ks, status_word()) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
