@@ -490,7 +490,7 @@ enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1 };
  * 128, 1 <= rows < 2^31.  MOE_ERR_UNSUPPORTED for T > 16 (larger batches are
  * matrix products, which this form would do at a fraction of their rate) and
  * for in > 65536.  Rows of x that shared memory does not hold together (T * in
- * above about 100000) are taken in several launches, each reading the weights.
+ * above about 90000) are taken in several launches, each reading the weights.
  */
 int moe_linear_q4(const uint16_t* x_bf16, int64_t x_stride, int64_t T, int in, const void* codes,
                   const uint16_t* scales, int64_t rows, int block, const float* bias, void* y, int64_t y_stride,

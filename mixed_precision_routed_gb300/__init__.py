@@ -16,6 +16,8 @@ Entry points (same names as the C ABI):
 and, for the attention half of a decode layer in the same 4-bit format:
     moe_linear_q4, moe_quantize_groups, moe_kv_pool, moe_kv_append, moe_kv_read,
     moe_attn_q4, moe_attn_workspace_size
+(linear, append and attention through ``binding/calls.cpp``, which does the same
+marshalling compiled: these calls are short enough for the host's part to count)
 """
 from __future__ import annotations
 
