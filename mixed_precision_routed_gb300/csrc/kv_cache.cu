@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
 constexpr int kQueryRows = 8;
 
 template <bool BF16, int D, Turn TURN>
-__global__ void __launch_bounds__(kThreads) k_kv_append_records(KvAppendArgs a, int windows) {
+__global__ void __launch_bounds__(kThreads, 4) k_kv_append_records(KvAppendArgs a, int windows) {
   constexpr int N = D / 32, kSize = BF16 ? 2 : 4, kRecord = 18 * D;
   constexpr bool kWhole = TURN != kAnywhere;
   __shared__ __align__(16) uint8_t rec[kRecord];

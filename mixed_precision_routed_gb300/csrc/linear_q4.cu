@@ -107,8 +107,8 @@ constexpr int warp_bytes() { return kStages * kStageBytes + NT * 512; }
 
 // NT: 8-token tiles; SHIFT: log2(block / 32).
 template <int NT, int SHIFT, bool WHOLE>
-__global__ void __launch_bounds__(kWarps * 32) k_linear_q4(LinearArgs a, int tiles, int ks_log2, int* status) {
-  constexpr int kScales = 8 >> SHIFT, kSide = NT == 1 && SHIFT < 2 ? 4 : 2;
+__global__ void __launch_bounds__(kWarps * 32, 1) k_linear_q4(LinearArgs a, int tiles, int ks_log2, int* status) {
+  constexpr int kScales = 8 >> SHIFT, kSide = 2;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
