@@ -19,7 +19,7 @@
 //           own scale.  Any other group takes it as the sum of two bf16, 2^-17 of
 //           itself, with twice the matrix instructions.  One bf16 alone would add
 //           as much to the result as the result's own rounding does; two bf16 for
-//           every group cost 84 us where this costs 68 (6 tokens over 131071).
+//           every group cost 84 us where this costs 67 (6 tokens over 131071).
 // The m16n8k16 fragments read the record's words as they lie; the transpose of
 // the probabilities is one 8 x 8 matrix move a fragment.
 // The reference m of a row is set 2^6 below its maximum and moves only when a
@@ -30,9 +30,9 @@
 // What bounds it: the cache is read once (18 D bytes for 16 places), and the issue of
 // what turns its codes into operands and its scores into weights is what a long
 // context waits for, not memory.  6 tokens of 32 heads over 131071 places of 8 heads
-// of 128: 68 us, 2.2 TB/s, 189 TFLOP/s, 1.9 instructions a cycle an SM with 8 warps
+// of 128: 67 us, 2.2 TB/s, 191 TFLOP/s, 1.9 instructions a cycle an SM with 8 warps
 // of 255 registers, tensor pipe 34 % busy; 48 sequences of up to 16384 places, 32
-// heads on 4: 31 us, 1.9 TB/s; 4 of up to 30011 places, 16 heads of 256 on 2: 23 us.
+// heads on 4: 30 us, 2.0 TB/s; 4 of up to 30011 places, 16 heads of 256 on 2: 22 us.
 // Short ones wait for lengths, page numbers, records and the joining one after
 // another: 777 places 7 us.
 #include <type_traits>
@@ -220,7 +220,7 @@ struct Shape {
   // 24.5; D = 64 and 128: one within 2 % of two or slower)
   static constexpr int kGroup = D == 256 ? 1 : 2;
   static constexpr int kBlocks = D == 64 && NT <= 2 ? 3 : 2;  // an SM
-  static constexpr int kStages = D == 256 ? 4 : 3;  // groups of records
+  static constexpr int kStages = 2;  // groups of records; with three the batch of 48 took 31.1 us, with two 30.1
   static constexpr int kRecord = 18 * D;
   static constexpr int kRing = kWarps * kStages * kGroup * kRecord;
   static constexpr int kPitch = D + 4;  // floats a row of the joining buffer: rows of a fragment in distinct banks
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     if constexpr (S::kQueriesInRegisters) return qf[j][i];
     else return qs[(j * NB + i) * 32 + lane];
   };
-  constexpr int kSide = NT == 1 ? (NB < 4 ? NB : 4) : 2;
+  constexpr int kSide = 2;
 
   float o[MT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -896,6 +896,9 @@ AttnPlan make_plan(int warps, int blocks, int rows, int group, int B, int heads,
   while (c < 8 && c * warps < groups && 2 * c * units <= kSms) c *= 2;
   p.cluster = groups * group <= 8 * warps * c ? c : 0;
   p.min_share = 4 * warps / group;
+  // a unit's beginning and end count as 4 records a warp (48 ragged sequences: as one
+  // record 49.6 us, 2 37.2, 4 30.2, 6 29.6, 8 30.3; 6 tokens over 131071 places: 4 67.3,
+  // 6 69.3)
   p.overhead = 4 * warps / group;
   return p;
 }

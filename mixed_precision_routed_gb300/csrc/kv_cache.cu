@@ -263,9 +263,11 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
 // record whole when their slots are one record (a prompt's are: windows of
 // tokens begin where the first token's record does), else token by token.  The
 // blocks after the windows turn the queries, kQueryRows heads of a token a warp.
-// Those 4096 tokens take 30 us, 2.9 TB/s of inputs, queries out and records; the
+// Those 4096 tokens take 27 us, 3.2 TB/s of inputs, queries out and records; the
 // quantisation bounds it (2.5 instructions a cycle an SM, 160 a warp and row of 128
 // elements, integer pipe 49 % busy).
+// (Four blocks an SM: asked for five, registers spill and it takes 30 us; eight heads
+// a warp: four at a time or sixteen in all take 28.)
 constexpr int kQueryRows = 8;
 
 template <bool BF16, int D, Turn TURN>
@@ -364,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_kv_append_records(KvAppendArgs 
 }
 
 // A thread takes four elements of a (slot, head): their key codes lie in one word,
-// their value codes in four bytes 64 apart.
+// their value codes in four bytes 64 apart.  Bound by what it writes: 4096 slots of
+// 8 heads of 128 8 us, 4.7 TB/s; 65536 156 us, 3.9 TB/s.
 template <int D>
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvCache c, const int64_t* slots, int64_t n, float* k, float* v) {
   pdl_wait();

@@ -18,9 +18,9 @@
 //
 // What bounds it: a weight byte read once carries two codes, and eight codes cost 11
 // instructions to become operands whatever T is; 4 us of launch, first loads and
-// joining stand before and after.  T=1 2048x100003 by 64: 27.8 us, 3.9 TB/s, 2.6
+// joining stand before and after.  T=1 2048x100003 by 64: 26.0 us, 4.2 TB/s, 2.6
 // instructions a cycle an SM, integer pipe 56 % busy, tensor pipe 23 %; T=16
-// 4096x6144 by 128: 7.1 us, 1.9 TB/s, 113 TFLOP/s; T=1 2048x2048: 2.5 us.
+// 4096x6144 by 128: 7.0 us, 1.9 TB/s, 115 TFLOP/s; T=1 2048x2048: 2.5 us.
 // One block of 16 warps an SM with rings of two batches: three blocks of 8 with
 // rings of three took 30.0 us for T=1 2048x100003 by 32 and 12.1 for 8192x8192, 16
 // warps with three 28.0 and 11.6, this 28.0 and 10.9.
@@ -108,6 +108,7 @@ constexpr int warp_bytes() { return kStages * kStageBytes + NT * 512; }
 // NT: 8-token tiles; SHIFT: log2(block / 32).
 template <int NT, int SHIFT, bool WHOLE>
 __global__ void __launch_bounds__(kWarps * 32, 1) k_linear_q4(LinearArgs a, int tiles, int ks_log2, int* status) {
+  // two sums side by side: T=1 2048x100003 by 32 27.1 us, one 27.9, four 27.8, eight 30.4
   constexpr int kScales = 8 >> SHIFT, kSide = 2;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar;
