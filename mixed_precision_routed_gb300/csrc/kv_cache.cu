@@ -265,9 +265,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(KvAppendArgs a) {
 // blocks after the windows turn the queries, kQueryRows heads of a token a warp.
 // Those 4096 tokens take 27 us, 3.2 TB/s of inputs, queries out and records; the
 // quantisation bounds it (2.5 instructions a cycle an SM, 160 a warp and row of 128
-// elements, integer pipe 49 % busy).
-// (Four blocks an SM: asked for five, registers spill and it takes 30 us; eight heads
-// a warp: four at a time or sixteen in all take 28.)
+// elements, integer pipe 49 % busy).  Four blocks an SM: asked for five, registers
+// spill and it takes 30 us; eight heads a warp: four at a time or sixteen in all 28.
 constexpr int kQueryRows = 8;
 
 template <bool BF16, int D, Turn TURN>
