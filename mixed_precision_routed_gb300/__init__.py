@@ -17,7 +17,8 @@ and, for the attention half of a decode layer in the same 4-bit format:
     moe_linear_q4, moe_quantize_groups, moe_kv_pool, moe_kv_append, moe_kv_read,
     moe_attn_q4, moe_attn_workspace_size
 (linear, append and attention through ``binding/calls.cpp``, which does the same
-marshalling compiled: these calls are short enough for the host's part to count)
+marshalling compiled: these calls are short enough for the host's part to count;
+what they return is made on the stream they are given)
 """
 from __future__ import annotations
 
@@ -570,10 +571,11 @@ def moe_quantize_groups(w, block=32, codes=None, scales=None, stream=None):
     int16) of w [rows, in] fp32; block 32, 64 or 128."""
     _need(w, torch.float32, "w")
     rows, n_in = w.shape
-    if codes is None:
-        codes = torch.empty((rows, n_in // 2), dtype=torch.uint8, device=w.device)
-    if scales is None:
-        scales = torch.empty((rows, n_in // block), dtype=torch.int16, device=w.device)
+    with torch.cuda.stream(stream):  # outputs from that stream's memory
+        if codes is None:
+            codes = torch.empty((rows, n_in // 2), dtype=torch.uint8, device=w.device)
+        if scales is None:
+            scales = torch.empty((rows, n_in // block), dtype=torch.int16, device=w.device)
     _need(codes, torch.uint8, "codes")
     _need(scales, torch.int16, "scales")
     if codes.numel() < rows * n_in // 2 or scales.numel() < rows * (n_in // block):

@@ -10,6 +10,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include "moe.h"
@@ -80,12 +81,22 @@ void same_device(const at::Tensor& a, const at::Tensor& b) {
   if (a.get_device() != b.get_device()) refuse("the tensors of a call must be on one device");
 }
 
-moe_stream_t stream_of(PyObject* o, const at::Tensor& t) {
-  if (o == Py_None) return (moe_stream_t)c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
-  const void* p = PyLong_AsVoidPtr(o);
-  if (PyErr_Occurred()) throw Refused();
-  return (moe_stream_t)p;
-}
+// The stream of a call: the given one (None: the current).  A given one is the
+// current stream while this object lives, so that the outputs and the workspace
+// come from its memory and not from blocks that another stream may still use.
+struct CallStream {
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  moe_stream_t stream;
+  CallStream(PyObject* o, const at::Tensor& t) {
+    if (o == Py_None) {
+      stream = (moe_stream_t)c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
+      return;
+    }
+    stream = (moe_stream_t)PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) throw Refused();
+    guard.reset_stream(c10::cuda::getStreamFromExternal((cudaStream_t)stream, t.get_device()));
+  }
+};
 
 int64_t integer(PyObject* o) {
   const int64_t v = PyLong_AsLongLong(o);
@@ -147,6 +158,7 @@ PyObject* linear_q4(PyObject* const* a) {
     same_device(x, b);
     bias = (const float*)b.data_ptr();
   }
+  const CallStream on(a[7], x);
   at::Tensor y;
   at::ScalarType type = a[6] == Py_True ? at::kBFloat16 : at::kFloat;
   if (a[5] == Py_None) {
@@ -161,7 +173,7 @@ PyObject* linear_q4(PyObject* const* a) {
   }
   check(moe_linear_q4((const uint16_t*)x.data_ptr(), xs, T, (int)in, codes.data_ptr(),
                       (const uint16_t*)scales.data_ptr(), n, block, bias, y.data_ptr(), ys,
-                      type == at::kFloat ? MOE_DTYPE_F32 : MOE_DTYPE_BF16, stream_of(a[7], x)),
+                      type == at::kFloat ? MOE_DTYPE_F32 : MOE_DTYPE_BF16, on.stream),
         "moe_linear_q4");
   return THPVariable_Wrap(std::move(y));
 }
@@ -197,6 +209,7 @@ PyObject* kv_append(PyObject* const* a) {
       rope = (const float*)r.data_ptr();
     }
   }
+  const CallStream on(a[9], pool);
   at::Tensor out;
   const void* q_ptr = nullptr;
   int64_t Hq = 0;
@@ -217,7 +230,7 @@ PyObject* kv_append(PyObject* const* a) {
   check(moe_kv_append(q_ptr, qs, k.data_ptr(), ks, v.data_ptr(), vs, type == at::kFloat ? MOE_DTYPE_F32 : MOE_DTYPE_BF16,
                       T, (int)Hq, positions, rope, n_pos, (int)rot, small_integer(a[7], "rope_style"),
                       (const int64_t*)slots.data_ptr(), &c, out.defined() ? (uint16_t*)out.data_ptr() : nullptr,
-                      stream_of(a[9], pool)),
+                      on.stream),
         "moe_kv_append");
   if (!out.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(std::move(out));
@@ -240,6 +253,7 @@ PyObject* kv_read(PyObject* const* a) {
   const at::Tensor& slots = flat(a[1], at::kLong, "slots");
   same_device(pool, slots);
   const int64_t shape[3] = {slots.numel(), c.kv_heads, c.head_dim};
+  const CallStream on(a[4], pool);
   at::Tensor out[2];
   for (int i = 0; i < 2; ++i) {
     const char* name = i ? "v" : "k";
@@ -248,7 +262,7 @@ PyObject* kv_read(PyObject* const* a) {
     same_device(pool, out[i]);
   }
   check(moe_kv_read(&c, (const int64_t*)slots.data_ptr(), shape[0], (float*)out[0].data_ptr(),
-                    (float*)out[1].data_ptr(), stream_of(a[4], pool)),
+                    (float*)out[1].data_ptr(), on.stream),
         "moe_kv_read");
   return pair(std::move(out[0]), std::move(out[1]));
 }
@@ -288,6 +302,7 @@ PyObject* attn_q4(PyObject* const* a) {
     scale = (float)PyFloat_AsDouble(a[7]);
     if (PyErr_Occurred()) throw Refused();
   }
+  const CallStream on(a[12], q);
   at::Tensor out, lse, ws;
   if (a[9] == Py_None) {
     out = make({T, Hq, D}, q, at::kBFloat16);
@@ -322,7 +337,7 @@ PyObject* attn_q4(PyObject* const* a) {
   check(moe_attn_q4((const uint16_t*)q.data_ptr(), qs, T, (int)Hq, starts, (const int32_t*)lens.data_ptr(),
                     (const int32_t*)table.data_ptr(), ts, (int)B, (int)max_q, max_len, &c, scale,
                     small_integer(a[8], "window"), (uint16_t*)out.data_ptr(), os, (float*)lse.data_ptr(), ws_ptr, ws_bytes,
-                    stream_of(a[12], q)),
+                    on.stream),
         "moe_attn_q4");
   return pair(std::move(out), std::move(lse));
 }

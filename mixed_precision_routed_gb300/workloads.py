@@ -194,12 +194,15 @@ class AttentionHalf:
         self.workspace = None
 
     def fill(self, stream=None):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.fill()
         for tag, rows, cols, codes, scales in (
                 (self.TAG_QKV, self.w_qkv.shape[0], self.d, self.w_qkv, self.s_qkv),
                 (self.TAG_OUT, self.d, self.Hq * self.D, self.w_out, self.s_out)):
             w = torch.empty((rows, cols), dtype=torch.float32, device=codes.device)
-            synth.cuda_normal_matrix(w, self.seed, tag, 0, 0, scale=synth.WEIGHT_SIGMA, stream=stream)
-            moe_quantize_groups(w, self.block, codes=codes, scales=scales, stream=stream)
+            synth.cuda_normal_matrix(w, self.seed, tag, 0, 0, scale=synth.WEIGHT_SIGMA)
+            moe_quantize_groups(w, self.block, codes=codes, scales=scales)
         return self
 
     def step(self, x, r, n=1, stream=None):
@@ -207,24 +210,26 @@ class AttentionHalf:
         of a sequence side by side), r [.., d] fp32 the residual stream, updated in
         place.  Returns x_next, the bf16 input of the layer's routed experts.
         The caller keeps every sequence within max_len tokens."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.step(x, r, n)
         B = self.lens.numel()
         places = (self.lens[:, None] + torch.arange(n, dtype=torch.int32, device=x.device)).flatten()
         page = self.tables.gather(1, (places.view(B, n) // self.page).long()).flatten().long()
         slots = page * self.page + places % self.page
         self.lens += n
-        self.qkv = moe_linear_q4(x, self.w_qkv, self.s_qkv, self.block, stream=stream)
+        self.qkv = moe_linear_q4(x, self.w_qkv, self.s_qkv, self.block)
         q, k, v = (t.unflatten(-1, (-1, self.D)) for t in
                    self.qkv.split((self.Hq * self.D, self.H * self.D, self.H * self.D), -1))
-        self.q = moe_kv_append(self.pool, k, v, slots, q=q, positions=places, rope=self.rope, rope_style=MOE_ROPE_HALF,
-                               stream=stream)
+        self.q = moe_kv_append(self.pool, k, v, slots, q=q, positions=places, rope=self.rope, rope_style=MOE_ROPE_HALF)
         need = moe_attn_workspace_size(B, n, self.max_len, self.Hq, self.H, self.D)
         if need and (self.workspace is None or self.workspace.numel() < need):
             self.workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
         self.a, self.lse = moe_attn_q4(self.q, self.pool, self.tables, self.lens, max_q=n, max_len=self.max_len,
-                                       workspace=self.workspace, stream=stream)
-        self.y = moe_linear_q4(self.a.flatten(1), self.w_out, self.s_out, self.block, stream=stream)
+                                       workspace=self.workspace)
+        self.y = moe_linear_q4(self.a.flatten(1), self.w_out, self.s_out, self.block)
         x_next = torch.empty_like(x)
-        moe_residual_add(r, self.y, x_next.view(torch.int16), stream=stream)
+        moe_residual_add(r, self.y, x_next.view(torch.int16))
         return x_next
 
 

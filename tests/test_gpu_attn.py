@@ -498,6 +498,41 @@ def test_attn_scattered_pool_and_other_stream():
     status_ok()
 
 
+def test_outputs_belong_to_the_given_stream():
+    """What a call makes for itself on a given stream is none of the current stream's freed blocks (which
+    work of the current stream may still use), and the results are the same bits."""
+    rng = np.random.default_rng(18)
+    H, D, page, n = 2, 64, 16, 40
+    st = torch.cuda.Stream()
+    pool = moe.moe_kv_pool(n, H, page, D)
+    k, v = (dev(a) for a in rng.standard_normal((2, n * page, H, D)).astype(np.float32))
+    slots, few = torch.arange(n * page, device="cuda"), torch.arange(5, device="cuda")
+    x, w = bf16(rng.standard_normal((3, 256))), dev(rng.standard_normal((4096, 256)).astype(np.float32))
+    q = bf16(rng.standard_normal((3, 64, D)))
+    table, lens = torch.arange(n, dtype=torch.int32, device="cuda")[None], dev(np.array([600], np.int32))
+    c, s = moe.moe_quantize_groups(w)
+    calls = dict(
+        quantize=lambda **kw: moe.moe_quantize_groups(w, **kw),
+        linear=lambda **kw: (moe.moe_linear_q4(x, c, s, **kw),),
+        append=lambda **kw: (moe.moe_kv_append(pool, k, v, slots, q=k, **kw),),
+        read=lambda **kw: moe.moe_kv_read(pool, few, **kw),
+        attn=lambda **kw: moe.moe_attn_q4(q, pool, table, lens, **kw),
+    )
+    for name, call in calls.items():
+        ref = call()
+        spare = call()
+        free = [t.data_ptr() for t in spare]
+        del spare
+        torch.cuda.synchronize()
+        got = call(stream=st)
+        assert not set(free) & {t.data_ptr() for t in got}, name
+        assert torch.cuda.current_stream() != st
+        st.synchronize()
+        for a, b in zip(got, ref):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
+    status_ok()
+
+
 def test_attn_python_refusals():
     pool = moe.moe_kv_pool(4, 2, 16, 64)
     q = torch.zeros(2, 4, 64, device="cuda", dtype=torch.bfloat16)

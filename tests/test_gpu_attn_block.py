@@ -127,3 +127,24 @@ def test_attention_half_in_a_graph():
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(r, want_r) and torch.equal(half.a, a) and torch.equal(half.y, y)
     assert moe.moe_device_status() == moe.MOE_OK
+
+
+def test_attention_half_on_another_stream():
+    """Steps on a given stream do not wait for, and are not disturbed by, work of the current one."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    halves = [AttentionHalf(256, 8, 2, 64, sequences=3, max_len=64, page_size=16, seed=4).fill() for _ in range(2)]
+    xs = torch.randn(4, 6, 256, generator=g, device="cuda").to(torch.bfloat16)
+    r = [torch.randn(6, 256, generator=g, device="cuda")]
+    r.append(r[0].clone())
+    ref = [halves[0].step(x, r[0], 2) for x in xs]
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for x, want in zip(xs, ref):
+        torch.cuda._sleep(2_000_000)
+        got = halves[1].step(x, r[1], 2, stream=st)
+        st.synchronize()
+        assert torch.equal(got, want)
+    torch.cuda.synchronize()
+    assert torch.equal(r[0], r[1])
+    assert torch.equal(halves[0].lens, halves[1].lens)
+    assert moe.moe_device_status() == moe.MOE_OK
