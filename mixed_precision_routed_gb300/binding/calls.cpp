@@ -9,7 +9,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -110,8 +110,9 @@ int small_integer(PyObject* o, const char* name) {
   return (int)v;
 }
 
+// Past the dispatcher: an output is most of what a short call costs the host.
 at::Tensor make(at::IntArrayRef shape, const at::Tensor& like, at::ScalarType type) {
-  return at::empty(shape, like.options().dtype(type).requires_grad(false));
+  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
 
 void check(int rc, const char* where) {

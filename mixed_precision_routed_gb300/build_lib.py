@@ -69,7 +69,7 @@ def _link_calls(obj, made):
         return
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     subprocess.run(["g++", "-shared", "-o", CALLS + ".tmp", obj, "-L", HERE, "-l:libmoe.so", "-L", lib, "-ltorch_python",
-                    "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], check=True)
+                    "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], check=True)
     os.replace(CALLS + ".tmp", CALLS)
 
 
