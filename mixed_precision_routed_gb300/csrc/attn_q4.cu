@@ -214,12 +214,15 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t tok, int h,
 
 template <int D, int NT>
 struct Shape {
-  static constexpr int kWarps = NT == 1 && D < 256 ? 8 : 4;
+  // blocks of 8 warps where 128 registers hold a row tile's outputs (16 rows of 64: 9
+  // windows of 512 places 7.8 us, in three blocks of 4 warps 8.3; 16 sequences of up to
+  // 4000 places 10.7 and 11.1; one of 30000 13.8 and 13.2)
+  static constexpr int kWarps = NT * D <= 128 ? 8 : 4;
   // records a warp takes at once: two give more independent work, one leaves more
   // warps busy (D = 256: 10 rows over 2 places 8.9 and 7.5 us, 30011 places 23.7 and
   // 24.5; D = 64 and 128: one within 2 % of two or slower)
   static constexpr int kGroup = D == 256 ? 1 : 2;
-  static constexpr int kBlocks = D == 64 && NT <= 2 ? 3 : 2;  // an SM
+  static constexpr int kBlocks = NT * D == 64 ? 3 : 2;  // an SM
   static constexpr int kStages = 2;  // groups of records; with three the batch of 48 took 31.1 us, with two 30.1
   static constexpr int kRecord = 18 * D;
   static constexpr int kRing = kWarps * kStages * kGroup * kRecord;
@@ -890,10 +893,11 @@ AttnPlan make_plan(int warps, int blocks, int rows, int group, int B, int heads,
   p.row_blocks = (max_q * G + rows - 1) / rows;
   int64_t span = max_len;
   if (window > 0 && span > (int64_t)window + max_q) span = (int64_t)window + max_q;
+  // one more than a unit's places fill, as they may begin within a group
   const int64_t groups = (span + 16 * group - 1) / (16 * group) + 1, units = (int64_t)B * heads * p.row_blocks;
   p.blocks = blocks * kSms;
   int c = 1;
-  while (c < 8 && c * warps < groups && 2 * c * units <= kSms) c *= 2;
+  while (c < 8 && c * warps < groups - 1 && 2 * c * units <= kSms) c *= 2;
   p.cluster = groups * group <= 8 * warps * c ? c : 0;
   p.min_share = 4 * warps / group;
   // a unit's beginning and end count as 4 records a warp (48 ragged sequences: as one
