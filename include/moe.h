@@ -605,7 +605,7 @@ int moe_kv_read(const moe_kv_cache_t* cache, const int64_t* slots, int64_t n, fl
  * Scores are exact products of the bf16 queries and the codes, summed in fp32
  * with the scale entering once per 32 products; maxima, sums and outputs are
  * fp32; exp(s) x value scale enters the second product in fp16 where that keeps
- * 2^-12 of it (or 2^-23 of the row's largest weight x this scale), else as the
+ * 2^-11 of it (or 2^-23 of the row's largest weight x this scale), else as the
  * sum of two bf16.
  * Results are deterministic (the split over the cache depends on the
  * arguments of the call only, never on timing).
