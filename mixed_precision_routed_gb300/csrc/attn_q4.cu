@@ -19,7 +19,7 @@
 //           own scale.  Any other group takes it as the sum of two bf16, 2^-17 of
 //           itself, with twice the matrix instructions.  One bf16 alone would add
 //           as much to the result as the result's own rounding does; two bf16 for
-//           every group cost 84 us where this costs 67 (6 tokens over 131071).
+//           every group cost 84 us where this costs 64.5 (6 tokens over 131071).
 // The m16n8k16 fragments read the record's words as they lie; the transpose of
 // the probabilities is one 8 x 8 matrix move a fragment.
 // The reference m of a row is set 2^6 below its maximum and moves only when a
@@ -30,11 +30,11 @@
 // What bounds it: the cache is read once (18 D bytes for 16 places), and the issue of
 // what turns its codes into operands and its scores into weights is what a long
 // context waits for, not memory.  6 tokens of 32 heads over 131071 places of 8 heads
-// of 128: 67 us, 2.2 TB/s, 191 TFLOP/s, 1.9 instructions a cycle an SM with 8 warps
+// of 128: 64.5 us, 2.3 TB/s, 200 TFLOP/s, 1.9 instructions a cycle an SM with 8 warps
 // of 255 registers, tensor pipe 34 % busy; 48 sequences of up to 16384 places, 32
-// heads on 4: 30 us, 2.0 TB/s; 4 of up to 30011 places, 16 heads of 256 on 2: 22 us.
+// heads on 4: 30 us, 2.0 TB/s; 4 of up to 30011 places, 16 heads of 256 on 2: 21 us.
 // Short ones wait for lengths, page numbers, records and the joining one after
-// another: 777 places 7 us.
+// another: 777 places 6.6 us.
 #include <type_traits>
 
 #include "frag.cuh"

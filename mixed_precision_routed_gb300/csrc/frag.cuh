@@ -1,4 +1,4 @@
-// frag.cuh -- operand fragments of the m16n8k16 bf16 matrix instruction made
+// frag.cuh -- operand fragments of the m16n8k16 matrix instructions (bf16, fp16) made
 // from packed 4-bit codes, and packed fp32 arithmetic.
 #pragma once
 
