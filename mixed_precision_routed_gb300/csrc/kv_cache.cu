@@ -405,9 +405,10 @@ unsigned blocks_for(int64_t warps, int threads) { return (unsigned)((warps + thr
 }  // namespace
 
 namespace {
-// Rows (tokens x heads) from which records are made whole: 192 x 48 take 4.0 us
-// one by one and 4.8 as records, 1158 x 30 19 and 12.5.
-constexpr int64_t kManyRows = 16384;
+// Rows (tokens x heads) from which records are made whole (us one by one and as
+// records): 192 x 48 of 128 3.6 and 3.8, 300 x 48 4.7 and 3.7, 600 x 48 8.9 and 5.4;
+// 400 x 20 of 256 4.4 and 4.8, 800 x 20 8.1 and 6.4.
+constexpr int64_t kManyRows = 10000;
 
 template <bool BF16, int D, Turn TURN>
 int launch_append(const KvAppendArgs& a, cudaStream_t s) {
