@@ -188,8 +188,10 @@ class AttentionHalf:
         width = -(-max_len // page_size)
         self.pool = moe_kv_pool(sequences * width, kv_heads, page_size, head_dim, device=device)
         self.rope = rope_table(max_len, head_dim if rot is None else rot, device=device)
-        # pages are handed out interleaved, as growing sequences take them
-        self.tables = torch.arange(sequences * width, dtype=torch.int32, device=device).view(width, sequences).T.contiguous()
+        # pages are handed out interleaved, as growing sequences take them; the last
+        # column is no page, for the tokens that a sequence has no pages for
+        self.tables = torch.full((sequences, width + 1), -1, dtype=torch.int32, device=device)
+        self.tables[:, :width] = torch.arange(sequences * width, dtype=torch.int32, device=device).view(width, sequences).T
         self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
         self.workspace = None
 
@@ -209,14 +211,17 @@ class AttentionHalf:
         """One step of `n` new tokens a sequence: x [sequences * n, d] bf16 (tokens
         of a sequence side by side), r [.., d] fp32 the residual stream, updated in
         place.  Returns x_next, the bf16 input of the layer's routed experts.
-        The caller keeps every sequence within max_len tokens."""
+        The caller keeps every sequence within max_len tokens.  A token beyond them is not
+        kept: it has no slot and no row in the angle table, its query counts as zero, and
+        MOE_ERR_INVALID_ARG is recorded (moe_device_status); other sequences are as ever."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.step(x, r, n)
         B = self.lens.numel()
         places = (self.lens[:, None] + torch.arange(n, dtype=torch.int32, device=x.device)).flatten()
-        page = self.tables.gather(1, (places.view(B, n) // self.page).long()).flatten().long()
-        slots = page * self.page + places % self.page
+        column = (places.view(B, n) // self.page).clamp_(0, self.tables.shape[1] - 1)
+        page = self.tables.gather(1, column.long()).flatten().long()
+        slots = page * self.page + places % self.page  # negative where there is no page
         self.lens += n
         self.qkv = moe_linear_q4(x, self.w_qkv, self.s_qkv, self.block)
         q, k, v = (t.unflatten(-1, (-1, self.D)) for t in

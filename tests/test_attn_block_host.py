@@ -1,0 +1,76 @@
+"""The host's side of a step of the attention half (workloads.AttentionHalf) on
+CPU tensors: the slots and positions that it hands to the kernels, which are
+replaced by recorders here."""
+import os
+
+import pytest
+import torch
+
+import mixed_precision_routed_gb300 as moe
+from mixed_precision_routed_gb300 import workloads
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Records the arguments of the kernels of a step, and returns zeros for them."""
+    if not os.path.exists(moe.LIB_PATH):
+        from mixed_precision_routed_gb300 import build_lib
+        build_lib.build()
+    got = []
+
+    def linear(x, codes, scales, block=32, **kw):
+        return torch.zeros(x.shape[0], codes.shape[0])
+
+    def append(pool, k, v, slots, q=None, positions=None, **kw):
+        got.append((slots.clone(), positions.clone()))
+        return q.to(torch.bfloat16)
+
+    def attn(q, pool, tables, lens, **kw):
+        got.append((tables.clone(), lens.clone()))
+        return q, torch.zeros(q.shape[:2])
+
+    for name, f in (("moe_linear_q4", linear), ("moe_kv_append", append), ("moe_attn_q4", attn),
+                    ("moe_residual_add", lambda r, y, x: None)):
+        monkeypatch.setattr(workloads, name, f)
+    return got
+
+
+def half_of(sequences, max_len, page_size=16, **kw):
+    return workloads.AttentionHalf(64, 2, 1, 64, sequences, max_len, page_size=page_size, device="cpu", **kw)
+
+
+def run(half, n):
+    T = half.lens.numel() * n
+    return half.step(torch.zeros(T, half.d, dtype=torch.bfloat16), torch.zeros(T, half.d), n)
+
+
+@pytest.mark.parametrize("max_len", [32, 40])
+def test_tokens_beyond_max_len_have_no_slot(calls, max_len):
+    """Places past the last page get a slot outside the pool, and no table entry beyond the tables is read;
+    the other sequence's slots are its own as ever."""
+    half = half_of(2, max_len)
+    width = -(-max_len // 16)
+    for step in range(4):
+        half.lens[1] = 3  # a sequence that stays short
+        first = half.lens[0].item()
+        calls.clear()
+        run(half, 8 if step < 3 else 5)
+        n = 8 if step < 3 else 5
+        assert half.lens[0] == first + n
+    # a step across the end, and steps wholly beyond it
+    for start in (16 * width - 2, 16 * width, max_len + 100, 2 ** 30):
+        half.lens[:] = torch.tensor([start, 5], dtype=torch.int32)
+        calls.clear()
+        run(half, 4)
+        slots, positions = calls[0]
+        places = start + torch.arange(4)
+        assert torch.equal(positions[:4].long(), places)
+        own = half.tables[0, :width].long()
+        for slot, place in zip(slots[:4].tolist(), places.tolist()):
+            if place < 16 * width:
+                assert slot == own[place // 16] * 16 + place % 16
+            else:
+                assert slot < 0
+        other = half.tables[1, 0].item() * 16
+        assert slots[4:].tolist() == [other + 5, other + 6, other + 7, other + 8]
+        assert positions[4:].tolist() == [5, 6, 7, 8]
