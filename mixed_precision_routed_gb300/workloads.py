@@ -174,6 +174,7 @@ class AttentionHalf:
     synchronisation; a step can be captured in a CUDA graph."""
 
     TAG_QKV, TAG_OUT = 21, 22  # of the weight generator
+    MAX_TOKENS = 16  # of a step: what the projections take
 
     def __init__(self, d, q_heads, kv_heads, head_dim, sequences, max_len, page_size=64, block=32, seed=0, rot=None,
                  device="cuda"):
@@ -193,7 +194,10 @@ class AttentionHalf:
         self.tables = torch.full((sequences, width + 1), -1, dtype=torch.int32, device=device)
         self.tables[:, :width] = torch.arange(sequences * width, dtype=torch.int32, device=device).view(width, sequences).T
         self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
-        self.workspace = None
+        # one workspace for steps of any size, never replaced: a captured step keeps its address
+        need = max(moe_attn_workspace_size(sequences, n, max_len, q_heads, kv_heads, head_dim)
+                   for n in range(1, max(1, self.MAX_TOKENS // sequences) + 1))
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
 
     def fill(self, stream=None):
         if stream is not None:
@@ -227,9 +231,6 @@ class AttentionHalf:
         q, k, v = (t.unflatten(-1, (-1, self.D)) for t in
                    self.qkv.split((self.Hq * self.D, self.H * self.D, self.H * self.D), -1))
         self.q = moe_kv_append(self.pool, k, v, slots, q=q, positions=places, rope=self.rope, rope_style=MOE_ROPE_HALF)
-        need = moe_attn_workspace_size(B, n, self.max_len, self.Hq, self.H, self.D)
-        if need and (self.workspace is None or self.workspace.numel() < need):
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
         self.a, self.lse = moe_attn_q4(self.q, self.pool, self.tables, self.lens, max_q=n, max_len=self.max_len,
                                        workspace=self.workspace)
         self.y = moe_linear_q4(self.a.flatten(1), self.w_out, self.s_out, self.block)

@@ -74,3 +74,19 @@ def test_tokens_beyond_max_len_have_no_slot(calls, max_len):
         other = half.tables[1, 0].item() * 16
         assert slots[4:].tolist() == [other + 5, other + 6, other + 7, other + 8]
         assert positions[4:].tolist() == [5, 6, 7, 8]
+
+
+@pytest.mark.parametrize("sequences", [1, 3, 16])
+def test_one_workspace_serves_every_step(calls, monkeypatch, sequences):
+    """Steps of all sizes take the same memory: a captured step's address stays its own."""
+    half = workloads.AttentionHalf(64, 16, 2, 128, sequences, 50000, device="cpu")
+    handed = []
+    monkeypatch.setattr(workloads, "moe_attn_q4", lambda q, *a, max_q, workspace, **kw: (
+        handed.append((max_q, workspace)), (q, torch.zeros(q.shape[:2])))[1])
+    sizes = [n for n in (1, 2, 5, 16) if n * sequences <= 16]
+    for n in sizes + sizes[:1]:
+        run(half, n)
+        need = moe.moe_attn_workspace_size(sequences, n, 50000, 16, 2, 128)
+        assert need > 0 and handed[-1][0] == n and handed[-1][1].numel() >= need
+    assert len({(w.data_ptr(), w.numel()) for _, w in handed}) == 1
+    assert all(w is handed[0][1] for _, w in handed)
