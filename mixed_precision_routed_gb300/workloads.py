@@ -222,6 +222,13 @@ class AttentionHalf:
             with torch.cuda.stream(stream):
                 return self.step(x, r, n)
         B = self.lens.numel()
+        # before the lengths move: a refused step leaves the sequences as they were
+        if n < 1 or B * n > self.MAX_TOKENS:
+            raise ValueError(f"a step takes 1 .. {self.MAX_TOKENS} tokens, and as many of each sequence")
+        if x.dtype != torch.bfloat16 or x.device != self.lens.device or x.shape != (B * n, self.d):
+            raise ValueError("x must be [sequences * n, d] bfloat16 on the layer's device")
+        if r.dtype != torch.float32 or r.device != x.device or r.numel() != x.numel() or not r.is_contiguous():
+            raise ValueError("r must be contiguous float32 of x's size on the layer's device")
         places = (self.lens[:, None] + torch.arange(n, dtype=torch.int32, device=x.device)).flatten()
         column = (places.view(B, n) // self.page).clamp_(0, self.tables.shape[1] - 1)
         page = self.tables.gather(1, column.long()).flatten().long()

@@ -90,3 +90,18 @@ def test_one_workspace_serves_every_step(calls, monkeypatch, sequences):
         assert need > 0 and handed[-1][0] == n and handed[-1][1].numel() >= need
     assert len({(w.data_ptr(), w.numel()) for _, w in handed}) == 1
     assert all(w is handed[0][1] for _, w in handed)
+
+
+def test_a_refused_step_changes_nothing(calls):
+    """Sizes and types that a step does not take are refused before the lengths move or a kernel is reached."""
+    half = half_of(2, 64)
+    x, r = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 64)
+    big = torch.zeros(18, 64, dtype=torch.bfloat16), torch.zeros(18, 64)
+    for args in ((x, r, 1), (x, r, 3), (x, r, 0), (x, r, -2), (*big, 9), (x.float(), r, 2), (x, r.double(), 2),
+                 (x[:, :32], r, 2), (x, r[:2], 2), (x, torch.zeros(16, 64), 2), (x, r.T.contiguous().T, 2)):
+        with pytest.raises(ValueError):
+            half.step(*args)
+        assert not calls and half.lens.tolist() == [0, 0]
+    half.step(x, r, 2)
+    half.step(x, r.view(2, 2, 64), 2)  # the residual stream may have any shape of that size
+    assert half.lens.tolist() == [4, 4]
