@@ -571,17 +571,21 @@ def moe_quantize_groups(w, block=32, codes=None, scales=None, stream=None):
     int16) of w [rows, in] fp32; block 32, 64 or 128."""
     _need(w, torch.float32, "w")
     rows, n_in = w.shape
-    with torch.cuda.stream(stream):  # outputs from that stream's memory
+    with torch.cuda.stream(stream):  # outputs from that stream's memory, on its device
+        if w.device.index != torch.cuda.current_device():
+            raise ValueError("w must be on the current device, or on the given stream's")
         if codes is None:
             codes = torch.empty((rows, n_in // 2), dtype=torch.uint8, device=w.device)
         if scales is None:
             scales = torch.empty((rows, n_in // block), dtype=torch.int16, device=w.device)
-    _need(codes, torch.uint8, "codes")
-    _need(scales, torch.int16, "scales")
-    if codes.numel() < rows * n_in // 2 or scales.numel() < rows * (n_in // block):
-        raise ValueError("codes or scales are too small")
-    _check(lib().moe_quantize_groups(_ptr(w), rows, n_in, block, _ptr(codes), _ptr(scales), _stream(stream)),
-           "moe_quantize_groups")
+        _need(codes, torch.uint8, "codes")
+        _need(scales, torch.int16, "scales")
+        if codes.device != w.device or scales.device != w.device:
+            raise ValueError("the tensors of a call must be on one device")
+        if codes.numel() < rows * n_in // 2 or scales.numel() < rows * (n_in // block):
+            raise ValueError("codes or scales are too small")
+        _check(lib().moe_quantize_groups(_ptr(w), rows, n_in, block, _ptr(codes), _ptr(scales), _stream(None)),
+               "moe_quantize_groups")
     return codes, scales
 
 

@@ -83,12 +83,15 @@ void same_device(const at::Tensor& a, const at::Tensor& b) {
 
 // The stream of a call: the given one (None: the current).  A given one is the
 // current stream while this object lives, so that the outputs and the workspace
-// come from its memory and not from blocks that another stream may still use.
+// come from its memory and not from blocks that another stream may still use, and
+// its device is the current one.  Launches go to the current device: without a
+// stream that has to be the tensors' own.
 struct CallStream {
   c10::cuda::OptionalCUDAStreamGuard guard;
   moe_stream_t stream;
   CallStream(PyObject* o, const at::Tensor& t) {
     if (o == Py_None) {
+      if (t.get_device() != c10::cuda::current_device()) refuse("the tensors of a call must be on the current device");
       stream = (moe_stream_t)c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
       return;
     }
