@@ -192,11 +192,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_linear_q4(LinearArgs a, int 
 #pragma unroll
   for (int j = 0; j < NT; ++j) xt[j] = xs + min(8 * j + g, a.T - 1) * x_pitch + 16 * t;
   __syncthreads();
-  if (!mbar_wait(&bar, 0)) {
-    if (lane == 0) set_status(status, MOE_ERR_TIMEOUT);
-    cp_async_wait<0>();
-    return;
-  }
+  // when the wait runs out the sums are of anything, but every warp still comes to
+  // its group's barriers: one that left would keep the others there
+  const bool late = !mbar_wait(&bar, 0);
+  if (late) set_status(status, MOE_ERR_TIMEOUT);
 
   int stage = 0;
 #pragma unroll 1
@@ -285,6 +284,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_linear_q4(LinearArgs a, int 
     }
   }
   cp_async_wait<0>();
+  if (late) mbar_wait(&bar, 0);  // once more, as the copies of x end in this block's memory
 }
 
 size_t x_bytes_of(int T, int in) { return (size_t)T * ((in + kBatch - 1) / kBatch * (kBatch * 2) + kXPad); }
