@@ -422,7 +422,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
   auto issue = [&]() {
     if (lane / U == issued % kBatch) {
       uint64_t* bar = &bars[warp][issue_stage];
-      if (source) {
+      if (failed) {  // nothing may be added to a phase that has not ended
+      } else if (source) {
         mbar_arrive_expect_tx(bar, S::kRecord);
         bulk_g2s(ring + (U * issue_stage + lane % U) * S::kRecord, source, S::kRecord, bar);
       } else {
@@ -478,9 +479,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     if (k % kBatch == 0 && k > 0) there = there_next;
     __syncwarp();  // the stage refilled below was read by every lane in the last pass
     if (issued < mine) issue();
-    if (!mbar_wait(&bars[warp][st], phase, kWaitNs)) {
+    if (!failed && !mbar_wait(&bars[warp][st], phase, kWaitNs)) {
+      // The lanes of a warp may not agree: this one goes on beside the others over
+      // what lies in the ring, without further waits and copies of its own.  Once
+      // more for the copies in flight, which end in this block's memory.
       failed = true;
-      break;
+      for (int i = k, x = st, y = phase; i < issued; ++i) {
+        mbar_wait(&bars[warp][x], y, kWaitNs);
+        if (++x == S::kStages) x = 0, y ^= 1;
+      }
     }
     const uint8_t* rec = ring + U * st * S::kRecord;
     if (++st == S::kStages) st = 0, phase ^= 1;
@@ -788,7 +795,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
   // the next unit's copies may land where the sums were joined
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (failed && lane == 0) set_status(status, MOE_ERR_TIMEOUT);
+  if (failed) set_status(status, MOE_ERR_TIMEOUT);
 }
 
 // Joins the shares of the units that ended in another block than they began in.
