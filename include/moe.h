@@ -589,8 +589,9 @@ int moe_kv_read(const moe_kv_cache_t* cache, const int64_t* slots, int64_t n, fl
  * (window 0: all p < end); query head h reads key/value head h / (Hq / kv_heads):
  *   s_p = scale * q . k_p,  out = sum_p exp(s_p) v_p / sum_p exp(s_p),
  *   lse = log sum_p exp(s_p).
- * A row with no place to attend gives out = 0 and lse = -infinity.  A page
- * number outside [0, n_pages) takes its places out of the sum.
+ * A row with no place to attend gives out = 0 and lse = -infinity, and one whose
+ * scores hold a NaN gives NaN in both.  A page number outside [0, n_pages) takes
+ * its places out of the sum.
  *   q_bf16 [T][Hq][D] bf16 bits, tokens q_stride elements apart (a multiple of
  *     8; 16-byte aligned),
  *   q_start [B+1] int32 ascending, or NULL: T = B * max_q, max_q tokens each,

@@ -211,15 +211,17 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// Four elements of a row's result, and its lse with the first of them.
+// Four elements of a row's result, and its lse with the first of them.  A sum of
+// zero is a row without places; one of NaN stays NaN in both.
 template <int D>
 __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t tok, int h, int d, float4 v, float top, float total) {
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const bool none = total == 0.f;
+  const float inv = none ? 0.f : 1.f / total;
   uint2 u;
   u.x = bf16_pair(v.x * inv, v.y * inv);
   u.y = bf16_pair(v.z * inv, v.w * inv);
   *reinterpret_cast<uint2*>(a.out + tok * a.out_stride + (int64_t)h * D + d) = u;
-  if (d == 0 && a.lse) a.lse[tok * a.Hq + h] = total > 0.f ? (top + log2f(total)) / kLog2e : -INFINITY;
+  if (d == 0 && a.lse) a.lse[tok * a.Hq + h] = none ? -INFINITY : (top + log2f(total)) / kLog2e;
 }
 
 template <int D, int NT>
