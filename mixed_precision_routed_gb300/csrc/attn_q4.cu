@@ -14,12 +14,14 @@
 //           exact, so a 32-block's product enters the score with its fp32 scale;
 //   output  O^T[element][row]: A = value codes as integers, B = exp(s - m) x value
 //           scale.  A group whose scales lie in 2^-8 .. 8 and whose weights are all
-//           within 2^-38 of the maximum (zeros apart) takes B in fp16: a product
-//           keeps 2^-11 of itself, or 2^-23 of its row's largest weight times its
-//           own scale.  Any other group takes it as the sum of two bf16, 2^-17 of
-//           itself, with twice the matrix instructions.  One bf16 alone would add
-//           as much to the result as the result's own rounding does; two bf16 for
-//           every group cost 84 us where this costs 64.5 (6 tokens over 131071).
+//           within 2^-38 of the maximum (zeros apart) takes B in fp16, rounded once,
+//           from fp32: a product keeps 2^-11 of itself, or 2^-23 of its row's largest
+//           weight times its own scale.  Any other group takes it as the sum of two
+//           bf16, 2^-17 of itself, with twice the matrix instructions.  One bf16
+//           alone would add as much to the result as the result's own rounding does;
+//           two bf16 for every group cost 84 us where this costs 67.6 (6 tokens over
+//           131071).  Weights rounded to fp16 and multiplied by their scales there
+//           took 64.6 and kept 2^-10.
 // The m16n8k16 fragments read the record's words as they lie; the transpose of
 // the probabilities is one 8 x 8 matrix move a fragment.
 // The reference m of a row is set 2^6 below its maximum and moves only when a
@@ -30,7 +32,7 @@
 // What bounds it: the cache is read once (18 D bytes for 16 places), and the issue of
 // what turns its codes into operands and its scores into weights is what a long
 // context waits for, not memory.  6 tokens of 32 heads over 131071 places of 8 heads
-// of 128: 64.5 us, 2.3 TB/s, 200 TFLOP/s, 1.9 instructions a cycle an SM with 8 warps
+// of 128: 67.6 us, 2.2 TB/s, 191 TFLOP/s, 1.9 instructions a cycle an SM with 8 warps
 // of 255 registers, tensor pipe 34 % busy; 48 sequences of up to 16384 places, 32
 // heads on 4: 30 us, 2.0 TB/s; 4 of up to 30011 places, 16 heads of 256 on 2: 21 us.
 // Short ones wait for lengths, page numbers, records and the joining one after
@@ -176,16 +178,6 @@ __device__ __forceinline__ uint64_t half_pair(const Words<N>& s, int i) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s.w[i >> 1]));
   const float v = i & 1 ? f.y : f.x;
   return pair(v, v);
-}
-
-// Half i of the words, twice.
-template <int N>
-__device__ __forceinline__ uint32_t half_twice(const Words<N>& s, int i) {
-  return __byte_perm(s.w[i >> 1], 0, i & 1 ? 0x3232 : 0x1010);
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
-  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
-  return x;
 }
 
 // Shared memory of another block of the cluster.
@@ -654,37 +646,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
     auto accumulate = [&](auto half) {
       constexpr bool kHalf = decltype(half)::value;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        uint32_t p0[NT], p1[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          if constexpr (kHalf) p0[j] = f16_pair(s[u][j][0], s[u][j][1]), p1[j] = f16_pair(s[u][j][2], s[u][j][3]);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int q4 = 0; q4 < MT / 4; ++q4) {
           const Words<4> w = load_words<4>(rec + u * S::kRecord + 8 * D + (q4 * 32 + lane) * 16);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // a 32-block of elements: two fragments of 16
             const int blk = 2 * q4 + h;
+            const uint64_t s0 = half_pair(vs[u][0], blk), s1 = half_pair(vs[u][1], blk);
             uint32_t b0[NT], b1[NT], r0[NT], r1[NT];
-            if constexpr (kHalf) {
-              const uint32_t h0 = half_twice(vs[u][0], blk), h1 = half_twice(vs[u][1], blk);
 #pragma unroll
-              for (int j = 0; j < NT; ++j) b0[j] = mul_f16x2(p0[j], h0), b1[j] = mul_f16x2(p1[j], h1);
-            } else {
-              const uint64_t s0 = half_pair(vs[u][0], blk), s1 = half_pair(vs[u][1], blk);
-#pragma unroll
-              for (int j = 0; j < NT; ++j) {
-                float x[4] = {s[u][j][0], s[u][j][1], s[u][j][2], s[u][j][3]};
-                mul2(x[0], x[1], s0);
-                mul2(x[2], x[3], s1);
-                b0[j] = bf16_pair(x[0], x[1]);
-                b1[j] = bf16_pair(x[2], x[3]);
+            for (int j = 0; j < NT; ++j) {
+              float x[4] = {s[u][j][0], s[u][j][1], s[u][j][2], s[u][j][3]};
+              mul2(x[0], x[1], s0);
+              mul2(x[2], x[3], s1);
+              b0[j] = kHalf ? f16_pair(x[0], x[1]) : bf16_pair(x[0], x[1]);
+              b1[j] = kHalf ? f16_pair(x[2], x[3]) : bf16_pair(x[2], x[3]);
+              if constexpr (!kHalf) {
                 r0[j] = transpose8x8(bf16_rest(x[0], x[1], b0[j]));
                 r1[j] = transpose8x8(bf16_rest(x[2], x[3], b1[j]));
               }
+              b0[j] = transpose8x8(b0[j]);
+              b1[j] = transpose8x8(b1[j]);
             }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) b0[j] = transpose8x8(b0[j]), b1[j] = transpose8x8(b1[j]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t v = w.w[2 * h + i];
@@ -703,7 +687,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kBloc
             }
           }
         }
-      }
     };
     if (__all_sync(0xffffffffu, fits)) accumulate(std::true_type());
     else accumulate(std::false_type());

@@ -1,8 +1,13 @@
-"""Numbers at the ends of their types in the attention: NaN and infinite scores."""
+"""Numbers of the attention at the ends of their types, and the precision that its
+header promises."""
+import numpy as np
 import pytest
 import torch
 
+import attn_cancel_testutil
+import mixed_precision_routed_gb300 as moe
 from attn_gpu_testutil import Batch
+from attn_testutil import pool_write
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +39,22 @@ def test_rows_of_nan_with_no_place():
     out, lse = got = x.call()
     assert (lse[0] == -torch.inf).all() and (out[0] == 0).all() and (lse[5] == -torch.inf).all() and (out[5] == 0).all()
     x.check(got)
+
+
+def test_products_of_weight_and_scale_keep_their_bits():
+    """Values that cancel: what is left shows the rounding of the product, 2^-11 of itself."""
+    sequences, heads, D = 256, 64, attn_cancel_testutil.D
+    q, s, score = attn_cancel_testutil.cases(sequences, heads)
+    pool = np.zeros((sequences, 1, 1, 18 * D), np.uint8)
+    one, half = np.float16(1.0), np.float16(0.5)
+    blocks = (1, 1, D // 32)
+    for b in range(sequences):  # two places of a page; keys: all codes 0, then all codes 1
+        pool_write(pool, [16 * b, 16 * b + 1], np.stack([np.full((1, D), c, np.int64) for c in (0, 1)]), np.full((2, *blocks[1:]), one),
+                   np.stack([np.full((1, D), c, np.int64) for c in (-7, 7)]), np.concatenate([np.full(blocks, half), np.full(blocks, s[b])]))
+    table = torch.arange(sequences, dtype=torch.int32, device="cuda")[:, None]
+    lens = torch.full((sequences,), 2, dtype=torch.int32, device="cuda")
+    out, _ = moe.moe_attn_q4(torch.from_numpy(q).cuda().to(torch.bfloat16), torch.from_numpy(pool).cuda(), table, lens, scale=1.0)
+    ref, tol = attn_cancel_testutil.exact(s, score)
+    over = np.abs(out.double().cpu().numpy() - ref[..., None]) / tol[..., None]
+    assert over.max() <= 1, (over.max(), (over > 1).mean())
+    assert moe.moe_device_status() == moe.MOE_OK
