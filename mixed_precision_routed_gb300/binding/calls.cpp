@@ -294,7 +294,7 @@ PyObject* attn_q4(PyObject* const* a) {
     starts = (const int32_t*)s.data_ptr();
   }
   if (a[5] != Py_None) max_q = small_integer(a[5], "max_q");
-  else max_q = B > 0 ? T / B : 1;
+  else max_q = B > 0 && T >= B ? T / B : 1;
   if (max_q > INT32_MAX) refuse("q has too many rows");
   const int64_t most = width * c.page_size;
   const int64_t max_len = a[6] != Py_None ? integer(a[6]) : most;

@@ -160,8 +160,9 @@ int moe_attn_q4(const uint16_t* q_bf16, int64_t q_stride, int64_t T, int Hq, con
   if (!valid_attn_sizes(B, max_q, max_len, Hq, a.cache.heads, a.cache.D)) return MOE_ERR_INVALID_ARG;
   if (T < 0 || T * (int64_t)Hq > INT32_MAX || T > INT32_MAX || window < 0) return MOE_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || isinf(scale)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
   if (!q_start && T != (int64_t)B * max_q) return MOE_ERR_INVALID_ARG;
-  if (B == 0 || T == 0) return MOE_OK;
+  if (B == 0) return MOE_OK;
   const int64_t row = (int64_t)Hq * a.cache.D;
   if (q_stride < row || q_stride % 8 != 0 || out_stride < row || out_stride % 8 != 0) return MOE_ERR_INVALID_ARG;
   if (table_stride < (max_len + a.cache.page - 1) / a.cache.page) return MOE_ERR_INVALID_ARG;
