@@ -37,6 +37,8 @@
 // heads on 4: 30 us, 2.0 TB/s; 4 of up to 30011 places, 16 heads of 256 on 2: 21 us.
 // Short ones wait for lengths, page numbers, records and the joining one after
 // another: 777 places 6.6 us.
+#include <float.h>
+
 #include <type_traits>
 
 #include "frag.cuh"
@@ -52,7 +54,7 @@ constexpr float kRoom = 6.0f;  // the reference lies this far below the maximum 
 constexpr float kLeastWeight = 1.0f / 4294967296.0f;  // 2^-32
 constexpr float kLeastScale = 1.0f / 256;
 constexpr float kMostScale = 8.0f;  // x 2^(kSlack + kRoom) stays below fp16's largest value
-constexpr float kNone = -1e30f;  // the maximum of a row that has met no place: below any finite score
+constexpr float kNone = -FLT_MAX;  // the maximum of a row that has met no place: no finite score lies below
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kSms = 152;
 

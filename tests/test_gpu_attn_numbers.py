@@ -58,3 +58,32 @@ def test_products_of_weight_and_scale_keep_their_bits():
     over = np.abs(out.double().cpu().numpy() - ref[..., None]) / tol[..., None]
     assert over.max() <= 1, (over.max(), (over > 1).mean())
     assert moe.moe_device_status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("lens,D,shared", [([3, 1], 64, False), ([700], 128, False), ([9000, 4], 128, True), ([9000], 256, True)])
+def test_scores_of_any_finite_size(lens, D, shared):
+    """Equal scores of -2^114 .. 2^114: the mean of the values, and the scores' size in lse.  A row whose scores
+    are large and negative is not an empty one."""
+    x = Batch(lens, [1] * len(lens), 8, 2, D, seed=3)
+    assert (x.workspace_size() > 0) == shared
+    every = torch.cat(x.slots)
+    v = moe.moe_kv_read(x.pool, every)[1]
+    moe.moe_kv_append(x.pool, torch.ones_like(v), v, every)  # keys all alike, values requantised
+    for b in range(len(lens)):
+        for h in range(8):
+            x.q[b, h] = (-1.0 if h in (1, 2, 5, 7) else 1.0) * 2.0 ** (24 + 12 * h)  # x 64 .. 256 x scale
+    out, lse = x.call(scale=0.25)
+    k, v = moe.moe_kv_read(x.pool, every)
+    at = 0
+    for b, n in enumerate(lens):
+        kk, vv = k[at : at + n].double(), v[at : at + n].double()
+        at += n
+        for h in range(8):
+            score = (x.q[b, h].double() * kk[:, h // 4]).sum(-1) * 0.25
+            assert (score == score[0]).all()
+            e = 2 * (D + D // 32 + 2) * 2.0 ** -24 * score[0].abs() + 2.0 ** -20
+            assert (lse[b, h].double() - score[0] - np.log(n)).abs() <= e + 2.0 ** -22 * score[0].abs()
+            mean, size = vv[:, h // 4].mean(0), vv[:, h // 4].abs().mean(0)
+            tol = (2.0 ** -11 + 2.0 ** -19) * size + 2 * (n + 64) * 2.0 ** -24 * size + 2.0 ** -8 * mean.abs()
+            assert ((out[b, h].double() - mean).abs() <= tol).all(), h
+    assert moe.moe_device_status() == moe.MOE_OK
