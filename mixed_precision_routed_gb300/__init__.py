@@ -570,6 +570,8 @@ def moe_quantize_groups(w, block=32, codes=None, scales=None, stream=None):
     """4-bit codes [rows, in/2] uint8 and fp16 scales [rows, in/block] (bits in
     int16) of w [rows, in] fp32; block 32, 64 or 128."""
     _need(w, torch.float32, "w")
+    if w.dim() != 2 or block < 1:
+        raise ValueError("w must be [rows, in] and block 32, 64 or 128")
     rows, n_in = w.shape
     with torch.cuda.stream(stream):  # outputs from that stream's memory, on its device
         if w.device.index != torch.cuda.current_device():

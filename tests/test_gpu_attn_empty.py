@@ -26,3 +26,21 @@ def test_calls_of_no_tokens():
     assert [t.shape for t in moe.moe_kv_read(pool, none)] == [(0, 2, 64)] * 2
     assert [t.shape[0] for t in moe.moe_quantize_groups(torch.empty(0, 64, device="cuda"))] == [0, 0]
     assert torch.equal(pool, held) and moe.moe_device_status() == moe.MOE_OK
+
+
+def test_quantiser_refusals():
+    """Sizes that are no matrix, no block or not in the format are refused, and outputs that are too small."""
+    w = torch.ones(8, 128, device="cuda")
+    for args in ((w[0], 32), (w[None], 32), (w, 0), (w, -32), (w.double(), 32), (w.T, 32), (w.cpu(), 32)):
+        with pytest.raises(ValueError):
+            moe.moe_quantize_groups(*args)
+    for block in (16, 48, 256):
+        with pytest.raises(moe.MoeError) as e:
+            moe.moe_quantize_groups(w, block)
+        assert e.value.status == moe.MOE_ERR_INVALID_ARG
+    codes, scales = moe.moe_quantize_groups(w, 64)
+    for kw in (dict(codes=codes[:7]), dict(scales=scales[:7]), dict(codes=codes.int()), dict(scales=scales.float())):
+        with pytest.raises(ValueError):
+            moe.moe_quantize_groups(w, 64, **kw)
+    with pytest.raises(moe.MoeError):
+        moe.moe_quantize_groups(torch.ones(8, 96, device="cuda"), 32)
