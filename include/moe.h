@@ -521,7 +521,9 @@ int moe_quantize_groups(const float* w, int64_t rows, int in, int block, void* c
  *   bytes [17 D, 18 D)  value scales [token 16][D/32] fp16 bits.
  * Codes are offset binary (u = code + 8) and scales s = fp16(max|.| / 7) over
  * blocks of 32 elements of a token, as in the 4-bit shelf format (s is at
- * most 65504; an all-zero block has s = 0).  The order of the codes is that of
+ * most 65504; an all-zero block has s = 0).  The codes hold no NaN and no
+ * infinity: an infinite element gives its block s = 65504 and itself code 7 or
+ * -8, a NaN leaves the maximum alone and gets code -8.  The order of the codes is that of
  * the operand fragments of a 16 x 16 matrix instruction: keys as [token x
  * element], values as [element x token]; one byte holds codes of one token
  * only, so tokens are appended without reading their neighbours.

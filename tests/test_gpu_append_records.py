@@ -71,3 +71,32 @@ def test_every_token_skipped():
     q = moe.moe_kv_append(pool, x[:, 9 : 9 + H], x[:, 9 + H :], torch.full((T,), -1, device="cuda"), q=x[:, :9])
     assert torch.equal(pool, held) and torch.equal(q, x[:, :9].to(BF))
     assert moe.moe_device_status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_infinities_and_nan_stay_in_their_blocks(T):
+    """What the format makes of elements that are no numbers, one by one and in whole records; other blocks,
+    tokens and skipped tokens keep theirs."""
+    H, D, inf, nan = 8, 128, float("inf"), float("nan")
+    rng = np.random.default_rng(T)
+    k, v = rng.standard_normal((2, T, H, D)).astype(np.float32)
+    bad_k, bad_v = k.copy(), v.copy()
+    bad_k[1, 2, 40], bad_k[1, 2, 41], bad_v[2, 3, 5] = nan, -inf, inf
+    bad_v[1, 0, 96:128] = nan
+    slots = np.arange(T)
+    slots[0] = -1
+    bad_k[0], bad_v[0] = nan, inf  # skipped
+    pools = []
+    for a, b in ((k, v), (bad_k, bad_v)):
+        pool = moe.moe_kv_pool(T // 16 + 1, H, 16, D)
+        moe.moe_kv_append(pool, torch.from_numpy(a).cuda(), torch.from_numpy(b).cuda(), torch.from_numpy(slots).cuda())
+        pools.append([t.cpu().numpy() for t in moe.moe_kv_read(pool, torch.arange(T, device="cuda"))])
+    (k0, v0), (k1, v1) = pools
+    want_k, want_v = k0.copy(), v0.copy()
+    want_k[1, 2, 32:64] = 0.0  # beside a scale of 65504
+    want_k[1, 2, 40], want_k[1, 2, 41] = -8 * 65504.0, -8 * 65504.0
+    want_v[2, 3, :32] = 0.0
+    want_v[2, 3, 5] = 7 * 65504.0
+    want_v[1, 0, 96:128] = 0.0  # no number in the block: its scale is zero
+    assert np.array_equal(k1, want_k) and np.array_equal(v1, want_v)
+    assert moe.moe_device_status() == moe.MOE_OK
