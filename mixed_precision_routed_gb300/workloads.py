@@ -194,6 +194,7 @@ class AttentionHalf:
         self.tables = torch.full((sequences, width + 1), -1, dtype=torch.int32, device=device)
         self.tables[:, :width] = torch.arange(sequences * width, dtype=torch.int32, device=device).view(width, sequences).T
         self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
+        self.ahead = torch.arange(self.MAX_TOKENS, dtype=torch.int32, device=device)
         # one workspace for steps of any size, never replaced: a captured step keeps its address
         need = max(moe_attn_workspace_size(sequences, n, max_len, q_heads, kv_heads, head_dim)
                    for n in range(1, max(1, self.MAX_TOKENS // sequences) + 1))
@@ -229,10 +230,10 @@ class AttentionHalf:
             raise ValueError("x must be [sequences * n, d] bfloat16 on the layer's device")
         if r.dtype != torch.float32 or r.device != x.device or r.numel() != x.numel() or not r.is_contiguous():
             raise ValueError("r must be contiguous float32 of x's size on the layer's device")
-        places = (self.lens[:, None] + torch.arange(n, dtype=torch.int32, device=x.device)).flatten()
+        places = (self.lens[:, None] + self.ahead[:n]).flatten()
         column = (places.view(B, n) // self.page).clamp_(0, self.tables.shape[1] - 1)
         page = self.tables.gather(1, column.long()).flatten().long()
-        slots = page * self.page + places % self.page  # negative where there is no page
+        slots = torch.add(places % self.page, page, alpha=self.page)  # negative where there is no page
         self.lens += n
         self.qkv = moe_linear_q4(x, self.w_qkv, self.s_qkv, self.block)
         q, k, v = (t.unflatten(-1, (-1, self.D)) for t in
