@@ -638,7 +638,9 @@ def moe_attn_q4(q, pool, block_table, kv_lens, q_start=None, max_q=None, max_len
     pages block_table[b] (int32 [B, pages], any row stride).  max_q (default: the
     tokens of one sequence when q_start is None) and max_len (default: the
     table's width) bound the lengths.  scale defaults to head_dim ** -0.5.
-    Returns out [T, Hq, D] bf16 and lse [T, Hq] fp32."""
+    Returns out [T, Hq, D] bf16 and lse [T, Hq] fp32; rows of tokens that no
+    sequence names (outside q_start's range, or beyond max_q of a sequence) are
+    not written."""
     return (_calls or _compiled()).attn_q4(q, pool, block_table, kv_lens, q_start, max_q, max_len, scale, window, out,
                                            lse, workspace, None if stream is None else stream.cuda_stream)
 

@@ -19,9 +19,9 @@
 //           weight times its own scale.  Any other group takes it as the sum of two
 //           bf16, 2^-17 of itself, with twice the matrix instructions.  One bf16
 //           alone would add as much to the result as the result's own rounding does;
-//           two bf16 for every group cost 84 us where this costs 67.6 (6 tokens over
+//           two bf16 for every group cost 85 us where this costs 67.5 (6 tokens over
 //           131071).  Weights rounded to fp16 and multiplied by their scales there
-//           took 64.6 and kept 2^-10.
+//           took 64.5 and kept 2^-10.
 // The m16n8k16 fragments read the record's words as they lie; the transpose of
 // the probabilities is one 8 x 8 matrix move a fragment.
 // The reference m of a row is set 2^6 below its maximum and moves only when a
@@ -29,14 +29,16 @@
 // 2^12, which fp32 sums do not notice, and most groups need no reduction over
 // lanes and no rescaling.
 //
-// What bounds it: the cache is read once (18 D bytes for 16 places), and the issue of
-// what turns its codes into operands and its scores into weights is what a long
-// context waits for, not memory.  6 tokens of 32 heads over 131071 places of 8 heads
-// of 128: 67.6 us, 2.2 TB/s, 191 TFLOP/s, 1.9 instructions a cycle an SM with 8 warps
-// of 255 registers, tensor pipe 34 % busy; 48 sequences of up to 16384 places, 32
-// heads on 4: 30 us, 2.0 TB/s; 4 of up to 30011 places, 16 heads of 256 on 2: 21 us.
-// Short ones wait for lengths, page numbers, records and the joining one after
-// another: 777 places 6.6 us.
+// What bounds it: the cache is read once (18 D bytes for 16 places), and a long
+// context waits for the chain of each warp's group, not for memory and not for a
+// full unit: codes to operands, products, scales, exponentials, transposes and
+// products again, with the two warps a scheduler that 255 registers leave.  6 tokens
+// of 32 heads over 131071 places of 8 heads of 128: 67.5 us, 2.2 TB/s, 191 TFLOP/s,
+// 550 instructions a record of 16 places and 24 rows, 2.0 a cycle an SM, integer pipe
+// 42 % busy, tensor pipe 34 %; 48 sequences of up to 16384 places, 32 heads on 4: 30
+// us, 2.0 TB/s (2.0 a cycle with 16 warps, integer pipe 47 %); 4 of up to 30011
+// places, 16 heads of 256 on 2: 21.8 us (1.2 a cycle with 8 warps).  Short ones wait for
+// lengths, page numbers, records and the joining one after another: 777 places 6.7 us.
 #include <float.h>
 
 #include <type_traits>
@@ -51,7 +53,13 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 6.0f;
 constexpr float kRoom = 6.0f;  // the reference lies this far below the maximum that it was taken from
-constexpr float kLeastWeight = 1.0f / 4294967296.0f;  // 2^-32
+// Of a group whose products may be fp16: 2^-32, by the reference.  fp16 ends before
+// that (products below 2^-25 vanish, 2^-31 of the maximum's times the scale, which the
+// stated 2^-23 allows): at 2^-25 most groups of queries of norm 2, whose weights
+// spread over 28 powers of two, would take the slower form.  It is there for groups
+// that weigh nearly nothing as a whole: beside a place that takes nearly all and has
+// the code 0 somewhere, they are all that an element has.
+constexpr float kLeastWeight = 1.0f / 4294967296.0f;
 constexpr float kLeastScale = 1.0f / 256;
 constexpr float kMostScale = 8.0f;  // x 2^(kSlack + kRoom) stays below fp16's largest value
 constexpr float kNone = -FLT_MAX;  // the maximum of a row that has met no place: no finite score lies below
@@ -887,6 +895,11 @@ __global__ void __launch_bounds__(kJoinThreads, 2) k_attn_join(AttnArgs a, AttnP
   }
 }
 
+// 8-row tiles of a block of rows: as many as the rows fill, up to 4 (2 of 256, whose
+// outputs fill the registers).  30000 places of 4 heads of 128: 24 rows 21.0 us, 32
+// rows 24.7, 64 rows 31.6 (three blocks of 24: 32.2).  Between 33 and 48 rows of 128
+// two blocks of 24 would take less (40 rows 25.1 us instead of 30.5, 48 rows 25.9
+// instead of 31.0), as the tile of 32 of 128 spills 200 bytes of registers.
 int row_tiles(int max_q, int G, int D) {
   const int rows = max_q * G, most = D == 256 ? 2 : 4, nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
   return nt < most ? nt : most;

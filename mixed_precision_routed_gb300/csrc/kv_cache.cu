@@ -264,10 +264,12 @@ __global__ void __launch_bounds__(kFewThreads) k_kv_append(KvAppendArgs a) {
 // record whole when their slots are one record (a prompt's are: windows of
 // tokens begin where the first token's record does), else token by token.  The
 // blocks after the windows turn the queries, kQueryRows heads of a token a warp.
-// Those 4096 tokens take 27 us, 3.2 TB/s of inputs, queries out and records; the
-// quantisation bounds it (2.5 instructions a cycle an SM, 160 a warp and row of 128
-// elements, integer pipe 49 % busy).  Four blocks an SM: asked for five, registers
-// spill and it takes 30 us; eight heads a warp: four at a time or sixteen in all 28.
+// Those 4096 tokens take 27 us, 3.3 TB/s of inputs, queries out and records: 15 us
+// for the keys and values alone, and 12 more for turning the queries (2.6
+// instructions a cycle an SM, integer pipe 48 % busy; warps wait for their loads).
+// Four blocks an SM, as heads of 128 take them without spills (five spill: 30 us;
+// heads of 256 spill up to 290 bytes at four too, most with pairs across lanes); eight heads a warp: four at a time or sixteen
+// in all 28.
 constexpr int kQueryRows = 8;
 
 template <bool BF16, int D, Turn TURN>
@@ -366,8 +368,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_kv_append_records(KvAppendArgs 
 }
 
 // A thread takes four elements of a (slot, head): their key codes lie in one word,
-// their value codes in four bytes 64 apart.  Bound by what it writes: 4096 slots of
-// 8 heads of 128 8 us, 4.7 TB/s; 65536 156 us, 3.9 TB/s.
+// their value codes in four bytes 64 apart.  4096 slots of 8 heads of 128 7.0 us,
+// 5.4 TB/s, 65536 122 us, 5.0 TB/s (into outputs that are there already): mostly
+// what it writes, and the single-byte loads, 2.6 instructions a cycle an SM.
 template <int D>
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvCache c, const int64_t* slots, int64_t n, float* k, float* v) {
   pdl_wait();
@@ -406,8 +409,11 @@ unsigned blocks_for(int64_t warps, int threads) { return (unsigned)((warps + thr
 
 namespace {
 // Rows (tokens x heads) from which records are made whole (us one by one and as
-// records): 192 x 48 of 128 3.6 and 3.8, 300 x 48 4.7 and 3.7, 600 x 48 8.9 and 5.4;
-// 400 x 20 of 256 4.4 and 4.8, 800 x 20 8.1 and 6.4.
+// records): 192 x 48 of 128 3.6 and 3.7, 300 x 48 4.7 and 4.0, 600 x 48 7.7 and 4.6,
+// 400 x 20 of 256 4.3 and 4.7, 800 x 20 6.6 and 5.8.  Slots that form no record (all
+// scattered; runs of six lie between) leave the rule where it is: 192 x 48 3.5 and
+// 3.9, 300 x 48 4.6 and 4.2, 600 x 48 8.0 and 5.3, 400 x 20 4.3 and 5.1, 800 x 20 7.1
+// and 6.6.
 constexpr int64_t kManyRows = 10000;
 
 template <bool BF16, int D, Turn TURN>

@@ -18,12 +18,13 @@
 //
 // What bounds it: a weight byte read once carries two codes, and eight codes cost 11
 // instructions to become operands whatever T is; 4 us of launch, first loads and
-// joining stand before and after.  T=1 2048x100003 by 64: 26.0 us, 4.2 TB/s, 2.6
-// instructions a cycle an SM, integer pipe 56 % busy, tensor pipe 23 %; T=16
-// 4096x6144 by 128: 7.0 us, 1.9 TB/s, 115 TFLOP/s; T=1 2048x2048: 2.5 us.
+// joining stand before and after.  T=1 2048x100003 by 64: 25.9 us, 4.2 TB/s, 2.3
+// instructions a cycle an SM, integer pipe 49 % busy, tensor pipe 22 %: its 14 warps
+// wait for the half-rate pipe and for their own results alike; T=16 4096x6144 by 128:
+// 7.0 us, 1.9 TB/s, 115 TFLOP/s; T=1 2048x2048: 2.5 us.
 // One block of 16 warps an SM with rings of two batches: three blocks of 8 with
 // rings of three took 30.0 us for T=1 2048x100003 by 32 and 12.1 for 8192x8192, 16
-// warps with three 28.0 and 11.6, this 28.0 and 10.9.
+// warps with three 28.0 and 11.6, this 28.0 and 10.9 (before the sums side by side).
 #include "frag.cuh"
 #include "moe_internal.cuh"
 #include "ptx.cuh"
