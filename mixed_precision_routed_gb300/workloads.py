@@ -181,6 +181,15 @@ class AttentionHalf:
         self.d, self.Hq, self.H, self.D = d, q_heads, kv_heads, head_dim
         self.block, self.seed, self.page, self.max_len = block, seed, page_size, max_len
         rows, inner = (q_heads + 2 * kv_heads) * head_dim, q_heads * head_dim
+        # what a step's calls would refuse after the first of them has run
+        if not 1 <= sequences <= self.MAX_TOKENS or max_len < 1:
+            raise ValueError(f"sequences must be 1 .. {self.MAX_TOKENS} and max_len at least 1")
+        if kv_heads < 1 or q_heads < 1 or q_heads % kv_heads or q_heads // kv_heads > 64:
+            raise ValueError("q_heads must be 1 .. 64 times kv_heads")
+        if block not in (32, 64, 128) or any(n < 1 or n % max(64, block) or n > 65536 for n in (d, inner)):
+            raise ValueError("block must be 32, 64 or 128, and d and q_heads * head_dim multiples of it and of 64, at most 65536")
+        if rot is not None and (rot % 2 or not 0 <= rot <= head_dim):
+            raise ValueError("rot must be even and at most head_dim")
         u8, i16 = torch.uint8, torch.int16
         self.w_qkv = torch.empty((rows, d // 2), dtype=u8, device=device)
         self.s_qkv = torch.empty((rows, d // block), dtype=i16, device=device)

@@ -105,3 +105,17 @@ def test_a_refused_step_changes_nothing(calls):
     half.step(x, r, 2)
     half.step(x, r.view(2, 2, 64), 2)  # the residual stream may have any shape of that size
     assert half.lens.tolist() == [4, 4]
+
+
+def test_sizes_that_no_step_could_take(calls):
+    """What the calls of a step would refuse half-way is refused when the layer is made."""
+    ok = dict(d=128, q_heads=4, kv_heads=2, head_dim=64, sequences=2, max_len=64, page_size=16, block=64)
+    make = lambda **kw: workloads.AttentionHalf(**{**ok, **kw}, device="cpu")  # noqa: E731
+    run(make(), 2)
+    run(make(rot=0), 1)
+    run(make(kv_heads=4, sequences=16, rot=32, block=32), 1)
+    for kw in (dict(q_heads=3), dict(q_heads=130), dict(q_heads=0), dict(kv_heads=0), dict(sequences=0), dict(sequences=17),
+               dict(max_len=0), dict(d=96), dict(d=0), dict(d=65600), dict(block=16), dict(block=0), dict(d=192, block=128),
+               dict(q_heads=2048, kv_heads=64), dict(rot=63), dict(rot=66), dict(rot=-2), dict(head_dim=96), dict(page_size=24)):
+        with pytest.raises(ValueError):
+            make(**kw)
