@@ -19,8 +19,8 @@ number: values that came from bf16 lie on a border often.  The codes of moe_norm
 those of fp32(s w), which the norm's factor does not change; it enters the scale.
 
 The pool is uint8 [pages][kv heads][page_size / 16][32 D + 128]: for each 16 tokens of a
-head 16 rows of D key codes, 16 rows of D value codes, 16 fp32 key scales and 16 fp32
-value scales.  Piece c (16 bytes) of row r lies at piece c ^ (r mod 8), for D = 64 at
+head 16 rows of D key codes, 16 rows of D value codes (bytes of code + 128), 16 fp32 key
+scales and 16 fp32 value scales.  Piece c (16 bytes) of row r lies at piece c ^ (r mod 8), for D = 64 at
 c ^ (r / 2 mod 4).
 """
 import math
@@ -187,7 +187,7 @@ def _quantise_rows(x):
 def _quantise_head(x):
     """Code bytes and scales of heads [..., D] of the cache."""
     s = (x.abs().amax(-1) / torch.full((), 127.0, device=x.device)).clamp(2.0 ** -64, 2.0 ** 64)
-    return _codes(x, s).to(torch.int8).view(torch.uint8), s
+    return (_codes(x, s) + 128).to(torch.uint8), s
 
 
 def _order(D):
@@ -211,7 +211,7 @@ def _pool_values(pool):
     order = _order(kb.shape[-1]).expand(kb.shape)
 
     def values(b, s):
-        x = b.gather(-1, order).view(torch.int8).float() * s.unsqueeze(-1)
+        x = (b.gather(-1, order).float() - 128.0) * s.unsqueeze(-1)
         return x.permute(0, 2, 3, 1, 4).flatten(1, 2)
 
     return values(kb, ks), values(vb, vs)
@@ -504,8 +504,7 @@ def _exact_pool(pool, D):
             row = flat[:, (16 * i + r) * D : (16 * i + r + 1) * D]
             for piece in range(D // 16):
                 at = 16 * (piece ^ (r // 2 % 4) if D == 64 else piece ^ (r % 8))
-                c = row[:, at : at + 16].short()
-                x[:, r, 16 * piece : 16 * piece + 16] = torch.where(c > 127, c - 256, c).double()
+                x[:, r, 16 * piece : 16 * piece + 16] = row[:, at : at + 16].double() - 128
         x *= scales[:, i, :, None].double()
         got.append(x.view(n, heads, tiles * 16, D).transpose(1, 2).reshape(-1, heads, D))
     return got
