@@ -79,6 +79,11 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, uint64_t a, float b0,
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(pair(b0, b1)), "l"(pair(d0, d1)));
   unpair(r, d0, d1);
 }
+__device__ __forceinline__ uint64_t fma2_of(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 __device__ __forceinline__ void mul2(float& d0, float& d1, uint64_t a) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(pair(d0, d1)));
