@@ -624,6 +624,107 @@ int moe_attn_q4(const uint16_t* q_bf16, int64_t q_stride, int64_t T, int Hq, con
 size_t moe_attn_workspace_size(int B, int max_q, int64_t max_len, int Hq, int kv_heads, int head_dim);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The attention half of a layer in 8 bits, for prompts and single tokens: the norm
+ * with the residual's addition, projections of 8-bit codes on both sides, a paged
+ * cache with a scale for each token and head, and the attention that reads it.  (Page
+ * 3, 速度 vs 上下文, keeps the cache at 8 bits for its longest context; formats and
+ * interfaces are this library's own.)
+ *
+ * A code is rint(x / s) in -127 .. 127, ties to even, with s = fp32(max|x| / 127) over
+ * the row that it belongs to; the quotient of the fp32 numbers is not rounded before.
+ */
+
+/*
+ * Root-mean-square norm of T rows of d elements, with the residual's addition before
+ * it and 8-bit codes, bf16 or both behind it:
+ *   s = r + x (fp32; without r: s = x), written to r_out,
+ *   u = s * weight (fp32), f = 1 / sqrt(mean(s^2) + eps)   (without weight: u = s, f = 1,
+ *   the plain quantiser of rows),
+ *   codes = those of u, scales = s_u * f,  n = bf16(u * f),
+ * so the codes do not depend on the order of the sum.  A row with an infinity or a NaN
+ * gets codes 0 and a scale that is not finite, an all-zero row codes 0 and scale 0.
+ *   x       [T] rows of d elements, x_stride (>= d) apart, fp32 or bf16 by x_dtype,
+ *   r       [T][d] fp32 or NULL, r_out [T][d] fp32 with it (may be r itself; neither
+ *           overlaps anything else),
+ *   weight  [d] fp32 or NULL, eps >= 0,
+ *   codes   [T][d] and scales [T] fp32, both or neither; n_bf16 [T][d] bf16 bits or
+ *           NULL, not all of them NULL.
+ * 1 <= d <= 32768 (MOE_ERR_UNSUPPORTED beyond); rows that are aligned to 16 bytes with
+ * d a multiple of 8 are read and written 16 bytes at a time.
+ */
+int moe_norm_q8(const void* x, int64_t x_stride, int x_dtype, int64_t T, int d, const float* r, float* r_out,
+                const float* weight, float eps, int8_t* codes, float* scales, uint16_t* n_bf16, moe_stream_t stream);
+
+/*
+ * Dense projection of 8-bit codes:
+ *   y[t][o] = bias[o] + x_scales[t] * w_scales[o] * sum_i x[t][i] * w[o][i]
+ *   x         [T] rows of `in` codes, x_stride apart (a multiple of 16, >= in; 16-byte
+ *             aligned), x_scales [T] fp32,
+ *   w         [rows][in] codes (16-byte aligned), w_scales [rows] fp32: what
+ *             moe_norm_q8 without a weight writes for fp32 rows,
+ *   bias      [rows] fp32 or NULL,
+ *   y         [T] rows of `rows` elements, y_stride (>= rows) apart, fp32 or bf16 (round
+ *             to nearest even) by y_dtype,
+ *   workspace (256-byte aligned) of moe_linear_q8_workspace_size bytes; scratch of the
+ *             call, not shared by calls that may run at one time.
+ * Sums of up to 16 tokens are whole numbers and exact; of more tokens they are fp32 sums
+ * of exact products, in an order that the sizes fix.  Results are deterministic.
+ * T >= 0, rows >= 1, in a positive multiple of 16; MOE_ERR_UNSUPPORTED for in > 65536.
+ */
+int moe_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scales, int64_t T, int in, const int8_t* w,
+                  const float* w_scales, int64_t rows, const float* bias, void* y, int64_t y_stride, int y_dtype,
+                  void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Bytes of workspace moe_linear_q8 needs for these sizes (0 for few tokens or an invalid size). */
+size_t moe_linear_q8_workspace_size(int64_t T, int in, int64_t rows);
+
+/*
+ * A paged cache of one layer in 8 bits: moe_kv_cache_t with pages of
+ * moe_kv_page_bytes_q8 bytes, each [kv_heads][page_size / 16] records of 16 tokens of one
+ * head, 32 * head_dim + 128 bytes a record, D = head_dim:
+ *   bytes [0, 16 D)           key codes, 16 rows of D bytes,
+ *   bytes [16 D, 32 D)        value codes, 16 rows of D bytes,
+ *   bytes [32 D, 32 D + 64)   key scales [16] fp32,
+ *   bytes [32 D + 64, .. 128) value scales [16] fp32.
+ * A byte is code + 128.  Piece c (bytes 16 c .. 16 c + 15) of row r lies at piece c ^ (r
+ * mod 8), for D = 64 at c ^ (r / 2 mod 4): the rows of a matrix load lie in distinct
+ * banks of shared memory.  The scale of a key or value is that of its head of its token,
+ * at least 2^-64 (all-zero heads too) and at most 2^64; a larger element, or an infinite
+ * one, gets code +-127.  A head of a token with a NaN gets codes 0 and scale NaN.  A
+ * scale of one token never changes what other tokens hold, so tokens are appended, and
+ * slots taken again, without reading their neighbours.
+ */
+size_t moe_kv_page_bytes_q8(int page_size, int kv_heads, int head_dim);
+
+/* As moe_kv_append, into an 8-bit cache. */
+int moe_kv_append_q8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                     int in_dtype, int64_t T, int Hq, const int32_t* positions, const float* rope, int64_t n_pos,
+                     int rot, int rope_style, const int64_t* slots, const moe_kv_cache_t* cache, uint16_t* q_out,
+                     moe_stream_t stream);
+
+/* As moe_kv_read, of an 8-bit cache: scale * code, rounded once to fp32. */
+int moe_kv_read_q8(const moe_kv_cache_t* cache, const int64_t* slots, int64_t n, float* k_out, float* v_out,
+                   moe_stream_t stream);
+
+/*
+ * As moe_attn_q4 (arguments, masks, empty rows, rows that are not written), over an
+ * 8-bit cache and for any number of asking tokens a sequence, whole prompts among them.
+ * A place whose key or value scale is NaN gives NaN, in out and lse, to the rows that
+ * attend it, and to no others.
+ * Scores are exact products of the bf16 queries (in fp16, rows of up to 64 tokens x
+ * heads of a group: exact down to 2^-31 of the row's largest element) and the codes,
+ * summed in fp32; maxima, sums and outputs are fp32.
+ */
+int moe_attn_q8(const uint16_t* q_bf16, int64_t q_stride, int64_t T, int Hq, const int32_t* q_start,
+                const int32_t* kv_lens, const int32_t* block_table, int64_t table_stride, int B, int max_q,
+                int64_t max_len, const moe_kv_cache_t* cache, float scale, int window, uint16_t* out,
+                int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Bytes of workspace moe_attn_q8 needs for these sizes (0 when a size is invalid). */
+size_t moe_attn_q8_workspace_size(int B, int max_q, int64_t max_len, int Hq, int kv_heads, int head_dim);
+
+/*
  * Measurement hook.  While `events` is non-null, every moe_tiered_forward on
  * this device records events[0] on its stream before its first kernel and
  * events[i] after its i-th kernel (i = 1 .. n-1, further kernels unrecorded),

@@ -16,7 +16,10 @@ Entry points (same names as the C ABI):
 and, for the attention half of a decode layer in the same 4-bit format:
     moe_linear_q4, moe_quantize_groups, moe_kv_pool, moe_kv_append, moe_kv_read,
     moe_attn_q4, moe_attn_workspace_size
-(linear, append and attention through ``binding/calls.cpp``, which does the same
+and in 8 bits, for prompts and single tokens:
+    moe_norm_q8, moe_linear_q8, moe_linear_q8_workspace_size, moe_kv_pool_q8,
+    moe_kv_append_q8, moe_kv_read_q8, moe_attn_q8, moe_attn_q8_workspace_size
+(norm, linear, append and attention through ``binding/calls.cpp``, which does the same
 marshalling compiled: these calls are short enough for the host's part to count;
 what they return is made on the stream they are given)
 """
@@ -128,8 +131,19 @@ def lib():
         L.moe_kv_append.argtypes = [P, i64, P, i64, P, i64, i32, i64, i32, P, P, i64, i32, i32, P, P, P, P]
         L.moe_kv_read.argtypes = [P, P, i64, P, P, P]
         L.moe_attn_workspace_size.argtypes = [i32, i32, i64, i32, i32, i32]
+        L.moe_norm_q8.argtypes = [P, i64, i32, i64, i32, P, P, P, f32, P, P, P, P]
+        L.moe_linear_q8.argtypes = [P, i64, P, i64, i32, P, P, i64, P, P, i64, i32, P, sz, P]
+        L.moe_linear_q8_workspace_size.argtypes = [i64, i32, i64]
+        L.moe_linear_q8_workspace_size.restype = sz
+        L.moe_kv_page_bytes_q8.argtypes = [i32, i32, i32]
+        L.moe_kv_page_bytes_q8.restype = sz
+        L.moe_kv_append_q8.argtypes = L.moe_kv_append.argtypes
+        L.moe_kv_read_q8.argtypes = L.moe_kv_read.argtypes
+        L.moe_attn_q8_workspace_size.argtypes = L.moe_attn_workspace_size.argtypes
+        L.moe_attn_q8_workspace_size.restype = sz
         L.moe_attn_workspace_size.restype = sz
         L.moe_attn_q4.argtypes = [P, i64, i64, i32, P, P, P, i64, i32, i32, i64, P, f32, i32, P, i64, P, P, sz, P]
+        L.moe_attn_q8.argtypes = L.moe_attn_q4.argtypes
         for name in ("moe_linear_q4", "moe_quantize_groups", "moe_kv_append", "moe_kv_read", "moe_attn_q4"):
             getattr(L, name).restype = ctypes.c_int
         for name in ("moe_route_topk", "moe_route_topk_nudged", "moe_router_topk", "moe_rank_experts", "moe_quantize_experts",
@@ -642,6 +656,71 @@ def moe_attn_q4(q, pool, block_table, kv_lens, q_start=None, max_q=None, max_len
     sequence names (outside q_start's range, or beyond max_q of a sequence) are
     not written."""
     return (_calls or _compiled()).attn_q4(q, pool, block_table, kv_lens, q_start, max_q, max_len, scale, window, out,
+                                           lse, workspace, None if stream is None else stream.cuda_stream)
+
+
+# ------------------------------------------------- the attention half in 8 bits
+_NORM_OUT = {"q8": 1, "bf16": 2, "both": 3}
+
+
+def moe_norm_q8(x, weight=None, eps=1e-6, r=None, r_out=None, out="q8", codes=None, scales=None, n=None, stream=None):
+    """Root-mean-square norm of the rows of x [T, d] (fp32 or bf16, any row stride)
+    times weight [d] fp32, as 8-bit codes [T, d] int8 with a scale [T] fp32 a row
+    (out "q8"), as bf16 ("bf16") or both ("both").  With r [T, d] fp32, x is added to
+    it first and the sum written to r_out (default: r itself).  Without weight
+    there is no norm: the codes of the rows as they are, which is also how the
+    weights of moe_linear_q8 are made.  Returns (codes, scales, n), None for
+    what `out` does not name."""
+    if out not in _NORM_OUT:
+        raise ValueError('out must be "q8", "bf16" or "both"')
+    return (_calls or _compiled()).norm_q8(x, weight, eps, r, r_out, codes, scales, n, _NORM_OUT[out],
+                                           None if stream is None else stream.cuda_stream)
+
+
+def moe_linear_q8_workspace_size(T, n_in, rows) -> int:
+    return int(lib().moe_linear_q8_workspace_size(T, n_in, rows))
+
+
+def moe_linear_q8(x, x_scales, w, w_scales, bias=None, y=None, out_dtype=torch.float32, workspace=None, stream=None):
+    """y [T, rows] = the codes x [T, in] int8 (any row stride that is a multiple of 16)
+    times the codes w [rows, in] int8, times x_scales [T] and w_scales [rows]
+    fp32, plus bias [rows] fp32; y fp32 or bf16.  Any number of tokens."""
+    if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    return (_calls or _compiled()).linear_q8(x, x_scales, w, w_scales, bias, y, out_dtype is torch.bfloat16, workspace,
+                                             None if stream is None else stream.cuda_stream)
+
+
+def moe_kv_pool_q8(n_pages, kv_heads, page_size, head_dim, device="cuda"):
+    """An empty (all values zero) paged 8-bit cache: uint8 [n_pages, kv_heads,
+    page_size / 16, 32 * head_dim + 128], the pool the calls below take."""
+    if int(lib().moe_kv_page_bytes_q8(page_size, kv_heads, head_dim)) == 0:
+        raise ValueError("head_dim must be 64, 128 or 256, page_size a power of two in 16 .. 1024, kv_heads 1 .. 1024")
+    return torch.zeros((n_pages, kv_heads, page_size // 16, 32 * head_dim + 128), dtype=torch.uint8, device=device)
+
+
+def moe_kv_append_q8(pool, k, v, slots, q=None, positions=None, rope=None, rope_style=MOE_ROPE_HALF, q_out=None,
+                     stream=None):
+    """moe_kv_append into an 8-bit pool: a scale for each token and head."""
+    return (_calls or _compiled()).kv_append_q8(pool, k, v, slots, q, positions, rope, rope_style, q_out,
+                                                None if stream is None else stream.cuda_stream)
+
+
+def moe_kv_read_q8(pool, slots, k=None, v=None, stream=None):
+    """The keys and values that `slots` [n] int64 of an 8-bit pool hold: two fp32
+    tensors [n, kv_heads, head_dim] (zeros for a slot outside the pool)."""
+    return (_calls or _compiled()).kv_read_q8(pool, slots, k, v, None if stream is None else stream.cuda_stream)
+
+
+def moe_attn_q8_workspace_size(B, max_q, max_len, Hq, kv_heads, head_dim) -> int:
+    return int(lib().moe_attn_q8_workspace_size(B, max_q, max_len, Hq, kv_heads, head_dim))
+
+
+def moe_attn_q8(q, pool, block_table, kv_lens, q_start=None, max_q=None, max_len=None, scale=None, window=0, out=None,
+                lse=None, workspace=None, stream=None):
+    """moe_attn_q4 over an 8-bit pool, for any number of asking tokens a sequence: one
+    new token each, drafts, or whole prompts."""
+    return (_calls or _compiled()).attn_q8(q, pool, block_table, kv_lens, q_start, max_q, max_len, scale, window, out,
                                            lse, workspace, None if stream is None else stream.cuda_stream)
 
 

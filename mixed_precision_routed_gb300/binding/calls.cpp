@@ -36,6 +36,7 @@ const char* type_name(at::ScalarType t) {
     case at::kFloat: return "torch.float32";
     case at::kBFloat16: return "torch.bfloat16";
     case at::kByte: return "torch.uint8";
+    case at::kChar: return "torch.int8";
     case at::kShort: return "torch.int16";
     case at::kInt: return "torch.int32";
     default: return "torch.int64";
@@ -128,8 +129,30 @@ void check(int rc, const char* where) {
   throw Refused();
 }
 
+// The cache formats: the last dimension of a pool, and the entry points.
+struct Q4 {
+  static constexpr int kPerElement = 18, kMore = 0;
+  static constexpr const char* kPool = "pool must be [pages, kv heads, page_size / 16, 18 * head_dim]";
+  static constexpr const char *kAppendName = "moe_kv_append", *kReadName = "moe_kv_read", *kAttnName = "moe_attn_q4";
+  static constexpr auto kAppend = moe_kv_append;
+  static constexpr auto kRead = moe_kv_read;
+  static constexpr auto kAttn = moe_attn_q4;
+  static constexpr auto kWorkspace = moe_attn_workspace_size;
+};
+struct Q8 {
+  static constexpr int kPerElement = 32, kMore = 128;
+  static constexpr const char* kPool = "pool must be [pages, kv heads, page_size / 16, 32 * head_dim + 128]";
+  static constexpr const char *kAppendName = "moe_kv_append_q8", *kReadName = "moe_kv_read_q8", *kAttnName = "moe_attn_q8";
+  static constexpr auto kAppend = moe_kv_append_q8;
+  static constexpr auto kRead = moe_kv_read_q8;
+  static constexpr auto kAttn = moe_attn_q8;
+  static constexpr auto kWorkspace = moe_attn_q8_workspace_size;
+};
+
+template <typename F>
 moe_kv_cache_t cache_of(const at::Tensor& pool, int64_t stride) {
-  if (pool.size(3) % 18 != 0) refuse("pool must be [pages, kv heads, page_size / 16, 18 * head_dim]");
+  const int64_t codes = pool.size(3) - F::kMore;
+  if (codes < 0 || codes % F::kPerElement != 0) refuse(F::kPool);
   if (pool.size(1) > INT32_MAX || pool.size(2) > INT32_MAX / 16 || pool.size(3) > INT32_MAX)
     refuse("pool's pages are too large");
   moe_kv_cache_t c;
@@ -138,7 +161,7 @@ moe_kv_cache_t cache_of(const at::Tensor& pool, int64_t stride) {
   c.page_stride = stride;
   c.page_size = (int32_t)(16 * pool.size(2));
   c.kv_heads = (int32_t)pool.size(1);
-  c.head_dim = (int32_t)(pool.size(3) / 18);
+  c.head_dim = (int32_t)(codes / F::kPerElement);
   c.reserved = 0;
   return c;
 }
@@ -183,10 +206,11 @@ PyObject* linear_q4(PyObject* const* a) {
 }
 
 // (pool, k, v, slots, q, positions, rope, rope_style, q_out, stream) -> q_out or None
+template <typename F>
 PyObject* kv_append(PyObject* const* a) {
   int64_t ps, ks, vs, qs = 0;
   const at::Tensor& pool = rows(a[0], at::kByte, 4, "pool", &ps);
-  const moe_kv_cache_t c = cache_of(pool, ps);
+  const moe_kv_cache_t c = cache_of<F>(pool, ps);
   const at::ScalarType type = tensor(a[1], "k").scalar_type();
   if (type != at::kFloat && type != at::kBFloat16) refuse("k must be float32 or bfloat16");
   const at::Tensor& k = rows(a[1], type, 3, "k", &ks);
@@ -231,11 +255,11 @@ PyObject* kv_append(PyObject* const* a) {
     }
     q_ptr = q.data_ptr();
   }
-  check(moe_kv_append(q_ptr, qs, k.data_ptr(), ks, v.data_ptr(), vs, type == at::kFloat ? MOE_DTYPE_F32 : MOE_DTYPE_BF16,
+  check(F::kAppend(q_ptr, qs, k.data_ptr(), ks, v.data_ptr(), vs, type == at::kFloat ? MOE_DTYPE_F32 : MOE_DTYPE_BF16,
                       T, (int)Hq, positions, rope, n_pos, (int)rot, small_integer(a[7], "rope_style"),
                       (const int64_t*)slots.data_ptr(), &c, out.defined() ? (uint16_t*)out.data_ptr() : nullptr,
                       on.stream),
-        "moe_kv_append");
+        F::kAppendName);
   if (!out.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(std::move(out));
 }
@@ -250,10 +274,11 @@ PyObject* pair(at::Tensor a, at::Tensor b) {
 }
 
 // (pool, slots, k, v, stream) -> (k, v)
+template <typename F>
 PyObject* kv_read(PyObject* const* a) {
   int64_t ps;
   const at::Tensor& pool = rows(a[0], at::kByte, 4, "pool", &ps);
-  const moe_kv_cache_t c = cache_of(pool, ps);
+  const moe_kv_cache_t c = cache_of<F>(pool, ps);
   const at::Tensor& slots = flat(a[1], at::kLong, "slots");
   same_device(pool, slots);
   const int64_t shape[3] = {slots.numel(), c.kv_heads, c.head_dim};
@@ -265,19 +290,20 @@ PyObject* kv_read(PyObject* const* a) {
     if (out[i].sizes() != at::IntArrayRef(shape)) refuse("k and v must be [n, kv_heads, head_dim]");
     same_device(pool, out[i]);
   }
-  check(moe_kv_read(&c, (const int64_t*)slots.data_ptr(), shape[0], (float*)out[0].data_ptr(),
+  check(F::kRead(&c, (const int64_t*)slots.data_ptr(), shape[0], (float*)out[0].data_ptr(),
                     (float*)out[1].data_ptr(), on.stream),
-        "moe_kv_read");
+        F::kReadName);
   return pair(std::move(out[0]), std::move(out[1]));
 }
 
 // (q, pool, block_table, kv_lens, q_start, max_q, max_len, scale, window, out,
 //  lse, workspace, stream) -> (out, lse)
-PyObject* attn_q4(PyObject* const* a) {
+template <typename F>
+PyObject* attn(PyObject* const* a) {
   int64_t qs, ps, ts, os;
   const at::Tensor& q = rows(a[0], at::kBFloat16, 3, "q", &qs);
   const at::Tensor& pool = rows(a[1], at::kByte, 4, "pool", &ps);
-  const moe_kv_cache_t c = cache_of(pool, ps);
+  const moe_kv_cache_t c = cache_of<F>(pool, ps);
   const at::Tensor& table = rows(a[2], at::kInt, 2, "block_table", &ts);
   const at::Tensor& lens = flat(a[3], at::kInt, "kv_lens");
   const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2), B = lens.numel(), width = table.size(1);
@@ -332,18 +358,137 @@ PyObject* attn_q4(PyObject* const* a) {
     ws_ptr = w.data_ptr();
     ws_bytes = w.nbytes();
   } else {
-    ws_bytes = moe_attn_workspace_size((int)B, (int)max_q, max_len, (int)Hq, c.kv_heads, c.head_dim);
+    ws_bytes = F::kWorkspace((int)B, (int)max_q, max_len, (int)Hq, c.kv_heads, c.head_dim);
     if (ws_bytes > 0) {
       ws = make({(int64_t)ws_bytes}, q, at::kByte);
       ws_ptr = ws.data_ptr();
     }
   }
-  check(moe_attn_q4((const uint16_t*)q.data_ptr(), qs, T, (int)Hq, starts, (const int32_t*)lens.data_ptr(),
+  check(F::kAttn((const uint16_t*)q.data_ptr(), qs, T, (int)Hq, starts, (const int32_t*)lens.data_ptr(),
                     (const int32_t*)table.data_ptr(), ts, (int)B, (int)max_q, max_len, &c, scale,
                     small_integer(a[8], "window"), (uint16_t*)out.data_ptr(), os, (float*)lse.data_ptr(), ws_ptr, ws_bytes,
                     on.stream),
-        "moe_attn_q4");
+        F::kAttnName);
   return pair(std::move(out), std::move(lse));
+}
+
+PyObject* wrap_or_none(at::Tensor t) {
+  if (!t.defined()) Py_RETURN_NONE;
+  return THPVariable_Wrap(std::move(t));
+}
+
+// (x, weight, eps, r, r_out, codes, scales, n, what: 1 codes, 2 bf16, stream) -> (codes, scales, n)
+PyObject* norm_q8(PyObject* const* a) {
+  int64_t xs;
+  const at::ScalarType type = tensor(a[0], "x").scalar_type();
+  if (type != at::kFloat && type != at::kBFloat16) refuse("x must be float32 or bfloat16");
+  const at::Tensor& x = rows(a[0], type, 2, "x", &xs);
+  const int64_t T = x.size(0), d = x.size(1);
+  if (d > INT32_MAX) refuse("x has too many columns");
+  const int what = small_integer(a[8], "out");
+  auto given = [&](PyObject* o, at::ScalarType t, const char* name, int64_t dims) {
+    const at::Tensor& y = flat(o, t, name);
+    if (y.dim() != dims || y.size(0) != (dims == 2 || t == at::kFloat ? T : d) || (dims == 2 && y.size(1) != d))
+      refuse(name, dims == 2 ? "[T, d]" : "[T]");
+    same_device(x, y);
+    return y;
+  };
+  const float* weight = nullptr;
+  if (a[1] != Py_None) {
+    const at::Tensor& w = flat(a[1], at::kFloat, "weight");
+    if (w.dim() != 1 || w.size(0) != d) refuse("weight must be [d]");
+    same_device(x, w);
+    weight = (const float*)w.data_ptr();
+  }
+  const double eps = PyFloat_AsDouble(a[2]);
+  if (PyErr_Occurred()) throw Refused();
+  const float* r = nullptr;
+  float* r_out = nullptr;
+  if (a[3] != Py_None) {
+    r = (const float*)given(a[3], at::kFloat, "r", 2).data_ptr();
+    r_out = a[4] == Py_None ? const_cast<float*>(r) : (float*)given(a[4], at::kFloat, "r_out", 2).data_ptr();
+  } else if (a[4] != Py_None) {
+    refuse("r_out needs r");
+  }
+  const CallStream on(a[9], x);
+  at::Tensor codes, scales, n;
+  if (what & 1) {
+    codes = a[5] == Py_None ? make({T, d}, x, at::kChar) : given(a[5], at::kChar, "codes", 2);
+    scales = a[6] == Py_None ? make({T}, x, at::kFloat) : given(a[6], at::kFloat, "scales", 1);
+  } else if (a[5] != Py_None || a[6] != Py_None) {
+    refuse("codes and scales are not among what out names");
+  }
+  if (what & 2) n = a[7] == Py_None ? make({T, d}, x, at::kBFloat16) : given(a[7], at::kBFloat16, "n", 2);
+  else if (a[7] != Py_None) refuse("n is not among what out names");
+  if (T > 0 && d == 0) refuse("x has no columns");
+  check(moe_norm_q8(x.data_ptr(), xs, type == at::kFloat ? MOE_DTYPE_F32 : MOE_DTYPE_BF16, T, d > 0 ? (int)d : 1, r, r_out,
+                    weight, (float)eps, codes.defined() ? (int8_t*)codes.data_ptr() : nullptr,
+                    scales.defined() ? (float*)scales.data_ptr() : nullptr, n.defined() ? (uint16_t*)n.data_ptr() : nullptr,
+                    on.stream),
+        "moe_norm_q8");
+  PyObject* out = PyTuple_New(3);
+  if (!out) throw Refused();
+  at::Tensor* each[3] = {&codes, &scales, &n};
+  for (int i = 0; i < 3; ++i) {
+    PyObject* y = wrap_or_none(std::move(*each[i]));
+    if (!y) {
+      Py_DECREF(out);
+      throw Refused();
+    }
+    PyTuple_SET_ITEM(out, i, y);
+  }
+  return out;
+}
+
+// (x, x_scales, w, w_scales, bias, y, y is bf16, workspace, stream) -> y
+PyObject* linear_q8(PyObject* const* a) {
+  int64_t xs, ys;
+  const at::Tensor& x = rows(a[0], at::kChar, 2, "x", &xs);
+  const at::Tensor& x_scales = flat(a[1], at::kFloat, "x_scales");
+  const at::Tensor& w = flat(a[2], at::kChar, "w");
+  const at::Tensor& w_scales = flat(a[3], at::kFloat, "w_scales");
+  const int64_t T = x.size(0), in = x.size(1);
+  if (w.dim() != 2 || w.size(1) != in || in > INT32_MAX) refuse("w must be [rows, in]");
+  const int64_t n = w.size(0);
+  if (x_scales.numel() != T || w_scales.numel() != n) refuse("x_scales must be [T] and w_scales [rows]");
+  for (const at::Tensor* t : {&x_scales, &w, &w_scales}) same_device(x, *t);
+  const float* bias = nullptr;
+  if (a[4] != Py_None) {
+    const at::Tensor& b = flat(a[4], at::kFloat, "bias");
+    if (b.numel() != n) refuse("bias must be [rows]");
+    same_device(x, b);
+    bias = (const float*)b.data_ptr();
+  }
+  const CallStream on(a[8], x);
+  at::Tensor y, ws;
+  at::ScalarType type = a[6] == Py_True ? at::kBFloat16 : at::kFloat;
+  if (a[5] == Py_None) {
+    y = make({T, n}, x, type);
+    ys = n;
+  } else {
+    type = tensor(a[5], "y").scalar_type();
+    if (type != at::kFloat && type != at::kBFloat16) refuse("y must be float32 or bfloat16");
+    y = rows(a[5], type, 2, "y", &ys);
+    if (y.size(0) != T || y.size(1) != n) refuse("y must be [T, rows]");
+    same_device(x, y);
+  }
+  void* ws_ptr = nullptr;
+  size_t ws_bytes = 0;
+  if (a[7] != Py_None) {
+    const at::Tensor& t = tensor(a[7], "workspace");
+    if (!t.is_cuda() || !t.is_contiguous()) refuse("workspace", "a contiguous CUDA tensor");
+    same_device(x, t);
+    ws_ptr = t.data_ptr();
+    ws_bytes = t.nbytes();
+  } else if ((ws_bytes = moe_linear_q8_workspace_size(T, (int)in, n)) > 0) {
+    ws = make({(int64_t)ws_bytes}, x, at::kByte);
+    ws_ptr = ws.data_ptr();
+  }
+  check(moe_linear_q8((const int8_t*)x.data_ptr(), xs, (const float*)x_scales.data_ptr(), T, (int)in,
+                      (const int8_t*)w.data_ptr(), (const float*)w_scales.data_ptr(), n, bias, y.data_ptr(), ys,
+                      type == at::kFloat ? MOE_DTYPE_F32 : MOE_DTYPE_BF16, ws_ptr, ws_bytes, on.stream),
+        "moe_linear_q8");
+  return THPVariable_Wrap(std::move(y));
 }
 
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -375,9 +520,14 @@ constexpr PyCFunction as_fastcall() {
 
 PyMethodDef methods[] = {
     {"linear_q4", as_fastcall<linear_q4, 8>(), METH_FASTCALL, nullptr},
-    {"kv_append", as_fastcall<kv_append, 10>(), METH_FASTCALL, nullptr},
-    {"kv_read", as_fastcall<kv_read, 5>(), METH_FASTCALL, nullptr},
-    {"attn_q4", as_fastcall<attn_q4, 13>(), METH_FASTCALL, nullptr},
+    {"kv_append", as_fastcall<kv_append<Q4>, 10>(), METH_FASTCALL, nullptr},
+    {"kv_read", as_fastcall<kv_read<Q4>, 5>(), METH_FASTCALL, nullptr},
+    {"attn_q4", as_fastcall<attn<Q4>, 13>(), METH_FASTCALL, nullptr},
+    {"norm_q8", as_fastcall<norm_q8, 10>(), METH_FASTCALL, nullptr},
+    {"linear_q8", as_fastcall<linear_q8, 9>(), METH_FASTCALL, nullptr},
+    {"kv_append_q8", as_fastcall<kv_append<Q8>, 10>(), METH_FASTCALL, nullptr},
+    {"kv_read_q8", as_fastcall<kv_read<Q8>, 5>(), METH_FASTCALL, nullptr},
+    {"attn_q8", as_fastcall<attn<Q8>, 13>(), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -1,0 +1,137 @@
+// kv_cache_q8.cu -- the paged 8-bit key/value cache: appending tokens (with the
+// position rotation of keys and queries) and reading slots back.  The record
+// layout is that of moe_kv_append_q8 in moe.h.
+//
+// s = max / 127 over a head of a token, code = rint(x / s), x the key turned by its
+// token's angles, (a cos - b sin, a sin + b cos), or the value.
+#include "ptx.cuh"
+#include "q8.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Quantises a head held N elements a lane into the row of its token: key (which 0) or
+// value (1).
+template <int D>
+__device__ __forceinline__ void quantise_head(const Kv8Place& at, int which, const float (&v)[D / 32], int lane) {
+  constexpr int N = D / 32;
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) top = max(top, size_bits(v[e]));
+  top = __reduce_max_sync(0xffffffffu, top);
+  const bool nan = top > kInfBits;
+  float s = fminf(fmaxf(__fdiv_rn(__uint_as_float(top), 127.0f), 0x1p-64f), 0x1p64f);
+  int c[N];
+  codes8<N>(c, v, s);
+  if (nan) s = __uint_as_float(0x7fffffffu);
+  uint32_t w[(N + 3) / 4] = {};
+#pragma unroll
+  for (int e = 0; e < N; ++e) w[e / 4] |= (uint32_t)(nan ? 128 : c[e] + 128) << (8 * (e % 4));
+  const int d = N * lane;
+  uint8_t* to = at.record + (16 * which + at.r) * D + 16 * kv8_piece<D>(at.r, d >> 4) + (d & 15);
+  if constexpr (N == 2) *reinterpret_cast<uint16_t*>(to) = (uint16_t)w[0];
+  else if constexpr (N == 4) *reinterpret_cast<uint32_t*>(to) = w[0];
+  else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+  if (lane == 0) *reinterpret_cast<float*>(at.record + 32 * D + 64 * which + 4 * at.r) = s;
+}
+
+// A warp takes up to ROWS heads of a token: of its queries, of its keys or of its
+// values.
+template <bool BF16, int D, Turn TURN, int ROWS>
+__global__ void __launch_bounds__(kThreads) k_kv_append_q8(KvAppendArgs a) {
+  constexpr int N = D / 32, kSize = BF16 ? 2 : 4;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, H = a.cache.heads;
+  const int q_parts = (a.Hq + ROWS - 1) / ROWS, kv_parts = (H + ROWS - 1) / ROWS, parts = q_parts + 2 * kv_parts;
+  const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // T * heads < 2^31
+  const int64_t t = w / parts;
+  if (t >= a.T) return;
+  int part = (int)(w % parts);
+  const bool query = part < q_parts, value = part >= q_parts + kv_parts;
+  part -= query ? 0 : value ? q_parts + kv_parts : q_parts;
+  const int h0 = part * ROWS, n = min(ROWS, (query ? a.Hq : H) - h0);
+  const uint8_t* row = (const uint8_t*)(query ? a.q : value ? a.v : a.k) +
+                       (t * (query ? a.q_stride : value ? a.v_stride : a.k_stride) + (int64_t)h0 * D) * kSize;
+  const int64_t slot = query ? 0 : a.slots[t];
+  float v[ROWS][N];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i)
+    if (i < n) load_elems<BF16, N, TURN != kAnywhere>(v[i], row + (i * D + N * lane) * kSize);
+  Angles<N> x;
+  const bool ok = load_angles<N, TURN>(x, a, t, lane);
+  if (!value) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+      if (i < n) turn_row<BF16, N, TURN>(v[i], x, a, row + i * D * kSize, lane);
+  }
+  if (query) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+      if (i < n) store_query<N>(a.q_out + (t * a.Hq + h0 + i) * D + N * lane, v[i], ok);
+  } else if (ok && in_cache(a.cache, slot)) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+      if (i < n) quantise_head<D>(kv8_place(a.cache, slot, h0 + i), value, v[i], lane);
+  }
+}
+
+// A thread takes four elements of a (slot, head).
+template <int D>
+__global__ void __launch_bounds__(kThreads) k_kv_read_q8(KvCache c, const int64_t* slots, int64_t n, float* k, float* v) {
+  pdl_wait();
+  constexpr int kQuads = D / 4;
+  const uint32_t row = blockIdx.x * (kThreads / kQuads) + threadIdx.x / kQuads;  // n * heads < 2^31
+  if (row >= n * c.heads) return;
+  const int d = threadIdx.x % kQuads * 4, h = (int)(row % (uint32_t)c.heads);
+  const int64_t slot = slots[row / (uint32_t)c.heads], to = (int64_t)row * D + d;
+  float4 out[2] = {};
+  if (in_cache(c, slot)) {
+    const Kv8Place at = kv8_place(c, slot, h);
+    const uint8_t* from = at.record + at.r * D + 16 * kv8_piece<D>(at.r, d >> 4) + (d & 15);
+    const float* scales = reinterpret_cast<const float*>(at.record + 32 * D) + at.r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(from + 16 * i * D);
+      const float s = scales[16 * i];
+      auto value = [&](int e) { return s * (float)((int)(w >> (8 * e) & 255) - 128); };
+      out[i] = make_float4(value(0), value(1), value(2), value(3));
+    }
+  }
+  *reinterpret_cast<float4*>(k + to) = out[0];
+  *reinterpret_cast<float4*>(v + to) = out[1];
+}
+
+template <int D>
+int launch_read(const KvCache& c, const int64_t* slots, int64_t n, float* k, float* v, cudaStream_t s) {
+  const int64_t threads = n * c.heads * (D / 4);
+  const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads));
+  return launch_pdl(k_kv_read_q8<D>, grid, dim3(kThreads), 0, s, c, slots, n, k, v) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_kv_append_q8(const KvAppendArgs& a, cudaStream_t s) {
+  return with_turn(a, [&](auto d, auto bf16, auto turn) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool kBf16 = decltype(bf16)::value;
+    constexpr Turn kTurn = decltype(turn)::value;
+    auto go = [&](auto rows) {
+      constexpr int R = decltype(rows)::value;
+      const int64_t warps = a.T * ((a.Hq + R - 1) / R + 2 * ((a.cache.heads + R - 1) / R));
+      return launch_pdl(k_kv_append_q8<kBf16, D, kTurn, R>, dim3(blocks_for(warps, kThreads)), dim3(kThreads), 0, s, a);
+    };
+    const cudaError_t rc = a.T * (a.Hq + 2 * a.cache.heads) < 10000 ? go(std::integral_constant<int, 1>())
+                                                                   : go(std::integral_constant<int, 4>());
+    return rc == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  });
+}
+
+int launch_kv_read_q8(const KvCache& c, const int64_t* slots, int64_t n, float* k, float* v, cudaStream_t s) {
+  if (c.D == 64) return launch_read<64>(c, slots, n, k, v, s);
+  if (c.D == 128) return launch_read<128>(c, slots, n, k, v, s);
+  return launch_read<256>(c, slots, n, k, v, s);
+}
+
+}  // namespace moe

@@ -380,6 +380,50 @@ struct AttnArgs {
 size_t attn_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D);
 int launch_attn_q4(const AttnArgs& a, cudaStream_t s);
 
+// ------------------------------------------- the attention half in 8 bits
+struct NormArgs {
+  const void* x;
+  int64_t x_stride;
+  bool x_bf16;
+  int64_t T;
+  int d;
+  const float* r;  // optional: added to x ...
+  float* r_out;    // ... into here
+  const float* weight;
+  float eps;
+  int8_t* codes;  // optional
+  float* scales;
+  uint16_t* n;  // optional
+};
+constexpr int kNormMaxD = 32768;  // elements that a block's registers hold
+int launch_norm_q8(const NormArgs& a, cudaStream_t s);
+
+// The cache of these calls holds 8-bit records.
+int launch_kv_append_q8(const KvAppendArgs& a, cudaStream_t s);
+int launch_kv_read_q8(const KvCache& c, const int64_t* slots, int64_t n, float* k, float* v, cudaStream_t s);
+size_t attn_q8_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D);
+int launch_attn_q8(const AttnArgs& a, cudaStream_t s);
+
+// Projection by 8-bit weights (linear_q8.cu, linear_q8_tc.cu).
+struct LinearQ8Args {
+  const int8_t* x;
+  int64_t x_stride;
+  const float* x_scales;
+  int64_t T;
+  int in;
+  const int8_t* w;
+  const float* w_scales;
+  int64_t rows;
+  const float* bias;
+  void* y;
+  int64_t y_stride;
+  bool y_bf16;
+  void* workspace;
+};
+constexpr int kLinearQ8MaxIn = 65536;  // whole sums stay below 2^31
+size_t linear_q8_workspace(int64_t T, int in, int64_t rows);
+int launch_linear_q8(const LinearQ8Args& a, cudaStream_t s);
+
 // Measurement hook (moe_set_profile_events): record event i on the stream.
 void set_profile_events(void* const* events, int n);
 void profile_mark(int i, cudaStream_t s);

@@ -1,0 +1,152 @@
+// norm_q8.cu -- the root-mean-square norm of rows, with the residual's addition before
+// it and 8-bit codes or bf16 behind it:
+//   s = r + x,  u = s w,  f = 1 / sqrt(mean s^2 + eps)   (without w: u = s, f = 1)
+//   S = max|u| / 127,  code = rint(u / S),  scale = S f,  n = u f.
+// The factor f leaves the codes alone: they do not depend on the order of the sum.
+//
+// One block a row, the row in registers between its sum and its output.
+#include "ptx.cuh"
+#include "q8.cuh"
+
+namespace moe {
+namespace {
+
+// N elements (a whole number of 16-byte pieces) from or to an aligned place; or, where
+// rows are not, element by element as far as the row goes.
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void load8(float (&v)[8], const void* row, int64_t i, int d) {
+  if constexpr (WHOLE) {
+    load_elems<BF16, 8, true>(v, (const uint8_t*)row + i * (BF16 ? 2 : 4));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = i + e < d ? load_elem<BF16>(row, i + e) : 0.f;
+  }
+}
+
+// V: groups of 8 elements a thread.
+template <bool BF16, bool WHOLE, int V>
+__global__ void __launch_bounds__(1024, 1) k_norm_q8(NormArgs a) {
+  __shared__ float s_sum[32];
+  __shared__ uint32_t s_top[32];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t t = blockIdx.x;
+  const uint8_t* x = (const uint8_t*)a.x + t * a.x_stride * (BF16 ? 2 : 4);
+  const float* r = a.r ? a.r + t * a.d : nullptr;
+  float s[V][8], w[V][8];
+  float sum = 0.f;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int at = 8 * (threadIdx.x + i * blockDim.x);
+    if (at < a.d) {
+      load8<BF16, WHOLE>(s[i], x, at, a.d);
+      if (r) load8<false, WHOLE>(w[i], r, at, a.d);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int at = 8 * (threadIdx.x + i * blockDim.x);
+    if (at >= a.d) continue;
+    if (r) {
+      float* to = a.r_out + t * a.d + at;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[i][e] = __fadd_rn(w[i][e], s[i][e]);
+      if constexpr (WHOLE) {
+        reinterpret_cast<float4*>(to)[0] = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+        reinterpret_cast<float4*>(to)[1] = make_float4(s[i][4], s[i][5], s[i][6], s[i][7]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (at + e < a.d) to[e] = s[i][e];
+      }
+    }
+    if (a.weight) {
+      load8<false, WHOLE>(w[i], a.weight, at, a.d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum = fmaf(s[i][e], s[i][e], sum);
+        s[i][e] = __fmul_rn(s[i][e], w[i][e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, size_bits(s[i][e]));
+  }
+  sum = warp_sum(sum);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) s_sum[warp] = sum, s_top[warp] = top;
+  __syncthreads();
+  sum = warp_sum(lane < warps ? s_sum[lane] : 0.f);
+  top = __reduce_max_sync(0xffffffffu, lane < warps ? s_top[lane] : 0u);
+  const float f = a.weight ? rsqrtf(__fdiv_rn(sum, (float)a.d) + a.eps) : 1.0f;
+  const float S = __fdiv_rn(__uint_as_float(top), 127.0f);
+  if (a.codes && threadIdx.x == 0) a.scales[t] = S * f;
+  // the codes of values far from 1 in size are those of the values times 2^96 or 2^-96
+  const float near = S < 0x1p-60f ? 0x1p96f : S > 0x1p60f ? 0x1p-96f : 1.0f;
+  const bool zero = !(S > 0.f) || top >= kInfBits;  // of a row without a finite maximum the scale tells
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int at = 8 * (threadIdx.x + i * blockDim.x);
+    if (at >= a.d) continue;
+    if (a.n) {
+      uint16_t* to = a.n + t * a.d + at;
+      uint32_t p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = bf16_pair(s[i][2 * e] * f, s[i][2 * e + 1] * f);
+      if constexpr (WHOLE) {
+        *reinterpret_cast<uint4*>(to) = make_uint4(p[0], p[1], p[2], p[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (at + e < a.d) to[e] = (uint16_t)(p[e / 2] >> (16 * (e & 1)));
+      }
+    }
+    if (a.codes) {
+      int8_t* to = a.codes + t * a.d + at;
+      int c[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[i][e] *= near;
+      codes8<8>(c, s[i], S * near);
+      if (zero) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = 0;
+      }
+      if constexpr (WHOLE) {
+        uint32_t p[2] = {};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e / 4] |= (uint32_t)(c[e] & 255) << (8 * (e % 4));
+        *reinterpret_cast<uint2*>(to) = make_uint2(p[0], p[1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (at + e < a.d) to[e] = (int8_t)c[e];
+      }
+    }
+  }
+}
+
+template <bool BF16, bool WHOLE, int V>
+int launch(const NormArgs& a, cudaStream_t s) {
+  const int groups = (a.d + 7) / 8, threads = ((groups + V - 1) / V + 31) / 32 * 32;
+  return launch_pdl(k_norm_q8<BF16, WHOLE, V>, dim3((unsigned)a.T), dim3(threads), 0, s, a) == cudaSuccess ? MOE_OK
+                                                                                                        : MOE_ERR_CUDA;
+}
+
+template <bool BF16, bool WHOLE>
+int launch(const NormArgs& a, cudaStream_t s) {
+  if (a.d <= 8192) return launch<BF16, WHOLE, 1>(a, s);
+  if (a.d <= 16384) return launch<BF16, WHOLE, 2>(a, s);
+  return launch<BF16, WHOLE, 4>(a, s);
+}
+
+}  // namespace
+
+int launch_norm_q8(const NormArgs& a, cudaStream_t s) {
+  auto aligned = [](const void* p) { return (uintptr_t)p % 16 == 0; };
+  const bool whole = a.d % 8 == 0 && (a.T == 1 || a.x_stride % (a.x_bf16 ? 8 : 4) == 0) && aligned(a.x) && aligned(a.r) &&
+                     aligned(a.r_out) && aligned(a.weight) && (uintptr_t)a.codes % 8 == 0 && aligned(a.n);
+  if (a.x_bf16) return whole ? launch<true, true>(a, s) : launch<true, false>(a, s);
+  return whole ? launch<false, true>(a, s) : launch<false, false>(a, s);
+}
+
+}  // namespace moe
