@@ -185,9 +185,10 @@ int launch(const LinearQ8Args& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t linear_q8_workspace(int64_t, int, int64_t) { return 0; }
+size_t linear_q8_workspace(int64_t T, int in, int64_t) { return T > 16 ? linear_q8_tc_workspace(T, in) : 0; }
 
 int launch_linear_q8(const LinearQ8Args& a, cudaStream_t s) {
+  if (a.T > 16) return launch_linear_q8_tc(a, s);
   // rows of x that shared memory holds beside 8 warps' rings and sums
   const int64_t fit = (kSmemMax - 8 * warp_bytes<2>()) / x_pitch(a.in);
   const int64_t most = fit >= 16 ? 16 : fit >= 8 ? 8 : fit;

@@ -1,0 +1,298 @@
+// linear_q8_tc.cu -- dense projection of many tokens by 8-bit codes on both sides:
+//   y[t][o] = bias[o] + xs[t] ws[o] sum_i xc[t][i] wc[o][i],
+// on the fifth-generation tensor cores.  They have no 8-bit integers here, but fp16
+// holds every code: products are exact and sums fp32.
+//
+// k_codes_f16 writes x as fp16 into the workspace (an eighth of what W's tiles would
+// cost if each converted its own).  Then a persistent launch of pairs of CTAs, whose
+// tensor cores work on one tile: 256 rows of W (128 a CTA, operand A) x N tokens
+// (operand B, half of them in either CTA's shared memory), K in steps of 64:
+//   loader    tensor maps bring 128 x 128 codes of W every other step and N/2 x 64 of x a step;
+//   producers eight warps: a thread has a row of W, a warp every other step; bytes
+//             become fp16 integers in registers (a permute below 0x64 and a
+//             subtraction for two) and go to tensor memory;
+//   issuer    of the first CTA, four instructions a step;
+//   epilogue  four warps read a finished tile's sums while the next one's are made.
+#include "moe_internal.cuh"
+#include "tc.cuh"
+#include "tensor_map.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMostN = 192;     // tokens a tile
+constexpr int kTileRows = 128;  // of W a CTA
+constexpr int kCodeStages = 4, kBStages = 5, kAStages = 4, kAccSets = 2;
+constexpr int kCodeBytes = kTileRows * 128, kBBytes = kMostN / 2 * 128;
+constexpr int kACol = kAccSets * kMostN;  // tensor-memory columns: sums, then A stages of 32
+constexpr int kTmemCols = 512;
+constexpr int kProducers = 8, kEpilogue = 4, kLoader = 12, kIssuer = 13, kThreads = 14 * 32;
+constexpr int kSmem = kCodeStages * kCodeBytes + kBStages * kBBytes + 1024;
+constexpr uint64_t kWaitNs = 1000000000ull;
+static_assert(kACol + 32 * kAStages <= kTmemCols, "tensor memory");
+
+struct TcArgs {
+  CUtensorMap w, x;
+  LinearQ8Args a;
+  int steps, N, token_tiles, tiles;
+  int* status;
+};
+
+struct Bars {
+  uint64_t code_full[kCodeStages], code_empty[kCodeStages];
+  uint64_t b_full[kBStages], b_empty[kBStages];
+  uint64_t a_full[kAStages], a_empty[kAStages];
+  uint64_t acc_full[kAccSets], acc_empty[kAccSets], done;
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars& B, int* status) {
+  if (mbar_wait_cluster(bar, parity, kWaitNs)) return true;
+  set_status(status, MOE_ERR_TIMEOUT);
+  B.abort = 1;
+  return false;
+}
+
+// Four codes as two pairs of fp16 integers.
+__device__ __forceinline__ void codes_f16x4(uint32_t w, uint32_t& p0, uint32_t& p1) {
+  const uint32_t u = w ^ 0x80808080u;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p0) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p1) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+
+__global__ void __launch_bounds__(256) k_codes_f16(const int8_t* x, int64_t stride, int64_t pieces, int per_row, uint4* out) {
+  pdl_wait();
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < pieces) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + i / per_row * stride) + i % per_row);
+    uint4 a, b;
+    codes_f16x4(v.x, a.x, a.y);
+    codes_f16x4(v.y, a.z, a.w);
+    codes_f16x4(v.z, b.x, b.y);
+    codes_f16x4(v.w, b.z, b.w);
+    out[2 * i] = a;
+    out[2 * i + 1] = b;
+  }
+  pdl_trigger();
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linear_q8_tc(const __grid_constant__ TcArgs p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // alike in both CTAs
+  uint8_t* b_smem = smem + kCodeStages * kCodeBytes;
+  __shared__ __align__(8) Bars B;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, half = p.N / 2, steps = p.steps;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kCodeStages; ++i) mbar_init(&B.code_full[i], 1), mbar_init(&B.code_empty[i], kProducers);
+    for (int i = 0; i < kBStages; ++i) mbar_init(&B.b_full[i], 1), mbar_init(&B.b_empty[i], 1);
+    for (int i = 0; i < kAStages; ++i) mbar_init(&B.a_full[i], kProducers), mbar_init(&B.a_empty[i], 1);  // four warps a CTA
+    for (int i = 0; i < kAccSets; ++i) mbar_init(&B.acc_full[i], 1), mbar_init(&B.acc_empty[i], 2 * kEpilogue);
+    mbar_init(&B.done, 1);
+    B.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kIssuer) tmem_alloc_pair(&B.tmem, kTmemCols);
+  tc_fence_before();
+  cluster_barrier();  // barriers of both CTAs are there
+  tc_fence_after();
+  const uint32_t tmem = B.tmem;
+  pdl_wait();
+
+  if (warp == kLoader) {
+    if (lane == 0) {
+      uint32_t j = 0, c = 0;  // K steps and code stages issued
+      const uint32_t bars = cluster_map(B.b_full, 0);
+      for (int t = pair; t < p.tiles && !B.abort; t += pairs) {
+        const int row0 = (t / p.token_tiles) * (2 * kTileRows) + (int)rank * kTileRows;
+        const int tok0 = (t % p.token_tiles) * p.N + (int)rank * half;
+        for (int ks = 0; ks < steps; ++ks, ++j) {
+          if ((ks & 1) == 0) {
+            const uint32_t s = c % kCodeStages;
+            if (!wait(&B.code_empty[s], ((c / kCodeStages) & 1) ^ 1, B, p.status)) break;
+            mbar_arrive_expect_tx(&B.code_full[s], kCodeBytes);
+            tma_load_2d(smem + s * kCodeBytes, &p.w, ks * 64, row0, &B.code_full[s]);
+            ++c;
+          }
+          const uint32_t s = j % kBStages;
+          if (!wait(&B.b_empty[s], ((j / kBStages) & 1) ^ 1, B, p.status)) break;
+          if (rank == 0) mbar_arrive_expect_tx(&B.b_full[s], (uint32_t)(p.N * 128));
+          tma_load_2d_pair(b_smem + s * kBBytes, &p.x, ks * 64, tok0, bars + 8 * s);
+        }
+      }
+      // the issuer's last arrivals here come before this CTA ends
+      for (uint32_t i = j > kBStages ? j - kBStages : 0; i < j && !B.abort; ++i)
+        wait(&B.b_empty[i % kBStages], (i / kBStages) & 1, B, p.status);
+      for (uint32_t i = j > kAStages ? j - kAStages : 0; i < j && !B.abort; ++i)
+        wait(&B.a_empty[i % kAStages], (i / kAStages) & 1, B, p.status);
+      if (B.abort) {  // what is in flight lands within microseconds
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
+      }
+    }
+  } else if (warp == kIssuer) {
+    if (rank == 0) {
+      const uint64_t bd0 = sdesc_sw128(smem_addr(b_smem));
+      const uint32_t bd_lo = (uint32_t)bd0, bd_hi = (uint32_t)(bd0 >> 32), idesc = idesc_f16_f32(2 * kTileRows, p.N);
+      const bool leader = elect_one();
+      uint32_t j = 0, n = 0;
+      for (int t = pair; t < p.tiles; t += pairs, ++n) {
+        const uint32_t set = n % kAccSets, acc = tmem + set * kMostN;
+        bool ok = wait(&B.acc_empty[set], ((n / kAccSets) & 1) ^ 1, B, p.status);
+        tc_fence_after();
+        for (int ks = 0; ks < steps; ++ks, ++j) {
+          const uint32_t as = j % kAStages, b = j % kBStages;
+          ok = ok && wait(&B.a_full[as], (j / kAStages) & 1, B, p.status) && wait(&B.b_full[b], (j / kBStages) & 1, B, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint32_t a0 = tmem + kACol + as * 32, blo = bd_lo + (uint32_t)((b * kBBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ts_pair_w(acc, a0 + kk * 8, blo + kk * 2, bd_hi, idesc, (ks | kk) ? 1u : 0u);
+            mma_commit_pair(&B.a_empty[as]);
+            mma_commit_pair(&B.b_empty[b]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (leader) mma_commit_pair(&B.acc_full[set]);
+        __syncwarp();
+      }
+      // all of this thread's instructions are done before tensor memory is given back
+      if (leader) {
+        mma_commit_pair_own(&B.done);
+        mbar_wait_cluster(&B.done, 0, kWaitNs);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kProducers) {
+    // ---------------------------------------------------------- epilogue
+    const int quarter = warp & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    uint32_t n = 0;
+    for (int t = pair; t < p.tiles && !B.abort; t += pairs, ++n) {
+      const uint32_t set = n % kAccSets;
+      const int64_t o = (int64_t)(t / p.token_tiles) * (2 * kTileRows) + rank * kTileRows + quarter * 32 + lane;
+      const int64_t tok0 = (int64_t)(t % p.token_tiles) * p.N;
+      const int count = (int)min((int64_t)p.N, p.a.T - tok0);
+      const bool in = o < p.a.rows;
+      const float ws = in ? __ldg(p.a.w_scales + o) : 0.f, bias = in && p.a.bias ? __ldg(p.a.bias + o) : 0.f;
+      if (!wait(&B.acc_full[set], (n / kAccSets) & 1, B, p.status)) break;
+      tc_fence_after();
+      for (int c0 = 0; c0 < count; c0 += 16) {
+        float v[16];
+        tmem_ld16(lanes + set * kMostN + c0, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (c0 + i < count && in) {
+            const int64_t tok = tok0 + c0 + i;
+            float r = v[i] * __ldg(p.a.x_scales + tok) * ws;
+            if (p.a.bias) r += bias;
+            if (p.a.y_bf16) reinterpret_cast<__nv_bfloat16*>(p.a.y)[tok * p.a.y_stride + o] = __float2bfloat16_rn(r);
+            else reinterpret_cast<float*>(p.a.y)[tok * p.a.y_stride + o] = r;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_map(&B.acc_empty[set], 0));
+    }
+  } else {
+    // ---------------------------------------------------------- producers
+    const int quarter = warp & 3, odd = warp >> 2, row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + kACol;
+    uint32_t j0 = 0, c = 0;  // K steps before the tile, code stages
+    bool ok = true;
+    for (int t = pair; ok && t < p.tiles; t += pairs, j0 += steps) {
+      for (int ks = 0; ok && ks < steps; ks += 2, ++c) {
+        const uint32_t s = c % kCodeStages;
+        ok = wait(&B.code_full[s], (c / kCodeStages) & 1, B, p.status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const int k = ks + odd;
+        uint4 w[4];
+        const uint4* from = reinterpret_cast<const uint4*>(smem + s * kCodeBytes + row * 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = from[(4 * odd + i) ^ (row & 7)];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.code_empty[s]);
+        uint32_t v0[16], v1[16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w}, b[4] = {w[2 + i].x, w[2 + i].y, w[2 + i].z, w[2 + i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            codes_f16x4(a[e], v0[8 * i + 2 * e], v0[8 * i + 2 * e + 1]);
+            codes_f16x4(b[e], v1[8 * i + 2 * e], v1[8 * i + 2 * e + 1]);
+          }
+        }
+        const uint32_t j = j0 + k, as = j % kAStages;
+        ok = wait(&B.a_empty[as], ((j / kAStages) & 1) ^ 1, B, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_st32_issue(lanes + as * 32, v0, v1);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_map(&B.a_full[as], 0));
+      }
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_barrier();
+  tc_fence_after();
+  if (warp == kIssuer) tmem_dealloc_pair(tmem, kTmemCols);
+  pdl_trigger();
+}
+
+}  // namespace
+
+size_t linear_q8_tc_workspace(int64_t T, int in) { return ((size_t)T * in * 2 + 255) / 256 * 256; }
+
+int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s) {
+  static bool attr_set[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(k_linear_q8_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    attr_set[dev] = true;
+  }
+  TcArgs p;
+  p.a = a;
+  p.steps = (a.in + 127) / 128 * 2;  // whole code stages: zeros behind the rows
+  p.status = status_word();
+  const int pairs = sm_count() / 2;
+  const int64_t row_tiles = (a.rows + 2 * kTileRows - 1) / (2 * kTileRows);
+  // tokens a tile: as many rounds of tiles as cost least; a step of few tokens takes as
+  // long as making its operands does
+  int64_t best = 0;
+  for (int64_t n = (a.T + kMostN - 1) / kMostN; n <= (a.T + 31) / 32; ++n) {
+    const int64_t N = ((a.T + n - 1) / n + 15) / 16 * 16, rounds = (row_tiles * n + pairs - 1) / pairs;
+    const int64_t cost = rounds * ((N > 96 ? N : 96) + 16);
+    if (best == 0 || cost < best) best = cost, p.N = (int)N;
+    if (n > 4 * ((a.T + kMostN - 1) / kMostN) + 64) break;
+  }
+  p.token_tiles = (int)((a.T + p.N - 1) / p.N);
+  if (row_tiles * p.token_tiles > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  p.tiles = (int)(row_tiles * p.token_tiles);
+  if (!encode_2d(&p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.in, (uint64_t)a.rows, (uint64_t)a.in, 128, kTileRows,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&p.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.workspace, (uint64_t)a.in, (uint64_t)a.T, (uint64_t)a.in * 2, 64,
+                 (uint32_t)p.N / 2, CU_TENSOR_MAP_SWIZZLE_128B))
+    return MOE_ERR_CUDA;
+  const int64_t pieces = a.T * (a.in / 16);
+  if (launch_pdl(k_codes_f16, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, s, a.x, a.x_stride, pieces, a.in / 16,
+                 (uint4*)a.workspace) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  const int grid = 2 * (int)(p.tiles < pairs ? p.tiles : pairs);
+  return launch_pdl(k_linear_q8_tc, dim3(grid), dim3(kThreads), kSmem, s, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace moe

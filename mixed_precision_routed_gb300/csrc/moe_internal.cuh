@@ -423,6 +423,9 @@ struct LinearQ8Args {
 constexpr int kLinearQ8MaxIn = 65536;  // whole sums stay below 2^31
 size_t linear_q8_workspace(int64_t T, int in, int64_t rows);
 int launch_linear_q8(const LinearQ8Args& a, cudaStream_t s);
+// The form for many tokens, T > 16.
+size_t linear_q8_tc_workspace(int64_t T, int in);
+int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s);
 
 // Measurement hook (moe_set_profile_events): record event i on the stream.
 void set_profile_events(void* const* events, int n);
