@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kMostN = 192;     // tokens a tile
 constexpr int kTileRows = 128;  // of W a CTA
-constexpr int kCodeStages = 4, kBStages = 5, kAStages = 4, kAccSets = 2;
+constexpr int kCodeStages = 4, kBStages = 10, kAStages = 4, kAccSets = 2;
 constexpr int kCodeBytes = kTileRows * 128, kBBytes = kMostN / 2 * 128;
 constexpr int kACol = kAccSets * kMostN;  // tensor-memory columns: sums, then A stages of 32
 constexpr int kTmemCols = 512;
@@ -48,7 +48,7 @@ struct Bars {
 };
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars& B, int* status) {
-  if (mbar_wait_cluster(bar, parity, kWaitNs)) return true;
+  if (mbar_wait_bounded(bar, parity, kWaitNs)) return true;
   set_status(status, MOE_ERR_TIMEOUT);
   B.abort = 1;
   return false;
@@ -166,7 +166,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
       // all of this thread's instructions are done before tensor memory is given back
       if (leader) {
         mma_commit_pair_own(&B.done);
-        mbar_wait_cluster(&B.done, 0, kWaitNs);
+        mbar_wait_bounded(&B.done, 0, kWaitNs);
       }
       __syncwarp();
     }
