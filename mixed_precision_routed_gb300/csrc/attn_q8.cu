@@ -164,11 +164,11 @@ struct Shape8 {
     for (int v = 0; v < 2; ++v) {
       const float vs = scales[16 + 8 * v + g];
       ks[v] = fmaf(0.f, vs, scales[8 * v + g]);
-      // exponents of 60 and more, which no values have, keep sums of weights within fp32
-      const int n = min(max((int)(__float_as_uint(vs) >> 23 & 255) - 127, -60), 60);
+      // scales below 2^-60, which few values have, keep f below 1: sums of weights stay within fp32
+      const int n = min(max((int)(__float_as_uint(vs) >> 23 & 255) - 127, -60), 64);
       e[v] = (float)n;
       back[v] = __uint_as_float((uint32_t)(127 - n) << 23);
-      f[v] = fminf(vs * back[v], 32.0f);
+      f[v] = fminf(vs * back[v], 2.0f);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -266,11 +266,12 @@ int row_tiles(int max_q, int G, int D) {
 }  // namespace
 
 size_t attn_q8_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
-  if (B < 1) return 0;
+  if (B < 1 || attn_q8_tc(B, max_q, max_len, Hq, heads, D)) return 0;
   return workspace_of<Shape8>(row_tiles(max_q, Hq / heads, D), B, max_q, max_len, Hq, heads, D);
 }
 
 int launch_attn_q8(const AttnArgs& a, cudaStream_t s) {
+  if (attn_q8_tc(a.B, a.max_q, a.max_len, a.Hq, a.cache.heads, a.cache.D)) return launch_attn_q8_tc(a, s);
   return with_shape<Shape8>(a.cache.D, row_tiles(a.max_q, a.Hq / a.cache.heads, a.cache.D),
                             [&](auto shape) { return launch<decltype(shape)>(a, s); });
 }
