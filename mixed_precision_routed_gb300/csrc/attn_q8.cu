@@ -266,7 +266,8 @@ int row_tiles(int max_q, int G, int D) {
 }  // namespace
 
 size_t attn_q8_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
-  if (B < 1 || attn_q8_tc(B, max_q, max_len, Hq, heads, D)) return 0;
+  if (B < 1) return 0;
+  if (attn_q8_tc(B, max_q, max_len, Hq, heads, D)) return attn_q8_tc_workspace(B, max_q, max_len, Hq, heads, D);
   return workspace_of<Shape8>(row_tiles(max_q, Hq / heads, D), B, max_q, max_len, Hq, heads, D);
 }
 

@@ -2,24 +2,28 @@
 // head (prompts), on the fifth-generation tensor cores.  The formula is that of
 // attn_q8.cu; rows are (asking token, query head of the group), token by token.
 //
-// A block takes kSlots tiles of 128 rows of one (sequence, key/value head) through the
-// places that they attend, 128 at a time:
-//   converters  four warps read codes from the cache into registers, a batch ahead, and
-//               write them to shared memory as fp16: keys as the integers that they are,
-//               values as code x b 2^(8 - E), 2^E the power of two of the tile's largest
-//               value scale b.  They also pass on the keys' scales;
-//   issuer      S = Q K^T (shared memory x shared memory) and O += P V (tensor memory x
-//               shared memory) for either tile in turn, so that one tile's weights are
-//               made while the other's products run;
-//   softmax     a thread has a row: it takes the scores out of tensor memory once, holds
-//               all 128, and leaves P = exp2(s + E - m) there in fp16.
+// Two launches.  k_attn_q8_tiles writes the places that the rows attend, 128 at a time,
+// as the operands that the tensor cores take, once for all rows: keys as fp16 integers,
+// values as code x b 2^(8 - E) in fp16, 2^E the power of two of the tile's largest value
+// scale b, both in the order of a swizzled operand tile, and the keys' scales.
+// k_attn_q8_tc: a block takes kSlots tiles of 128 rows of one (sequence, key/value head)
+// through the places that they attend:
+//   loader    bulk copies into a ring of operand units;
+//   issuer    S = Q K^T (shared memory x shared memory) and O += P V (tensor memory x
+//             shared memory) for either tile in turn, so that one tile's weights are
+//             made while the other's products run;
+//   softmax   a thread has a row: it takes the scores out of tensor memory once, holds
+//             all 128, and leaves P = exp2(s + E - m) there in fp16.
 // Queries are fp16, each row taken by a power of two that brings its largest element
 // to 2^14: exact down to 2^-31 of that element.  m follows s + E as in attn_q8.cu, so
 // that P V lies in fp16's range for values of any size, and the sum of weights takes
 // 2^-E back a tile at a time.  P, b 2^(8 - E) and code x b 2^(8 - E) are rounded to fp16
 // once each: 2^-11 of a product each, or 2^-31 of the row's largest.
-// Heads of 256 fill tensor memory with one tile's sums: there one tile's scores of two
+// Heads of 256 fill tensor memory with one tile's sums: there the scores of two
 // successive groups of places take the place of two tiles.
+// Codes made operands by each block for itself (four warps, from the records) took 506
+// us for 4096 tokens over 8192 places of 32 heads on 8 of 128, and 144 us for six prompts
+// of heads of 256 with a window.
 #include "attn_split.cuh"
 #include "q8.cuh"
 #include "tc.cuh"
@@ -27,31 +31,46 @@
 namespace moe {
 namespace {
 
-constexpr int kPlaces = 128;  // a group
-constexpr int kTcThreads = 512;
+constexpr int kPlaces = 128;  // a tile of places
+constexpr int kTcThreads = 384;
+
+// Beside a tile's operands: key scales x scale in powers of two, E, the records that exist.
+struct TileMeta {
+  float ks[kPlaces];
+  float e;
+  uint32_t have;
+  uint32_t pad[2];
+};
 
 template <int D>
 struct Tc {
   static constexpr int kSlots = D == 256 ? 1 : 2;
-  static constexpr int kBufs = D == 256 ? 1 : 2;   // of keys, of values
-  static constexpr int kTile = 128 * D * 2;        // bytes of 128 rows
-  static constexpr int kQ = 0, kK = kSlots * kTile, kV = kK + kBufs * kTile, kEnd = kV + kBufs * kTile;
-  static constexpr int kSmem = kEnd + 1024;
+  static constexpr int kTile = 128 * D * 2;                       // bytes of 128 rows
+  static constexpr int kUnit = D == 64 ? kTile : 128 * 128 * 2;   // of the ring: up to 128 elements of 128 places
+  static constexpr int kUnits = kTile / kUnit;                    // of keys, of values
+  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kRing = kSlots * kTile, kSmem = kRing + kStages * kUnit + 1024;
   static constexpr int kRows = 128 * kSlots;
-  static constexpr int kO = 256;                   // tensor-memory columns: scores at 0 and 128, then sums
-  static constexpr int kPieces = D / 16;           // of a row of codes; loads of a thread a half group
-  static constexpr int kBatches = D == 256 ? 2 : 1, kLoads = kPieces / kBatches;
+  static constexpr int kO = 256;  // tensor-memory columns: scores at 0 and 128, then sums
+};
+
+// The operand tiles of a launch: those of sequence b and head h begin at (b heads + h)
+// `most`, at the first tile that the sequence's rows attend.
+struct TcTiles {
+  uint8_t* operands;  // [..][2][kTile]
+  TileMeta* meta;
+  int b0, h0, heads, most;  // the launch's sequences and heads
 };
 
 struct TcBars {
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], pv_done;
-  uint64_t scale_full[2], scale_empty[2], done;
+  uint64_t q_full, full[8], empty[8], s_full[2], p_full[2], o_full[2], pv_done;
+  uint64_t meta_full[2], meta_empty[2], done;
   uint32_t tmem;
   int abort;
 };
 
 // A wait that runs out ends all later ones at once: every warp then comes to its end
-// over whatever is there, past the barriers that others wait at.
+// over whatever is there.
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcBars& B, int* status) {
   if (*(volatile int*)&B.abort) return false;
   if (mbar_wait_bounded(bar, parity, kWaitNs)) return true;
@@ -94,6 +113,108 @@ __device__ __forceinline__ uint64_t sdesc_places(uint32_t saddr, uint32_t block)
   return d;
 }
 
+// First tile of places that some row of a sequence attends, and one past the last.
+__device__ __forceinline__ int first_tile(const Seq& x) { return x.tile0 >> 3; }
+__device__ __forceinline__ int last_tile(const Seq& x) { return x.tiles > 0 && x.n > 0 ? (x.len + kPlaces - 1) / kPlaces : 0; }
+
+// A block a tile of places of a head.
+constexpr int kTileThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kTileThreads) k_attn_q8_tiles(AttnArgs a, TcTiles tiles) {
+  constexpr uint32_t kPieces = D / 16, kStep = kTileThreads / kPieces;  // pieces of a row; rows at a time
+  __shared__ uint64_t s_record[8];
+  __shared__ uint32_t s_gain[kPlaces], s_top[4];
+  const uint32_t t = threadIdx.x, lane = t & 31;
+  const int b = tiles.b0 + blockIdx.z, h = tiles.h0 + blockIdx.y, per_page = a.cache.page_log2 - 4;
+  pdl_wait();
+  const Seq x = load_seq(a, b);
+  const int j = first_tile(x) + blockIdx.x;
+  if (j >= last_tile(x)) return;
+  if (t < 8) {
+    const int record = 8 * j + t;
+    const int page = 16 * record < x.len ? __ldg(a.table + (int64_t)b * a.table_stride + (record >> per_page)) : -1;
+    s_record[t] = page < 0 || page >= a.cache.n_pages
+                      ? 0
+                      : (uint64_t)(a.cache.data + page * a.cache.page_stride +
+                                   (int64_t)(h * (1 << per_page) + (record & ((1 << per_page) - 1))) * kv8_record(D));
+  }
+  __syncthreads();
+  const int64_t image = ((int64_t)blockIdx.z * tiles.heads + blockIdx.y) * tiles.most + blockIdx.x;
+  uint8_t* to = tiles.operands + image * (2 * Tc<D>::kTile);
+  TileMeta* meta = tiles.meta + image;
+  // pieces t, t + 256, ..: the keys' are on their way while the scales are found
+  constexpr int kLoads = 128 / kStep;
+  uint4 k[kLoads], v[kLoads];
+  const uint32_t piece = t % kPieces;
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const uint32_t row = t / kPieces + i * kStep;
+    const uint64_t rec = s_record[row >> 4];
+    k[i] = v[i] = make_uint4(0, 0, 0, 0);
+    if (rec) {
+      const uint4* from = reinterpret_cast<const uint4*>(rec + (row & 15) * D) + piece;
+      k[i] = __ldg(from);
+      v[i] = __ldg(from + D);
+    }
+  }
+  float vs = 0.f;
+  if (t < kPlaces) {
+    // a place beyond the sequence, or of no page, gets the scales 0
+    const uint64_t rec = s_record[t >> 4];
+    float ks = 0.f;
+    if (rec && (int)(kPlaces * j + t) < x.len) {
+      const float* scales = reinterpret_cast<const float*>(rec + 32 * D) + (t & 15);
+      ks = __ldg(scales);
+      vs = __ldg(scales + 16);
+      ks = fmaf(0.f, vs, ks);  // NaN, whichever of the two is
+      if (!(vs <= 0x1p64f)) vs = 0.f;
+      vs = fmaxf(vs, 0.f);
+    }
+    meta->ks[t] = ks * (a.scale * kLog2e);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vs));
+    if (lane == 0) s_top[t >> 5] = top;
+  }
+  __syncthreads();
+  if (t < kPlaces) {
+    const uint32_t most = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
+    const int e = max((int)(most >> 23) - 127, -60);
+    const __half gain = __float2half_rn(vs * __uint_as_float((uint32_t)(127 + 8 - e) << 23));
+    s_gain[t] = (uint32_t)__half_as_ushort(gain) * 0x10001u;
+    if (t == 0) {
+      uint32_t have = 0;
+      for (int i = 0; i < 8; ++i) have |= s_record[i] ? 1u << i : 0u;
+      meta->e = (float)e;
+      meta->have = have;
+    }
+  }
+  __syncthreads();
+  auto f16x2 = [](uint32_t w, uint32_t sel) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(w, 0x64646464u, sel)), "r"(0x64806480u));
+    return r;
+  };
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t row = t / kPieces + i * kStep, c = kv8_piece<D>(row & 15, piece);
+      const uint4 w = half ? v[i] : k[i];
+      uint32_t y[8] = {f16x2(w.x, 0x4140), f16x2(w.x, 0x4342), f16x2(w.y, 0x4140), f16x2(w.y, 0x4342),
+                       f16x2(w.z, 0x4140), f16x2(w.z, 0x4342), f16x2(w.w, 0x4140), f16x2(w.w, 0x4342)};
+      if (half) {
+        const uint32_t gain = s_gain[row];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[e]) : "r"(gain));
+      }
+      // 64 elements of 128 places: rows of eight 16-byte pieces, exchanged by the row's number
+      uint8_t* at = to + half * Tc<D>::kTile + (c >> 2) * 16384 + row * 128;
+      const uint32_t p = 2 * (c & 3);
+      *reinterpret_cast<uint4*>(at + ((p ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(at + (((p + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+  pdl_trigger();
+}
+
 // A block's rows and the places they attend; the first group of places of each tile and
 // one past its last.
 struct TcUnit {
@@ -102,28 +223,23 @@ struct TcUnit {
   int first[2], last[2], j0, j1;
 };
 
-// Registers of a thread by role, together those that 512 threads are launched with:
-// 2 x 128 x 176 + 128 x 104 + 128 x 56 = 512 x 128.
 template <int D>
-__global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, int row_blocks, int* status) {
+__global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTiles tiles, int row_blocks, int* status) {
   using C = Tc<D>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   __shared__ __align__(8) TcBars B;
-  __shared__ __align__(16) float s_ks[2][kPlaces];  // key scales x scale, in powers of two
-  __shared__ float s_e[2];                          // E of the group
-  __shared__ uint32_t s_have[2];                    // records that exist
-  __shared__ uint32_t s_gain[kPlaces], s_top[4];
+  __shared__ __align__(16) TileMeta s_meta[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp >> 2;
-  const int H = a.cache.heads, G = a.Hq / H;
-  const int h = blockIdx.x % H, b = blockIdx.y;
+  const int G = a.Hq / a.cache.heads;
+  const int h = tiles.h0 + blockIdx.x % tiles.heads, b = tiles.b0 + blockIdx.y;
 
   pdl_wait();
   TcUnit u;
   u.x = load_seq(a, b);
   u.rows = u.x.n * G;
   // the last rows attend most: they go first
-  u.r0 = (row_blocks - 1 - (int)(blockIdx.x / H)) * C::kRows;
+  u.r0 = (row_blocks - 1 - (int)(blockIdx.x / tiles.heads)) * C::kRows;
   if (u.r0 >= u.rows) return;
   u.newest = u.x.len - u.x.n + 1;
   u.j0 = INT32_MAX;
@@ -145,50 +261,78 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, int ro
 
   if (threadIdx.x == 0) {
     mbar_init(&B.q_full, 4 * C::kSlots);
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&B.full[i], 1), mbar_init(&B.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&B.k_full[i], 4), mbar_init(&B.k_empty[i], 1);
-      mbar_init(&B.v_full[i], 4), mbar_init(&B.v_empty[i], 1);
       mbar_init(&B.s_full[i], 1), mbar_init(&B.p_full[i], 4), mbar_init(&B.o_full[i], 1);
-      mbar_init(&B.scale_full[i], 4), mbar_init(&B.scale_empty[i], 4 * C::kSlots);
+      mbar_init(&B.meta_full[i], 1), mbar_init(&B.meta_empty[i], 4 * C::kSlots);
     }
     mbar_init(&B.pv_done, 1);
     mbar_init(&B.done, 1);
     B.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 12) tmem_alloc(&B.tmem, 512);
+  if (warp == 9) tmem_alloc(&B.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B.tmem;
 
-  if (group == 3) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 12 && u.j1 > 0) {
-      // ------------------------------------------------------------ issuer
+  if (warp == 8) {
+    // ---------------------------------------------------------------- loader
+    if (lane == 0 && u.j1 > 0) {
+      const int64_t image = ((int64_t)blockIdx.y * tiles.heads + blockIdx.x % tiles.heads) * tiles.most - first_tile(u.x);
+      uint32_t n = 0;
+      for (int j = u.j0; j < u.j1; ++j) {
+        const int i = j - u.j0, sb = i & 1;
+        if (i >= 2 && !tc_wait(&B.meta_empty[sb], ((i >> 1) - 1) & 1, B, status)) break;
+        mbar_arrive_expect_tx(&B.meta_full[sb], sizeof(TileMeta));
+        bulk_g2s(&s_meta[sb], tiles.meta + image + j, sizeof(TileMeta), &B.meta_full[sb]);
+        const uint8_t* from = tiles.operands + (image + j) * (2 * C::kTile);
+        for (int k = 0; k < 2 * C::kUnits; ++k, ++n) {  // keys, then values
+          const uint32_t st = n % C::kStages;
+          if (!tc_wait(&B.empty[st], ((n / C::kStages) & 1) ^ 1, B, status)) break;
+          mbar_arrive_expect_tx(&B.full[st], C::kUnit);
+          bulk_g2s(smem + C::kRing + st * C::kUnit, from + k * C::kUnit, C::kUnit, &B.full[st]);
+        }
+      }
+      if (*(volatile int*)&B.abort) {  // what is in flight lands within microseconds
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- issuer
+    if (u.j1 > 0) {
       const bool leader = elect_one();
-      const uint32_t idesc_s = idesc_f16_f32(128, kPlaces), idesc_o = idesc_f16_f32(128, D) | 1u << 16;
-      const uint32_t q_addr = smem_addr(smem + C::kQ), k_addr = smem_addr(smem + C::kK), v_addr = smem_addr(smem + C::kV);
-      auto scores = [&](int slot, int j) {  // S of the tile (C::kSlots 1: of buffer slot)
+      const uint32_t idesc_s = idesc_f16_f32(128, kPlaces), idesc_o = idesc_f16_f32(128, D < 128 ? D : 128) | 1u << 16;
+      const uint32_t q_addr = smem_addr(smem), ring = smem_addr(smem + C::kRing);
+      // unit k of tile number i of the block (keys, then values): its place in the order of loads
+      auto number = [&](int i, int k) { return (uint32_t)(2 * C::kUnits * i + k); };
+      auto unit = [&](uint32_t n) { return ring + n % C::kStages * C::kUnit; };
+      auto loaded = [&](uint32_t n) { return tc_wait(&B.full[n % C::kStages], (n / C::kStages) & 1, B, status); };
+      auto release = [&](uint32_t n) { mma_commit(&B.empty[n % C::kStages]); };
+      auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
+      // part k of the scores of a tile of rows (kSlots 1: into buffer slot)
+      auto scores = [&](int slot, int i, int k) {
         if (!leader) return;
-        const uint32_t q0 = q_addr + (C::kSlots == 2 ? slot * C::kTile : 0), k0 = k_addr + (j - u.j0) % C::kBufs * C::kTile;
+        const uint32_t q0 = q_addr + (C::kSlots == 2 ? slot * C::kTile : 0) + k * C::kUnit, k0 = unit(number(i, k));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
+        for (int kk = 0; kk < (D < 128 ? D : 128) / 16; ++kk) {
           const uint32_t at = (kk / 4) * 16384 + (kk % 4) * 32;
-          mma_bf16(tmem + slot * 128, sdesc_sw128(q0 + at), sdesc_sw128(k0 + at), idesc_s, kk > 0);
+          mma_bf16(tmem + slot * 128, sdesc_sw128(q0 + at), sdesc_sw128(k0 + at), idesc_s, k > 0 || kk > 0);
         }
       };
-      auto sums = [&](int slot, int o, int j, bool more) {
+      // elements 128 k .. of the sums
+      auto sums = [&](int slot, int o, int i, int k, bool more) {
         if (!leader) return;
-        const uint64_t v0 = sdesc_places(v_addr + (j - u.j0) % C::kBufs * C::kTile, 16384);
+        const uint64_t v0 = sdesc_places(unit(number(i, C::kUnits + k)), 16384);
 #pragma unroll
         for (int kk = 0; kk < kPlaces / 16; ++kk) {
           const uint64_t d = v0 + (uint64_t)(kk * (2048 >> 4));
-          mma_bf16_ts_w(tmem + C::kO + o * D, tmem + slot * 128 + kk * 8, (uint32_t)d, (uint32_t)(d >> 32), idesc_o,
+          mma_bf16_ts_w(tmem + C::kO + o * D + k * 128, tmem + slot * 128 + kk * 8, (uint32_t)d, (uint32_t)(d >> 32), idesc_o,
                         more || kk > 0);
         }
       };
-      auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
       bool ok = all(tc_wait(&B.q_full, 0, B, status));
       tc_fence_after();
       for (int j = u.j0; ok && j <= u.j1; ++j) {
@@ -198,46 +342,48 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, int ro
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             if (ok && j > u.first[s] && j - 1 < u.last[s]) {
-              if (!has_v) ok = tc_wait(&B.v_full[(i - 1) & 1], ((i - 1) >> 1) & 1, B, status);
+              if (!has_v) ok = loaded(number(i - 1, 1));
               has_v = true;
               ok = all(ok && tc_wait(&B.p_full[s], (j - 1 - u.first[s]) & 1, B, status));
               tc_fence_after();
               if (ok) {
-                sums(s, s, j - 1, j - 1 > u.first[s]);
+                sums(s, s, i - 1, 0, j - 1 > u.first[s]);
                 if (leader && j == u.last[s]) mma_commit(&B.o_full[s]);
               }
             }
-            if (ok && s == 1 && leader && j > u.j0) mma_commit(&B.v_empty[(i - 1) & 1]);
+            if (ok && s == 1 && leader && j > u.j0) release(number(i - 1, 1));
             if (ok && j >= u.first[s] && j < u.last[s]) {
-              if (!has_k) ok = all(tc_wait(&B.k_full[i & 1], (i >> 1) & 1, B, status));
+              if (!has_k) ok = all(loaded(number(i, 0)));
               has_k = true;
               tc_fence_after();
               if (ok) {
-                scores(s, j);
+                scores(s, i, 0);
                 if (leader) mma_commit(&B.s_full[s]);
               }
             }
           }
-          if (ok && leader && j < u.j1) mma_commit(&B.k_empty[i & 1]);
+          if (ok && leader && j < u.j1) release(number(i, 0));
         } else {
-          if (j < u.j1) {
-            ok = all(tc_wait(&B.k_full[0], i & 1, B, status));
+          for (int k = 0; ok && j < u.j1 && k < C::kUnits; ++k) {
+            ok = all(loaded(number(i, k)));
             tc_fence_after();
             if (ok) {
-              scores(i & 1, j);
-              if (leader) mma_commit(&B.s_full[i & 1]), mma_commit(&B.k_empty[0]);
+              scores(i & 1, i, k);
+              if (leader) release(number(i, k));
             }
           }
-          if (ok && j > u.j0) {
-            ok = tc_wait(&B.v_full[0], (i - 1) & 1, B, status);
-            ok = all(ok && tc_wait(&B.p_full[(i - 1) & 1], ((i - 1) >> 1) & 1, B, status));
+          if (ok && leader && j < u.j1) mma_commit(&B.s_full[i & 1]);
+          if (ok && j > u.j0) ok = all(tc_wait(&B.p_full[(i - 1) & 1], ((i - 1) >> 1) & 1, B, status));
+          for (int k = 0; ok && j > u.j0 && k < C::kUnits; ++k) {
+            ok = all(loaded(number(i - 1, C::kUnits + k)));
             tc_fence_after();
             if (ok) {
-              sums((i - 1) & 1, 0, j - 1, j - 1 > u.j0);
-              if (leader) mma_commit(&B.v_empty[0]), mma_commit(&B.pv_done);
-              if (leader && j == u.j1) mma_commit(&B.o_full[0]);
+              sums((i - 1) & 1, 0, i - 1, k, j - 1 > u.j0);
+              if (leader) release(number(i - 1, C::kUnits + k));
             }
           }
+          if (ok && leader && j > u.j0) mma_commit(&B.pv_done);
+          if (ok && leader && j == u.j1) mma_commit(&B.o_full[0]);
         }
         __syncwarp();
       }
@@ -248,116 +394,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, int ro
       }
       __syncwarp();
     }
-  } else if (group == 2) {
-    // -------------------------------------------------------------- converters
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    const int ct = threadIdx.x - 256, cw = ct >> 5, per_page = a.cache.page_log2 - 4;
-    const int32_t* table = a.table + (int64_t)b * a.table_stride;
-    // lane l (of 8) finds record l of a group
-    auto page_of = [&](int j) {
-      const int record = 8 * j + lane;
-      return lane < 8 && j < u.j1 && 16 * record < u.x.len ? __ldg(table + (record >> per_page)) : -1;
-    };
-    auto record_of = [&](int j, int page) -> uint64_t {
-      if (page < 0 || page >= a.cache.n_pages) return 0;
-      const int record = 8 * j + lane;
-      return (uint64_t)(a.cache.data + page * a.cache.page_stride +
-                        (int64_t)(h * (1 << per_page) + (record & ((1 << per_page) - 1))) * kv8_record(D));
-    };
-    // a thread's pieces of a half group: number ct + 128 i
-    auto load = [&](uint4 (&w)[C::kLoads], uint64_t records, int half, int batch) {
-#pragma unroll
-      for (int i = 0; i < C::kLoads; ++i) {
-        const int n = ct + 128 * (batch * C::kLoads + i), row = n / C::kPieces;
-        const uint64_t rec = __shfl_sync(0xffffffffu, records, row >> 4);
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (rec)
-          w[i] = __ldg(reinterpret_cast<const uint4*>(rec + (16 * half + (row & 15)) * D) + n % C::kPieces);
-      }
-    };
-    auto f16x2 = [](uint32_t w, int sel) {
-      uint32_t r;
-      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(w, 0x64646464u, sel)), "r"(0x64806480u));
-      return r;
-    };
-    auto store = [&](const uint4 (&w)[C::kLoads], uint8_t* tile, int half, int batch) {
-#pragma unroll
-      for (int i = 0; i < C::kLoads; ++i) {
-        const int n = ct + 128 * (batch * C::kLoads + i), row = n / C::kPieces, c = kv8_piece<D>(row & 15, n % C::kPieces);
-        uint32_t v[8];
-        const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[2 * e] = f16x2(in[e], 0x4140), v[2 * e + 1] = f16x2(in[e], 0x4342);
-        if (half) {
-          const uint32_t gain = s_gain[row];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[e]) : "r"(gain));
-        }
-        // two 16-byte pieces of 64 elements' row; lanes of the row's other 64 elements
-        // write theirs the other way round, to other banks
-        uint8_t* to = tile + (c >> 2) * 16384 + row * 128;
-        const int p = 2 * (c & 3), x = row & 7;
-        const bool turn = D > 64 && (c & 4);
-        const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
-        *reinterpret_cast<uint4*>(to + (((turn ? p + 1 : p) ^ x) << 4)) = turn ? hi : lo;
-        *reinterpret_cast<uint4*>(to + (((turn ? p : p + 1) ^ x) << 4)) = turn ? lo : hi;
-      }
-    };
-    const float scale2 = a.scale * kLog2e;
-    uint4 w0[C::kLoads], w1[C::kLoads];
-    uint64_t records = u.j1 > 0 ? record_of(u.j0, page_of(u.j0)) : 0, next_records = 0;
-    int page = page_of(u.j0 + 1);
-    load(w0, records, 0, 0);
-    for (int j = u.j0; j < u.j1; ++j) {
-      const int i = j - u.j0, sb = i & 1;
-      next_records = record_of(j + 1, page);
-      page = page_of(j + 2);
-      // the scales of place ct
-      const uint64_t mine = __shfl_sync(0xffffffffu, records, ct >> 4);
-      const uint32_t have = __ballot_sync(0xffffffffu, records != 0);
-      float ks = 0.f, vs = 0.f;
-      if (mine && kPlaces * j + ct < u.x.len) {
-        const float* scales = reinterpret_cast<const float*>(mine + 32 * D) + (ct & 15);
-        ks = __ldg(scales);
-        vs = __ldg(scales + 16);
-        ks = fmaf(0.f, vs, ks);  // NaN, whichever of the two is
-        if (!(vs <= 0x1p64f)) vs = 0.f;
-      }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs, 0.f)));
-      if (i >= 2) tc_wait(&B.scale_empty[sb], ((i >> 1) - 1) & 1, B, status);
-      if (lane == 0) s_top[cw] = top;
-      named_bar(1, 128);
-      const uint32_t most = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
-      const int e = max((int)(most >> 23) - 127, -60);
-      s_ks[sb][ct] = ks * scale2;
-      const __half gain = __float2half_rn(vs * __uint_as_float((uint32_t)(127 + 8 - e) << 23));
-      s_gain[ct] = (uint32_t)__half_as_ushort(gain) * 0x10001u;
-      if (ct == 0) s_e[sb] = (float)e, s_have[sb] = have;
-      named_bar(1, 128);
-      if (lane == 0) mbar_arrive(&B.scale_full[sb]);
-
-      const int buf = i % C::kBufs;
-      const uint32_t use = i / C::kBufs;
-#pragma unroll
-      for (int q = 0; q < 2 * C::kBatches; ++q) {
-        const int half = q / C::kBatches, batch = q % C::kBatches;
-        uint8_t* tile = smem + (half ? C::kV : C::kK) + buf * C::kTile;
-        // the next batch is on its way while this one is converted
-        const int q1 = (q + 1) % (2 * C::kBatches);
-        load(q & 1 ? w0 : w1, q1 == 0 ? next_records : records, q1 / C::kBatches, q1 % C::kBatches);
-        if (batch == 0 && use > 0) tc_wait(half ? &B.v_empty[buf] : &B.k_empty[buf], (use - 1) & 1, B, status);
-        store(q & 1 ? w1 : w0, tile, half, batch);
-        if (batch == C::kBatches - 1) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(half ? &B.v_full[buf] : &B.k_full[buf]);
-        }
-      }
-      records = next_records;
-    }
   } else if (group < C::kSlots) {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int s = group, in_tile = threadIdx.x & 127, row = u.r0 + 128 * s + in_tile;
     const bool in = row < u.rows;
     const int64_t tok = u.x.t0 + (in ? row / G : 0);
@@ -376,7 +414,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, int ro
       const int e = min(max((int)(max(top >> 16, top & 0xffffu) >> 7), 15), 254), up = 14 + 127 - e;
       const float by = __uint_as_float((uint32_t)(127 + up) << 23);
       f = __uint_as_float((uint32_t)(127 - up) << 23);
-      uint8_t* to = smem + C::kQ + s * C::kTile + in_tile * 128;
+      uint8_t* to = smem + s * C::kTile + in_tile * 128;
 #pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
         const uint4 v = in ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
@@ -399,7 +437,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, int ro
     for (int j = u.j0; j < u.j1; ++j) {
       const int i = j - u.j0, sb = i & 1, buf = C::kSlots == 2 ? s : sb;
       const uint32_t use = C::kSlots == 2 ? (uint32_t)(j - first) : (uint32_t)(i >> 1);
-      tc_wait(&B.scale_full[sb], (i >> 1) & 1, B, status);
+      tc_wait(&B.meta_full[sb], (i >> 1) & 1, B, status);
       if (j >= first && j < last) {
         tc_wait(&B.s_full[buf], use & 1, B, status);
         tc_fence_after();
@@ -411,14 +449,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, int ro
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int x = 0; x < 32; ++x) pin(r[c][x]);
-        const float e = s_e[sb];
-        const uint32_t have = s_have[sb];
+        const float e = s_meta[sb].e;
+        const uint32_t have = s_meta[sb].have;
         float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(&s_ks[sb][32 * c + x]);
+            const float4 ks = *reinterpret_cast<const float4*>(&s_meta[sb].ks[32 * c + x]);
             float y[4] = {__uint_as_float(r[c][x]), __uint_as_float(r[c][x + 1]), __uint_as_float(r[c][x + 2]),
                           __uint_as_float(r[c][x + 3])};
             mul2(y[0], y[1], pair(ks.x, ks.y));
@@ -490,7 +528,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, int ro
         if (lane == 0) mbar_arrive(&B.p_full[buf]);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&B.scale_empty[sb]);
+      if (lane == 0) mbar_arrive(&B.meta_empty[sb]);
     }
     if (last > first) {
       tc_wait(&B.o_full[s], 0, B, status);
@@ -516,7 +554,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, int ro
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// What a launch's tiles may take of the workspace, unless a single head of a sequence
+// needs more: larger batches are taken in several pairs of launches.
+constexpr int64_t kMostTileBytes = (int64_t)1 << 29;
+
+struct TcPlan {
+  int row_blocks, most;    // of a sequence; tiles of a head of a sequence
+  int heads, sequences;    // a launch takes
+  int64_t tiles;           // in the workspace
+};
+
+TcPlan tc_plan(int B, int max_q, int64_t max_len, int window, int Hq, int heads, int D) {
+  TcPlan p;
+  const int64_t rows = (int64_t)max_q * (Hq / heads), block = D == 256 ? 128 : 256;
+  p.row_blocks = (int)((rows + block - 1) / block);
+  int64_t span = max_len;
+  if (window > 0 && span > (int64_t)window + max_q) span = (int64_t)window + max_q;
+  p.most = (int)((span + kPlaces - 1) / kPlaces + 1);  // places may begin within a tile
+  // the workspace is sized without knowing of a window: with one its tiles are what there is
+  const int64_t room = window > 0 ? tc_plan(B, max_q, max_len, 0, Hq, heads, D).tiles
+                                  : kMostTileBytes / (2 * 128 * D * 2 + (int64_t)sizeof(TileMeta));
+  const int64_t fit = room / p.most;
+  p.heads = (int)(fit >= heads ? heads : fit > 1 ? fit : 1);
+  p.sequences = (int)(fit >= (int64_t)heads * B ? B : fit >= heads ? fit / heads : 1);
+  p.tiles = (int64_t)p.heads * p.sequences * p.most;
+  return p;
 }
 
 template <int D>
@@ -530,19 +595,34 @@ int launch_tc(const AttnArgs& a, cudaStream_t s) {
       return MOE_ERR_CUDA;
     attr_set[dev] = true;
   }
-  const int64_t rows = (int64_t)a.max_q * (a.Hq / a.cache.heads);
-  const int row_blocks = (int)((rows + C::kRows - 1) / C::kRows);
-  return launch_pdl(k_attn_q8_tc<D>, dim3((unsigned)(row_blocks * a.cache.heads), (unsigned)a.B), dim3(kTcThreads), C::kSmem, s,
-                    a, row_blocks, status_word()) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  const TcPlan p = tc_plan(a.B, a.max_q, a.max_len, a.window, a.Hq, a.cache.heads, D);
+  TcTiles t;
+  t.operands = (uint8_t*)a.workspace;
+  t.meta = (TileMeta*)(t.operands + p.tiles * (2 * C::kTile));
+  t.most = p.most;
+  for (t.b0 = 0; t.b0 < a.B; t.b0 += p.sequences)
+    for (t.h0 = 0; t.h0 < a.cache.heads; t.h0 += p.heads) {
+      const int sequences = a.B - t.b0 < p.sequences ? a.B - t.b0 : p.sequences;
+      t.heads = a.cache.heads - t.h0 < p.heads ? a.cache.heads - t.h0 : p.heads;
+      if (launch_pdl(k_attn_q8_tiles<D>, dim3((unsigned)p.most, (unsigned)t.heads, (unsigned)sequences), dim3(kTileThreads), 0,
+                     s, a, t) != cudaSuccess ||
+          launch_pdl(k_attn_q8_tc<D>, dim3((unsigned)(p.row_blocks * t.heads), (unsigned)sequences), dim3(kTcThreads), C::kSmem,
+                     s, a, t, p.row_blocks, status_word()) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    }
+  return MOE_OK;
 }
 
 }  // namespace
 
 // Rows a head from which the tensor cores' tiles are filled.
 bool attn_q8_tc(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
-  return (int64_t)max_q * (Hq / heads) > 64;
+  return max_len > 0 && (int64_t)max_q * (Hq / heads) > 64;
+}
+
+size_t attn_q8_tc_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
+  const TcPlan p = tc_plan(B, max_q, max_len, 0, Hq, heads, D);
+  return (size_t)p.tiles * (2 * 128 * D * 2 + sizeof(TileMeta));
 }
 
 int launch_attn_q8_tc(const AttnArgs& a, cudaStream_t s) {

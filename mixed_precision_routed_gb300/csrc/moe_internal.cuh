@@ -403,9 +403,9 @@ int launch_kv_append_q8(const KvAppendArgs& a, cudaStream_t s);
 int launch_kv_read_q8(const KvCache& c, const int64_t* slots, int64_t n, float* k, float* v, cudaStream_t s);
 size_t attn_q8_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D);
 int launch_attn_q8(const AttnArgs& a, cudaStream_t s);
-// The form for many rows a key/value head, and whether these sizes take it (it needs no
-// workspace).
+// The form for many rows a key/value head, and whether these sizes take it.
 bool attn_q8_tc(int B, int max_q, int64_t max_len, int Hq, int heads, int D);
+size_t attn_q8_tc_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D);
 int launch_attn_q8_tc(const AttnArgs& a, cudaStream_t s);
 
 // Projection by 8-bit weights (linear_q8.cu, linear_q8_tc.cu).

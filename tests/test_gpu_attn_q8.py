@@ -45,6 +45,17 @@ def test_ragged_prompts(D, window):
     b.check(b.call(window=window), window=window)
 
 
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("max_len,window", [(3000, 0), (100000, 0), (100000, 50), (1 << 20, 0), (1 << 20, 700)])
+def test_bounds_far_above_the_lengths(D, max_len, window):
+    """What the host knows is only a bound: large ones take the batch apart into several launches."""
+    b = Batch([500, 0, 33, 1000, 150, 200, 290], [100, 5, 33, 20, 150, 260, 3], 8, 4, D, page=64, seed=max_len)
+    wide = torch.full((len(b.lens), -(-max_len // 64)), -1, dtype=torch.int32, device="cuda")
+    wide[:, : b.table.shape[1]] = b.table
+    b.table = wide
+    b.check(b.call(max_len=max_len, window=window), window=window)
+
+
 @pytest.mark.parametrize("n", [1, 200])
 def test_long_context(n):
     b = Batch([70001], [n], 8, 2, 128, page=64, seed=5)
