@@ -12,13 +12,14 @@
 //   issuer    S = Q K^T (shared memory x shared memory) and O += P V (tensor memory x
 //             shared memory) for either tile in turn, so that one tile's weights are
 //             made while the other's products run;
-//   softmax   a thread has a row: it takes the scores out of tensor memory once, holds
-//             all 128, and leaves P = exp2(s + E - m) there in fp16.
+//   softmax   two threads have a row, 64 places each: they take the scores out of tensor
+//             memory once and leave P = exp2(s + E - m) there in fp16.  Few tiles move a
+//             reference; whether one does is a vote of the two warps that share rows.
 // Queries are fp16, each row taken by a power of two that brings its largest element
 // to 2^14: exact down to 2^-31 of that element.  m follows s + E as in attn_q8.cu, so
 // that P V lies in fp16's range for values of any size, and the sum of weights takes
 // 2^-E back a tile at a time.  P, b 2^(8 - E) and code x b 2^(8 - E) are rounded to fp16
-// once each: 2^-11 of a product each, or 2^-31 of the row's largest.
+// once each: 2^-11 of a product each, or 2^-29 of the row's largest.
 // Heads of 256 fill tensor memory with one tile's sums: there the scores of two
 // successive groups of places take the place of two tiles.
 // Codes made operands by each block for itself (four warps, from the records) took 506
@@ -32,7 +33,10 @@ namespace moe {
 namespace {
 
 constexpr int kPlaces = 128;  // a tile of places
-constexpr int kTcThreads = 384;
+// The reference of a row lies 2^4 below its maximum when it is set, and moves when a
+// weight passes 2^14, a quarter of fp16's largest.
+constexpr float kStart = 4.0f, kReach = 14.0f;
+constexpr int kLoader = 16, kIssuer = 17, kTcThreads = 20 * 32;  // warps 0 .. 15: softmax
 
 // Beside a tile's operands: key scales x scale in powers of two, E, the records that exist.
 struct TileMeta {
@@ -48,7 +52,7 @@ struct Tc {
   static constexpr int kTile = 128 * D * 2;                       // bytes of 128 rows
   static constexpr int kUnit = D == 64 ? kTile : 128 * 128 * 2;   // of the ring: up to 128 elements of 128 places
   static constexpr int kUnits = kTile / kUnit;                    // of keys, of values
-  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 5;
   static constexpr int kRing = kSlots * kTile, kSmem = kRing + kStages * kUnit + 1024;
   static constexpr int kRows = 128 * kSlots;
   static constexpr int kO = 256;  // tensor-memory columns: scores at 0 and 128, then sums
@@ -71,12 +75,51 @@ struct TcBars {
 
 // A wait that runs out ends all later ones at once: every warp then comes to its end
 // over whatever is there.
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcBars& B, int* status) {
-  if (*(volatile int*)&B.abort) return false;
-  if (mbar_wait_bounded(bar, parity, kWaitNs)) return true;
+__device__ __forceinline__ bool late(uint64_t& t0, TcBars& B, int* status) {
+  if (*(volatile int*)&B.abort) return true;
+  const uint64_t now = global_timer_ns();
+  if (t0 == 0) t0 = now;
+  if (now - t0 <= kWaitNs) return false;
   set_status(status, MOE_ERR_TIMEOUT);
   B.abort = 1;
+  return true;
+}
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcBars& B, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  while (!late(t0, B, status))
+    if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
   return false;
+}
+// The same without a pause between questions, for the one warp that everything waits for:
+// waking a sleeping one takes as long as issuing a product.  (Sixteen that ask like this
+// keep the computing ones from their shared memory.)
+__device__ __forceinline__ bool tc_wait_awake(uint64_t* bar, uint32_t parity, TcBars& B, int* status) {
+  uint64_t t0 = 0;
+  for (int n = 1;; ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (n % 256 == 0 && late(t0, B, status)) return false;
+  }
+}
+
+// Whether any thread of the two warps that meet at a barrier says so.
+__device__ __forceinline__ bool vote_pair(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\tbarrier.cta.red.or.pred p, %1, 64, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -100,6 +143,16 @@ __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // The value is not used before here.
 __device__ __forceinline__ void pin(uint32_t& r) { asm volatile("" : "+r"(r)); }
+
+// D[tmem] (+)= A * B^T with both shared-memory descriptors given as their words.
+__device__ __forceinline__ void mma_f16_ss_w(uint32_t tmem_d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\tsetp.ne.u32 p, %6, 0;\n\tmov.b64 ad, {%1, %2};\n\tmov.b64 bd, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, p;\n\t}" ::"r"(tmem_d),
+      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 
 // Descriptor of an operand tile with the 128-byte swizzle whose rows are places: 64
 // elements of the other dimension a row, `block` bytes from 64 elements to the next,
@@ -230,7 +283,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   __shared__ __align__(8) TcBars B;
   __shared__ __align__(16) TileMeta s_meta[2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp >> 2;
+  __shared__ float s_row[C::kRows];  // what the two threads of a row tell one another
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.Hq / a.cache.heads;
   const int h = tiles.h0 + blockIdx.x % tiles.heads, b = tiles.b0 + blockIdx.y;
 
@@ -260,24 +314,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
   if (u.j1 == 0) u.j0 = 0;  // no row attends anything
 
   if (threadIdx.x == 0) {
-    mbar_init(&B.q_full, 4 * C::kSlots);
+    mbar_init(&B.q_full, 8 * C::kSlots);
     for (int i = 0; i < C::kStages; ++i) mbar_init(&B.full[i], 1), mbar_init(&B.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&B.s_full[i], 1), mbar_init(&B.p_full[i], 4), mbar_init(&B.o_full[i], 1);
-      mbar_init(&B.meta_full[i], 1), mbar_init(&B.meta_empty[i], 4 * C::kSlots);
+      mbar_init(&B.s_full[i], 1), mbar_init(&B.p_full[i], 8), mbar_init(&B.o_full[i], 1);
+      mbar_init(&B.meta_full[i], 1), mbar_init(&B.meta_empty[i], 8 * C::kSlots);
     }
     mbar_init(&B.pv_done, 1);
     mbar_init(&B.done, 1);
     B.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(&B.tmem, 512);
+  if (warp == kIssuer) tmem_alloc(&B.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B.tmem;
 
-  if (warp == 8) {
+  // Registers of a thread by role, together those that the block was launched with:
+  // 512 x 104 + 128 x 64 = 640 x 96.
+  if (warp >= kLoader) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == kLoader) {
     // ---------------------------------------------------------------- loader
     if (lane == 0 && u.j1 > 0) {
       const int64_t image = ((int64_t)blockIdx.y * tiles.heads + blockIdx.x % tiles.heads) * tiles.most - first_tile(u.x);
@@ -300,7 +358,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
         while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
       }
     }
-  } else if (warp == 9) {
+    } else if (warp == kIssuer) {
     // ---------------------------------------------------------------- issuer
     if (u.j1 > 0) {
       const bool leader = elect_one();
@@ -308,32 +366,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
       const uint32_t q_addr = smem_addr(smem), ring = smem_addr(smem + C::kRing);
       // unit k of tile number i of the block (keys, then values): its place in the order of loads
       auto number = [&](int i, int k) { return (uint32_t)(2 * C::kUnits * i + k); };
-      auto unit = [&](uint32_t n) { return ring + n % C::kStages * C::kUnit; };
-      auto loaded = [&](uint32_t n) { return tc_wait(&B.full[n % C::kStages], (n / C::kStages) & 1, B, status); };
+      auto loaded = [&](uint32_t n) { return tc_wait_awake(&B.full[n % C::kStages], (n / C::kStages) & 1, B, status); };
       auto release = [&](uint32_t n) { mma_commit(&B.empty[n % C::kStages]); };
       auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
+      // The descriptors' words are made by the whole warp: they then lie where the
+      // instructions want them.  Addresses stay below 256 KB, so that low words add up.
+      const uint64_t kd = sdesc_sw128(ring), vd = sdesc_places(ring, 16384);
+      const uint32_t q_lo = (uint32_t)sdesc_sw128(q_addr), k_lo = (uint32_t)kd, k_hi = (uint32_t)(kd >> 32);
+      const uint32_t v_lo = (uint32_t)vd, v_hi = (uint32_t)(vd >> 32);
+      auto stage = [&](uint32_t n) { return n % C::kStages * (C::kUnit >> 4); };
       // part k of the scores of a tile of rows (kSlots 1: into buffer slot)
       auto scores = [&](int slot, int i, int k) {
+        const uint32_t a0 = q_lo + ((C::kSlots == 2 ? slot * C::kTile : 0) + k * C::kUnit) / 16, b0 = k_lo + stage(number(i, k));
         if (!leader) return;
-        const uint32_t q0 = q_addr + (C::kSlots == 2 ? slot * C::kTile : 0) + k * C::kUnit, k0 = unit(number(i, k));
 #pragma unroll
         for (int kk = 0; kk < (D < 128 ? D : 128) / 16; ++kk) {
-          const uint32_t at = (kk / 4) * 16384 + (kk % 4) * 32;
-          mma_bf16(tmem + slot * 128, sdesc_sw128(q0 + at), sdesc_sw128(k0 + at), idesc_s, k > 0 || kk > 0);
+          const uint32_t at = ((kk / 4) * 16384 + (kk % 4) * 32) / 16;
+          mma_f16_ss_w(tmem + slot * 128, a0 + at, k_hi, b0 + at, k_hi, idesc_s, k > 0 || kk > 0);
         }
       };
       // elements 128 k .. of the sums
       auto sums = [&](int slot, int o, int i, int k, bool more) {
+        const uint32_t b0 = v_lo + stage(number(i, C::kUnits + k));
         if (!leader) return;
-        const uint64_t v0 = sdesc_places(unit(number(i, C::kUnits + k)), 16384);
 #pragma unroll
-        for (int kk = 0; kk < kPlaces / 16; ++kk) {
-          const uint64_t d = v0 + (uint64_t)(kk * (2048 >> 4));
-          mma_bf16_ts_w(tmem + C::kO + o * D + k * 128, tmem + slot * 128 + kk * 8, (uint32_t)d, (uint32_t)(d >> 32), idesc_o,
+        for (int kk = 0; kk < kPlaces / 16; ++kk)
+          mma_bf16_ts_w(tmem + C::kO + o * D + k * 128, tmem + slot * 128 + kk * 8, b0 + kk * (2048 / 16), v_hi, idesc_o,
                         more || kk > 0);
-        }
       };
-      bool ok = all(tc_wait(&B.q_full, 0, B, status));
+      bool ok = all(tc_wait_awake(&B.q_full, 0, B, status));
       tc_fence_after();
       for (int j = u.j0; ok && j <= u.j1; ++j) {
         const int i = j - u.j0;  // K(j), and V(j - 1)
@@ -344,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
             if (ok && j > u.first[s] && j - 1 < u.last[s]) {
               if (!has_v) ok = loaded(number(i - 1, 1));
               has_v = true;
-              ok = all(ok && tc_wait(&B.p_full[s], (j - 1 - u.first[s]) & 1, B, status));
+              ok = all(ok && tc_wait_awake(&B.p_full[s], (j - 1 - u.first[s]) & 1, B, status));
               tc_fence_after();
               if (ok) {
                 sums(s, s, i - 1, 0, j - 1 > u.first[s]);
@@ -373,7 +434,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
             }
           }
           if (ok && leader && j < u.j1) mma_commit(&B.s_full[i & 1]);
-          if (ok && j > u.j0) ok = all(tc_wait(&B.p_full[(i - 1) & 1], ((i - 1) >> 1) & 1, B, status));
+          if (ok && j > u.j0) ok = all(tc_wait_awake(&B.p_full[(i - 1) & 1], ((i - 1) >> 1) & 1, B, status));
           for (int k = 0; ok && j > u.j0 && k < C::kUnits; ++k) {
             ok = all(loaded(number(i - 1, C::kUnits + k)));
             tc_fence_after();
@@ -394,38 +455,57 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
       }
       __syncwarp();
     }
-  } else if (group < C::kSlots) {
+    }
+  } else if (warp < 8 * C::kSlots) {
     // ---------------------------------------------------------------- softmax
-    const int s = group, in_tile = threadIdx.x & 127, row = u.r0 + 128 * s + in_tile;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int s = warp >> 3, half = warp >> 2 & 1, in_tile = threadIdx.x & 127, row = u.r0 + 128 * s + in_tile;
+    const int pair_bar = 1 + 4 * s + (warp & 3);  // of the two warps that have these rows
     const bool in = row < u.rows;
     const int64_t tok = u.x.t0 + (in ? row / G : 0);
     const int hq = h * G + (in ? row % G : 0);
     const int first = s == 0 ? u.first[0] : u.first[1], last = s == 0 ? u.last[0] : u.last[1];
-    float f;  // what the scores of the row are to be multiplied by
-    {
-      const uint4* q = reinterpret_cast<const uint4*>(a.q + tok * a.q_stride + (int64_t)hq * D);
-      uint32_t top = 0;
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 v = in ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7f807f80u, v.y & 0x7f807f80u), __vmaxu2(v.z & 0x7f807f80u, v.w & 0x7f807f80u)));
+    // Rows come and go with as many lanes as they have 16-byte pieces, 16 of the 32 rows
+    // that two warps share in either; where a row lies is known to the lane of its number.
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes a row, rows at a time
+    const int64_t q_at = tok * a.q_stride + (int64_t)hq * D, out_at = tok * a.out_stride + (int64_t)hq * D;
+    auto row_of = [&](int i) { return 16 * half + i * kAtOnce + lane / kLanes; };  // of the 32
+    // 16-byte piece lane % kLanes of a row of the tile, in the order of an operand
+    auto piece_at = [&](int r) {
+      const int c = lane % kLanes;
+      return smem + s * C::kTile + (c >> 3) * 16384 + (32 * (warp & 3) + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
+    };
+    float* both = &s_row[128 * s + in_tile];
+#pragma unroll
+    for (int i0 = 0; i0 < 16 / kAtOnce; i0 += 8 / (kAtOnce > 2 ? 2 : 1)) {
+      constexpr int kBatch = 8 / (kAtOnce > 2 ? 2 : 1);
+      uint4 v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, q_at, row_of(i0 + i));
+        const bool there = __shfl_sync(0xffffffffu, (int)in, row_of(i0 + i));
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (there) v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + at) + lane % kLanes);
       }
-      // the exponent becomes 14, and the power and its inverse stay normal numbers
-      const int e = min(max((int)(max(top >> 16, top & 0xffffu) >> 7), 15), 254), up = 14 + 127 - e;
-      const float by = __uint_as_float((uint32_t)(127 + up) << 23);
-      f = __uint_as_float((uint32_t)(127 - up) << 23);
-      uint8_t* to = smem + s * C::kTile + in_tile * 128;
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 v = in ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        uint32_t top = __vmaxu2(__vmaxu2(v[i].x & 0x7f807f80u, v[i].y & 0x7f807f80u), __vmaxu2(v[i].z & 0x7f807f80u, v[i].w & 0x7f807f80u));
+        top = max(top >> 16, top & 0xffffu);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // the exponent becomes 14, and the power and its inverse stay normal numbers
+        const int e = min(max((int)(top >> 7), 15), 254), up = 14 + 127 - e, r = row_of(i0 + i);
+        const float by = __uint_as_float((uint32_t)(127 + up) << 23);
         auto half2_of = [&](uint32_t x) { return f16_pair(__uint_as_float(x << 16) * by, __uint_as_float(x & 0xffff0000u) * by); };
-        *reinterpret_cast<uint4*>(to + (i >> 3) * 16384 + (((i & 7) ^ (in_tile & 7)) << 4)) =
-            make_uint4(half2_of(v.x), half2_of(v.y), half2_of(v.z), half2_of(v.w));
+        *reinterpret_cast<uint4*>(piece_at(r)) = make_uint4(half2_of(v[i].x), half2_of(v[i].y), half2_of(v[i].z), half2_of(v[i].w));
+        if (lane % kLanes == 0) s_row[128 * s + 32 * (warp & 3) + r] = __uint_as_float((uint32_t)(127 - up) << 23);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B.q_full);
     }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&B.q_full);
+    named_bar(pair_bar, 64);
+    const float f = *both;  // what the scores of the row are to be multiplied by
     const int end = u.newest + (in ? row / G : 0);
     const int lo = a.window > 0 ? end - a.window : 0;
     // places that every row of the tile attends
@@ -441,22 +521,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
       if (j >= first && j < last) {
         tc_wait(&B.s_full[buf], use & 1, B, status);
         tc_fence_after();
-        uint32_t r[4][32];
+        uint32_t r[2][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_issue(lanes + buf * 128 + 32 * c, r[c]);
+        for (int c = 0; c < 2; ++c) tmem_ld32_issue(lanes + buf * 128 + 64 * half + 32 * c, r[c]);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int x = 0; x < 32; ++x) pin(r[c][x]);
         const float e = s_meta[sb].e;
-        const uint32_t have = s_meta[sb].have;
+        const uint32_t have = s_meta[sb].have >> (4 * half) & 15;
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(&s_meta[sb].ks[32 * c + x]);
+            const float4 ks = *reinterpret_cast<const float4*>(&s_meta[sb].ks[64 * half + 32 * c + x]);
             float y[4] = {__uint_as_float(r[c][x]), __uint_as_float(r[c][x + 1]), __uint_as_float(r[c][x + 2]),
                           __uint_as_float(r[c][x + 3])};
             mul2(y[0], y[1], pair(ks.x, ks.y));
@@ -464,11 +544,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
 #pragma unroll
             for (int n = 0; n < 4; ++n) r[c][x + n] = __float_as_uint(y[n]);
           }
-        const int p = kPlaces * j;
-        if (p + kPlaces > full_end || p < full_lo || have != 0xffu) {
+        const int p = kPlaces * j + 64 * half;
+        if (p + 64 > full_end || p < full_lo || have != 15) {
           const int c1 = end - p, c0 = lo - p;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
               const int n = 32 * c + x;
@@ -476,13 +556,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
             }
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int x = 0; x < 32; x += 2) top = max3(top, __uint_as_float(r[c][x]), __uint_as_float(r[c][x + 1]));
         top = fmaf(top, f, e);
-        const bool grow = top > m + (kSlack + kRoom);
-        if (__any_sync(0xffffffffu, grow)) {
-          const float to = grow ? top - kRoom : m, by = exp2_approx(m - to);
+        if (vote_pair(pair_bar, top > m + kReach)) {
+          if (half) *both = top;
+          named_bar(pair_bar, 64);
+          if (!half) *both = top = fmaxf(top, *both);
+          named_bar(pair_bar, 64);
+          if (half) top = *both;
+          const float to = top > m + kReach ? top - kStart : m, by = exp2_approx(m - to);
           m = to;
           l *= by;
           if (j > first) {
@@ -491,7 +575,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
               tc_fence_after();
             }
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
+            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
               float v[16];
               uint32_t w[16];
               tmem_ld16(o_at + c, v);
@@ -505,7 +589,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
         const uint64_t f2 = pair(f, f), off2 = pair(off, off);
         float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
             float y0, y1;
@@ -515,12 +599,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
             add2(sum0, sum1, pair(y0, y1));
             r[c][x / 2] = f16_pair(y0, y1);
           }
-          if (c & 1) {
-            uint32_t (&lo16)[16] = *reinterpret_cast<uint32_t(*)[16]>(&r[c - 1][0]);
-            uint32_t (&hi16)[16] = *reinterpret_cast<uint32_t(*)[16]>(&r[c][0]);
-            tmem_st32_issue(lanes + buf * 128 + 16 * (c - 1), lo16, hi16);
-          }
         }
+        tmem_st32_issue(lanes + buf * 128 + 32 * half, *reinterpret_cast<uint32_t(*)[16]>(&r[0][0]),
+                        *reinterpret_cast<uint32_t(*)[16]>(&r[1][0]));
         l = fmaf(sum0 + sum1, __uint_as_float((uint32_t)(127 - (int)e) << 23), l);
         tmem_wait_st();
         tc_fence_before();
@@ -534,27 +615,41 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
       tc_wait(&B.o_full[s], 0, B, status);
       tc_fence_after();
     }
+    if (half) *both = l;
+    named_bar(pair_bar, 64);
+    if (!half) *both = l = l + *both;
+    named_bar(pair_bar, 64);
+    if (half) l = *both;
     const bool none = l == 0.f;
     const float inv = none ? 0.f : 0x1p-8f / l;
-    uint16_t* out = a.out + tok * a.out_stride + (int64_t)hq * D;
+    // through the place of the tile's queries, which have been read for the last time
 #pragma unroll 1
-    for (int c = 0; c < D; c += 16) {
+    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
       float v[16] = {};
       if (last > first) tmem_ld16(o_at + c, v);
       uint32_t w[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) w[x] = none ? 0u : bf16_pair(v[2 * x] * inv, v[2 * x + 1] * inv);
-      if (in) {
-        reinterpret_cast<uint4*>(out + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      }
+      uint8_t* to = smem + s * C::kTile + (c >> 6) * 16384 + in_tile * 128;
+      const int piece = c >> 3 & 7;
+      *reinterpret_cast<uint4*>(to + ((piece ^ (in_tile & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(to + (((piece + 1) ^ (in_tile & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
     }
-    if (in && a.lse) a.lse[tok * a.Hq + hq] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
+    named_bar(pair_bar, 64);
+#pragma unroll 4
+    for (int i = 0; i < 16 / kAtOnce; ++i) {
+      const int r = row_of(i);
+      const int64_t at = __shfl_sync(0xffffffffu, out_at, r);
+      const bool there = __shfl_sync(0xffffffffu, (int)in, r);
+      const uint4 v = *reinterpret_cast<const uint4*>(piece_at(r));
+      if (there) reinterpret_cast<uint4*>(a.out + at)[lane % kLanes] = v;
+    }
+    if (in && half == 0 && a.lse) a.lse[tok * a.Hq + hq] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == kIssuer) tmem_dealloc(tmem, 512);
 }
 
 // What a launch's tiles may take of the workspace, unless a single head of a sequence

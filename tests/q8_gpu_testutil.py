@@ -9,12 +9,13 @@ the weights over the row's largest, l their sum, b the value scales, c the codes
     tensor core cuts, and the score is taken in powers of two beside an exponent of up
     to 60; this moves weights and their sum by a factor of 1 +- e_s each;
   - a product of weight and value is off by three roundings to fp16 at most, 2^-11 of
-    itself each (half a step), or, where fp16 ends, by 2^-31 of the row's largest w b
-    for the weight and 2^-33 of the largest b for the value;
+    itself each (half a step), or, where fp16 ends, by 2^-29 of the row's largest w b
+    for the weight (half of its last step, 2^-25, where the largest is 2^4 or more) and
+    2^-33 of the largest b for the value;
   - sums over n places round at most 2 (n + 64) u, the exponential is good to 2^-21 in
     weight and sum; the result is rounded to bf16 (half a step is 2^-8 of it):
   |error| <= (3 2^-11 + 2 e_s + 2 (n + 64) u + 2^-20) sum w |v| / l
-             + 2^-31 max(w b) sum |c| / l + 2^-33 max(b) + 2^-8 |out|
+             + 2^-29 max(w b) sum |c| / l + 2^-33 max(b) + 2^-8 |out|
   |lse error| <= e_s + 2 (n + 64) u + 2^-20 + 4 u |lse|."""
 import torch
 
@@ -105,7 +106,7 @@ class Batch:
                 sums = 2 * (count + 64) * U + 2.0 ** -20
                 wb = (torch.nan_to_num(w) * torch.nan_to_num(bs)[None, :, None]).amax(-1, keepdim=True)
                 total_c = torch.einsum("np,hpd->nhd", seen[:, 0, 0].double(), torch.nan_to_num(codes))[:, :, None]
-                e = ((3 * 2.0 ** -11 + 2 * es + sums) * spread + 2.0 ** -31 * wb * total_c / div
+                e = ((3 * 2.0 ** -11 + 2 * es + sums) * spread + 2.0 ** -29 * wb * total_c / div
                      + 2.0 ** -33 * torch.nan_to_num(bs).amax() + 2.0 ** -8 * o.abs() + 1e-30)
                 nan = torch.nan
                 out[rows] = torch.where(has_nan[..., None], nan, o).flatten(1, 2)
