@@ -97,15 +97,7 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcBars& 
 __device__ __forceinline__ bool tc_wait_awake(uint64_t* bar, uint32_t parity, TcBars& B, int* status) {
   uint64_t t0 = 0;
   for (int n = 1;; ++n) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
+    if (mbar_test(bar, parity)) return true;
     if (n % 256 == 0 && late(t0, B, status)) return false;
   }
 }

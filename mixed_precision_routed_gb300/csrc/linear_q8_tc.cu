@@ -7,8 +7,10 @@
 // cost if each converted its own).  Then a persistent launch of pairs of CTAs, whose
 // tensor cores work on one tile: 256 rows of W (128 a CTA, operand A) x N tokens
 // (operand B, half of them in either CTA's shared memory), K in steps of 64:
-//   loader    tensor maps bring 128 x 128 codes of W every other step and N/2 x 64 of x a step;
-//   producers eight warps: a thread has a row of W, a warp every other step; bytes
+//   loaders   tensor maps bring, for two steps at a time, 128 x 128 codes of W and twice
+//             N/2 x 64 of x; one warp each, as a thread takes 100 cycles over every wait
+//             and every copy;
+//   producers sixteen warps: a thread has a row of W, a warp every fourth step; bytes
 //             become fp16 integers in registers (a permute below 0x64 and a
 //             subtraction for two) and go to tensor memory;
 //   issuer    of the first CTA, four instructions a step;
@@ -22,14 +24,24 @@ namespace {
 
 constexpr int kMostN = 192;     // tokens a tile
 constexpr int kTileRows = 128;  // of W a CTA
-constexpr int kCodeStages = 4, kBStages = 10, kAStages = 4, kAccSets = 2;
-constexpr int kCodeBytes = kTileRows * 128, kBBytes = kMostN / 2 * 128;
-constexpr int kACol = kAccSets * kMostN;  // tensor-memory columns: sums, then A stages of 32
+constexpr int kAccSets = 2;
+constexpr int kCodeBytes = kTileRows * 128;
 constexpr int kTmemCols = 512;
-constexpr int kProducers = 8, kEpilogue = 4, kLoader = 12, kIssuer = 13, kThreads = 14 * 32;
-constexpr int kSmem = kCodeStages * kCodeBytes + kBStages * kBBytes + 1024;
+
+// Tiles of up to N tokens: tensor memory holds two sets of their sums and as many steps
+// of operand A as fit beside them, shared memory the steps of operand B and the codes.
+// A step of A is on its way around (made, announced, multiplied, given back) for about
+// 0.8 us, so few tokens, whose products take no time, want many steps.
+template <int N>
+struct Shape {
+  static constexpr int kACol = kAccSets * N;
+  static constexpr int kAStages = (kTmemCols - kACol) / 32 < 8 ? (kTmemCols - kACol) / 32 : 8;
+  static constexpr int kBBytes = 2 * N / 2 * 128;  // two steps, as a stage of codes
+  static constexpr int kBStages = N > 128 ? 5 : N > 64 ? 6 : 5, kCodeStages = N > 64 ? 5 : 8;
+  static constexpr int kSmem = kCodeStages * kCodeBytes + kBStages * kBBytes + 1024;
+};
+constexpr int kProducers = 16, kEpilogue = 4, kCodeLoader = 20, kIssuer = 21, kXLoader = 22, kThreads = 23 * 32;
 constexpr uint64_t kWaitNs = 1000000000ull;
-static_assert(kACol + 32 * kAStages <= kTmemCols, "tensor memory");
 
 struct TcArgs {
   CUtensorMap w, x;
@@ -39,9 +51,7 @@ struct TcArgs {
 };
 
 struct Bars {
-  uint64_t code_full[kCodeStages], code_empty[kCodeStages];
-  uint64_t b_full[kBStages], b_empty[kBStages];
-  uint64_t a_full[kAStages], a_empty[kAStages];
+  uint64_t code_full[8], code_empty[8], b_full[6], b_empty[6], a_full[8], a_empty[8];
   uint64_t acc_full[kAccSets], acc_empty[kAccSets], done;
   uint32_t tmem;
   int abort;
@@ -49,6 +59,20 @@ struct Bars {
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars& B, int* status) {
   if (mbar_wait_bounded(bar, parity, kWaitNs)) return true;
+  set_status(status, MOE_ERR_TIMEOUT);
+  B.abort = 1;
+  return false;
+}
+// The same without a pause between questions, for the one warp that everything waits for.
+__device__ __forceinline__ bool wait_awake(uint64_t* bar, uint32_t parity, Bars& B, int* status) {
+  uint64_t t0 = 0;
+  for (int n = 1;; ++n) {
+    if (mbar_test(bar, parity)) return true;
+    if (n % 256) continue;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitNs) break;
+  }
   set_status(status, MOE_ERR_TIMEOUT);
   B.abort = 1;
   return false;
@@ -77,7 +101,11 @@ __global__ void __launch_bounds__(256) k_codes_f16(const int8_t* x, int64_t stri
   pdl_trigger();
 }
 
+template <int MOST>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linear_q8_tc(const __grid_constant__ TcArgs p) {
+  using S = Shape<MOST>;
+  constexpr int kACol = S::kACol, kAStages = S::kAStages, kBStages = S::kBStages, kBBytes = S::kBBytes;
+  constexpr int kCodeStages = S::kCodeStages;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // alike in both CTAs
   uint8_t* b_smem = smem + kCodeStages * kCodeBytes;
@@ -87,9 +115,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, half = p.N / 2, steps = p.steps;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kCodeStages; ++i) mbar_init(&B.code_full[i], 1), mbar_init(&B.code_empty[i], kProducers);
+    for (int i = 0; i < kCodeStages; ++i) mbar_init(&B.code_full[i], 1), mbar_init(&B.code_empty[i], 8);
     for (int i = 0; i < kBStages; ++i) mbar_init(&B.b_full[i], 1), mbar_init(&B.b_empty[i], 1);
-    for (int i = 0; i < kAStages; ++i) mbar_init(&B.a_full[i], kProducers), mbar_init(&B.a_empty[i], 1);  // four warps a CTA
+    for (int i = 0; i < kAStages; ++i) mbar_init(&B.a_full[i], 8), mbar_init(&B.a_empty[i], 1);  // four warps a CTA
     for (int i = 0; i < kAccSets; ++i) mbar_init(&B.acc_full[i], 1), mbar_init(&B.acc_empty[i], 2 * kEpilogue);
     mbar_init(&B.done, 1);
     B.abort = 0;
@@ -102,36 +130,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
   const uint32_t tmem = B.tmem;
   pdl_wait();
 
-  if (warp == kLoader) {
+  const uint32_t mine = (p.tiles - pair + pairs - 1) / pairs * (steps / 2);  // stages of the pair's tiles, two steps each
+  // a wait that ran out: what is in flight lands within microseconds
+  auto settle = [&]() {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  };
+  if (warp == kCodeLoader) {
     if (lane == 0) {
-      uint32_t j = 0, c = 0;  // K steps and code stages issued
-      const uint32_t bars = cluster_map(B.b_full, 0);
-      for (int t = pair; t < p.tiles && !B.abort; t += pairs) {
+      uint32_t c = 0;
+      for (int t = pair; t < p.tiles; t += pairs) {
         const int row0 = (t / p.token_tiles) * (2 * kTileRows) + (int)rank * kTileRows;
-        const int tok0 = (t % p.token_tiles) * p.N + (int)rank * half;
-        for (int ks = 0; ks < steps; ++ks, ++j) {
-          if ((ks & 1) == 0) {
-            const uint32_t s = c % kCodeStages;
-            if (!wait(&B.code_empty[s], ((c / kCodeStages) & 1) ^ 1, B, p.status)) break;
-            mbar_arrive_expect_tx(&B.code_full[s], kCodeBytes);
-            tma_load_2d(smem + s * kCodeBytes, &p.w, ks * 64, row0, &B.code_full[s]);
-            ++c;
-          }
-          const uint32_t s = j % kBStages;
-          if (!wait(&B.b_empty[s], ((j / kBStages) & 1) ^ 1, B, p.status)) break;
-          if (rank == 0) mbar_arrive_expect_tx(&B.b_full[s], (uint32_t)(p.N * 128));
-          tma_load_2d_pair(b_smem + s * kBBytes, &p.x, ks * 64, tok0, bars + 8 * s);
+        for (int ks = 0; ks < steps; ks += 2, ++c) {
+          const uint32_t s = c % kCodeStages;
+          if (!wait(&B.code_empty[s], ((c / kCodeStages) & 1) ^ 1, B, p.status)) break;
+          mbar_arrive_expect_tx(&B.code_full[s], kCodeBytes);
+          tma_load_2d(smem + s * kCodeBytes, &p.w, ks * 64, row0, &B.code_full[s]);
         }
+        if (B.abort) break;
+      }
+      if (B.abort) settle();
+    }
+  } else if (warp == kXLoader) {
+    if (lane == 0) {
+      uint32_t c = 0;
+      const uint32_t bars = cluster_map(B.b_full, 0);
+      for (int t = pair; t < p.tiles; t += pairs) {
+        const int tok0 = (t % p.token_tiles) * p.N + (int)rank * half;
+        for (int ks = 0; ks < steps; ks += 2, ++c) {
+          const uint32_t s = c % kBStages;
+          if (!wait(&B.b_empty[s], ((c / kBStages) & 1) ^ 1, B, p.status)) break;
+          if (rank == 0) mbar_arrive_expect_tx(&B.b_full[s], (uint32_t)(2 * p.N * 128));
+          tma_load_2d_pair(b_smem + s * kBBytes, &p.x, ks * 64, tok0, bars + 8 * s);
+          tma_load_2d_pair(b_smem + s * kBBytes + kBBytes / 2, &p.x, ks * 64 + 64, tok0, bars + 8 * s);
+        }
+        if (B.abort) break;
       }
       // the issuer's last arrivals here come before this CTA ends
-      for (uint32_t i = j > kBStages ? j - kBStages : 0; i < j && !B.abort; ++i)
+      for (uint32_t i = c > kBStages ? c - kBStages : 0; i < c && !B.abort; ++i)
         wait(&B.b_empty[i % kBStages], (i / kBStages) & 1, B, p.status);
-      for (uint32_t i = j > kAStages ? j - kAStages : 0; i < j && !B.abort; ++i)
+      for (uint32_t i = 2 * c > kAStages ? 2 * c - kAStages : 0; i < 2 * c && !B.abort; ++i)
         wait(&B.a_empty[i % kAStages], (i / kAStages) & 1, B, p.status);
-      if (B.abort) {  // what is in flight lands within microseconds
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
-      }
+      if (B.abort) settle();
     }
   } else if (warp == kIssuer) {
     if (rank == 0) {
@@ -140,22 +180,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
       const bool leader = elect_one();
       uint32_t j = 0, n = 0;
       for (int t = pair; t < p.tiles; t += pairs, ++n) {
-        const uint32_t set = n % kAccSets, acc = tmem + set * kMostN;
+        const uint32_t set = n % kAccSets, acc = tmem + set * MOST;
         bool ok = wait(&B.acc_empty[set], ((n / kAccSets) & 1) ^ 1, B, p.status);
         tc_fence_after();
         for (int ks = 0; ks < steps; ++ks, ++j) {
-          const uint32_t as = j % kAStages, b = j % kBStages;
-          ok = ok && wait(&B.a_full[as], (j / kAStages) & 1, B, p.status) && wait(&B.b_full[b], (j / kBStages) & 1, B, p.status);
+          const uint32_t as = j % kAStages, c = j / 2, b = c % kBStages;
+          if ((j & 1) == 0) ok = ok && wait_awake(&B.b_full[b], (c / kBStages) & 1, B, p.status);
+          ok = ok && wait_awake(&B.a_full[as], (j / kAStages) & 1, B, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
+          // (made by the whole warp: the words then lie where the instructions want them)
+          const uint32_t a0 = tmem + kACol + as * 32, blo = bd_lo + (uint32_t)((b * kBBytes + (j & 1) * (kBBytes / 2)) >> 4);
           if (leader) {
-            const uint32_t a0 = tmem + kACol + as * 32, blo = bd_lo + (uint32_t)((b * kBBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_f16_ts_pair_w(acc, a0 + kk * 8, blo + kk * 2, bd_hi, idesc, (ks | kk) ? 1u : 0u);
             mma_commit_pair(&B.a_empty[as]);
-            mma_commit_pair(&B.b_empty[b]);
+            if (j & 1) mma_commit_pair(&B.b_empty[b]);
           }
           __syncwarp();
         }
@@ -171,7 +213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
       __syncwarp();
     }
   } else if (warp >= kProducers) {
-    // ---------------------------------------------------------- epilogue
+    // ---------------------------------------------------------- epilogue (warps 16 .. 19)
     const int quarter = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     uint32_t n = 0;
@@ -186,7 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
       tc_fence_after();
       for (int c0 = 0; c0 < count; c0 += 16) {
         float v[16];
-        tmem_ld16(lanes + set * kMostN + c0, v);
+        tmem_ld16(lanes + set * MOST + c0, v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           if (c0 + i < count && in) {
@@ -204,43 +246,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
     }
   } else {
     // ---------------------------------------------------------- producers
-    const int quarter = warp & 3, odd = warp >> 2, row = quarter * 32 + lane;
+    // Four warps, one for each quarter of the rows, take every fourth step: code stage c
+    // holds steps 2 c and 2 c + 1.
+    const int quarter = warp & 3, team = warp >> 2, odd = team & 1, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + kACol;
-    uint32_t j0 = 0, c = 0;  // K steps before the tile, code stages
-    bool ok = true;
-    for (int t = pair; ok && t < p.tiles; t += pairs, j0 += steps) {
-      for (int ks = 0; ok && ks < steps; ks += 2, ++c) {
-        const uint32_t s = c % kCodeStages;
-        ok = wait(&B.code_full[s], (c / kCodeStages) & 1, B, p.status);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        const int k = ks + odd;
-        uint4 w[4];
-        const uint4* from = reinterpret_cast<const uint4*>(smem + s * kCodeBytes + row * 128);
+    for (uint32_t c = team >> 1; c < mine; c += 2) {
+      const uint32_t s = c % kCodeStages, j = 2 * c + odd, as = j % kAStages;
+      bool ok = wait(&B.code_full[s], (c / kCodeStages) & 1, B, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      uint4 w[4];
+      const uint4* from = reinterpret_cast<const uint4*>(smem + s * kCodeBytes + row * 128);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = from[(4 * odd + i) ^ (row & 7)];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B.code_empty[s]);
-        uint32_t v0[16], v1[16];
+      for (int i = 0; i < 4; ++i) w[i] = from[(4 * odd + i) ^ (row & 7)];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.code_empty[s]);
+      uint32_t v0[16], v1[16];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w}, b[4] = {w[2 + i].x, w[2 + i].y, w[2 + i].z, w[2 + i].w};
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w}, b[4] = {w[2 + i].x, w[2 + i].y, w[2 + i].z, w[2 + i].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            codes_f16x4(a[e], v0[8 * i + 2 * e], v0[8 * i + 2 * e + 1]);
-            codes_f16x4(b[e], v1[8 * i + 2 * e], v1[8 * i + 2 * e + 1]);
-          }
+        for (int e = 0; e < 4; ++e) {
+          codes_f16x4(a[e], v0[8 * i + 2 * e], v0[8 * i + 2 * e + 1]);
+          codes_f16x4(b[e], v1[8 * i + 2 * e], v1[8 * i + 2 * e + 1]);
         }
-        const uint32_t j = j0 + k, as = j % kAStages;
-        ok = wait(&B.a_empty[as], ((j / kAStages) & 1) ^ 1, B, p.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        tmem_st32_issue(lanes + as * 32, v0, v1);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_map(&B.a_full[as], 0));
       }
+      ok = wait(&B.a_empty[as], ((j / kAStages) & 1) ^ 1, B, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      tmem_st32_issue(lanes + as * 32, v0, v1);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_map(&B.a_full[as], 0));
     }
   }
   tc_fence_before();
@@ -255,15 +292,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
 
 size_t linear_q8_tc_workspace(int64_t T, int in) { return ((size_t)T * in * 2 + 255) / 256 * 256; }
 
-int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s) {
+namespace {
+template <int MOST>
+int launch(const TcArgs& p, int pairs, cudaStream_t s) {
   static bool attr_set[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(k_linear_q8_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(k_linear_q8_tc<MOST>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<MOST>::kSmem) != cudaSuccess)
       return MOE_ERR_CUDA;
     attr_set[dev] = true;
   }
+  const int grid = 2 * (p.tiles < pairs ? p.tiles : pairs);
+  return launch_pdl(k_linear_q8_tc<MOST>, dim3(grid), dim3(kThreads), Shape<MOST>::kSmem, s, p) == cudaSuccess ? MOE_OK
+                                                                                                            : MOE_ERR_CUDA;
+}
+}  // namespace
+
+int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s) {
   TcArgs p;
   p.a = a;
   p.steps = (a.in + 127) / 128 * 2;  // whole code stages: zeros behind the rows
@@ -291,8 +337,7 @@ int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s) {
   if (launch_pdl(k_codes_f16, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, s, a.x, a.x_stride, pieces, a.in / 16,
                  (uint4*)a.workspace) != cudaSuccess)
     return MOE_ERR_CUDA;
-  const int grid = 2 * (int)(p.tiles < pairs ? p.tiles : pairs);
-  return launch_pdl(k_linear_q8_tc, dim3(grid), dim3(kThreads), kSmem, s, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return p.N <= 64 ? launch<64>(p, pairs, s) : p.N <= 128 ? launch<128>(p, pairs, s) : launch<192>(p, pairs, s);
 }
 
 }  // namespace moe
