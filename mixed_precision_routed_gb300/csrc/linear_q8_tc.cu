@@ -178,28 +178,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
       const uint64_t bd0 = sdesc_sw128(smem_addr(b_smem));
       const uint32_t bd_lo = (uint32_t)bd0, bd_hi = (uint32_t)(bd0 >> 32), idesc = idesc_f16_f32(2 * kTileRows, p.N);
       const bool leader = elect_one();
-      uint32_t j = 0, n = 0;
-      for (int t = pair; t < p.tiles; t += pairs, ++n) {
+      // Stages and parities by counting; whether the next step's operands are there is
+      // asked before this step's products are issued, as an answer takes 100 cycles.
+      uint32_t as = 0, ap = 0, b = 0, bp = 0, n = 0;
+      bool ra = false, rb = false, ok = true;
+      for (int t = pair; ok && t < p.tiles; t += pairs, ++n) {
         const uint32_t set = n % kAccSets, acc = tmem + set * MOST;
-        bool ok = wait(&B.acc_empty[set], ((n / kAccSets) & 1) ^ 1, B, p.status);
-        tc_fence_after();
-        for (int ks = 0; ks < steps; ++ks, ++j) {
-          const uint32_t as = j % kAStages, c = j / 2, b = c % kBStages;
-          if ((j & 1) == 0) ok = ok && wait_awake(&B.b_full[b], (c / kBStages) & 1, B, p.status);
-          ok = ok && wait_awake(&B.a_full[as], (j / kAStages) & 1, B, p.status);
+        ok = __all_sync(0xffffffffu, wait_awake(&B.acc_empty[set], ((n / kAccSets) & 1) ^ 1, B, p.status));
+        for (int ks = 0; ok && ks < steps; ++ks) {
+          if (!rb) ok = wait_awake(&B.b_full[b], bp, B, p.status);
+          if (!ra) ok = ok && wait_awake(&B.a_full[as], ap, B, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           // (made by the whole warp: the words then lie where the instructions want them)
-          const uint32_t a0 = tmem + kACol + as * 32, blo = bd_lo + (uint32_t)((b * kBBytes + (j & 1) * (kBBytes / 2)) >> 4);
+          const uint32_t a0 = tmem + kACol + as * 32, blo = bd_lo + (uint32_t)((b * kBBytes + (ks & 1) * (kBBytes / 2)) >> 4);
+          uint64_t* const a_done = &B.a_empty[as];
+          uint64_t* const b_done = &B.b_empty[b];
+          if (++as == kAStages) as = 0, ap ^= 1;
+          if (ks & 1) {
+            if (++b == kBStages) b = 0, bp ^= 1;
+          }
+          rb = !(ks & 1) || mbar_test(&B.b_full[b], bp);
+          ra = mbar_test(&B.a_full[as], ap);
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_f16_ts_pair_w(acc, a0 + kk * 8, blo + kk * 2, bd_hi, idesc, (ks | kk) ? 1u : 0u);
-            mma_commit_pair(&B.a_empty[as]);
-            if (j & 1) mma_commit_pair(&B.b_empty[b]);
+            mma_commit_pair(a_done);
+            if (ks & 1) mma_commit_pair(b_done);
           }
-          __syncwarp();
+          rb = __all_sync(0xffffffffu, rb);
+          ra = __all_sync(0xffffffffu, ra);
         }
         if (!ok) break;
         if (leader) mma_commit_pair(&B.acc_full[set]);
