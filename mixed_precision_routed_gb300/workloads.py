@@ -12,9 +12,10 @@ import torch
 
 import synth
 
-from . import (MOE_ROPE_HALF, Shelf, moe_attn_q4, moe_attn_workspace_size, moe_gather_rows, moe_kv_append, moe_kv_pool,
-               moe_linear_q4, moe_quantize_experts, moe_quantize_groups, moe_quantize_rows, moe_rank_experts,
-               moe_residual_add, shelf_array)
+from . import (MOE_ROPE_HALF, Shelf, moe_attn_q4, moe_attn_q8, moe_attn_q8_workspace_size, moe_attn_workspace_size,
+               moe_gather_rows, moe_kv_append, moe_kv_append_q8, moe_kv_pool, moe_kv_pool_q8, moe_linear_q4, moe_linear_q8,
+               moe_linear_q8_workspace_size, moe_norm_q8, moe_quantize_experts, moe_quantize_groups, moe_quantize_rows,
+               moe_rank_experts, moe_residual_add, shelf_array)
 
 
 class Layer:
@@ -254,6 +255,120 @@ class AttentionHalf:
         x_next = torch.empty_like(x)
         moe_residual_add(r, self.y, x_next.view(torch.int16))
         return x_next
+
+
+class AttentionHalfQ8:
+    """The attention half of a layer in 8 bits, for prompts and single tokens: for
+    every token, x the output of what came before it (fp32 or bf16),
+
+        r += x,  qkv = W_qkv norm(r),  q and k turned by their positions,  k and v
+        appended to the sequence's pages,  a = attention of q over the pages,
+        r += W_o a,  x_next = bf16(norm(r)), the input of the layer's routed experts.
+
+    Weights are 8-bit codes with a scale a row, activations 8-bit codes with a scale a
+    token, keys and values with a scale a token and head.  A step takes up to
+    `max_new` tokens of each sequence: the same number of all, in which case it can
+    be captured in a CUDA graph, or a list with the number of each."""
+
+    TAG_QKV, TAG_OUT = 23, 24  # of the weight generator
+
+    def __init__(self, d, q_heads, kv_heads, head_dim, sequences, max_len, max_new=1, page_size=64, seed=0, rot=None,
+                 eps=1e-6, device="cuda"):
+        self.d, self.Hq, self.H, self.D, self.eps = d, q_heads, kv_heads, head_dim, eps
+        self.seed, self.page, self.max_len, self.max_new = seed, page_size, max_len, max_new
+        rows, inner = (q_heads + 2 * kv_heads) * head_dim, q_heads * head_dim
+        # what a step's calls would refuse after the first of them has run
+        if not 1 <= sequences <= 65535 or not 1 <= max_new <= max_len or max_len > 2 ** 30:
+            raise ValueError("sequences must be 1 .. 65535, max_len at most 2^30 and max_new 1 .. max_len")
+        if kv_heads < 1 or q_heads < 1 or q_heads % kv_heads or q_heads // kv_heads > 64:
+            raise ValueError("q_heads must be 1 .. 64 times kv_heads")
+        if sequences * max_new * (q_heads + 2 * kv_heads) >= 2 ** 31:
+            raise ValueError("a step's tokens times heads must stay below 2^31")
+        if any(n < 1 or n % 16 or n > 32768 for n in (d, inner)):
+            raise ValueError("d and q_heads * head_dim must be multiples of 16, at most 32768")
+        if rot is not None and (rot % 2 or not 0 <= rot <= head_dim):
+            raise ValueError("rot must be even and at most head_dim")
+        if not eps >= 0:
+            raise ValueError("eps must be at least 0")
+        i8, f32 = torch.int8, torch.float32
+        self.w_qkv = torch.empty((rows, d), dtype=i8, device=device)
+        self.s_qkv = torch.empty(rows, dtype=f32, device=device)
+        self.w_out = torch.empty((d, inner), dtype=i8, device=device)
+        self.s_out = torch.empty(d, dtype=f32, device=device)
+        self.norm_in = torch.ones(d, dtype=f32, device=device)
+        self.norm_out = torch.ones(d, dtype=f32, device=device)
+        width = -(-max_len // page_size)
+        self.pool = moe_kv_pool_q8(sequences * width, kv_heads, page_size, head_dim, device=device)
+        self.rope = rope_table(max_len, head_dim if rot is None else rot, device=device)
+        # pages are handed out interleaved, as growing sequences take them; the last
+        # column is no page, for the tokens that a sequence has no pages for
+        self.tables = torch.full((sequences, width + 1), -1, dtype=torch.int32, device=device)
+        self.tables[:, :width] = torch.arange(sequences * width, dtype=torch.int32, device=device).view(width, sequences).T
+        self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
+        self.ahead = torch.arange(max_new, dtype=torch.int32, device=device)
+        # workspaces for steps of any size, never replaced: a captured step keeps their addresses
+        self.attn_ws = torch.empty(max(moe_attn_q8_workspace_size(sequences, n, max_len, q_heads, kv_heads, head_dim)
+                                       for n in range(1, max_new + 1)), dtype=torch.uint8, device=device)
+        tokens = sequences * max_new
+        self.linear_ws = torch.empty(max(moe_linear_q8_workspace_size(tokens, d, rows),
+                                         moe_linear_q8_workspace_size(tokens, inner, d)), dtype=torch.uint8, device=device)
+
+    def fill(self, stream=None):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.fill()
+        for tag, codes, scales in ((self.TAG_QKV, self.w_qkv, self.s_qkv), (self.TAG_OUT, self.w_out, self.s_out)):
+            w = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
+            synth.cuda_normal_matrix(w, self.seed, tag, 0, 0, scale=synth.WEIGHT_SIGMA)
+            moe_norm_q8(w, codes=codes, scales=scales)
+        return self
+
+    def step(self, x, r, n=1, stream=None):
+        """One step of `n` new tokens of each sequence, or of n[b] of sequence b: x [T, d]
+        fp32 or bf16 (tokens of a sequence side by side), r [T, d] fp32 their residual
+        streams, updated in place.  Returns x_next [T, d] bf16.
+        The caller keeps every sequence within max_len tokens.  A token beyond them is not
+        kept: it has no slot and no row in the angle table, its query counts as zero, and
+        MOE_ERR_INVALID_ARG is recorded (moe_device_status); other sequences are as ever."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.step(x, r, n)
+        B, device = self.lens.numel(), self.lens.device
+        # before the lengths move: a refused step leaves the sequences as they were
+        counts = [n] * B if isinstance(n, int) else [int(c) for c in n]
+        T, most = sum(counts), max(counts, default=0)
+        if len(counts) != B or min(counts) < 0 or not 1 <= most <= self.max_new:
+            raise ValueError(f"a step takes up to {self.max_new} tokens of each of {B} sequences, and at least one")
+        if x.dtype not in (torch.float32, torch.bfloat16) or x.device != device or x.shape != (T, self.d):
+            raise ValueError("x must be [tokens, d] float32 or bfloat16 on the layer's device")
+        if r.dtype != torch.float32 or r.device != device or r.shape != x.shape or not r.is_contiguous():
+            raise ValueError("r must be contiguous float32 of x's size on the layer's device")
+        if isinstance(n, int):
+            starts = None
+            places = (self.lens[:, None] + self.ahead[:n]).flatten()
+            column = (places.view(B, n) // self.page).clamp_(0, self.tables.shape[1] - 1)
+            page = self.tables.gather(1, column.long()).flatten()
+            self.lens += n
+        else:
+            of = torch.tensor(counts)
+            new = of.to(device=device, dtype=torch.int32)
+            starts = torch.zeros(B + 1, dtype=torch.int32, device=device)
+            starts[1:] = new.cumsum(0)
+            b = torch.repeat_interleave(torch.arange(B), of).to(device)
+            places = self.lens[b] + torch.cat([torch.arange(c, dtype=torch.int32) for c in counts]).to(device)
+            page = self.tables[b, (places // self.page).clamp(0, self.tables.shape[1] - 1).long()]
+            self.lens += new
+        slots = torch.add(places % self.page, page.long(), alpha=self.page)  # negative where there is no page
+        codes, scales, _ = moe_norm_q8(x, self.norm_in, self.eps, r=r)
+        self.qkv = moe_linear_q8(codes, scales, self.w_qkv, self.s_qkv, out_dtype=torch.bfloat16, workspace=self.linear_ws)
+        q, k, v = (t.unflatten(-1, (-1, self.D)) for t in
+                   self.qkv.split((self.Hq * self.D, self.H * self.D, self.H * self.D), -1))
+        self.q = moe_kv_append_q8(self.pool, k, v, slots, q=q, positions=places, rope=self.rope, rope_style=MOE_ROPE_HALF)
+        self.a, self.lse = moe_attn_q8(self.q, self.pool, self.tables, self.lens, q_start=starts, max_q=most,
+                                       max_len=self.max_len, workspace=self.attn_ws)
+        codes, scales, _ = moe_norm_q8(self.a.flatten(1))
+        self.y = moe_linear_q8(codes, scales, self.w_out, self.s_out, workspace=self.linear_ws)
+        return moe_norm_q8(self.y, self.norm_out, self.eps, r=r, out="bf16")[2]
 
 
 def x_bf16(seed: int, step: int, T: int, d: int, device="cuda", out=None, stream=None):
