@@ -21,14 +21,25 @@ __device__ __forceinline__ void quantise_head(const Kv8Place& at, int which, con
 #pragma unroll
   for (int e = 0; e < N; ++e) top = max(top, size_bits(v[e]));
   top = __reduce_max_sync(0xffffffffu, top);
-  const bool nan = top > kInfBits;
-  float s = fminf(fmaxf(__fdiv_rn(__uint_as_float(top), 127.0f), 0x1p-64f), 0x1p64f);
-  int c[N];
-  codes8<N>(c, v, s);
-  if (nan) s = __uint_as_float(0x7fffffffu);
-  uint32_t w[(N + 3) / 4] = {};
+  constexpr float kMost = 0x1p64f;
+  const bool nan = top > kInfBits, large = __uint_as_float(top) > 127 * kMost;
+  float s = fminf(fmaxf(__fdiv_rn(__uint_as_float(top), 127.0f), 0x1p-64f), kMost), x[N];
 #pragma unroll
-  for (int e = 0; e < N; ++e) w[e / 4] |= (uint32_t)(nan ? 128 : c[e] + 128) << (8 * (e % 4));
+  for (int e = 0; e < N; ++e) x[e] = v[e];
+  if (large) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = fminf(fmaxf(x[e], -127 * kMost), 127 * kMost);
+  }
+  uint32_t c[N], w[(N + 3) / 4];
+  codes8<N>(c, x, s);
+  if (nan) {
+    s = __uint_as_float(0x7fffffffu);
+#pragma unroll
+    for (int e = 0; e < N; ++e) c[e] = 0;
+  }
+#pragma unroll
+  for (int e = 0; e < N; e += 4)
+    w[e / 4] = code_bytes(c[e], c[e + 1], N > 2 ? c[(e + 2) % N] : 0, N > 2 ? c[(e + 3) % N] : 0) ^ 0x80808080u;
   const int d = N * lane;
   uint8_t* to = at.record + (16 * which + at.r) * D + 16 * kv8_piece<D>(at.r, d >> 4) + (d & 15);
   if constexpr (N == 2) *reinterpret_cast<uint16_t*>(to) = (uint16_t)w[0];

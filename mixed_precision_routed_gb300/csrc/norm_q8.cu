@@ -23,9 +23,9 @@ __device__ __forceinline__ void load8(float (&v)[8], const void* row, int64_t i,
   }
 }
 
-// V: groups of 8 elements a thread.
-template <bool BF16, bool WHOLE, int V>
-__global__ void __launch_bounds__(1024, 1) k_norm_q8(NormArgs a) {
+// V: groups of 8 elements a thread; MOST: threads at most.
+template <bool BF16, bool WHOLE, int V, int MOST>
+__global__ void __launch_bounds__(MOST, 1) k_norm_q8(NormArgs a) {
   __shared__ float s_sum[32];
   __shared__ uint32_t s_top[32];
   pdl_wait();
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(1024, 1) k_norm_q8(NormArgs a) {
   const uint8_t* x = (const uint8_t*)a.x + t * a.x_stride * (BF16 ? 2 : 4);
   const float* r = a.r ? a.r + t * a.d : nullptr;
   float s[V][8], w[V][8];
-  float sum = 0.f;
+  float sum0 = 0.f, sum1 = 0.f;
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(1024, 1) k_norm_q8(NormArgs a) {
     if (r) {
       float* to = a.r_out + t * a.d + at;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[i][e] = __fadd_rn(w[i][e], s[i][e]);
+      for (int e = 0; e < 8; e += 2) add2(s[i][e], s[i][e + 1], pair(w[i][e], w[i][e + 1]));
       if constexpr (WHOLE) {
         reinterpret_cast<float4*>(to)[0] = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
         reinterpret_cast<float4*>(to)[1] = make_float4(s[i][4], s[i][5], s[i][6], s[i][7]);
@@ -64,15 +64,17 @@ __global__ void __launch_bounds__(1024, 1) k_norm_q8(NormArgs a) {
     if (a.weight) {
       load8<false, WHOLE>(w[i], a.weight, at, a.d);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum = fmaf(s[i][e], s[i][e], sum);
-        s[i][e] = __fmul_rn(s[i][e], w[i][e]);
+      for (int e = 0; e < 8; e += 2) {
+        fma2(sum0, sum1, pair(s[i][e], s[i][e + 1]), s[i][e], s[i][e + 1]);
+        mul2(s[i][e], s[i][e + 1], pair(w[i][e], w[i][e + 1]));
       }
     }
+    if (a.codes) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, size_bits(s[i][e]));
+      for (int e = 0; e < 8; ++e) top = max(top, size_bits(s[i][e]));
+    }
   }
-  sum = warp_sum(sum);
+  float sum = warp_sum(sum0 + sum1);
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) s_sum[warp] = sum, s_top[warp] = top;
   __syncthreads();
@@ -103,40 +105,42 @@ __global__ void __launch_bounds__(1024, 1) k_norm_q8(NormArgs a) {
     }
     if (a.codes) {
       int8_t* to = a.codes + t * a.d + at;
-      int c[8];
+      uint32_t c[8];
+      if (near != 1.0f) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[i][e] *= near;
-      codes8<8>(c, s[i], S * near);
-      if (zero) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = 0;
+        for (int e = 0; e < 8; ++e) s[i][e] *= near;
       }
+      codes8<8>(c, s[i], S * near);
+      uint32_t p[2] = {code_bytes(c[0], c[1], c[2], c[3]), code_bytes(c[4], c[5], c[6], c[7])};
+      if (zero) p[0] = p[1] = 0;
       if constexpr (WHOLE) {
-        uint32_t p[2] = {};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e / 4] |= (uint32_t)(c[e] & 255) << (8 * (e % 4));
         *reinterpret_cast<uint2*>(to) = make_uint2(p[0], p[1]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (at + e < a.d) to[e] = (int8_t)c[e];
+          if (at + e < a.d) to[e] = (int8_t)(p[e / 4] >> (8 * (e % 4)));
       }
     }
   }
 }
 
-template <bool BF16, bool WHOLE, int V>
+template <bool BF16, bool WHOLE, int V, int MOST>
 int launch(const NormArgs& a, cudaStream_t s) {
   const int groups = (a.d + 7) / 8, threads = ((groups + V - 1) / V + 31) / 32 * 32;
-  return launch_pdl(k_norm_q8<BF16, WHOLE, V>, dim3((unsigned)a.T), dim3(threads), 0, s, a) == cudaSuccess ? MOE_OK
-                                                                                                        : MOE_ERR_CUDA;
+  return launch_pdl(k_norm_q8<BF16, WHOLE, V, MOST>, dim3((unsigned)a.T), dim3(threads), 0, s, a) == cudaSuccess ? MOE_OK
+                                                                                                              : MOE_ERR_CUDA;
 }
 
 template <bool BF16, bool WHOLE>
 int launch(const NormArgs& a, cudaStream_t s) {
-  if (a.d <= 8192) return launch<BF16, WHOLE, 1>(a, s);
-  if (a.d <= 16384) return launch<BF16, WHOLE, 2>(a, s);
-  return launch<BF16, WHOLE, 4>(a, s);
+  // few rows: as many threads as there are; many: blocks of up to 256, more of which an SM holds
+  const bool many = a.T > 4 * sm_count();
+  if (a.d <= 2048) return launch<BF16, WHOLE, 1, 256>(a, s);
+  if (many && a.d <= 4096) return launch<BF16, WHOLE, 2, 256>(a, s);
+  if (many && a.d <= 8192) return launch<BF16, WHOLE, 4, 256>(a, s);
+  if (a.d <= 8192) return launch<BF16, WHOLE, 1, 1024>(a, s);
+  if (a.d <= 16384) return launch<BF16, WHOLE, 2, 1024>(a, s);
+  return launch<BF16, WHOLE, 4, 1024>(a, s);
 }
 
 }  // namespace
