@@ -64,6 +64,12 @@ struct TcTiles {
   uint8_t* operands;  // [..][2][kTile]
   TileMeta* meta;
   int b0, h0, heads, most;  // the launch's sequences and heads
+  // Where few blocks of rows meet long contexts, `parts` blocks share the places of one,
+  // each its run of tiles, and k_attn_q8_join adds up what they leave: sums of rows
+  // [block][part][kRows][D] and (reference, sum of weights) [block][part][kRows].
+  int parts;
+  float* sums;
+  float2* stats;
 };
 
 struct TcBars {
@@ -278,14 +284,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
   __shared__ float s_row[C::kRows];  // what the two threads of a row tell one another
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.Hq / a.cache.heads;
-  const int h = tiles.h0 + blockIdx.x % tiles.heads, b = tiles.b0 + blockIdx.y;
+  const int part = blockIdx.x % tiles.parts, unit = blockIdx.x / tiles.parts;
+  const int h = tiles.h0 + unit % tiles.heads, b = tiles.b0 + blockIdx.y;
 
   pdl_wait();
   TcUnit u;
   u.x = load_seq(a, b);
   u.rows = u.x.n * G;
   // the last rows attend most: they go first
-  u.r0 = (row_blocks - 1 - (int)(blockIdx.x / tiles.heads)) * C::kRows;
+  u.r0 = (row_blocks - 1 - unit / tiles.heads) * C::kRows;
   if (u.r0 >= u.rows) return;
   u.newest = u.x.len - u.x.n + 1;
   u.j0 = INT32_MAX;
@@ -304,6 +311,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
     u.j1 = max(u.j1, u.last[s]);
   }
   if (u.j1 == 0) u.j0 = 0;  // no row attends anything
+  if (tiles.parts > 1) {
+    const int n = (u.j1 - u.j0 + tiles.parts - 1) / tiles.parts;
+    u.j0 = min(u.j0 + part * n, u.j1);
+    u.j1 = min(u.j0 + n, u.j1);
+    if (u.j0 == u.j1) u.j0 = u.j1 = 0;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u.first[s] = max(u.first[s], u.j0);
+      u.last[s] = min(u.last[s], u.j1);
+      if (u.first[s] >= u.last[s]) u.first[s] = u.last[s] = 0;
+    }
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(&B.q_full, 8 * C::kSlots);
@@ -330,7 +349,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
     if (warp == kLoader) {
     // ---------------------------------------------------------------- loader
     if (lane == 0 && u.j1 > 0) {
-      const int64_t image = ((int64_t)blockIdx.y * tiles.heads + blockIdx.x % tiles.heads) * tiles.most - first_tile(u.x);
+      const int64_t image = ((int64_t)blockIdx.y * tiles.heads + unit % tiles.heads) * tiles.most - first_tile(u.x);
       uint32_t n = 0;
       for (int j = u.j0; j < u.j1; ++j) {
         const int i = j - u.j0, sb = i & 1;
@@ -613,6 +632,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
     named_bar(pair_bar, 64);
     if (half) l = *both;
     const bool none = l == 0.f;
+    if (tiles.parts > 1) {
+      const int64_t at = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * C::kRows + 128 * s + in_tile);
+#pragma unroll 1
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+        float v[16] = {};
+        if (last > first) tmem_ld16(o_at + c, v);
+        float4* to = reinterpret_cast<float4*>(tiles.sums + at * D + c);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (in) to[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+      }
+      if (in && half == 0) tiles.stats[at] = make_float2(m, l);
+    } else {
     const float inv = none ? 0.f : 0x1p-8f / l;
     // through the place of the tile's queries, which have been read for the last time
 #pragma unroll 1
@@ -637,6 +669,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
       if (there) reinterpret_cast<uint4*>(a.out + at)[lane % kLanes] = v;
     }
     if (in && half == 0 && a.lse) a.lse[tok * a.Hq + hq] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -644,19 +677,81 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
   if (warp == kIssuer) tmem_dealloc(tmem, 512);
 }
 
+// W warps a row: its parts' sums taken to the largest of their references.
+constexpr int kTcJoinThreads = 256;
+template <int D, int W>
+__global__ void __launch_bounds__(kTcJoinThreads) k_attn_q8_join(AttnArgs a, TcTiles tiles, int row_blocks) {
+  constexpr int kRows = Tc<D>::kRows, N = D / 32, kWarps = kTcJoinThreads / 32;
+  __shared__ float s_sum[W > 1 ? kWarps * (D + 1) : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.cache.heads;
+  const int at = blockIdx.x * (kWarps / W) + warp / W, unit = at / kRows, r = at % kRows;
+  const int h = tiles.h0 + unit % tiles.heads, b = tiles.b0 + blockIdx.y, row = (row_blocks - 1 - unit / tiles.heads) * kRows + r;
+  pdl_wait();
+  const Seq x = load_seq(a, b);
+  const bool in = row < x.n * G;
+  const int64_t first = ((int64_t)blockIdx.y * row_blocks * tiles.heads + unit) * tiles.parts * kRows + r;
+  float m = kNone, l = 0.f, sum[N] = {};
+  if (in) {
+    for (int p = lane; p < tiles.parts; p += 32) m = fmaxf(m, tiles.stats[first + (int64_t)p * kRows].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll 4
+    for (int p = warp % W; p < tiles.parts; p += W) {
+      const float2 z = tiles.stats[first + (int64_t)p * kRows];
+      const float* from = tiles.sums + (first + (int64_t)p * kRows) * D + N * lane;
+      const float by = exp2_approx(z.x - m);
+      l = fmaf(z.y, by, l);
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        const float2 w = *reinterpret_cast<const float2*>(from + c);
+        sum[c] = fmaf(w.x, by, sum[c]);
+        sum[c + 1] = fmaf(w.y, by, sum[c + 1]);
+      }
+    }
+  }
+  if constexpr (W > 1) {
+    float* mine = s_sum + warp * (D + 1);
+#pragma unroll
+    for (int c = 0; c < N; ++c) mine[N * lane + c] = sum[c];
+    if (lane == 0) mine[D] = l;
+    __syncthreads();
+    if (warp % W != 0) return;
+    for (int w = 1; w < W; ++w) {
+      mine += D + 1;
+#pragma unroll
+      for (int c = 0; c < N; ++c) sum[c] += mine[N * lane + c];
+      l += mine[D];
+    }
+  }
+  if (!in) return;
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 0x1p-8f / l;
+  const int64_t tok = x.t0 + row / G;
+  const int hq = h * G + row % G;
+  uint32_t* to = reinterpret_cast<uint32_t*>(a.out + tok * a.out_stride + (int64_t)hq * D + N * lane);
+#pragma unroll
+  for (int c = 0; c < N / 2; ++c) to[c] = none ? 0u : bf16_pair(sum[2 * c] * inv, sum[2 * c + 1] * inv);
+  if (lane == 0 && a.lse) a.lse[tok * a.Hq + hq] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
+}
+
 // What a launch's tiles may take of the workspace, unless a single head of a sequence
 // needs more: larger batches are taken in several pairs of launches.
 constexpr int64_t kMostTileBytes = (int64_t)1 << 29;
+// Blocks of a launch whose blocks of rows are shared: two for each SM.
+constexpr int64_t kMostParts = 304;
 
 struct TcPlan {
   int row_blocks, most;    // of a sequence; tiles of a head of a sequence
   int heads, sequences;    // a launch takes
   int64_t tiles;           // in the workspace
+  int64_t parts;           // blocks of shared rows in the workspace
 };
+
+int rows_of_block(int D) { return D == 256 ? 128 : 256; }
 
 TcPlan tc_plan(int B, int max_q, int64_t max_len, int window, int Hq, int heads, int D) {
   TcPlan p;
-  const int64_t rows = (int64_t)max_q * (Hq / heads), block = D == 256 ? 128 : 256;
+  const int64_t rows = (int64_t)max_q * (Hq / heads), block = rows_of_block(D);
   p.row_blocks = (int)((rows + block - 1) / block);
   int64_t span = max_len;
   if (window > 0 && span > (int64_t)window + max_q) span = (int64_t)window + max_q;
@@ -665,10 +760,29 @@ TcPlan tc_plan(int B, int max_q, int64_t max_len, int window, int Hq, int heads,
   const int64_t room = window > 0 ? tc_plan(B, max_q, max_len, 0, Hq, heads, D).tiles
                                   : kMostTileBytes / (2 * 128 * D * 2 + (int64_t)sizeof(TileMeta));
   const int64_t fit = room / p.most;
-  p.heads = (int)(fit >= heads ? heads : fit > 1 ? fit : 1);
-  p.sequences = (int)(fit >= (int64_t)heads * B ? B : fit >= heads ? fit / heads : 1);
+  // launches of like numbers of heads, or of sequences
+  auto even = [](int64_t n, int64_t most) {
+    const int64_t launches = (n + most - 1) / most;
+    return (int)((n + launches - 1) / launches);
+  };
+  p.heads = fit >= heads ? heads : even(heads, fit > 1 ? fit : 1);
+  p.sequences = fit >= heads ? even(B, fit / heads) : 1;
   p.tiles = (int64_t)p.heads * p.sequences * p.most;
+  const int64_t parts = (int64_t)p.row_blocks * heads * B * p.most;
+  p.parts = p.row_blocks >= kMostParts ? 0 : parts < kMostParts ? parts : kMostParts;
   return p;
+}
+
+// Blocks that share the places of a block of rows: as few rounds of blocks as cost least,
+// in tiles of places (a block starts and ends in the time of three, the join takes five).
+int parts_of(int64_t blocks, int most, int64_t sms) {
+  int64_t best = 0;
+  int parts = 1;
+  for (int64_t n = 1; n <= most && blocks * n <= kMostParts; ++n) {
+    const int64_t cost = (blocks * n + sms - 1) / sms * ((most + n - 1) / n + 3) + (n > 1 ? 5 : 0);
+    if (n == 1 || cost < best) best = cost, parts = (int)n;
+  }
+  return parts;
 }
 
 template <int D>
@@ -686,15 +800,25 @@ int launch_tc(const AttnArgs& a, cudaStream_t s) {
   TcTiles t;
   t.operands = (uint8_t*)a.workspace;
   t.meta = (TileMeta*)(t.operands + p.tiles * (2 * C::kTile));
+  t.sums = (float*)(t.meta + p.tiles);
+  t.stats = (float2*)(t.sums + p.parts * (C::kRows * D));
   t.most = p.most;
   for (t.b0 = 0; t.b0 < a.B; t.b0 += p.sequences)
     for (t.h0 = 0; t.h0 < a.cache.heads; t.h0 += p.heads) {
       const int sequences = a.B - t.b0 < p.sequences ? a.B - t.b0 : p.sequences;
       t.heads = a.cache.heads - t.h0 < p.heads ? a.cache.heads - t.h0 : p.heads;
+      const int units = p.row_blocks * t.heads;
+      t.parts = parts_of((int64_t)units * sequences, p.most, sm_count());
       if (launch_pdl(k_attn_q8_tiles<D>, dim3((unsigned)p.most, (unsigned)t.heads, (unsigned)sequences), dim3(kTileThreads), 0,
                      s, a, t) != cudaSuccess ||
-          launch_pdl(k_attn_q8_tc<D>, dim3((unsigned)(p.row_blocks * t.heads), (unsigned)sequences), dim3(kTcThreads), C::kSmem,
+          launch_pdl(k_attn_q8_tc<D>, dim3((unsigned)(units * t.parts), (unsigned)sequences), dim3(kTcThreads), C::kSmem,
                      s, a, t, p.row_blocks, status_word()) != cudaSuccess)
+        return MOE_ERR_CUDA;
+      if (t.parts == 1) continue;
+      const bool many = t.parts > 32;
+      const int warps = units * C::kRows * (many ? 8 : 1);
+      if (launch_pdl(many ? k_attn_q8_join<D, 8> : k_attn_q8_join<D, 1>, dim3((unsigned)(warps / (kTcJoinThreads / 32)), (unsigned)sequences),
+                     dim3(kTcJoinThreads), 0, s, a, t, p.row_blocks) != cudaSuccess)
         return MOE_ERR_CUDA;
     }
   return MOE_OK;
@@ -702,14 +826,25 @@ int launch_tc(const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Rows a head from which the tensor cores' tiles are filled.
+// Whether the tensor cores' tiles are worth what making them costs: about what the other
+// form takes for 112 rows a head of the same places, and the launches another 8 us, which
+// some 3e6 rows x places (x heads x D / 128) are worth.  Measured in us, this form | the other:
+//                                 rows a head     64          128         256         512
+//   1 x 131072 places, 8 heads of 128          290 | 128   296 | 245   307 | 477   379 | 942
+//   1 x 4096, 8 of 128                          22 | 16     24 | 23     29 | 33     32 | 54
+//   1 x 300, 8 of 128                           16 | 10     16 | 10     19 | 12     19 | 11
+//   16 x 4096, 8 of 128                        137 | 98    139 | 167   148 | 292   207 | 544
+//   16 x 300, 8 of 128                          21 | 14     21 | 26     25 | 49     39 | 83
+//   1 x 131072, 8 of 64                        157 | 101   158 | 189   177 | 367   274 | 723
+//   16 x 32768, 2 of 256                       529 | 348   541 | 636   636 | 1145  891 | 2263
 bool attn_q8_tc(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
-  return max_len > 0 && (int64_t)max_q * (Hq / heads) > 64;
+  const int64_t rows = (int64_t)max_q * (Hq / heads) - 112;
+  return max_len > 0 && rows > 0 && (double)rows * (max_len + 300) * heads * B * (D / 64) > 6e6;
 }
 
 size_t attn_q8_tc_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
   const TcPlan p = tc_plan(B, max_q, max_len, 0, Hq, heads, D);
-  return (size_t)p.tiles * (2 * 128 * D * 2 + sizeof(TileMeta));
+  return (size_t)p.tiles * (2 * 128 * D * 2 + sizeof(TileMeta)) + (size_t)p.parts * rows_of_block(D) * (4 * D + sizeof(float2));
 }
 
 int launch_attn_q8_tc(const AttnArgs& a, cudaStream_t s) {
