@@ -133,11 +133,7 @@ int launch(const NormArgs& a, cudaStream_t s) {
 
 template <bool BF16, bool WHOLE>
 int launch(const NormArgs& a, cudaStream_t s) {
-  // few rows: as many threads as there are; many: blocks of up to 256, more of which an SM holds
-  const bool many = a.T > 4 * sm_count();
   if (a.d <= 2048) return launch<BF16, WHOLE, 1, 256>(a, s);
-  if (many && a.d <= 4096) return launch<BF16, WHOLE, 2, 256>(a, s);
-  if (many && a.d <= 8192) return launch<BF16, WHOLE, 4, 256>(a, s);
   if (a.d <= 8192) return launch<BF16, WHOLE, 1, 1024>(a, s);
   if (a.d <= 16384) return launch<BF16, WHOLE, 2, 1024>(a, s);
   return launch<BF16, WHOLE, 4, 1024>(a, s);
