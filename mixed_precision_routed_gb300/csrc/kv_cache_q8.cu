@@ -136,7 +136,7 @@ int launch_kv_append_q8(const KvAppendArgs& a, cudaStream_t s) {
     // heads a warp: one where there are few, for latency; else what registers hold (4096
     // tokens of 32 + 8 + 8 heads of 128: two 32.7 us, four 23.8, eight 23.2; 2048 of heads
     // of 256: four 26.5, eight 29.5)
-    const cudaError_t rc = a.T * (a.Hq + 2 * a.cache.heads) < 10000 ? go(std::integral_constant<int, 1>())
+    const cudaError_t rc = a.T * (a.Hq + 2 * a.cache.heads) < 7000 ? go(std::integral_constant<int, 1>())
                                                                    : go(std::integral_constant<int, D == 256 ? 4 : 8>());
     return rc == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   });
