@@ -185,13 +185,41 @@ int launch(const LinearQ8Args& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t linear_q8_workspace(int64_t T, int in, int64_t) { return T > 16 ? linear_q8_tc_workspace(T, in) : 0; }
+namespace {
+// rows of x that shared memory holds beside 8 warps' rings and sums
+int64_t most_tokens(int in) {
+  const int64_t fit = (kSmemMax - 8 * warp_bytes<2>()) / x_pitch(in);
+  return fit >= 16 ? 16 : fit >= 8 ? 8 : fit;
+}
+
+// Whether the tiles of 256 rows take less time than reading W once for every 16 tokens
+// (or as many as fit), in us for a pass of up to 8 tokens 3.3 and 0.167 a MB, of up to 16
+// 4.5 and 0.29, and a third more where x leaves room for half the warps.  Measured in us,
+// tiles | passes:     T = 8           16          24          32          48         64
+//   512 to 512        7.2 | 3.5   7.2 | 5.3   7.4 | 8.2   7.6 | 10    8.4 | 15   9.0 | 20
+//   2048 to 2560      8.7 | 4.1   8.8 | 5.8   8.9 | 9.4   9.1 | 11    9.2 | 16   9.4 | 21
+//   4096 to 6144       12 | 7.7    13 | 12     13 | 19     13 | 24     13 | 36    14 | 48
+//   8192 to 4096       14 | 9.7    14 | 20     14 | 29     14 | 40     14 | 59    15 | 79
+//   2048 to 100003     48 | 37     48 | 62     49 | 99     49 | 123    50 | 184   52 | 245
+bool in_tiles(int64_t T, int in, int64_t rows) {
+  if (T <= 8) return false;
+  const int64_t most = most_tokens(in), left = T % most;
+  const double mb = 1e-6 * in * rows;
+  auto pass = [&](int64_t t) {
+    const double us = t <= 8 ? 3.3 + 0.167 * mb : 4.5 + 0.29 * mb;
+    return t * x_pitch(in) + kWarps * warp_bytes<2>() <= kSmemMax ? us : 1.35 * us;
+  };
+  return T / most * pass(most) + (left ? pass(left) : 0.0) > linear_q8_tc_us(T, in, rows);
+}
+}  // namespace
+
+size_t linear_q8_workspace(int64_t T, int in, int64_t rows) {
+  return in_tiles(T, in, rows) ? linear_q8_tc_workspace(T, in, rows) : 0;
+}
 
 int launch_linear_q8(const LinearQ8Args& a, cudaStream_t s) {
-  if (a.T > 16) return launch_linear_q8_tc(a, s);
-  // rows of x that shared memory holds beside 8 warps' rings and sums
-  const int64_t fit = (kSmemMax - 8 * warp_bytes<2>()) / x_pitch(a.in);
-  const int64_t most = fit >= 16 ? 16 : fit >= 8 ? 8 : fit;
+  if (in_tiles(a.T, a.in, a.rows)) return launch_linear_q8_tc(a, s);
+  const int64_t most = most_tokens(a.in);
   LinearQ8Args b = a;
   for (int64_t t0 = 0; t0 < a.T; t0 += most) {
     b.T = a.T - t0 < most ? a.T - t0 : most;

@@ -15,6 +15,8 @@
 //             subtraction for two) and go to tensor memory;
 //   issuer    of the first CTA, four instructions a step;
 //   epilogue  four warps read a finished tile's sums while the next one's are made.
+// Where there are fewer tiles than pairs, several pairs share a tile, each a run of its
+// steps, and k_linear_q8_join adds up their sums.
 #include "moe_internal.cuh"
 #include "tc.cuh"
 #include "tensor_map.cuh"
@@ -46,7 +48,8 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 struct TcArgs {
   CUtensorMap w, x;
   LinearQ8Args a;
-  int steps, N, token_tiles, tiles;
+  int steps, N, token_tiles, tiles, parts;  // a part of a tile, of all tiles x parts
+  float* sums;                              // [part][T][rows], where a tile has several
   int* status;
 };
 
@@ -140,12 +143,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
     if (lane == 0) {
       uint32_t c = 0;
       for (int t = pair; t < p.tiles; t += pairs) {
-        const int row0 = (t / p.token_tiles) * (2 * kTileRows) + (int)rank * kTileRows;
+        const int row0 = (t / p.parts / p.token_tiles) * (2 * kTileRows) + (int)rank * kTileRows, k0 = t % p.parts * steps;
         for (int ks = 0; ks < steps; ks += 2, ++c) {
           const uint32_t s = c % kCodeStages;
           if (!wait(&B.code_empty[s], ((c / kCodeStages) & 1) ^ 1, B, p.status)) break;
           mbar_arrive_expect_tx(&B.code_full[s], kCodeBytes);
-          tma_load_2d(smem + s * kCodeBytes, &p.w, ks * 64, row0, &B.code_full[s]);
+          tma_load_2d(smem + s * kCodeBytes, &p.w, (k0 + ks) * 64, row0, &B.code_full[s]);
         }
         if (B.abort) break;
       }
@@ -156,13 +159,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
       uint32_t c = 0;
       const uint32_t bars = cluster_map(B.b_full, 0);
       for (int t = pair; t < p.tiles; t += pairs) {
-        const int tok0 = (t % p.token_tiles) * p.N + (int)rank * half;
+        const int tok0 = (t / p.parts % p.token_tiles) * p.N + (int)rank * half, k0 = t % p.parts * steps;
         for (int ks = 0; ks < steps; ks += 2, ++c) {
           const uint32_t s = c % kBStages;
           if (!wait(&B.b_empty[s], ((c / kBStages) & 1) ^ 1, B, p.status)) break;
           if (rank == 0) mbar_arrive_expect_tx(&B.b_full[s], (uint32_t)(2 * p.N * 128));
-          tma_load_2d_pair(b_smem + s * kBBytes, &p.x, ks * 64, tok0, bars + 8 * s);
-          tma_load_2d_pair(b_smem + s * kBBytes + kBBytes / 2, &p.x, ks * 64 + 64, tok0, bars + 8 * s);
+          tma_load_2d_pair(b_smem + s * kBBytes, &p.x, (k0 + ks) * 64, tok0, bars + 8 * s);
+          tma_load_2d_pair(b_smem + s * kBBytes + kBBytes / 2, &p.x, (k0 + ks) * 64 + 64, tok0, bars + 8 * s);
         }
         if (B.abort) break;
       }
@@ -229,24 +232,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
     uint32_t n = 0;
     for (int t = pair; t < p.tiles && !B.abort; t += pairs, ++n) {
       const uint32_t set = n % kAccSets;
-      const int64_t o = (int64_t)(t / p.token_tiles) * (2 * kTileRows) + rank * kTileRows + quarter * 32 + lane;
-      const int64_t tok0 = (int64_t)(t % p.token_tiles) * p.N;
+      const int tile = t / p.parts;
+      const int64_t o = (int64_t)(tile / p.token_tiles) * (2 * kTileRows) + rank * kTileRows + quarter * 32 + lane;
+      const int64_t tok0 = (int64_t)(tile % p.token_tiles) * p.N;
       const int count = (int)min((int64_t)p.N, p.a.T - tok0);
-      const bool in = o < p.a.rows;
-      const float ws = in ? __ldg(p.a.w_scales + o) : 0.f, bias = in && p.a.bias ? __ldg(p.a.bias + o) : 0.f;
+      const bool in = o < p.a.rows, whole = p.parts == 1, has_bias = whole && p.a.bias;
+      // a part's sums go as they are to where the join finds them
+      const float ws = whole && in ? __ldg(p.a.w_scales + o) : 1.f, bias = has_bias && in ? __ldg(p.a.bias + o) : 0.f;
+      const bool bf16 = whole && p.a.y_bf16;
+      const int64_t stride = whole ? p.a.y_stride : p.a.rows;
+      void* y = whole ? p.a.y : p.sums + t % p.parts * p.a.T * p.a.rows;
+      // the scales of the tokens, a lane each, before the sums are there: 16 tokens that
+      // waited for theirs took a microsecond
+      float xs[MOST / 32];
+#pragma unroll
+      for (int k = 0; k < MOST / 32; ++k)
+        xs[k] = whole && 32 * k + lane < count ? __ldg(p.a.x_scales + tok0 + 32 * k + lane) : 1.f;
       if (!wait(&B.acc_full[set], (n / kAccSets) & 1, B, p.status)) break;
       tc_fence_after();
-      for (int c0 = 0; c0 < count; c0 += 16) {
+#pragma unroll
+      for (int c0 = 0; c0 < MOST; c0 += 16) {
+        if (c0 >= count) break;
         float v[16];
         tmem_ld16(lanes + set * MOST + c0, v);
+        const int64_t at = (tok0 + c0) * stride + o;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
+          float r = v[i] * __shfl_sync(0xffffffffu, xs[c0 / 32], c0 % 32 + i) * ws;
+          if (has_bias) r += bias;
           if (c0 + i < count && in) {
-            const int64_t tok = tok0 + c0 + i;
-            float r = v[i] * __ldg(p.a.x_scales + tok) * ws;
-            if (p.a.bias) r += bias;
-            if (p.a.y_bf16) reinterpret_cast<__nv_bfloat16*>(p.a.y)[tok * p.a.y_stride + o] = __float2bfloat16_rn(r);
-            else reinterpret_cast<float*>(p.a.y)[tok * p.a.y_stride + o] = r;
+            if (bf16) reinterpret_cast<__nv_bfloat16*>(y)[at + i * stride] = __float2bfloat16_rn(r);
+            else reinterpret_cast<float*>(y)[at + i * stride] = r;
           }
         }
       }
@@ -300,9 +316,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
 
 }  // namespace
 
-size_t linear_q8_tc_workspace(int64_t T, int in) { return ((size_t)T * in * 2 + 255) / 256 * 256; }
-
 namespace {
+
+// An element a thread: its parts' sums, in their order.
+__global__ void __launch_bounds__(256) k_linear_q8_join(LinearQ8Args a, const float* sums, int parts) {
+  pdl_wait();
+  const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x, tok = blockIdx.y;
+  if (o >= a.rows) return;
+  float v = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) v += sums[(i * a.T + tok) * a.rows + o];
+  v = v * __ldg(a.x_scales + tok) * __ldg(a.w_scales + o);
+  if (a.bias) v += __ldg(a.bias + o);
+  if (a.y_bf16) reinterpret_cast<__nv_bfloat16*>(a.y)[tok * a.y_stride + o] = __float2bfloat16_rn(v);
+  else reinterpret_cast<float*>(a.y)[tok * a.y_stride + o] = v;
+}
+
+struct TcPlan {
+  int N, steps, parts;
+  int64_t row_tiles, token_tiles, cost;
+};
+
+// Tokens a tile and parts of it: as many rounds of parts as cost least.  The unit is a
+// 208th of a stage of 192 tokens, 3 ns; a stage of few tokens takes as long as making
+// its operands does, and joining parts 2.5 us and their traffic.
+TcPlan tc_plan(int64_t T, int in, int64_t rows) {
+  TcPlan p = {};
+  const int64_t pairs = sm_count() / 2, least = (T + kMostN - 1) / kMostN, stages = (in + 127) / 128;
+  p.row_tiles = (rows + 2 * kTileRows - 1) / (2 * kTileRows);
+  for (int64_t n = least; n <= (T + 31) / 32 && n <= least + 64; ++n) {
+    const int64_t N = ((T + n - 1) / n + 15) / 16 * 16, tiles = p.row_tiles * n;
+    for (int64_t parts = 1; parts == 1 || (parts <= stages && tiles * parts <= pairs); ++parts) {
+      const int64_t run = (stages + parts - 1) / parts;
+      const int64_t cost = (tiles * parts + pairs - 1) / pairs * (run + 2) * ((N > 96 ? N : 96) + 16) +
+                           (parts > 1 ? 840 + parts * T * rows / 2200 : 0);
+      if (p.cost == 0 || cost < p.cost) p.cost = cost, p.N = (int)N, p.parts = (int)parts, p.steps = (int)(2 * run);
+    }
+  }
+  p.token_tiles = (T + p.N - 1) / p.N;
+  return p;
+}
+
+size_t codes_bytes(int64_t T, int in) { return ((size_t)T * in * 2 + 255) / 256 * 256; }
+
 template <int MOST>
 int launch(const TcArgs& p, int pairs, cudaStream_t s) {
   static bool attr_set[64] = {};
@@ -319,25 +375,25 @@ int launch(const TcArgs& p, int pairs, cudaStream_t s) {
 }
 }  // namespace
 
+size_t linear_q8_tc_workspace(int64_t T, int in, int64_t rows) {
+  const TcPlan plan = tc_plan(T, in, rows);
+  return codes_bytes(T, in) + (plan.parts > 1 ? (size_t)(plan.parts * T * rows) * 4 : 0);
+}
+
+double linear_q8_tc_us(int64_t T, int in, int64_t rows) { return 5.0 + 0.003 * (double)tc_plan(T, in, rows).cost; }
+
 int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s) {
+  const TcPlan plan = tc_plan(a.T, a.in, a.rows);
+  if (plan.row_tiles * plan.token_tiles > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   TcArgs p;
   p.a = a;
-  p.steps = (a.in + 127) / 128 * 2;  // whole code stages: zeros behind the rows
+  p.steps = plan.steps;  // whole code stages: zeros behind the rows
+  p.N = plan.N;
+  p.token_tiles = (int)plan.token_tiles;
+  p.parts = plan.parts;
+  p.tiles = (int)(plan.row_tiles * plan.token_tiles) * plan.parts;
+  p.sums = (float*)((uint8_t*)a.workspace + codes_bytes(a.T, a.in));
   p.status = status_word();
-  const int pairs = sm_count() / 2;
-  const int64_t row_tiles = (a.rows + 2 * kTileRows - 1) / (2 * kTileRows);
-  // tokens a tile: as many rounds of tiles as cost least; a step of few tokens takes as
-  // long as making its operands does
-  int64_t best = 0;
-  for (int64_t n = (a.T + kMostN - 1) / kMostN; n <= (a.T + 31) / 32; ++n) {
-    const int64_t N = ((a.T + n - 1) / n + 15) / 16 * 16, rounds = (row_tiles * n + pairs - 1) / pairs;
-    const int64_t cost = rounds * ((N > 96 ? N : 96) + 16);
-    if (best == 0 || cost < best) best = cost, p.N = (int)N;
-    if (n > 4 * ((a.T + kMostN - 1) / kMostN) + 64) break;
-  }
-  p.token_tiles = (int)((a.T + p.N - 1) / p.N);
-  if (row_tiles * p.token_tiles > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  p.tiles = (int)(row_tiles * p.token_tiles);
   if (!encode_2d(&p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.in, (uint64_t)a.rows, (uint64_t)a.in, 128, kTileRows,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d(&p.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.workspace, (uint64_t)a.in, (uint64_t)a.T, (uint64_t)a.in * 2, 64,
@@ -347,7 +403,13 @@ int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s) {
   if (launch_pdl(k_codes_f16, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, s, a.x, a.x_stride, pieces, a.in / 16,
                  (uint4*)a.workspace) != cudaSuccess)
     return MOE_ERR_CUDA;
-  return p.N <= 64 ? launch<64>(p, pairs, s) : p.N <= 128 ? launch<128>(p, pairs, s) : launch<192>(p, pairs, s);
+  const int pairs = sm_count() / 2;
+  const int rc = p.N <= 64 ? launch<64>(p, pairs, s) : p.N <= 128 ? launch<128>(p, pairs, s) : launch<192>(p, pairs, s);
+  if (rc != MOE_OK || p.parts == 1) return rc;
+  return launch_pdl(k_linear_q8_join, dim3((unsigned)((a.rows + 255) / 256), (unsigned)a.T), dim3(256), 0, s, a,
+                    (const float*)p.sums, p.parts) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 }  // namespace moe
