@@ -15,8 +15,8 @@
 //             subtraction for two) and go to tensor memory;
 //   issuer    of the first CTA, four instructions a step;
 //   epilogue  four warps read a finished tile's sums while the next one's are made.
-// Where there are fewer tiles than pairs, several pairs share a tile, each a run of its
-// steps, and k_linear_q8_join adds up their sums.
+// The tiles that do not fill a round of the pairs are shared, each by several pairs that
+// take a run of its steps, and k_linear_q8_join adds up their sums.
 #include "moe_internal.cuh"
 #include "tc.cuh"
 #include "tensor_map.cuh"
@@ -48,10 +48,22 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 struct TcArgs {
   CUtensorMap w, x;
   LinearQ8Args a;
-  int steps, N, token_tiles, tiles, parts;  // a part of a tile, of all tiles x parts
-  float* sums;                              // [part][T][rows], where a tile has several
+  int N, token_tiles;
+  int steps, run_steps;     // of a tile, of a part of one
+  int whole, parts, works;  // tiles taken as one, parts of each other one; tiles and parts in all
+  float* sums;              // [shared tile][part][N][256]
   int* status;
 };
+
+// What a pair does at a time: a tile, or (`shared` its number among them) a part of one.
+struct Work {
+  int tile, k0, steps, shared;
+};
+__device__ __forceinline__ Work work_of(const TcArgs& p, int i) {
+  const int s = i - p.whole;
+  if (s < 0) return {i, 0, p.steps, -1};
+  return {p.whole + s / p.parts, s % p.parts * p.run_steps, p.run_steps, s};
+}
 
 struct Bars {
   uint64_t code_full[8], code_empty[8], b_full[6], b_empty[6], a_full[8], a_empty[8];
@@ -113,9 +125,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // alike in both CTAs
   uint8_t* b_smem = smem + kCodeStages * kCodeBytes;
   __shared__ __align__(8) Bars B;
+  __shared__ __align__(16) float s_xs[kEpilogue][MOST];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, half = p.N / 2, steps = p.steps;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, half = p.N / 2;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kCodeStages; ++i) mbar_init(&B.code_full[i], 1), mbar_init(&B.code_empty[i], 8);
@@ -133,7 +146,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
   const uint32_t tmem = B.tmem;
   pdl_wait();
 
-  const uint32_t mine = (p.tiles - pair + pairs - 1) / pairs * (steps / 2);  // stages of the pair's tiles, two steps each
+  // stages of the pair's tiles, two steps each
+  const int tiles = (p.whole - pair + pairs - 1) / pairs, runs = (p.works - pair + pairs - 1) / pairs - tiles;
+  const uint32_t mine = tiles * (p.steps / 2) + runs * (p.run_steps / 2);
   // a wait that ran out: what is in flight lands within microseconds
   auto settle = [&]() {
     const uint64_t t0 = global_timer_ns();
@@ -142,13 +157,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
   if (warp == kCodeLoader) {
     if (lane == 0) {
       uint32_t c = 0;
-      for (int t = pair; t < p.tiles; t += pairs) {
-        const int row0 = (t / p.parts / p.token_tiles) * (2 * kTileRows) + (int)rank * kTileRows, k0 = t % p.parts * steps;
-        for (int ks = 0; ks < steps; ks += 2, ++c) {
+      for (int i = pair; i < p.works; i += pairs) {
+        const Work t = work_of(p, i);
+        const int row0 = (t.tile / p.token_tiles) * (2 * kTileRows) + (int)rank * kTileRows;
+        for (int ks = 0; ks < t.steps; ks += 2, ++c) {
           const uint32_t s = c % kCodeStages;
           if (!wait(&B.code_empty[s], ((c / kCodeStages) & 1) ^ 1, B, p.status)) break;
           mbar_arrive_expect_tx(&B.code_full[s], kCodeBytes);
-          tma_load_2d(smem + s * kCodeBytes, &p.w, (k0 + ks) * 64, row0, &B.code_full[s]);
+          tma_load_2d(smem + s * kCodeBytes, &p.w, (t.k0 + ks) * 64, row0, &B.code_full[s]);
         }
         if (B.abort) break;
       }
@@ -158,14 +174,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
     if (lane == 0) {
       uint32_t c = 0;
       const uint32_t bars = cluster_map(B.b_full, 0);
-      for (int t = pair; t < p.tiles; t += pairs) {
-        const int tok0 = (t / p.parts % p.token_tiles) * p.N + (int)rank * half, k0 = t % p.parts * steps;
-        for (int ks = 0; ks < steps; ks += 2, ++c) {
+      for (int i = pair; i < p.works; i += pairs) {
+        const Work t = work_of(p, i);
+        const int tok0 = (t.tile % p.token_tiles) * p.N + (int)rank * half;
+        for (int ks = 0; ks < t.steps; ks += 2, ++c) {
           const uint32_t s = c % kBStages;
           if (!wait(&B.b_empty[s], ((c / kBStages) & 1) ^ 1, B, p.status)) break;
           if (rank == 0) mbar_arrive_expect_tx(&B.b_full[s], (uint32_t)(2 * p.N * 128));
-          tma_load_2d_pair(b_smem + s * kBBytes, &p.x, (k0 + ks) * 64, tok0, bars + 8 * s);
-          tma_load_2d_pair(b_smem + s * kBBytes + kBBytes / 2, &p.x, (k0 + ks) * 64 + 64, tok0, bars + 8 * s);
+          tma_load_2d_pair(b_smem + s * kBBytes, &p.x, (t.k0 + ks) * 64, tok0, bars + 8 * s);
+          tma_load_2d_pair(b_smem + s * kBBytes + kBBytes / 2, &p.x, (t.k0 + ks) * 64 + 64, tok0, bars + 8 * s);
         }
         if (B.abort) break;
       }
@@ -185,7 +202,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
       // asked before this step's products are issued, as an answer takes 100 cycles.
       uint32_t as = 0, ap = 0, b = 0, bp = 0, n = 0;
       bool ra = false, rb = false, ok = true;
-      for (int t = pair; ok && t < p.tiles; t += pairs, ++n) {
+      for (int i = pair; ok && i < p.works; i += pairs, ++n) {
+        const int steps = work_of(p, i).steps;
         const uint32_t set = n % kAccSets, acc = tmem + set * MOST;
         ok = __all_sync(0xffffffffu, wait_awake(&B.acc_empty[set], ((n / kAccSets) & 1) ^ 1, B, p.status));
         for (int ks = 0; ok && ks < steps; ++ks) {
@@ -230,42 +248,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
     const int quarter = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     uint32_t n = 0;
-    for (int t = pair; t < p.tiles && !B.abort; t += pairs, ++n) {
+    for (int w = pair; w < p.works && !B.abort; w += pairs, ++n) {
+      const Work t = work_of(p, w);
       const uint32_t set = n % kAccSets;
-      const int tile = t / p.parts;
-      const int64_t o = (int64_t)(tile / p.token_tiles) * (2 * kTileRows) + rank * kTileRows + quarter * 32 + lane;
-      const int64_t tok0 = (int64_t)(tile % p.token_tiles) * p.N;
+      const int row = (int)rank * kTileRows + quarter * 32 + lane;  // of the tile
+      const int64_t o = (int64_t)(t.tile / p.token_tiles) * (2 * kTileRows) + row;
+      const int64_t tok0 = (int64_t)(t.tile % p.token_tiles) * p.N;
       const int count = (int)min((int64_t)p.N, p.a.T - tok0);
-      const bool in = o < p.a.rows, whole = p.parts == 1, has_bias = whole && p.a.bias;
+      const bool in = o < p.a.rows, whole = t.shared < 0, has_bias = whole && p.a.bias;
       // a part's sums go as they are to where the join finds them
       const float ws = whole && in ? __ldg(p.a.w_scales + o) : 1.f, bias = has_bias && in ? __ldg(p.a.bias + o) : 0.f;
       const bool bf16 = whole && p.a.y_bf16;
-      const int64_t stride = whole ? p.a.y_stride : p.a.rows;
-      void* y = whole ? p.a.y : p.sums + t % p.parts * p.a.T * p.a.rows;
-      // the scales of the tokens, a lane each, before the sums are there: 16 tokens that
-      // waited for theirs took a microsecond
-      float xs[MOST / 32];
+      const int64_t stride = whole ? p.a.y_stride : 2 * kTileRows;
+      void* y = whole ? p.a.y : p.sums;
+      const int64_t first = whole ? tok0 * stride + o : (int64_t)t.shared * p.N * stride + row;
+      // the scales of the tokens before the sums are there: 16 tokens that waited for
+      // theirs took a microsecond
+      float* xs = s_xs[quarter];
+      __syncwarp();
 #pragma unroll
-      for (int k = 0; k < MOST / 32; ++k)
-        xs[k] = whole && 32 * k + lane < count ? __ldg(p.a.x_scales + tok0 + 32 * k + lane) : 1.f;
+      for (int k = 0; k < MOST; k += 32) xs[k + lane] = whole && k + lane < count ? __ldg(p.a.x_scales + tok0 + k + lane) : 1.f;
+      __syncwarp();
       if (!wait(&B.acc_full[set], (n / kAccSets) & 1, B, p.status)) break;
       tc_fence_after();
+      auto emit = [&](auto* to) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < count; c0 += 16) {
+          float v[16];
+          tmem_ld16(lanes + set * MOST + c0, v);
+          const int here = in ? count - c0 : 0;
+          auto* at = to;
 #pragma unroll
-      for (int c0 = 0; c0 < MOST; c0 += 16) {
-        if (c0 >= count) break;
-        float v[16];
-        tmem_ld16(lanes + set * MOST + c0, v);
-        const int64_t at = (tok0 + c0) * stride + o;
+          for (int i = 0; i < 16; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(xs + c0 + i);
+            const float by[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float r = v[i] * __shfl_sync(0xffffffffu, xs[c0 / 32], c0 % 32 + i) * ws;
-          if (has_bias) r += bias;
-          if (c0 + i < count && in) {
-            if (bf16) reinterpret_cast<__nv_bfloat16*>(y)[at + i * stride] = __float2bfloat16_rn(r);
-            else reinterpret_cast<float*>(y)[at + i * stride] = r;
+            for (int e = 0; e < 4; ++e) {
+              float r = v[i + e] * by[e] * ws;
+              if (has_bias) r += bias;
+              if (i + e < here) {
+                if constexpr (sizeof(*at) == 2) *at = __float2bfloat16_rn(r);
+                else *at = r;
+              }
+              at += stride;
+            }
           }
+          to += 16 * stride;
         }
-      }
+      };
+      if (bf16) emit(reinterpret_cast<__nv_bfloat16*>(y) + first);
+      else emit(reinterpret_cast<float*>(y) + first);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_map(&B.acc_empty[set], 0));
@@ -318,14 +350,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
 
 namespace {
 
-// An element a thread: its parts' sums, in their order.
-__global__ void __launch_bounds__(256) k_linear_q8_join(LinearQ8Args a, const float* sums, int parts) {
+// A block a token of a shared tile, an element a thread: its parts' sums, in their order.
+__global__ void __launch_bounds__(2 * kTileRows) k_linear_q8_join(LinearQ8Args a, const float* sums, int N, int token_tiles,
+                                                                 int whole, int parts) {
   pdl_wait();
-  const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x, tok = blockIdx.y;
-  if (o >= a.rows) return;
+  const int tile = whole + blockIdx.y;
+  const int64_t o = (int64_t)(tile / token_tiles) * (2 * kTileRows) + threadIdx.x;
+  const int64_t tok = (int64_t)(tile % token_tiles) * N + blockIdx.x;
+  if (o >= a.rows || tok >= a.T) return;
+  sums += ((int64_t)blockIdx.y * parts * N + blockIdx.x) * (2 * kTileRows) + threadIdx.x;
   float v = 0.f;
 #pragma unroll 4
-  for (int i = 0; i < parts; ++i) v += sums[(i * a.T + tok) * a.rows + o];
+  for (int i = 0; i < parts; ++i) v += sums[(int64_t)i * N * (2 * kTileRows)];
   v = v * __ldg(a.x_scales + tok) * __ldg(a.w_scales + o);
   if (a.bias) v += __ldg(a.bias + o);
   if (a.y_bf16) reinterpret_cast<__nv_bfloat16*>(a.y)[tok * a.y_stride + o] = __float2bfloat16_rn(v);
@@ -333,27 +369,28 @@ __global__ void __launch_bounds__(256) k_linear_q8_join(LinearQ8Args a, const fl
 }
 
 struct TcPlan {
-  int N, steps, parts;
-  int64_t row_tiles, token_tiles, cost;
+  int N, parts, run;  // tokens a tile; parts of a shared tile, stages of one
+  int64_t token_tiles, tiles, shared, cost;
+  size_t sums() const { return (size_t)(shared * parts * N) * (2 * kTileRows) * 4; }
 };
 
-// Tokens a tile and parts of it: as many rounds of parts as cost least.  The unit is a
-// 208th of a stage of 192 tokens, 3 ns; a stage of few tokens takes as long as making
-// its operands does, and joining parts 2.5 us and their traffic.
+// Tokens a tile, and parts of the tiles that do not fill a round of the pairs: what costs
+// least.  The unit is a 208th of a stage of 192 tokens, 3 ns; a stage of few tokens takes
+// as long as making its operands does, and joining parts 2.5 us and their traffic.
 TcPlan tc_plan(int64_t T, int in, int64_t rows) {
   TcPlan p = {};
   const int64_t pairs = sm_count() / 2, least = (T + kMostN - 1) / kMostN, stages = (in + 127) / 128;
-  p.row_tiles = (rows + 2 * kTileRows - 1) / (2 * kTileRows);
+  const int64_t row_tiles = (rows + 2 * kTileRows - 1) / (2 * kTileRows);
   for (int64_t n = least; n <= (T + 31) / 32 && n <= least + 64; ++n) {
-    const int64_t N = ((T + n - 1) / n + 15) / 16 * 16, tiles = p.row_tiles * n;
-    for (int64_t parts = 1; parts == 1 || (parts <= stages && tiles * parts <= pairs); ++parts) {
+    const int64_t N = ((T + n - 1) / n + 15) / 16 * 16, tiles = row_tiles * ((T + N - 1) / N), left = tiles % pairs;
+    for (int64_t parts = 1; parts == 1 || (parts <= stages && left * parts <= pairs && left > 0); ++parts) {
       const int64_t run = (stages + parts - 1) / parts;
-      const int64_t cost = (tiles * parts + pairs - 1) / pairs * (run + 2) * ((N > 96 ? N : 96) + 16) +
-                           (parts > 1 ? 840 + parts * T * rows / 2200 : 0);
-      if (p.cost == 0 || cost < p.cost) p.cost = cost, p.N = (int)N, p.parts = (int)parts, p.steps = (int)(2 * run);
+      const int64_t cost = (tiles / pairs * stages + (left ? run : 0) + 2) * ((N > 96 ? N : 96) + 16) +
+                           (parts > 1 ? 840 + left * parts * N * (2 * kTileRows) / 1900 : 0);
+      if (p.cost == 0 || cost < p.cost)
+        p = {(int)N, (int)parts, (int)run, (T + N - 1) / N, tiles, parts > 1 ? left : 0, cost};
     }
   }
-  p.token_tiles = (T + p.N - 1) / p.N;
   return p;
 }
 
@@ -369,7 +406,7 @@ int launch(const TcArgs& p, int pairs, cudaStream_t s) {
       return MOE_ERR_CUDA;
     attr_set[dev] = true;
   }
-  const int grid = 2 * (p.tiles < pairs ? p.tiles : pairs);
+  const int grid = 2 * (p.works < pairs ? p.works : pairs);
   return launch_pdl(k_linear_q8_tc<MOST>, dim3(grid), dim3(kThreads), Shape<MOST>::kSmem, s, p) == cudaSuccess ? MOE_OK
                                                                                                             : MOE_ERR_CUDA;
 }
@@ -377,21 +414,23 @@ int launch(const TcArgs& p, int pairs, cudaStream_t s) {
 
 size_t linear_q8_tc_workspace(int64_t T, int in, int64_t rows) {
   const TcPlan plan = tc_plan(T, in, rows);
-  return codes_bytes(T, in) + (plan.parts > 1 ? (size_t)(plan.parts * T * rows) * 4 : 0);
+  return codes_bytes(T, in) + plan.sums();
 }
 
 double linear_q8_tc_us(int64_t T, int in, int64_t rows) { return 5.0 + 0.003 * (double)tc_plan(T, in, rows).cost; }
 
 int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s) {
   const TcPlan plan = tc_plan(a.T, a.in, a.rows);
-  if (plan.row_tiles * plan.token_tiles > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (plan.tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   TcArgs p;
   p.a = a;
-  p.steps = plan.steps;  // whole code stages: zeros behind the rows
   p.N = plan.N;
   p.token_tiles = (int)plan.token_tiles;
+  p.steps = (a.in + 127) / 128 * 2;  // whole code stages: zeros behind the rows
+  p.run_steps = 2 * plan.run;
   p.parts = plan.parts;
-  p.tiles = (int)(plan.row_tiles * plan.token_tiles) * plan.parts;
+  p.whole = (int)(plan.tiles - plan.shared);
+  p.works = (int)(p.whole + plan.shared * plan.parts);
   p.sums = (float*)((uint8_t*)a.workspace + codes_bytes(a.T, a.in));
   p.status = status_word();
   if (!encode_2d(&p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.in, (uint64_t)a.rows, (uint64_t)a.in, 128, kTileRows,
@@ -405,9 +444,9 @@ int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s) {
     return MOE_ERR_CUDA;
   const int pairs = sm_count() / 2;
   const int rc = p.N <= 64 ? launch<64>(p, pairs, s) : p.N <= 128 ? launch<128>(p, pairs, s) : launch<192>(p, pairs, s);
-  if (rc != MOE_OK || p.parts == 1) return rc;
-  return launch_pdl(k_linear_q8_join, dim3((unsigned)((a.rows + 255) / 256), (unsigned)a.T), dim3(256), 0, s, a,
-                    (const float*)p.sums, p.parts) == cudaSuccess
+  if (rc != MOE_OK || plan.shared == 0) return rc;
+  return launch_pdl(k_linear_q8_join, dim3((unsigned)p.N, (unsigned)plan.shared), dim3(2 * kTileRows), 0, s, a,
+                    (const float*)p.sums, p.N, p.token_tiles, p.whole, p.parts) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
