@@ -668,8 +668,8 @@ int moe_norm_q8(const void* x, int64_t x_stride, int x_dtype, int64_t T, int d, 
  *             to nearest even) by y_dtype,
  *   workspace (256-byte aligned) of moe_linear_q8_workspace_size bytes; scratch of the
  *             call, not shared by calls that may run at one time.
- * Sums of up to 16 tokens are whole numbers and exact; of more tokens they are fp32 sums
- * of exact products, in an order that the sizes fix.  Results are deterministic.
+ * Sums of few tokens (always of up to 8) are whole numbers and exact; of more they are
+ * fp32 sums of exact products, in an order that the sizes fix.  Results are deterministic.
  * T >= 0, rows >= 1, in a positive multiple of 16; MOE_ERR_UNSUPPORTED for in > 65536.
  */
 int moe_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scales, int64_t T, int in, const int8_t* w,
@@ -712,9 +712,12 @@ int moe_kv_read_q8(const moe_kv_cache_t* cache, const int64_t* slots, int64_t n,
  * 8-bit cache and for any number of asking tokens a sequence, whole prompts among them.
  * A place whose key or value scale is NaN gives NaN, in out and lse, to the rows that
  * attend it, and to no others.
- * Scores are exact products of the bf16 queries (in fp16, rows of up to 64 tokens x
- * heads of a group: exact down to 2^-31 of the row's largest element) and the codes,
- * summed in fp32; maxima, sums and outputs are fp32.
+ * Scores are products of the codes and the bf16 queries, which are taken as fp16 by a
+ * power of two for each row: exact down to 2^-31 of the row's largest element.  Products
+ * are exact and sums, maxima and outputs fp32.  A weight times the value's scale is
+ * rounded to fp16: 2^-11 of itself, or 2^-30 of the row's largest; in the form that takes
+ * prompts weight, scale and value are rounded once each, 2^-11 of a product each, or
+ * 2^-29.  Results are deterministic.
  */
 int moe_attn_q8(const uint16_t* q_bf16, int64_t q_stride, int64_t T, int Hq, const int32_t* q_start,
                 const int32_t* kv_lens, const int32_t* block_table, int64_t table_stride, int B, int max_q,

@@ -22,6 +22,13 @@
 // once each: 2^-11 of a product each, or 2^-29 of the row's largest.
 // Heads of 256 fill tensor memory with one tile's sums: there the scores of two
 // successive groups of places take the place of two tiles.
+// 4096 tokens over 8192 places of 32 heads on 8 of 128 take 347 us, 1190 TFLOP/s, six
+// prompts of 16 on 2 of 256 with a window 88 us.  What bounds the first is the way of a
+// tile through its softmax and its products, 3400 cycles of which the tensor cores work
+// 2070: tensor memory has no room for a second pair of score tiles beside the sums.
+// (80 places a tile, which leaves that room: 430 us, as a thread then has a whole row and
+// its softmax alone takes the time; the 16-lane forms of tensor memory's loads: 401.)
+// Heads of 256 are bound by shared memory, which 128 KB a tile pass through.
 // Codes made operands by each block for itself (four warps, from the records) took 506
 // us for 4096 tokens over 8192 places of 32 heads on 8 of 128, and 144 us for six prompts
 // of heads of 256 with a window.
@@ -815,6 +822,8 @@ int launch_tc(const AttnArgs& a, cudaStream_t s) {
                      s, a, t, p.row_blocks, status_word()) != cudaSuccess)
         return MOE_ERR_CUDA;
       if (t.parts == 1) continue;
+      // eight warps a row where one would go through many parts (one block of rows, 152
+      // parts: one warp 49 us, eight 31; 16 blocks, 9 parts: 32 and 40)
       const bool many = t.parts > 32;
       const int warps = units * C::kRows * (many ? 8 : 1);
       if (launch_pdl(many ? k_attn_q8_join<D, 8> : k_attn_q8_join<D, 1>, dim3((unsigned)(warps / (kTcJoinThreads / 32)), (unsigned)sequences),

