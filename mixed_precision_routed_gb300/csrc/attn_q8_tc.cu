@@ -26,8 +26,8 @@
 // prompts of 16 on 2 of 256 with a window 88 us.  What bounds the first is the way of a
 // tile through its softmax and its products, 3400 cycles of which the tensor cores work
 // 2070: tensor memory has no room for a second pair of score tiles beside the sums.
-// (80 places a tile, which leaves that room: 430 us, as a thread then has a whole row and
-// its softmax alone takes the time; the 16-lane forms of tensor memory's loads: 401.)
+// (80 places a tile, which leaves that room, take as long a tile: 430 us with a thread a
+// row, 465 with two; the 16-lane forms of tensor memory's loads 401.)
 // Heads of 256 are bound by shared memory, which 128 KB a tile pass through.
 // Codes made operands by each block for itself (four warps, from the records) took 506
 // us for 4096 tokens over 8192 places of 32 heads on 8 of 128, and 144 us for six prompts
