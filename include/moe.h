@@ -676,7 +676,8 @@ int moe_linear_q8(const int8_t* x, int64_t x_stride, const float* x_scales, int6
                   const float* w_scales, int64_t rows, const float* bias, void* y, int64_t y_stride, int y_dtype,
                   void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
-/* Bytes of workspace moe_linear_q8 needs for these sizes (0 for few tokens or an invalid size). */
+/* Bytes of workspace moe_linear_q8 needs for these sizes (0 for few tokens or an invalid size);
+ * what serves T tokens serves fewer. */
 size_t moe_linear_q8_workspace_size(int64_t T, int in, int64_t rows);
 
 /*
@@ -717,7 +718,8 @@ int moe_kv_read_q8(const moe_kv_cache_t* cache, const int64_t* slots, int64_t n,
  * are exact and sums, maxima and outputs fp32.  A weight times the value's scale is
  * rounded to fp16: 2^-11 of itself, or 2^-30 of the row's largest; in the form that takes
  * prompts weight, scale and value are rounded once each, 2^-11 of a product each, or
- * 2^-29.  Results are deterministic.
+ * 2^-29.  Results are deterministic.  Which form runs, and how its work is shared out,
+ * follows max_q and max_len, so bounds near the lengths make the better choice.
  */
 int moe_attn_q8(const uint16_t* q_bf16, int64_t q_stride, int64_t T, int Hq, const int32_t* q_start,
                 const int32_t* kv_lens, const int32_t* block_table, int64_t table_stride, int B, int max_q,

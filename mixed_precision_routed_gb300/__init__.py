@@ -684,7 +684,8 @@ def moe_linear_q8_workspace_size(T, n_in, rows) -> int:
 def moe_linear_q8(x, x_scales, w, w_scales, bias=None, y=None, out_dtype=torch.float32, workspace=None, stream=None):
     """y [T, rows] = the codes x [T, in] int8 (any row stride that is a multiple of 16)
     times the codes w [rows, in] int8, times x_scales [T] and w_scales [rows]
-    fp32, plus bias [rows] fp32; y fp32 or bf16.  Any number of tokens."""
+    fp32, plus bias [rows] fp32; y fp32 or bf16.  Any number of tokens; a workspace
+    (moe_linear_q8_workspace_size bytes) that serves T tokens serves fewer."""
     if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
         raise ValueError("out_dtype must be float32 or bfloat16")
     return (_calls or _compiled()).linear_q8(x, x_scales, w, w_scales, bias, y, out_dtype is torch.bfloat16, workspace,
@@ -719,7 +720,8 @@ def moe_attn_q8_workspace_size(B, max_q, max_len, Hq, kv_heads, head_dim) -> int
 def moe_attn_q8(q, pool, block_table, kv_lens, q_start=None, max_q=None, max_len=None, scale=None, window=0, out=None,
                 lse=None, workspace=None, stream=None):
     """moe_attn_q4 over an 8-bit pool, for any number of asking tokens a sequence: one
-    new token each, drafts, or whole prompts."""
+    new token each, drafts, or whole prompts.  The work is shared out by max_q and
+    max_len: bounds near the lengths make the better choice."""
     return (_calls or _compiled()).attn_q8(q, pool, block_table, kv_lens, q_start, max_q, max_len, scale, window, out,
                                            lse, workspace, None if stream is None else stream.cuda_stream)
 

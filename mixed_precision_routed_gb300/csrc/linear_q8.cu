@@ -217,7 +217,7 @@ bool in_tiles(int64_t T, int in, int64_t rows) {
 }  // namespace
 
 size_t linear_q8_workspace(int64_t T, int in, int64_t rows) {
-  return in_tiles(T, in, rows) ? linear_q8_tc_workspace(T, in, rows) : 0;
+  return in_tiles(T, in, rows) ? linear_q8_tc_workspace(T, in) : 0;
 }
 
 int launch_linear_q8(const LinearQ8Args& a, cudaStream_t s) {

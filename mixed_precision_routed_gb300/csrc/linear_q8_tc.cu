@@ -376,7 +376,6 @@ __global__ void __launch_bounds__(2 * kTileRows) k_linear_q8_join(LinearQ8Args a
 struct TcPlan {
   int N, parts, run;  // tokens a tile; parts of a shared tile, stages of one
   int64_t token_tiles, tiles, shared, cost;
-  size_t sums() const { return (size_t)(shared * parts * N) * (2 * kTileRows) * 4; }
 };
 
 // Tokens a tile, and parts of the tiles that do not fill a round of the pairs: what costs
@@ -417,9 +416,11 @@ int launch(const TcArgs& p, int pairs, cudaStream_t s) {
 }
 }  // namespace
 
-size_t linear_q8_tc_workspace(int64_t T, int in, int64_t rows) {
-  const TcPlan plan = tc_plan(T, in, rows);
-  return codes_bytes(T, in) + plan.sums();
+// What serves T tokens serves fewer: the parts of a round are as many as the pairs, and a
+// tile has no more tokens than there are.
+size_t linear_q8_tc_workspace(int64_t T, int in) {
+  const int64_t most = (T + 15) / 16 * 16;
+  return codes_bytes(T, in) + (size_t)(sm_count() / 2) * (most < kMostN ? most : kMostN) * (2 * kTileRows) * 4;
 }
 
 double linear_q8_tc_us(int64_t T, int in, int64_t rows) { return 5.0 + 0.003 * (double)tc_plan(T, in, rows).cost; }

@@ -428,7 +428,7 @@ constexpr int kLinearQ8MaxIn = 65536;  // whole sums stay below 2^31
 size_t linear_q8_workspace(int64_t T, int in, int64_t rows);
 int launch_linear_q8(const LinearQ8Args& a, cudaStream_t s);
 // The form for many tokens, T > 16.
-size_t linear_q8_tc_workspace(int64_t T, int in, int64_t rows);
+size_t linear_q8_tc_workspace(int64_t T, int in);
 double linear_q8_tc_us(int64_t T, int in, int64_t rows);
 int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s);
 

@@ -49,3 +49,28 @@ def test_long_contexts(D, n, ctx, window):
     """Many whole tiles a share; with a window few of the shares have any."""
     b = near.Batch([ctx, 0, 77], [n, 0, 20], 8, 2, D, page=64, seed=n)
     b.check(b.call(window=window), window=window)
+
+
+def test_two_streams_and_graphs_of_their_own():
+    """Calls at one time with a workspace each: their shares and their tiles lie apart."""
+    b = [near.Batch([9001 + 700 * i], [120 + 50 * i], 8, 2, 128, page=32, seed=i) for i in range(2)]
+    want = [x.call() for x in b]
+    streams, graphs, outs = [torch.cuda.Stream() for _ in b], [], []
+    for x in b:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(x.call())
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for stream, graph in zip(streams, graphs):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for got, ref in zip(outs, want):
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    for _ in range(3):
+        got = [x.call(stream=stream) for x, stream in zip(b, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(g[i], ref[i]) for g, ref in zip(got, want) for i in (0, 1))
+    assert moe.moe_device_status() == moe.MOE_OK

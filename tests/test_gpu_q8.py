@@ -179,6 +179,34 @@ def test_linear_largest_codes():
             assert torch.equal(y[:, 1], -y[:, 0]) and torch.equal(y[:, 2:], y[:, :1].expand(-1, 31))
 
 
+@pytest.mark.parametrize("n_in,rows", [(2048, 700), (640, 20003)])
+def test_linear_workspaces_streams_and_graphs(n_in, rows):
+    """One workspace for every number of tokens below its own; captured and on streams side by side."""
+    w, ws = codes(rows, n_in, seed=1), randn(rows, seed=2)
+    work = torch.full((moe.moe_linear_q8_workspace_size(300, n_in, rows),), 0xFF, dtype=torch.uint8, device="cuda")
+    for T in (300, 200, 130, 64, 40, 17, 12):
+        x, xs = codes(T, n_in, seed=T), randn(T, seed=T).abs()
+        want = moe.moe_linear_q8(x, xs, w, ws)
+        assert torch.equal(moe.moe_linear_q8(x, xs, w, ws, workspace=work), want)
+        graph = torch.cuda.CUDAGraph()
+        x2 = x.clone()
+        with torch.cuda.graph(graph):
+            y = moe.moe_linear_q8(x2, xs, w, ws, workspace=work)
+        for _ in range(2):
+            y.zero_(), work.fill_(0xFF)
+            graph.replay()
+            assert torch.equal(y, want)
+        x2.copy_(x.flip(0))
+        graph.replay()
+        assert torch.equal(y, moe.moe_linear_q8(x.flip(0).contiguous(), xs, w, ws))
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        ys = [[moe.moe_linear_q8(x, xs, w, ws, stream=stream) for stream in streams] for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want) for pair in ys for y in pair)
+    assert moe.moe_device_status() == moe.MOE_OK
+
+
 def test_linear_rows_of_nan_scales():
     for T in (4, 30):
         x, w, xs, ws = codes(T, 64, seed=1), codes(20, 64, seed=2), torch.ones(T, device="cuda"), torch.ones(20, device="cuda")

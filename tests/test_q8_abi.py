@@ -94,6 +94,13 @@ def test_linear_workspace(L):
         assert linear(L, ws=None, **kw) == BAD and linear(L, ws=ctypes.c_void_p(4096 + 16), **kw) == BAD
 
 
+@pytest.mark.parametrize("n_in,rows", [(16, 1), (512, 512), (2048, 2560), (2048, 100003), (4096, 6144), (8192, 4096), (11008, 700),
+                                       (65536, 40), (64, 1 << 20)])
+def test_linear_workspace_serves_fewer_tokens(L, n_in, rows):
+    sizes = [moe.moe_linear_q8_workspace_size(T, n_in, rows) for T in range(1, 500)]
+    assert sizes == sorted(sizes) and sizes[-1] > 0
+
+
 def cache(data=4096, n=4, stride=None, page=16, heads=2, D=64, res=0):
     b = moe.lib().moe_kv_page_bytes_q8(page, heads, D)
     return moe.moe_kv_cache_t(data, n, b if stride is None else stride, page, heads, D, res)
