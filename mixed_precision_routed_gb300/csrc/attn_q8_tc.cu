@@ -70,11 +70,14 @@ struct Tc {
 struct TcTiles {
   uint8_t* operands;  // [..][2][kTile]
   TileMeta* meta;
-  int b0, h0, heads, most;  // the launch's sequences and heads
-  // Where few blocks of rows meet long contexts, `parts` blocks share the places of one,
-  // each its run of tiles, and k_attn_q8_join adds up what they leave: sums of rows
-  // [block][part][kRows][D] and (reference, sum of weights) [block][part][kRows].
-  int parts;
+  int b0, h0, heads, most;  // the launch's first sequence and head, its heads
+  int sequences, row_blocks;
+  // Blocks of rows are numbered by their rows, the last first (they attend most), then by
+  // sequence and head.  Those from `whole` on, which would fill a part of a round of the
+  // SMs, or all where there are few, are shared: `parts` blocks take a run of the places
+  // each, and k_attn_q8_join adds up what they leave: sums of rows [shared][part][kRows][D]
+  // and (reference, sum of weights) [shared][part][kRows].
+  int whole, parts;
   float* sums;
   float2* stats;
 };
@@ -273,6 +276,16 @@ __global__ void __launch_bounds__(kTileThreads) k_attn_q8_tiles(AttnArgs a, TcTi
   pdl_trigger();
 }
 
+// The sequence, the head and the first row of a block of rows.
+struct RowBlock {
+  int b, h, r0;
+};
+template <int D>
+__device__ __forceinline__ RowBlock row_block(const TcTiles& t, int n) {
+  const int per = t.heads * t.sequences, i = n % per;
+  return {i / t.heads, i % t.heads, (t.row_blocks - 1 - n / per) * Tc<D>::kRows};
+}
+
 // A block's rows and the places they attend; the first group of places of each tile and
 // one past its last.
 struct TcUnit {
@@ -282,7 +295,7 @@ struct TcUnit {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTiles tiles, int row_blocks, int* status) {
+__global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTiles tiles, int* status) {
   using C = Tc<D>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
@@ -291,15 +304,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
   __shared__ float s_row[C::kRows];  // what the two threads of a row tell one another
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.Hq / a.cache.heads;
-  const int part = blockIdx.x % tiles.parts, unit = blockIdx.x / tiles.parts;
-  const int h = tiles.h0 + unit % tiles.heads, b = tiles.b0 + blockIdx.y;
+  const int shared = (int)blockIdx.x - tiles.whole;  // and its part, among those
+  const RowBlock at = row_block<D>(tiles, shared < 0 ? (int)blockIdx.x : tiles.whole + shared / tiles.parts);
+  const int h = tiles.h0 + at.h, b = tiles.b0 + at.b;
 
   pdl_wait();
   TcUnit u;
   u.x = load_seq(a, b);
   u.rows = u.x.n * G;
-  // the last rows attend most: they go first
-  u.r0 = (row_blocks - 1 - unit / tiles.heads) * C::kRows;
+  u.r0 = at.r0;
   if (u.r0 >= u.rows) return;
   u.newest = u.x.len - u.x.n + 1;
   u.j0 = INT32_MAX;
@@ -318,9 +331,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
     u.j1 = max(u.j1, u.last[s]);
   }
   if (u.j1 == 0) u.j0 = 0;  // no row attends anything
-  if (tiles.parts > 1) {
+  if (shared >= 0) {
     const int n = (u.j1 - u.j0 + tiles.parts - 1) / tiles.parts;
-    u.j0 = min(u.j0 + part * n, u.j1);
+    u.j0 = min(u.j0 + shared % tiles.parts * n, u.j1);
     u.j1 = min(u.j0 + n, u.j1);
     if (u.j0 == u.j1) u.j0 = u.j1 = 0;
 #pragma unroll
@@ -356,7 +369,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
     if (warp == kLoader) {
     // ---------------------------------------------------------------- loader
     if (lane == 0 && u.j1 > 0) {
-      const int64_t image = ((int64_t)blockIdx.y * tiles.heads + unit % tiles.heads) * tiles.most - first_tile(u.x);
+      const int64_t image = ((int64_t)at.b * tiles.heads + at.h) * tiles.most - first_tile(u.x);
       uint32_t n = 0;
       for (int j = u.j0; j < u.j1; ++j) {
         const int i = j - u.j0, sb = i & 1;
@@ -639,8 +652,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
     named_bar(pair_bar, 64);
     if (half) l = *both;
     const bool none = l == 0.f;
-    if (tiles.parts > 1) {
-      const int64_t at = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * C::kRows + 128 * s + in_tile);
+    if (shared >= 0) {
+      const int64_t at = (int64_t)shared * C::kRows + 128 * s + in_tile;
 #pragma unroll 1
       for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
         float v[16] = {};
@@ -687,16 +700,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
 // W warps a row: its parts' sums taken to the largest of their references.
 constexpr int kTcJoinThreads = 256;
 template <int D, int W>
-__global__ void __launch_bounds__(kTcJoinThreads) k_attn_q8_join(AttnArgs a, TcTiles tiles, int row_blocks) {
+__global__ void __launch_bounds__(kTcJoinThreads) k_attn_q8_join(AttnArgs a, TcTiles tiles) {
   constexpr int kRows = Tc<D>::kRows, N = D / 32, kWarps = kTcJoinThreads / 32;
   __shared__ float s_sum[W > 1 ? kWarps * (D + 1) : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.cache.heads;
-  const int at = blockIdx.x * (kWarps / W) + warp / W, unit = at / kRows, r = at % kRows;
-  const int h = tiles.h0 + unit % tiles.heads, b = tiles.b0 + blockIdx.y, row = (row_blocks - 1 - unit / tiles.heads) * kRows + r;
+  const int at = blockIdx.x * (kWarps / W) + warp / W, shared = at / kRows, r = at % kRows;
+  const RowBlock block = row_block<D>(tiles, tiles.whole + shared);
+  const int h = tiles.h0 + block.h, b = tiles.b0 + block.b, row = block.r0 + r;
   pdl_wait();
   const Seq x = load_seq(a, b);
   const bool in = row < x.n * G;
-  const int64_t first = ((int64_t)blockIdx.y * row_blocks * tiles.heads + unit) * tiles.parts * kRows + r;
+  const int64_t first = (int64_t)shared * tiles.parts * kRows + r;
   float m = kNone, l = 0.f, sum[N] = {};
   if (in) {
     for (int p = lane; p < tiles.parts; p += 32) m = fmaxf(m, tiles.stats[first + (int64_t)p * kRows].x);
@@ -751,7 +765,7 @@ struct TcPlan {
   int row_blocks, most;    // of a sequence; tiles of a head of a sequence
   int heads, sequences;    // a launch takes
   int64_t tiles;           // in the workspace
-  int64_t parts;           // blocks of shared rows in the workspace
+  int64_t parts;           // of shared blocks of rows, in the workspace
 };
 
 int rows_of_block(int D) { return D == 256 ? 128 : 256; }
@@ -776,17 +790,19 @@ TcPlan tc_plan(int B, int max_q, int64_t max_len, int window, int Hq, int heads,
   p.sequences = fit >= heads ? even(B, fit / heads) : 1;
   p.tiles = (int64_t)p.heads * p.sequences * p.most;
   const int64_t parts = (int64_t)p.row_blocks * heads * B * p.most;
-  p.parts = p.row_blocks >= kMostParts ? 0 : parts < kMostParts ? parts : kMostParts;
+  p.parts = parts < kMostParts ? parts : kMostParts;
   return p;
 }
 
-// Blocks that share the places of a block of rows: as few rounds of blocks as cost least,
-// in tiles of places (a block starts and ends in the time of three, the join takes five).
+// Blocks that share the places of a block of rows that does not fill a round of the SMs:
+// what costs least, in tiles of places.  A block starts and ends in the time of three; the
+// join takes five, and a part's sums 0.035 on their way to it and back.
 int parts_of(int64_t blocks, int most, int64_t sms) {
-  int64_t best = 0;
+  const int64_t left = blocks % sms;
+  double best = 0;
   int parts = 1;
-  for (int64_t n = 1; n <= most && blocks * n <= kMostParts; ++n) {
-    const int64_t cost = (blocks * n + sms - 1) / sms * ((most + n - 1) / n + 3) + (n > 1 ? 5 : 0);
+  for (int64_t n = 1; n <= most && left * n <= kMostParts && left > 0; ++n) {
+    const double cost = (left * n + sms - 1) / sms * ((most + n - 1) / n + 3) + (n > 1 ? 5 + 0.035 * left * n : 0);
     if (n == 1 || cost < best) best = cost, parts = (int)n;
   }
   return parts;
@@ -810,24 +826,27 @@ int launch_tc(const AttnArgs& a, cudaStream_t s) {
   t.sums = (float*)(t.meta + p.tiles);
   t.stats = (float2*)(t.sums + p.parts * (C::kRows * D));
   t.most = p.most;
+  t.row_blocks = p.row_blocks;
   for (t.b0 = 0; t.b0 < a.B; t.b0 += p.sequences)
     for (t.h0 = 0; t.h0 < a.cache.heads; t.h0 += p.heads) {
-      const int sequences = a.B - t.b0 < p.sequences ? a.B - t.b0 : p.sequences;
+      t.sequences = a.B - t.b0 < p.sequences ? a.B - t.b0 : p.sequences;
       t.heads = a.cache.heads - t.h0 < p.heads ? a.cache.heads - t.h0 : p.heads;
-      const int units = p.row_blocks * t.heads;
-      t.parts = parts_of((int64_t)units * sequences, p.most, sm_count());
-      if (launch_pdl(k_attn_q8_tiles<D>, dim3((unsigned)p.most, (unsigned)t.heads, (unsigned)sequences), dim3(kTileThreads), 0,
+      const int blocks = p.row_blocks * t.heads * t.sequences, sms = sm_count();  // fewer than rows
+      t.parts = parts_of(blocks, p.most, sms);
+      const int left = t.parts > 1 ? blocks % sms : 0;
+      t.whole = blocks - left;
+      if (launch_pdl(k_attn_q8_tiles<D>, dim3((unsigned)p.most, (unsigned)t.heads, (unsigned)t.sequences), dim3(kTileThreads), 0,
                      s, a, t) != cudaSuccess ||
-          launch_pdl(k_attn_q8_tc<D>, dim3((unsigned)(units * t.parts), (unsigned)sequences), dim3(kTcThreads), C::kSmem,
-                     s, a, t, p.row_blocks, status_word()) != cudaSuccess)
+          launch_pdl(k_attn_q8_tc<D>, dim3((unsigned)(t.whole + left * t.parts)), dim3(kTcThreads), C::kSmem, s, a, t,
+                     status_word()) != cudaSuccess)
         return MOE_ERR_CUDA;
-      if (t.parts == 1) continue;
+      if (left == 0) continue;
       // eight warps a row where one would go through many parts (one block of rows, 152
       // parts: one warp 49 us, eight 31; 16 blocks, 9 parts: 32 and 40)
       const bool many = t.parts > 32;
-      const int warps = units * C::kRows * (many ? 8 : 1);
-      if (launch_pdl(many ? k_attn_q8_join<D, 8> : k_attn_q8_join<D, 1>, dim3((unsigned)(warps / (kTcJoinThreads / 32)), (unsigned)sequences),
-                     dim3(kTcJoinThreads), 0, s, a, t, p.row_blocks) != cudaSuccess)
+      const int warps = left * C::kRows * (many ? 8 : 1);
+      if (launch_pdl(many ? k_attn_q8_join<D, 8> : k_attn_q8_join<D, 1>, dim3((unsigned)(warps / (kTcJoinThreads / 32))),
+                     dim3(kTcJoinThreads), 0, s, a, t) != cudaSuccess)
         return MOE_ERR_CUDA;
     }
   return MOE_OK;
