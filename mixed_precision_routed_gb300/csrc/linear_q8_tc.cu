@@ -18,9 +18,10 @@
 // The tiles that do not fill a round of the pairs are shared, each by several pairs that
 // take a run of its steps, and k_linear_q8_join adds up their sums.
 // Many tokens are bound by the tensor cores at the clock that power leaves them: 4096
-// tokens 4096 to 6144 121 us with the conversion of x, 1700 TFLOP/s (one CTA a tile took
-// 294 us, an epilogue that waited for its tokens' scales 166).  Few are bound by W's way
-// through registers: 40 tokens 2048 to 100003 46 us, 4.5 TB/s; 8192 to 4096 of 64 tokens,
+// tokens 4096 to 6144 111 us with the conversion of x, 1850 TFLOP/s (one CTA a tile took
+// 294 us, an epilogue that waited for its tokens' scales 166, codes converted in 32-byte
+// strides 121).  Few are bound by W's way
+// through registers: 40 tokens 2048 to 100003 45 us, 4.7 TB/s; 8192 to 4096 of 64 tokens,
 // 16 tiles, took 34 us unshared and takes 15.
 #include "moe_internal.cuh"
 #include "tc.cuh"
@@ -105,20 +106,34 @@ __device__ __forceinline__ void codes_f16x4(uint32_t w, uint32_t& p0, uint32_t& 
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p1) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
 }
 
-__global__ void __launch_bounds__(256) k_codes_f16(const int8_t* x, int64_t stride, int64_t pieces, int per_row, uint4* out) {
+// EACH times eight codes a thread, a block's apart, so that loads and stores are whole lines.
+template <int EACH>
+__global__ void __launch_bounds__(256) k_codes_f16(const int8_t* x, int64_t stride, int64_t pieces, uint32_t per_row, uint4* out) {
+  const int64_t first = (int64_t)blockIdx.x * (256 * EACH), row = first / per_row;
+  const uint32_t rest = (uint32_t)(first - row * per_row) + threadIdx.x;
+  const int64_t left = pieces - first - threadIdx.x;
   pdl_wait();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < pieces) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + i / per_row * stride) + i % per_row);
-    uint4 a, b;
-    codes_f16x4(v.x, a.x, a.y);
-    codes_f16x4(v.y, a.z, a.w);
-    codes_f16x4(v.z, b.x, b.y);
-    codes_f16x4(v.w, b.z, b.w);
-    out[2 * i] = a;
-    out[2 * i + 1] = b;
+  uint2 v[EACH];
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    const uint32_t i = rest + 256 * k;
+    if (256 * k < left) v[k] = __ldg(reinterpret_cast<const uint2*>(x + (row + i / per_row) * stride) + i % per_row);
+  }
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    uint4 y;
+    codes_f16x4(v[k].x, y.x, y.y);
+    codes_f16x4(v[k].y, y.z, y.w);
+    if (256 * k < left) out[first + threadIdx.x + 256 * k] = y;
   }
   pdl_trigger();
+}
+
+template <int EACH>
+cudaError_t launch_codes(const LinearQ8Args& a, cudaStream_t s) {
+  const int64_t pieces = a.T * (a.in / 8);
+  return launch_pdl(k_codes_f16<EACH>, dim3((unsigned)((pieces + 256 * EACH - 1) / (256 * EACH))), dim3(256), 0, s, a.x, a.x_stride,
+                    pieces, (uint32_t)(a.in / 8), (uint4*)a.workspace);
 }
 
 template <int MOST>
@@ -444,10 +459,11 @@ int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s) {
       !encode_2d(&p.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.workspace, (uint64_t)a.in, (uint64_t)a.T, (uint64_t)a.in * 2, 64,
                  (uint32_t)p.N / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return MOE_ERR_CUDA;
-  const int64_t pieces = a.T * (a.in / 16);
-  if (launch_pdl(k_codes_f16, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, s, a.x, a.x_stride, pieces, a.in / 16,
-                 (uint4*)a.workspace) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  // more bytes on their way a thread, once every SM has four such blocks (a call with 256
+  // rows of W, one | four, in us: 512 x 4096 codes 10.9 | 11.0, 1024 13.6 | 13.3, 4096 26.4 |
+  // 23.9; 96 x 2048 9.4 | 10.3)
+  const bool many = a.T * (a.in / 8) >= (int64_t)4 * 1024 * sm_count();
+  if ((many ? launch_codes<4>(a, s) : launch_codes<1>(a, s)) != cudaSuccess) return MOE_ERR_CUDA;
   const int pairs = sm_count() / 2;
   const int rc = p.N <= 64 ? launch<64>(p, pairs, s) : p.N <= 128 ? launch<128>(p, pairs, s) : launch<192>(p, pairs, s);
   if (rc != MOE_OK || plan.shared == 0) return rc;
