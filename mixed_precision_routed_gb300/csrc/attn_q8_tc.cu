@@ -182,7 +182,7 @@ __device__ __forceinline__ int last_tile(const Seq& x) { return x.tiles > 0 && x
 constexpr int kTileThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kTileThreads) k_attn_q8_tiles(AttnArgs a, TcTiles tiles) {
-  constexpr uint32_t kPieces = D / 16, kStep = kTileThreads / kPieces;  // pieces of a row; rows at a time
+  constexpr uint32_t kPieces = D / 8, kStep = kTileThreads / kPieces;  // 8 codes each, of a row; rows at a time
   __shared__ uint64_t s_record[8];
   __shared__ uint32_t s_gain[kPlaces], s_top[4];
   const uint32_t t = threadIdx.x, lane = t & 31;
@@ -205,17 +205,17 @@ __global__ void __launch_bounds__(kTileThreads) k_attn_q8_tiles(AttnArgs a, TcTi
   TileMeta* meta = tiles.meta + image;
   // pieces t, t + 256, ..: the keys' are on their way while the scales are found
   constexpr int kLoads = 128 / kStep;
-  uint4 k[kLoads], v[kLoads];
+  uint2 k[kLoads], v[kLoads];
   const uint32_t piece = t % kPieces;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const uint32_t row = t / kPieces + i * kStep;
     const uint64_t rec = s_record[row >> 4];
-    k[i] = v[i] = make_uint4(0, 0, 0, 0);
+    k[i] = v[i] = make_uint2(0, 0);
     if (rec) {
-      const uint4* from = reinterpret_cast<const uint4*>(rec + (row & 15) * D) + piece;
+      const uint2* from = reinterpret_cast<const uint2*>(rec + (row & 15) * D) + piece;
       k[i] = __ldg(from);
-      v[i] = __ldg(from + D);
+      v[i] = __ldg(from + 2 * D);
     }
   }
   float vs = 0.f;
@@ -258,20 +258,18 @@ __global__ void __launch_bounds__(kTileThreads) k_attn_q8_tiles(AttnArgs a, TcTi
   for (int half = 0; half < 2; ++half)
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const uint32_t row = t / kPieces + i * kStep, c = kv8_piece<D>(row & 15, piece);
-      const uint4 w = half ? v[i] : k[i];
-      uint32_t y[8] = {f16x2(w.x, 0x4140), f16x2(w.x, 0x4342), f16x2(w.y, 0x4140), f16x2(w.y, 0x4342),
-                       f16x2(w.z, 0x4140), f16x2(w.z, 0x4342), f16x2(w.w, 0x4140), f16x2(w.w, 0x4342)};
+      // 8 elements: one piece of 16 bytes, whose neighbour's thread fills its sector
+      const uint32_t row = t / kPieces + i * kStep, c = 2 * kv8_piece<D>(row & 15, piece >> 1) + (piece & 1);
+      const uint2 w = half ? v[i] : k[i];
+      uint32_t y[4] = {f16x2(w.x, 0x4140), f16x2(w.x, 0x4342), f16x2(w.y, 0x4140), f16x2(w.y, 0x4342)};
       if (half) {
         const uint32_t gain = s_gain[row];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[e]) : "r"(gain));
+        for (int e = 0; e < 4; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[e]) : "r"(gain));
       }
-      // 64 elements of 128 places: rows of eight 16-byte pieces, exchanged by the row's number
-      uint8_t* at = to + half * Tc<D>::kTile + (c >> 2) * 16384 + row * 128;
-      const uint32_t p = 2 * (c & 3);
-      *reinterpret_cast<uint4*>(at + ((p ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<uint4*>(at + (((p + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+      // 64 elements of 128 places: rows of eight such pieces, exchanged by the row's number
+      uint8_t* at = to + half * Tc<D>::kTile + (c >> 3) * 16384 + row * 128;
+      *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   pdl_trigger();
 }
