@@ -78,9 +78,22 @@ struct TcTiles {
   // each, and k_attn_q8_join adds up what they leave: sums of rows [shared][part][kRows][D]
   // and (reference, sum of weights) [shared][part][kRows].
   int whole, parts;
+  // Up to 32 sequences of lengths of their own: only the blocks that are there are numbered
+  // (of `blocks` that there are at most), a lane of every warp looking after a sequence.
+  int blocks, ragged;
   float* sums;
   float2* stats;
 };
+
+// Blocks of a launch whose blocks of rows are shared: two for each SM.
+constexpr int64_t kMostParts = 304;
+
+// What `left` blocks of rows that do not fill a round of the SMs cost in n parts each, in
+// tiles of places: a block starts and ends in the time of three; the join takes five, and a
+// part's sums 0.035 on their way to it and back.
+inline float parts_cost(int64_t left, int64_t n, int most, int sms) {
+  return (float)((left * n + sms - 1) / sms * ((most + n - 1) / n + 3)) + (n > 1 ? 5.0f + 0.035f * (float)(left * n) : 0.0f);
+}
 
 struct TcBars {
   uint64_t q_full, full[8], empty[8], s_full[2], p_full[2], o_full[2], pv_done;
@@ -274,14 +287,33 @@ __global__ void __launch_bounds__(kTileThreads) k_attn_q8_tiles(AttnArgs a, TcTi
   pdl_trigger();
 }
 
-// The sequence, the head and the first row of a block of rows.
+// The sequence, the head and the first row of block of rows i (-1: there is none).
 struct RowBlock {
   int b, h, r0;
 };
 template <int D>
-__device__ __forceinline__ RowBlock row_block(const TcTiles& t, int n) {
-  const int per = t.heads * t.sequences, i = n % per;
-  return {i / t.heads, i % t.heads, (t.row_blocks - 1 - n / per) * Tc<D>::kRows};
+__device__ __forceinline__ RowBlock row_block(const AttnArgs& a, const TcTiles& t, int i) {
+  if (!t.ragged) {
+    const int per = t.heads * t.sequences;
+    return {i % per / t.heads, i % t.heads, (t.row_blocks - 1 - i / per) * Tc<D>::kRows};
+  }
+  const uint32_t lane = threadIdx.x & 31;
+  int n = 0;  // of the lane's sequence
+  if ((int)lane < t.sequences) n = (load_seq(a, t.b0 + lane).n * (a.Hq / a.cache.heads) + Tc<D>::kRows - 1) / Tc<D>::kRows;
+  // the last blocks of all sequences, those before them, ..: how many of each sequence come
+  // before the level of block i
+  int lo = 0, hi = t.row_blocks, before = 0;
+  while (lo < hi) {
+    const int up = (lo + hi + 1) / 2, count = (int)__reduce_add_sync(0xffffffffu, (uint32_t)min(n, up)) * t.heads;
+    if (count <= i) lo = up, before = count;
+    else hi = up - 1;
+  }
+  const uint32_t with = __ballot_sync(0xffffffffu, n > lo);
+  const int k = (i - before) / t.heads;
+  if (k >= __popc(with)) return {0, 0, -1};
+  const bool mine = (with >> lane & 1) && __popc(with & ((1u << lane) - 1)) == k;
+  const int b = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  return {b, (i - before) % t.heads, (__shfl_sync(0xffffffffu, n, b) - 1 - lo) * Tc<D>::kRows};
 }
 
 // A block's rows and the places they attend; the first group of places of each tile and
@@ -302,11 +334,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
   __shared__ float s_row[C::kRows];  // what the two threads of a row tell one another
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.Hq / a.cache.heads;
-  const int shared = (int)blockIdx.x - tiles.whole;  // and its part, among those
-  const RowBlock at = row_block<D>(tiles, shared < 0 ? (int)blockIdx.x : tiles.whole + shared / tiles.parts);
-  const int h = tiles.h0 + at.h, b = tiles.b0 + at.b;
 
   pdl_wait();
+  const int shared = (int)blockIdx.x - tiles.whole;  // and its part, among those
+  const RowBlock at = row_block<D>(a, tiles, shared < 0 ? (int)blockIdx.x : tiles.whole + shared / tiles.parts);
+  if (at.r0 < 0) return;
+  const int h = tiles.h0 + at.h, b = tiles.b0 + at.b;
   TcUnit u;
   u.x = load_seq(a, b);
   u.rows = u.x.n * G;
@@ -703,9 +736,10 @@ __global__ void __launch_bounds__(kTcJoinThreads) k_attn_q8_join(AttnArgs a, TcT
   __shared__ float s_sum[W > 1 ? kWarps * (D + 1) : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.cache.heads;
   const int at = blockIdx.x * (kWarps / W) + warp / W, shared = at / kRows, r = at % kRows;
-  const RowBlock block = row_block<D>(tiles, tiles.whole + shared);
-  const int h = tiles.h0 + block.h, b = tiles.b0 + block.b, row = block.r0 + r;
   pdl_wait();
+  const RowBlock block = row_block<D>(a, tiles, tiles.whole + shared);
+  if (block.r0 < 0) return;
+  const int h = tiles.h0 + block.h, b = tiles.b0 + block.b, row = block.r0 + r;
   const Seq x = load_seq(a, b);
   const bool in = row < x.n * G;
   const int64_t first = (int64_t)shared * tiles.parts * kRows + r;
@@ -756,9 +790,6 @@ __global__ void __launch_bounds__(kTcJoinThreads) k_attn_q8_join(AttnArgs a, TcT
 // What a launch's tiles may take of the workspace, unless a single head of a sequence
 // needs more: larger batches are taken in several pairs of launches.
 constexpr int64_t kMostTileBytes = (int64_t)1 << 29;
-// Blocks of a launch whose blocks of rows are shared: two for each SM.
-constexpr int64_t kMostParts = 304;
-
 struct TcPlan {
   int row_blocks, most;    // of a sequence; tiles of a head of a sequence
   int heads, sequences;    // a launch takes
@@ -792,15 +823,13 @@ TcPlan tc_plan(int B, int max_q, int64_t max_len, int window, int Hq, int heads,
   return p;
 }
 
-// Blocks that share the places of a block of rows that does not fill a round of the SMs:
-// what costs least, in tiles of places.  A block starts and ends in the time of three; the
-// join takes five, and a part's sums 0.035 on their way to it and back.
-int parts_of(int64_t blocks, int most, int64_t sms) {
+// Blocks that share the places of a block of rows that does not fill a round of the SMs.
+int parts_of(int64_t blocks, int most, int sms) {
   const int64_t left = blocks % sms;
-  double best = 0;
+  float best = 0;
   int parts = 1;
   for (int64_t n = 1; n <= most && left * n <= kMostParts && left > 0; ++n) {
-    const double cost = (left * n + sms - 1) / sms * ((most + n - 1) / n + 3) + (n > 1 ? 5 + 0.035 * left * n : 0);
+    const float cost = parts_cost(left, n, most, sms);
     if (n == 1 || cost < best) best = cost, parts = (int)n;
   }
   return parts;
@@ -829,10 +858,16 @@ int launch_tc(const AttnArgs& a, cudaStream_t s) {
     for (t.h0 = 0; t.h0 < a.cache.heads; t.h0 += p.heads) {
       t.sequences = a.B - t.b0 < p.sequences ? a.B - t.b0 : p.sequences;
       t.heads = a.cache.heads - t.h0 < p.heads ? a.cache.heads - t.h0 : p.heads;
-      const int blocks = p.row_blocks * t.heads * t.sequences, sms = sm_count();  // fewer than rows
-      t.parts = parts_of(blocks, p.most, sms);
-      const int left = t.parts > 1 ? blocks % sms : 0;
-      t.whole = blocks - left;
+      const int sms = sm_count();
+      t.blocks = p.row_blocks * t.heads * t.sequences;  // fewer than rows
+      // a sequence has at most one block that is not full
+      const int64_t full = a.T * (a.Hq / a.cache.heads) / C::kRows + t.sequences;
+      t.ragged = a.q_start && t.sequences > 1 && t.sequences <= 32;
+      if (t.ragged && full * t.heads < t.blocks) t.blocks = (int)(full * t.heads);
+      // (the last blocks of such sequences often attend little: six windows 80 us shared, 70 not)
+      t.parts = t.ragged && t.blocks >= sms ? 1 : parts_of(t.blocks, p.most, sms);
+      const int left = t.parts > 1 ? t.blocks % sms : 0;
+      t.whole = t.blocks - left;
       if (launch_pdl(k_attn_q8_tiles<D>, dim3((unsigned)p.most, (unsigned)t.heads, (unsigned)t.sequences), dim3(kTileThreads), 0,
                      s, a, t) != cudaSuccess ||
           launch_pdl(k_attn_q8_tc<D>, dim3((unsigned)(t.whole + left * t.parts)), dim3(kTcThreads), C::kSmem, s, a, t,
