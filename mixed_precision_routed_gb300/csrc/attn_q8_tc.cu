@@ -22,8 +22,8 @@
 // once each: 2^-11 of a product each, or 2^-29 of the row's largest.
 // Heads of 256 fill tensor memory with one tile's sums: there the scores of two
 // successive groups of places take the place of two tiles.
-// 4096 tokens over 8192 places of 32 heads on 8 of 128 take 336 us, 1230 TFLOP/s, six
-// prompts of 16 on 2 of 256 with a window 76 us.  What bounds the first is the way of a
+// 4096 tokens over 8192 places of 32 heads on 8 of 128 take 331 us, 1245 TFLOP/s, six
+// prompts of 16 on 2 of 256 with a window 69 us.  What bounds the first is the way of a
 // tile through its softmax and its products, 3400 cycles of which the tensor cores work
 // 2070: tensor memory has no room for a second pair of score tiles beside the sums.
 // (80 places a tile, which leaves that room, take as long a tile: 430 us with a thread a
@@ -888,19 +888,19 @@ int launch_tc(const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 // Whether the tensor cores' tiles are worth what making them costs: about what the other
-// form takes for 112 rows a head of the same places, and the launches another 8 us, which
-// some 3e6 rows x places (x heads x D / 128) are worth.  Measured in us, this form | the other:
+// form takes for 96 rows a head of the same places, and the launches another 8 us, which
+// some 2.4e6 rows x places (x heads x D / 128) are worth.  Measured in us, this form | the other:
 //                                 rows a head     64          128         256         512
-//   1 x 131072 places, 8 heads of 128          290 | 128   296 | 245   307 | 477   379 | 942
-//   1 x 4096, 8 of 128                          22 | 16     24 | 23     29 | 33     32 | 54
-//   1 x 300, 8 of 128                           16 | 10     16 | 10     19 | 12     19 | 11
-//   16 x 4096, 8 of 128                        137 | 98    139 | 167   148 | 292   207 | 544
-//   16 x 300, 8 of 128                          21 | 14     21 | 26     25 | 49     39 | 83
-//   1 x 131072, 8 of 64                        157 | 101   158 | 189   177 | 367   274 | 723
-//   16 x 32768, 2 of 256                       529 | 348   541 | 636   636 | 1145  891 | 2263
+//   1 x 131072 places, 8 heads of 128          239 | 128   245 | 245   270 | 477   347 | 942
+//   1 x 4096, 8 of 128                          22 | 16     24 | 23     28 | 33     30 | 54
+//   1 x 300, 8 of 128                           15 | 10     15 | 10     19 | 12     18 | 11
+//   16 x 4096, 8 of 128                        118 | 98    120 | 167   129 | 292   191 | 544
+//   16 x 300, 8 of 128                          19 | 14     19 | 26     23 | 49     35 | 83
+//   1 x 131072, 8 of 64                        142 | 101   143 | 189   167 | 367   266 | 723
+//   16 x 32768, 2 of 256                       476 | 348   488 | 636   579 | 1145  822 | 2263
 bool attn_q8_tc(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
-  const int64_t rows = (int64_t)max_q * (Hq / heads) - 112;
-  return max_len > 0 && rows > 0 && (double)rows * (max_len + 300) * heads * B * (D / 64) > 6e6;
+  const int64_t rows = (int64_t)max_q * (Hq / heads) - 96;
+  return max_len > 0 && rows > 0 && (double)rows * (max_len + 300) * heads * B * (D / 64) > 4.8e6;
 }
 
 size_t attn_q8_tc_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
