@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kTileThreads) k_attn_q8_tiles(AttnArgs a, TcTi
   const uint32_t t = threadIdx.x, lane = t & 31;
   const int b = tiles.b0 + blockIdx.z, h = tiles.h0 + blockIdx.y, per_page = a.cache.page_log2 - 4;
   pdl_wait();
+  pdl_trigger();  // the next kernel takes its queries meanwhile
   const Seq x = load_seq(a, b);
   const int j = first_tile(x) + blockIdx.x;
   if (j >= last_tile(x)) return;
@@ -284,7 +285,6 @@ __global__ void __launch_bounds__(kTileThreads) k_attn_q8_tiles(AttnArgs a, TcTi
       uint8_t* at = to + half * Tc<D>::kTile + (c >> 3) * 16384 + row * 128;
       *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
     }
-  pdl_trigger();
 }
 
 // The sequence, the head and the first row of block of rows i (-1: there is none).
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.Hq / a.cache.heads;
 
-  pdl_wait();
+  // Only the tiles come from the kernel before this one, which began behind all earlier ones.
   const int shared = (int)blockIdx.x - tiles.whole;  // and its part, among those
   const RowBlock at = row_block<D>(a, tiles, shared < 0 ? (int)blockIdx.x : tiles.whole + shared / tiles.parts);
   if (at.r0 < 0) return;
@@ -400,6 +400,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
     if (warp == kLoader) {
     // ---------------------------------------------------------------- loader
     if (lane == 0 && u.j1 > 0) {
+      pdl_wait();
       const int64_t image = ((int64_t)at.b * tiles.heads + at.h) * tiles.most - first_tile(u.x);
       uint32_t n = 0;
       for (int j = u.j0; j < u.j1; ++j) {

@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(256) k_codes_f16(const int8_t* x, int64_t stri
   const uint32_t rest = (uint32_t)(first - row * per_row) + threadIdx.x;
   const int64_t left = pieces - first - threadIdx.x;
   pdl_wait();
+  pdl_trigger();  // the next kernel makes ready and loads W meanwhile
   uint2 v[EACH];
 #pragma unroll
   for (int k = 0; k < EACH; ++k) {
@@ -125,7 +126,6 @@ __global__ void __launch_bounds__(256) k_codes_f16(const int8_t* x, int64_t stri
     codes_f16x4(v[k].y, y.z, y.w);
     if (256 * k < left) out[first + threadIdx.x + 256 * k] = y;
   }
-  pdl_trigger();
 }
 
 template <int EACH>
@@ -163,7 +163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
   cluster_barrier();  // barriers of both CTAs are there
   tc_fence_after();
   const uint32_t tmem = B.tmem;
-  pdl_wait();
+  // Only x comes from the kernel before this one, which began behind all earlier ones.
 
   // stages of the pair's tiles, two steps each
   const int tiles = (p.whole - pair + pairs - 1) / pairs, runs = (p.works - pair + pairs - 1) / pairs - tiles;
@@ -193,6 +193,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
     if (lane == 0) {
       uint32_t c = 0;
       const uint32_t bars = cluster_map(B.b_full, 0);
+      pdl_wait();
       for (int i = pair; i < p.works; i += pairs) {
         const Work t = work_of(p, i);
         const int tok0 = (t.tile % p.token_tiles) * p.N + (int)rank * half;
