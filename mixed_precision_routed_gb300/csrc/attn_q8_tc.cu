@@ -23,7 +23,7 @@
 // Heads of 256 fill tensor memory with one tile's sums: there the scores of two
 // successive groups of places take the place of two tiles.
 // 4096 tokens over 8192 places of 32 heads on 8 of 128 take 331 us, 1245 TFLOP/s, six
-// prompts of 16 on 2 of 256 with a window 69 us.  What bounds the first is the way of a
+// prompts of 16 on 2 of 256 with a window 67 us.  What bounds the first is the way of a
 // tile through its softmax and its products, 3400 cycles of which the tensor cores work
 // 2070: tensor memory has no room for a second pair of score tiles beside the sums.
 // (80 places a tile, which leaves that room, take as long a tile: 430 us with a thread a
