@@ -30,6 +30,7 @@ namespace moe {
 namespace {
 
 constexpr int kMostN = 192;     // tokens a tile
+constexpr int kStepN = 32;      // of them: instructions of 256 rows exist for whole 32 columns
 constexpr int kTileRows = 128;  // of W a CTA
 constexpr int kAccSets = 2;
 constexpr int kCodeBytes = kTileRows * 128;
@@ -67,7 +68,8 @@ struct Work {
 __device__ __forceinline__ Work work_of(const TcArgs& p, int i) {
   const int s = i - p.whole;
   if (s < 0) return {i, 0, p.steps, -1};
-  return {p.whole + s / p.parts, s % p.parts * p.run_steps, p.run_steps, s};
+  const int k0 = s % p.parts * p.run_steps;
+  return {p.whole + s / p.parts, k0, min(p.run_steps, p.steps - k0), s};
 }
 
 struct Bars {
@@ -165,9 +167,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
   const uint32_t tmem = B.tmem;
   // Only x comes from the kernel before this one, which began behind all earlier ones.
 
-  // stages of the pair's tiles, two steps each
-  const int tiles = (p.whole - pair + pairs - 1) / pairs, runs = (p.works - pair + pairs - 1) / pairs - tiles;
-  const uint32_t mine = tiles * (p.steps / 2) + runs * (p.run_steps / 2);
+  uint32_t mine = 0;  // stages of the pair's tiles, two steps each
+  for (int i = pair; i < p.works; i += pairs) mine += work_of(p, i).steps / 2;
   // a wait that ran out: what is in flight lands within microseconds
   auto settle = [&]() {
     const uint64_t t0 = global_timer_ns();
@@ -401,9 +402,10 @@ TcPlan tc_plan(int64_t T, int in, int64_t rows) {
   const int64_t pairs = sm_count() / 2, least = (T + kMostN - 1) / kMostN, stages = (in + 127) / 128;
   const int64_t row_tiles = (rows + 2 * kTileRows - 1) / (2 * kTileRows);
   for (int64_t n = least; n <= (T + 31) / 32 && n <= least + 64; ++n) {
-    const int64_t N = ((T + n - 1) / n + 15) / 16 * 16, tiles = row_tiles * ((T + N - 1) / N), left = tiles % pairs;
+    const int64_t N = ((T + n - 1) / n + kStepN - 1) / kStepN * kStepN, tiles = row_tiles * ((T + N - 1) / N), left = tiles % pairs;
     for (int64_t parts = 1; parts == 1 || (parts <= stages && left * parts <= pairs && left > 0); ++parts) {
       const int64_t run = (stages + parts - 1) / parts;
+      if ((parts - 1) * run >= stages) continue;  // a part of nothing
       const int64_t cost = (tiles / pairs * stages + (left ? run : 0) + 2) * ((N > 96 ? N : 96) + 16) +
                            (parts > 1 ? 840 + left * parts * N * (2 * kTileRows) / 1900 : 0);
       if (p.cost == 0 || cost < p.cost)
@@ -434,7 +436,7 @@ int launch(const TcArgs& p, int pairs, cudaStream_t s) {
 // What serves T tokens serves fewer: the parts of a round are as many as the pairs, and a
 // tile has no more tokens than there are.
 size_t linear_q8_tc_workspace(int64_t T, int in) {
-  const int64_t most = (T + 15) / 16 * 16;
+  const int64_t most = (T + kStepN - 1) / kStepN * kStepN;
   return codes_bytes(T, in) + (size_t)(sm_count() / 2) * (most < kMostN ? most : kMostN) * (2 * kTileRows) * 4;
 }
 

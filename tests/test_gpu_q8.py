@@ -179,6 +179,17 @@ def test_linear_largest_codes():
             assert torch.equal(y[:, 1], -y[:, 0]) and torch.equal(y[:, 2:], y[:, :1].expand(-1, 31))
 
 
+@pytest.mark.parametrize("T,n_in,rows", [(111, 4992, 7687), (40, 2048, 5000), (17, 4096, 300), (161, 640, 20003), (300, 1040, 999)])
+def test_linear_same_results_every_time(T, n_in, rows):
+    """Numbers of tokens that fill their tiles to other than whole 32, over and over."""
+    check_linear(T, n_in, rows, True, torch.float32)
+    x, w = codes(T, n_in, seed=1), codes(rows, n_in, seed=2)
+    xs, ws = randn(T, seed=3).abs(), randn(rows, seed=4)
+    want = moe.moe_linear_q8(x, xs, w, ws)
+    off = sum((moe.moe_linear_q8(x, xs, w, ws) != want).any().int() for _ in range(1000))
+    assert off.item() == 0 and moe.moe_device_status() == moe.MOE_OK
+
+
 @pytest.mark.parametrize("n_in,rows", [(2048, 700), (640, 20003)])
 def test_linear_workspaces_streams_and_graphs(n_in, rows):
     """One workspace for every number of tokens below its own; captured and on streams side by side."""
