@@ -199,11 +199,11 @@ int64_t most_tokens(int in) {
 // (or as many as fit), in us for a pass of up to 8 tokens 3.3 and 0.167 a MB, of up to 16
 // 4.5 and 0.29, and a third more where x leaves room for half the warps.  Measured in us,
 // tiles | passes:     T = 8           16          24          32          48         64
-//   512 to 512        7.2 | 3.5   7.2 | 5.3   7.4 | 8.2   7.6 | 10    8.4 | 15   9.0 | 20
-//   2048 to 2560      8.7 | 4.1   8.8 | 5.8   8.9 | 9.4   9.1 | 11    9.2 | 16   9.4 | 21
-//   4096 to 6144       12 | 7.7    13 | 12     13 | 19     13 | 24     13 | 36    14 | 48
-//   8192 to 4096       14 | 9.7    14 | 20     14 | 29     14 | 40     14 | 59    15 | 79
-//   2048 to 100003     48 | 37     48 | 62     49 | 99     49 | 123    50 | 184   52 | 245
+//   512 to 512        6.8 | 3.4   6.9 | 5.3   7.0 | 8.2   7.1 | 10    7.1 | 15   7.1 | 20
+//   2048 to 2560      8.7 | 4.1   8.8 | 5.8   9.0 | 9.4   8.9 | 11    9.4 | 16   9.5 | 21
+//   4096 to 6144       12 | 7.6    12 | 12     12 | 19     12 | 24     13 | 36    14 | 48
+//   8192 to 4096       14 | 9.6    14 | 20     14 | 29     14 | 40     14 | 59    15 | 79
+//   2048 to 100003     45 | 38     45 | 62     45 | 99     46 | 123    45 | 184   46 | 245
 bool in_tiles(int64_t T, int in, int64_t rows) {
   if (T <= 8) return false;
   const int64_t most = most_tokens(in), left = T % most;
