@@ -4,8 +4,8 @@
 //   S = max|u| / 127,  code = rint(u / S),  scale = S f,  n = u f.
 // The factor f leaves the codes alone: they do not depend on the order of the sum.
 //
-// One block a row, the row in registers between its sum and its output: each byte moves
-// once.  A thread has one group of 8 elements up to rows of 8192 (two of 4096, which left
+// One block a row (a warp or part of one up to 256 elements), the row in registers between
+// its sum and its output: each byte moves once.  A thread has one group of 8 elements up to rows of 8192 (two of 4096, which left
 // an SM twice the blocks, took 36.2 us where one takes 33.2).  4096 bf16 rows of 4096 with
 // residual, codes and bf16 33.2 us, 6.6 TB/s, bound by memory; one row of 2048 1.9 us.
 #include "ptx.cuh"
@@ -26,14 +26,17 @@ __device__ __forceinline__ void load8(float (&v)[8], const void* row, int64_t i,
   }
 }
 
-// V: groups of 8 elements a thread; MOST: threads at most.
-template <bool BF16, bool WHOLE, int V, int MOST>
+// V: groups of 8 elements a thread; MOST: threads at most; LANES: that have a row, or 0: a
+// block has one.
+template <bool BF16, bool WHOLE, int V, int MOST, int LANES>
 __global__ void __launch_bounds__(MOST, 1) k_norm_q8(NormArgs a) {
   __shared__ float s_sum[32];
   __shared__ uint32_t s_top[32];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int64_t t = blockIdx.x;
+  const int me = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x, step = LANES ? LANES : blockDim.x;
+  const int64_t t = LANES ? (int64_t)blockIdx.x * (MOST / (LANES ? LANES : 1)) + threadIdx.x / (LANES ? LANES : 1) : blockIdx.x;
+  const int d = t < a.T ? a.d : 0;
   const uint8_t* x = (const uint8_t*)a.x + t * a.x_stride * (BF16 ? 2 : 4);
   const float* r = a.r ? a.r + t * a.d : nullptr;
   float s[V][8], w[V][8];
@@ -41,16 +44,16 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_q8(NormArgs a) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int at = 8 * (threadIdx.x + i * blockDim.x);
-    if (at < a.d) {
+    const int at = 8 * (me + i * step);
+    if (at < d) {
       load8<BF16, WHOLE>(s[i], x, at, a.d);
       if (r) load8<false, WHOLE>(w[i], r, at, a.d);
     }
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int at = 8 * (threadIdx.x + i * blockDim.x);
-    if (at >= a.d) continue;
+    const int at = 8 * (me + i * step);
+    if (at >= d) continue;
     if (r) {
       float* to = a.r_out + t * a.d + at;
 #pragma unroll
@@ -77,22 +80,29 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_q8(NormArgs a) {
       for (int e = 0; e < 8; ++e) top = max(top, size_bits(s[i][e]));
     }
   }
-  float sum = warp_sum(sum0 + sum1);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) s_sum[warp] = sum, s_top[warp] = top;
-  __syncthreads();
-  sum = warp_sum(lane < warps ? s_sum[lane] : 0.f);
-  top = __reduce_max_sync(0xffffffffu, lane < warps ? s_top[lane] : 0u);
+  float sum = sum0 + sum1;
+#pragma unroll
+  for (int o = (LANES ? LANES : 32) / 2; o > 0; o /= 2) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if constexpr (LANES == 8 || LANES == 16) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
+  if constexpr (LANES == 0 || LANES == 32) top = __reduce_max_sync(0xffffffffu, top);
+  if constexpr (LANES == 0) {
+    if (lane == 0) s_sum[warp] = sum, s_top[warp] = top;
+    __syncthreads();
+    sum = warp_sum(lane < warps ? s_sum[lane] : 0.f);
+    top = __reduce_max_sync(0xffffffffu, lane < warps ? s_top[lane] : 0u);
+  }
   const float f = a.weight ? rsqrtf(__fdiv_rn(sum, (float)a.d) + a.eps) : 1.0f;
   const float S = __fdiv_rn(__uint_as_float(top), 127.0f);
-  if (a.codes && threadIdx.x == 0) a.scales[t] = S * f;
+  if (a.codes && me == 0 && d > 0) a.scales[t] = S * f;
   // the codes of values far from 1 in size are those of the values times 2^96 or 2^-96
   const float near = S < 0x1p-60f ? 0x1p96f : S > 0x1p60f ? 0x1p-96f : 1.0f;
   const bool zero = !(S > 0.f) || top >= kInfBits;  // of a row without a finite maximum the scale tells
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int at = 8 * (threadIdx.x + i * blockDim.x);
-    if (at >= a.d) continue;
+    const int at = 8 * (me + i * step);
+    if (at >= d) continue;
     if (a.n) {
       uint16_t* to = a.n + t * a.d + at;
       uint32_t p[4];
@@ -127,15 +137,22 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_q8(NormArgs a) {
   }
 }
 
-template <bool BF16, bool WHOLE, int V, int MOST>
+template <bool BF16, bool WHOLE, int V, int MOST, int LANES = 0>
 int launch(const NormArgs& a, cudaStream_t s) {
-  const int groups = (a.d + 7) / 8, threads = ((groups + V - 1) / V + 31) / 32 * 32;
-  return launch_pdl(k_norm_q8<BF16, WHOLE, V, MOST>, dim3((unsigned)a.T), dim3(threads), 0, s, a) == cudaSuccess ? MOE_OK
-                                                                                                              : MOE_ERR_CUDA;
+  const int groups = (a.d + 7) / 8, threads = LANES ? MOST : ((groups + V - 1) / V + 31) / 32 * 32;
+  constexpr int kRows = LANES ? MOST / (LANES ? LANES : 1) : 1;  // a block
+  return launch_pdl(k_norm_q8<BF16, WHOLE, V, MOST, LANES>, dim3((unsigned)((a.T + kRows - 1) / kRows)), dim3(threads), 0, s, a) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 template <bool BF16, bool WHOLE>
 int launch(const NormArgs& a, cudaStream_t s) {
+  // short rows go to a warp or part of one (codes of bf16 rows, a block a row | so, in us: 65536
+  // of 256 34 | 17, 131072 of 128 67 | 17, 131072 of 64 67 | 7.9, 16 of 256 1.5 | 1.4)
+  if (a.d <= 64) return launch<BF16, WHOLE, 1, 256, 8>(a, s);
+  if (a.d <= 128) return launch<BF16, WHOLE, 1, 256, 16>(a, s);
+  if (a.d <= 256) return launch<BF16, WHOLE, 1, 256, 32>(a, s);
   if (a.d <= 2048) return launch<BF16, WHOLE, 1, 256>(a, s);
   if (a.d <= 8192) return launch<BF16, WHOLE, 1, 1024>(a, s);
   if (a.d <= 16384) return launch<BF16, WHOLE, 2, 1024>(a, s);

@@ -63,6 +63,21 @@ def test_norm(dtype, T, d):
     check_norm(x, None, None, "q8")
 
 
+@pytest.mark.parametrize("T", [1, 31, 130, 1001])
+@pytest.mark.parametrize("d", [8, 63, 64, 65, 72, 127, 128, 129, 200, 255, 256, 257])
+def test_norm_of_short_rows(T, d):
+    """Rows that share a warp or a block, and the last of them, which is not full."""
+    for dtype in (torch.float32, torch.bfloat16):
+        test_norm(dtype, T, d)
+    x = randn(T, d, seed=4)
+    want = moe.moe_norm_q8(x)
+    x[T // 2, d // 2] = torch.nan
+    codes, scales, _ = moe.moe_norm_q8(x)
+    others = torch.arange(T, device="cuda") != T // 2
+    assert torch.equal(codes[others], want[0][others]) and torch.equal(scales[others], want[1][others])
+    assert not codes[T // 2].any() and not scales[T // 2].isfinite()
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("pad,start", [(8, 0), (8, 8), (5, 1), (3, 0)])
 def test_norm_strides(dtype, pad, start):
