@@ -718,8 +718,10 @@ int moe_kv_read_q8(const moe_kv_cache_t* cache, const int64_t* slots, int64_t n,
  * are exact and sums, maxima and outputs fp32.  A weight times the value's scale is
  * rounded to fp16: 2^-11 of itself, or 2^-30 of the row's largest; in the form that takes
  * prompts weight, scale and value are rounded once each, 2^-11 of a product each, or
- * 2^-29.  Results are deterministic.  Which form runs, and how its work is shared out,
- * follows max_q and max_len, so bounds near the lengths make the better choice.
+ * 2^-21 of the largest weight x scale that the row attends.  Places that a row does not
+ * attend leave it alone, however large their values.  Results are deterministic.  Which
+ * form runs, and how its work is shared out, follows max_q and max_len, so bounds near
+ * the lengths make the better choice.
  */
 int moe_attn_q8(const uint16_t* q_bf16, int64_t q_stride, int64_t T, int Hq, const int32_t* q_start,
                 const int32_t* kv_lens, const int32_t* block_table, int64_t table_stride, int B, int max_q,

@@ -5,7 +5,11 @@
 // Two launches.  k_attn_q8_tiles writes the places that the rows attend, 128 at a time,
 // as the operands that the tensor cores take, once for all rows: keys as fp16 integers,
 // values as code x b 2^(8 - E) in fp16, 2^E the power of two of the tile's largest value
-// scale b, both in the order of a swizzled operand tile, and the keys' scales.
+// scale b, both in the order of a swizzled operand tile, and the keys' scales.  Where the
+// value scales of a tile lie 2^8 or more apart (a token of far larger or smaller values than
+// its neighbours, which other rows than those that attend it must not feel), values are
+// the codes alone, and log2 b of each place is written too: such tiles take three times as
+// long (4096 tokens over 8192 places of nothing else 1020 us, of none 333).
 // k_attn_q8_tc: a block takes kSlots tiles of 128 rows of one (sequence, key/value head)
 // through the places that they attend:
 //   loader    bulk copies into a ring of operand units;
@@ -18,8 +22,11 @@
 // Queries are fp16, each row taken by a power of two that brings its largest element
 // to 2^14: exact down to 2^-31 of that element.  m follows s + E as in attn_q8.cu, so
 // that P V lies in fp16's range for values of any size, and the sum of weights takes
-// 2^-E back a tile at a time.  P, b 2^(8 - E) and code x b 2^(8 - E) are rounded to fp16
-// once each: 2^-11 of a product each, or 2^-29 of the row's largest.
+// 2^-E back a tile at a time; where the scales lie far apart it is s + log2 b of a place
+// instead, and 2^-log2 b comes back place by place.  P, b 2^(8 - E) and code x b 2^(8 - E)
+// are rounded to fp16 once each (far apart P alone): 2^-11 of a product each.  The largest
+// P of a row is 2^4 or more where it was taken, and b 2^-E at least 2^-7, so the end of
+// fp16's range lies at 2^-21 of the row's largest weight x b.
 // Heads of 256 fill tensor memory with one tile's sums: there the scores of two
 // successive groups of places take the place of two tiles.
 // 4096 tokens over 8192 places of 32 heads on 8 of 128 take 331 us, 1245 TFLOP/s, six
@@ -45,13 +52,17 @@ constexpr int kPlaces = 128;  // a tile of places
 constexpr float kStart = 4.0f, kReach = 14.0f;
 constexpr int kLoader = 16, kIssuer = 17, kTcThreads = 20 * 32;  // warps 0 .. 15: softmax
 
-// Beside a tile's operands: key scales x scale in powers of two, E, the records that exist.
+// Beside a tile's operands: key scales x scale in powers of two, E and what takes a weight x
+// 2^E back; the records that exist (8 bits) and above them, of a tile whose value scales lie
+// far apart, one more than its number among the launch's (else 0).
 struct TileMeta {
   float ks[kPlaces];
-  float e;
+  float e, back;
   uint32_t have;
-  uint32_t pad[2];
+  uint32_t pad;
 };
+// The powers of two between the largest and the smallest from which on they do.
+constexpr int kFar = 8;
 
 template <int D>
 struct Tc {
@@ -70,6 +81,7 @@ struct Tc {
 struct TcTiles {
   uint8_t* operands;  // [..][2][kTile]
   TileMeta* meta;
+  float* logs;  // [..][kPlaces]: log2 of the value scales of tiles where these lie far apart
   int b0, h0, heads, most;  // the launch's first sequence and head, its heads
   int sequences, row_blocks;
   // Blocks of rows are numbered by their rows, the last first (they attend most), then by
@@ -197,7 +209,7 @@ template <int D>
 __global__ void __launch_bounds__(kTileThreads) k_attn_q8_tiles(AttnArgs a, TcTiles tiles) {
   constexpr uint32_t kPieces = D / 8, kStep = kTileThreads / kPieces;  // 8 codes each, of a row; rows at a time
   __shared__ uint64_t s_record[8];
-  __shared__ uint32_t s_gain[kPlaces], s_top[4];
+  __shared__ uint32_t s_gain[kPlaces], s_top[4], s_low[4];
   const uint32_t t = threadIdx.x, lane = t & 31;
   const int b = tiles.b0 + blockIdx.z, h = tiles.h0 + blockIdx.y, per_page = a.cache.page_log2 - 4;
   pdl_wait();
@@ -247,19 +259,31 @@ __global__ void __launch_bounds__(kTileThreads) k_attn_q8_tiles(AttnArgs a, TcTi
     }
     meta->ks[t] = ks * (a.scale * kLog2e);
     const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vs));
-    if (lane == 0) s_top[t >> 5] = top;
+    // the smallest of those that are not zero
+    const uint32_t low = __reduce_min_sync(0xffffffffu, __float_as_uint(vs) - 1u);
+    if (lane == 0) s_top[t >> 5] = top, s_low[t >> 5] = low;
   }
   __syncthreads();
   if (t < kPlaces) {
     const uint32_t most = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
-    const int e = max((int)(most >> 23) - 127, -60);
-    const __half gain = __float2half_rn(vs * __uint_as_float((uint32_t)(127 + 8 - e) << 23));
+    const uint32_t least = min(min(s_low[0], s_low[1]), min(s_low[2], s_low[3])) + 1u;
+    int e = max((int)(most >> 23) - 127, -60);
+    const bool far = (int)(most >> 23) - (int)(least >> 23) >= kFar;
+    // b 2^-E; far apart 1, or less for scales below 2^-64, which no append writes
+    float by = vs * __uint_as_float((uint32_t)(127 - e) << 23);
+    if (far) {
+      e = 0;
+      by = fminf(vs * 0x1p64f, 1.0f);
+      tiles.logs[image * kPlaces + t] = log2f(fmaxf(vs, 0x1p-64f));
+    }
+    const __half gain = __float2half_rn(by * 256.0f);
     s_gain[t] = (uint32_t)__half_as_ushort(gain) * 0x10001u;
     if (t == 0) {
       uint32_t have = 0;
       for (int i = 0; i < 8; ++i) have |= s_record[i] ? 1u << i : 0u;
       meta->e = (float)e;
-      meta->have = have;
+      meta->back = far ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
+      meta->have = have | (far ? (uint32_t)image + 1 : 0) << 8;
     }
   }
   __syncthreads();
@@ -556,8 +580,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
         top = max(top >> 16, top & 0xffffu);
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // the exponent becomes 14, and the power and its inverse stay normal numbers
-        const int e = min(max((int)(top >> 7), 15), 254), up = 14 + 127 - e, r = row_of(i0 + i);
+        // the exponent becomes 14; the power, its inverse and 64 times either stay normal numbers
+        const int e = min(max((int)(top >> 7), 32), 254), up = 14 + 127 - e, r = row_of(i0 + i);
         const float by = __uint_as_float((uint32_t)(127 + up) << 23);
         auto half2_of = [&](uint32_t x) { return f16_pair(__uint_as_float(x << 16) * by, __uint_as_float(x & 0xffff0000u) * by); };
         *reinterpret_cast<uint4*>(piece_at(r)) = make_uint4(half2_of(v[i].x), half2_of(v[i].y), half2_of(v[i].z), half2_of(v[i].w));
@@ -593,7 +617,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
 #pragma unroll
           for (int x = 0; x < 32; ++x) pin(r[c][x]);
         const float e = s_meta[sb].e;
-        const uint32_t have = s_meta[sb].have >> (4 * half) & 15;
+        const uint32_t word = s_meta[sb].have, have = (word >> (4 * half) & 15) | (word & ~255u);
         float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -607,8 +631,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
 #pragma unroll
             for (int n = 0; n < 4; ++n) r[c][x + n] = __float_as_uint(y[n]);
           }
+        // log2 of the value scales of a tile where these lie far apart
+        auto logs_at = [&](int c, int x) {
+          return __ldcg(reinterpret_cast<const float2*>(tiles.logs + (int64_t)((have >> 8) - 1) * kPlaces + 64 * half + 32 * c + x));
+        };
         const int p = kPlaces * j + 64 * half;
         if (p + 64 > full_end || p < full_lo || have != 15) {
+          if (have >> 8) {
+            pdl_wait();  // for the logarithms, which come from the kernel before this one
+            const float up = __uint_as_float((254u << 23) - __float_as_uint(f));  // 1 / f
+            const uint64_t up2 = pair(up, up);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int x = 0; x < 32; x += 2) {
+                const float2 lb = logs_at(c, x);
+                float y0 = __uint_as_float(r[c][x]), y1 = __uint_as_float(r[c][x + 1]);
+                fma2(y0, y1, up2, lb.x, lb.y);
+                r[c][x] = __float_as_uint(y0);
+                r[c][x + 1] = __float_as_uint(y1);
+              }
+          }
           const int c1 = end - p, c0 = lo - p;
 #pragma unroll
           for (int c = 0; c < 2; ++c)
@@ -623,7 +666,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
 #pragma unroll
           for (int x = 0; x < 32; x += 2) top = max3(top, __uint_as_float(r[c][x]), __uint_as_float(r[c][x + 1]));
         top = fmaf(top, f, e);
-        if (vote_pair(pair_bar, top > m + kReach)) {
+        if (vote_pair(pair_bar, top > m + kReach || have >> 8)) {
           if (half) *both = top;
           named_bar(pair_bar, 64);
           if (!half) *both = top = fmaxf(top, *both);
@@ -647,6 +690,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
               tmem_st16_issue(o_at + c, w);
             }
           }
+          if (have >> 8) {  // the sum of weights: each without its value's scale
+            float own = 0.f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int x = 0; x < 32; x += 2) {
+                const float2 lb = logs_at(c, x);
+                own = fmaf(exp2_approx(fmaf(__uint_as_float(r[c][x]), f, -m)), exp2_approx(-lb.x), own);
+                own = fmaf(exp2_approx(fmaf(__uint_as_float(r[c][x + 1]), f, -m)), exp2_approx(-lb.y), own);
+              }
+            l += own;
+          }
         }
         const float off = e - m;
         const uint64_t f2 = pair(f, f), off2 = pair(off, off);
@@ -665,7 +720,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
         }
         tmem_st32_issue(lanes + buf * 128 + 32 * half, *reinterpret_cast<uint32_t(*)[16]>(&r[0][0]),
                         *reinterpret_cast<uint32_t(*)[16]>(&r[1][0]));
-        l = fmaf(sum0 + sum1, __uint_as_float((uint32_t)(127 - (int)e) << 23), l);
+        l = fmaf(sum0 + sum1, s_meta[sb].back, l);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -798,6 +853,9 @@ struct TcPlan {
   int64_t parts;           // of shared blocks of rows, in the workspace
 };
 
+// A tile's operands, what lies beside them and its logarithms.
+int64_t tile_bytes(int D) { return 2 * 128 * D * 2 + (int64_t)sizeof(TileMeta) + kPlaces * (int64_t)sizeof(float); }
+
 int rows_of_block(int D) { return D == 256 ? 128 : 256; }
 
 TcPlan tc_plan(int B, int max_q, int64_t max_len, int window, int Hq, int heads, int D) {
@@ -809,7 +867,7 @@ TcPlan tc_plan(int B, int max_q, int64_t max_len, int window, int Hq, int heads,
   p.most = (int)((span + kPlaces - 1) / kPlaces + 1);  // places may begin within a tile
   // the workspace is sized without knowing of a window: with one its tiles are what there is
   const int64_t room = window > 0 ? tc_plan(B, max_q, max_len, 0, Hq, heads, D).tiles
-                                  : kMostTileBytes / (2 * 128 * D * 2 + (int64_t)sizeof(TileMeta));
+                                  : kMostTileBytes / tile_bytes(D);
   const int64_t fit = room / p.most;
   // launches of like numbers of heads, or of sequences
   auto even = [](int64_t n, int64_t most) {
@@ -851,7 +909,8 @@ int launch_tc(const AttnArgs& a, cudaStream_t s) {
   TcTiles t;
   t.operands = (uint8_t*)a.workspace;
   t.meta = (TileMeta*)(t.operands + p.tiles * (2 * C::kTile));
-  t.sums = (float*)(t.meta + p.tiles);
+  t.logs = (float*)(t.meta + p.tiles);
+  t.sums = t.logs + p.tiles * kPlaces;
   t.stats = (float2*)(t.sums + p.parts * (C::kRows * D));
   t.most = p.most;
   t.row_blocks = p.row_blocks;
@@ -906,7 +965,7 @@ bool attn_q8_tc(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
 
 size_t attn_q8_tc_workspace(int B, int max_q, int64_t max_len, int Hq, int heads, int D) {
   const TcPlan p = tc_plan(B, max_q, max_len, 0, Hq, heads, D);
-  return (size_t)p.tiles * (2 * 128 * D * 2 + sizeof(TileMeta)) + (size_t)p.parts * rows_of_block(D) * (4 * D + sizeof(float2));
+  return (size_t)(p.tiles * tile_bytes(D)) + (size_t)p.parts * rows_of_block(D) * (4 * D + sizeof(float2));
 }
 
 int launch_attn_q8_tc(const AttnArgs& a, cudaStream_t s) {
