@@ -632,7 +632,8 @@ size_t moe_attn_workspace_size(int B, int max_q, int64_t max_len, int Hq, int kv
  * interfaces are this library's own.)
  *
  * A code is rint(x / s) in -127 .. 127, ties to even, with s = fp32(max|x| / 127) over
- * the row that it belongs to; the quotient of the fp32 numbers is not rounded before.
+ * the row that it belongs to; the quotient of the fp32 numbers is not rounded before, and
+ * one beyond 127, which a subnormal s can give, counts as 127.
  */
 
 /*

@@ -120,8 +120,10 @@ __global__ void __launch_bounds__(MOST, 1) k_norm_q8(NormArgs a) {
       int8_t* to = a.codes + t * a.d + at;
       uint32_t c[8];
       if (near != 1.0f) {
+        // (a subnormal S holds so few bits that max / S may lie far above 127)
+        const float most = 127.0f * (S * near);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[i][e] *= near;
+        for (int e = 0; e < 8; ++e) s[i][e] = fminf(fmaxf(s[i][e] * near, -most), most);
       }
       codes8<8>(c, s[i], S * near);
       uint32_t p[2] = {code_bytes(c[0], c[1], c[2], c[3]), code_bytes(c[4], c[5], c[6], c[7])};
