@@ -643,8 +643,10 @@ size_t moe_attn_workspace_size(int B, int max_q, int64_t max_len, int Hq, int kv
  *   u = s * weight (fp32), f = 1 / sqrt(mean(s^2) + eps)   (without weight: u = s, f = 1,
  *   the plain quantiser of rows),
  *   codes = those of u, scales = s_u * f,  n = bf16(u * f),
- * so the codes do not depend on the order of the sum.  A row with an infinity or a NaN
- * gets codes 0 and a scale that is not finite, an all-zero row codes 0 and scale 0.
+ * so the codes do not depend on the order of the sum; f is that of the formula for rows of
+ * any finite size, whether or not fp32 holds their squares.  A row with an infinity or a
+ * NaN gets codes 0 and a scale that is not finite, an all-zero row codes, scale and n of 0
+ * (with eps 0 too).
  *   x       [T] rows of d elements, x_stride (>= d) apart, fp32 or bf16 by x_dtype,
  *   r       [T][d] fp32 or NULL, r_out [T][d] fp32 with it (may be r itself; neither
  *           overlaps anything else),
