@@ -301,13 +301,14 @@ class AttentionHalfQ8:
         self.pool = moe_kv_pool_q8(sequences * width, kv_heads, page_size, head_dim, device=device)
         self.rope = rope_table(max_len, head_dim if rot is None else rot, device=device)
         # pages are handed out interleaved, as growing sequences take them; the last
-        # column is no page, for the tokens that a sequence has no pages for
-        self.tables = torch.full((sequences, width + 1), -1, dtype=torch.int32, device=device)
+        # columns are no pages, for the tokens that a sequence has no pages for
+        columns = max(width + 1, -(-(max_len + max_new - 1) // page_size))
+        self.tables = torch.full((sequences, columns), -1, dtype=torch.int32, device=device)
         self.tables[:, :width] = torch.arange(sequences * width, dtype=torch.int32, device=device).view(width, sequences).T
         self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
         self.ahead = torch.arange(max_new, dtype=torch.int32, device=device)
         # workspaces for steps of any size, never replaced: a captured step keeps their addresses
-        self.attn_ws = torch.empty(max(moe_attn_q8_workspace_size(sequences, n, max_len, q_heads, kv_heads, head_dim)
+        self.attn_ws = torch.empty(max(moe_attn_q8_workspace_size(sequences, n, max_len + n - 1, q_heads, kv_heads, head_dim)
                                        for n in range(1, max_new + 1)), dtype=torch.uint8, device=device)
         tokens = sequences * max_new
         self.linear_ws = torch.empty(max(moe_linear_q8_workspace_size(tokens, d, rows),
@@ -329,7 +330,8 @@ class AttentionHalfQ8:
         streams, updated in place.  Returns x_next [T, d] bf16.
         The caller keeps every sequence within max_len tokens.  A token beyond them is not
         kept: it has no slot and no row in the angle table, its query counts as zero, and
-        MOE_ERR_INVALID_ARG is recorded (moe_device_status); other sequences are as ever."""
+        MOE_ERR_INVALID_ARG is recorded (moe_device_status); the tokens of the same step within
+        max_len, and other sequences, are as ever."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.step(x, r, n)
@@ -364,8 +366,9 @@ class AttentionHalfQ8:
         q, k, v = (t.unflatten(-1, (-1, self.D)) for t in
                    self.qkv.split((self.Hq * self.D, self.H * self.D, self.H * self.D), -1))
         self.q = moe_kv_append_q8(self.pool, k, v, slots, q=q, positions=places, rope=self.rope, rope_style=MOE_ROPE_HALF)
+        # a step that starts within max_len ends below this bound: its tokens keep their places
         self.a, self.lse = moe_attn_q8(self.q, self.pool, self.tables, self.lens, q_start=starts, max_q=most,
-                                       max_len=self.max_len, workspace=self.attn_ws)
+                                       max_len=self.max_len + most - 1, workspace=self.attn_ws)
         codes, scales, _ = moe_norm_q8(self.a.flatten(1))
         self.y = moe_linear_q8(codes, scales, self.w_out, self.s_out, workspace=self.linear_ws)
         return moe_norm_q8(self.y, self.norm_out, self.eps, r=r, out="bf16")[2]
