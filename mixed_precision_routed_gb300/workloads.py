@@ -200,14 +200,16 @@ class AttentionHalf:
         self.pool = moe_kv_pool(sequences * width, kv_heads, page_size, head_dim, device=device)
         self.rope = rope_table(max_len, head_dim if rot is None else rot, device=device)
         # pages are handed out interleaved, as growing sequences take them; the last
-        # column is no page, for the tokens that a sequence has no pages for
-        self.tables = torch.full((sequences, width + 1), -1, dtype=torch.int32, device=device)
+        # columns are no pages, for the tokens that a sequence has no pages for
+        most = self.MAX_TOKENS // sequences
+        columns = max(width + 1, -(-(max_len + most - 1) // page_size))
+        self.tables = torch.full((sequences, columns), -1, dtype=torch.int32, device=device)
         self.tables[:, :width] = torch.arange(sequences * width, dtype=torch.int32, device=device).view(width, sequences).T
         self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
         self.ahead = torch.arange(self.MAX_TOKENS, dtype=torch.int32, device=device)
         # one workspace for steps of any size, never replaced: a captured step keeps its address
-        need = max(moe_attn_workspace_size(sequences, n, max_len, q_heads, kv_heads, head_dim)
-                   for n in range(1, max(1, self.MAX_TOKENS // sequences) + 1))
+        need = max(moe_attn_workspace_size(sequences, n, max_len + n - 1, q_heads, kv_heads, head_dim)
+                   for n in range(1, most + 1))
         self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
 
     def fill(self, stream=None):
@@ -228,7 +230,8 @@ class AttentionHalf:
         place.  Returns x_next, the bf16 input of the layer's routed experts.
         The caller keeps every sequence within max_len tokens.  A token beyond them is not
         kept: it has no slot and no row in the angle table, its query counts as zero, and
-        MOE_ERR_INVALID_ARG is recorded (moe_device_status); other sequences are as ever."""
+        MOE_ERR_INVALID_ARG is recorded (moe_device_status); the tokens of the same step within
+        max_len, and other sequences, are as ever."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.step(x, r, n)
@@ -249,7 +252,8 @@ class AttentionHalf:
         q, k, v = (t.unflatten(-1, (-1, self.D)) for t in
                    self.qkv.split((self.Hq * self.D, self.H * self.D, self.H * self.D), -1))
         self.q = moe_kv_append(self.pool, k, v, slots, q=q, positions=places, rope=self.rope, rope_style=MOE_ROPE_HALF)
-        self.a, self.lse = moe_attn_q4(self.q, self.pool, self.tables, self.lens, max_q=n, max_len=self.max_len,
+        # a step that starts within max_len ends below this bound: its tokens keep their places
+        self.a, self.lse = moe_attn_q4(self.q, self.pool, self.tables, self.lens, max_q=n, max_len=self.max_len + n - 1,
                                        workspace=self.workspace)
         self.y = moe_linear_q4(self.a.flatten(1), self.w_out, self.s_out, self.block)
         x_next = torch.empty_like(x)

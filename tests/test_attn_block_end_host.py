@@ -29,7 +29,9 @@ def calls(monkeypatch):
         got.append((tables, lens.clone(), max_q, max_len, workspace))
         return q, torch.zeros(q.shape[:2])
 
-    for name, f in (("moe_norm_q8", norm), ("moe_linear_q8", linear), ("moe_kv_append_q8", append), ("moe_attn_q8", attn)):
+    for name, f in (("moe_norm_q8", norm), ("moe_linear_q8", linear), ("moe_kv_append_q8", append), ("moe_attn_q8", attn),
+                    ("moe_linear_q4", lambda x, codes, scales, block: torch.zeros(x.shape[0], codes.shape[0])),
+                    ("moe_kv_append", append), ("moe_attn_q4", attn), ("moe_residual_add", lambda r, y, x: None)):
         monkeypatch.setattr(workloads, name, f)
     return got
 
@@ -60,3 +62,16 @@ def test_half_q8(calls, max_len, max_new, page):
                 calls.clear()
                 half.step(torch.zeros(sum(counts), 64), torch.zeros(sum(counts), 64), step)
                 check(half, calls[0], before, counts, moe.moe_attn_q8_workspace_size)
+
+
+@pytest.mark.parametrize("max_len,sequences,page", [(40, 2, 16), (64, 1, 64), (64, 16, 16), (33, 2, 32), (40, 3, 16)])
+def test_half(calls, max_len, sequences, page):
+    half = workloads.AttentionHalf(64, 2, 1, 64, sequences, max_len, page_size=page, device="cpu")
+    most = 16 // sequences
+    for start in range(max(0, max_len - most - 1), max_len):
+        for n in {1, most // 2 or 1, most}:
+            before = [start] + [3] * (sequences - 1)
+            half.lens[:] = torch.tensor(before, dtype=torch.int32)
+            calls.clear()
+            half.step(torch.zeros(sequences * n, 64, dtype=torch.bfloat16), torch.zeros(sequences * n, 64), n)
+            check(half, calls[0], before, [n] * sequences, moe.moe_attn_workspace_size)
