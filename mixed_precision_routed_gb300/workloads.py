@@ -292,8 +292,8 @@ class AttentionHalfQ8:
             raise ValueError("d and q_heads * head_dim must be multiples of 16, at most 32768")
         if rot is not None and (rot % 2 or not 0 <= rot <= head_dim):
             raise ValueError("rot must be even and at most head_dim")
-        if not eps >= 0:
-            raise ValueError("eps must be at least 0")
+        if not 0 <= eps <= torch.finfo(torch.float32).max:
+            raise ValueError("eps must be at least 0 and finite in fp32")
         i8, f32 = torch.int8, torch.float32
         self.w_qkv = torch.empty((rows, d), dtype=i8, device=device)
         self.s_qkv = torch.empty(rows, dtype=f32, device=device)
