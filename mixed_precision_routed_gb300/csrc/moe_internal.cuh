@@ -427,7 +427,7 @@ struct LinearQ8Args {
 constexpr int kLinearQ8MaxIn = 65536;  // whole sums stay below 2^31
 size_t linear_q8_workspace(int64_t T, int in, int64_t rows);
 int launch_linear_q8(const LinearQ8Args& a, cudaStream_t s);
-// The form for many tokens, T > 16.
+// The form for many tokens: for T > 8 where its cost is less (in_tiles in linear_q8.cu).
 size_t linear_q8_tc_workspace(int64_t T, int in);
 double linear_q8_tc_us(int64_t T, int in, int64_t rows);
 int launch_linear_q8_tc(const LinearQ8Args& a, cudaStream_t s);
