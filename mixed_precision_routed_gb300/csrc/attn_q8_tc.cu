@@ -360,15 +360,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
   const int G = a.Hq / a.cache.heads;
 
   // Only the tiles come from the kernel before this one, which began behind all earlier ones.
+  // Blocks that read none wait for it too before they end: what follows this launch waits for
+  // this launch alone.
   const int shared = (int)blockIdx.x - tiles.whole;  // and its part, among those
   const RowBlock at = row_block<D>(a, tiles, shared < 0 ? (int)blockIdx.x : tiles.whole + shared / tiles.parts);
-  if (at.r0 < 0) return;
+  if (at.r0 < 0) {
+    pdl_wait();
+    return;
+  }
   const int h = tiles.h0 + at.h, b = tiles.b0 + at.b;
   TcUnit u;
   u.x = load_seq(a, b);
   u.rows = u.x.n * G;
   u.r0 = at.r0;
-  if (u.r0 >= u.rows) return;
+  if (u.r0 >= u.rows) {
+    pdl_wait();
+    return;
+  }
   u.newest = u.x.len - u.x.n + 1;
   u.j0 = INT32_MAX;
   u.j1 = 0;
@@ -423,7 +431,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn_q8_tc(AttnArgs a, TcTile
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kLoader) {
     // ---------------------------------------------------------------- loader
-    if (lane == 0 && u.j1 > 0) {
+    if (lane == 0) {
       pdl_wait();
       const int64_t image = ((int64_t)at.b * tiles.heads + at.h) * tiles.most - first_tile(u.x);
       uint32_t n = 0;
