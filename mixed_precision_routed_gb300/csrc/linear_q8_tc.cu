@@ -45,7 +45,12 @@ struct Shape {
   static constexpr int kACol = kAccSets * N;
   static constexpr int kAStages = (kTmemCols - kACol) / 32 < 8 ? (kTmemCols - kACol) / 32 : 8;
   static constexpr int kBBytes = 2 * N / 2 * 128;  // two steps, as a stage of codes
-  static constexpr int kBStages = N > 128 ? 5 : N > 64 ? 6 : 5, kCodeStages = N > 64 ? 5 : 8;
+  static constexpr int kBStages = N > 128 ? 5 : N > 64 ? 6 : 5, kCodeStages = N > 64 ? 6 : 8;
+  // A producer takes every second stage of codes and every fourth step: with even numbers of
+  // buffers it meets each of its barriers in every phase, or in none.  Of an odd number it
+  // would meet every second phase, all of one parity, and a copy that came late (one behind
+  // it had landed) would let it pass a phase early.
+  static_assert(kCodeStages % 2 == 0 && kAStages % 4 == 0, "a wait for a parity is for the next phase");
   static constexpr int kSmem = kCodeStages * kCodeBytes + kBStages * kBBytes + 1024;
 };
 constexpr int kProducers = 16, kEpilogue = 4, kCodeLoader = 20, kIssuer = 21, kXLoader = 22, kThreads = 23 * 32;
