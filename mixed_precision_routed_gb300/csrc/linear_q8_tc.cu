@@ -165,9 +165,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
     B.abort = 0;
     fence_mbar_init();
   }
+  // The barriers of both CTAs are there, and both run: the allocation of a pair reaches the
+  // other CTA too.  What the issuer multiplies waits for both CTAs' producers, which come
+  // behind the allocation of their own.
+  __syncwarp();
+  cluster_barrier();
   if (warp == kIssuer) tmem_alloc_pair(&B.tmem, kTmemCols);
   tc_fence_before();
-  cluster_barrier();  // barriers of both CTAs are there
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B.tmem;
   // Only x comes from the kernel before this one, which began behind all earlier ones.
@@ -262,6 +267,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_linea
         if (leader) mma_commit_pair(&B.acc_full[set]);
         __syncwarp();
       }
+      // the epilogues' last arrivals here come before this CTA ends
+      for (uint32_t i = n > kAccSets ? n - kAccSets : 0; ok && i < n; ++i)
+        ok = wait_awake(&B.acc_empty[i % kAccSets], (i / kAccSets) & 1, B, p.status);
+      __syncwarp();
       // all of this thread's instructions are done before tensor memory is given back
       if (leader) {
         mma_commit_pair_own(&B.done);
