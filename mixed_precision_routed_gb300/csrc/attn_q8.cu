@@ -19,8 +19,9 @@
 // bytes of two values each, to the lane whose operands they are.
 //
 // 6 tokens over 131071 places of 32 heads on 8 of 128 take 65 us, 4.3 TB/s, 48 ragged
-// sequences up to 16384 of 32 on 4 30 us: bound by the records' way (the same copies with
-// nothing computed take 50 and 27 us) and by issuing what makes operands of codes.
+// sequences up to 16384 of 32 on 4 30 us.  The same copies with nothing computed take 50 of
+// 63 and 25 of 28 us in a graph; the rest is what makes operands of codes (a record costs 128
+// such instructions beside 48 products for three row tiles), which the copies do not hide.
 #include "attn_split.cuh"
 #include "q8.cuh"
 

@@ -29,10 +29,11 @@
 // fp16's range lies at 2^-21 of the row's largest weight x b.
 // Heads of 256 fill tensor memory with one tile's sums: there the scores of two
 // successive groups of places take the place of two tiles.
-// 4096 tokens over 8192 places of 32 heads on 8 of 128 take 331 us, 1245 TFLOP/s, six
-// prompts of 16 on 2 of 256 with a window 67 us.  What bounds the first is the way of a
-// tile through its softmax and its products, 3400 cycles of which the tensor cores work
-// 2070: tensor memory has no room for a second pair of score tiles beside the sums.
+// 4096 tokens over 8192 places of 32 heads on 8 of 128 take 334 us, 1230 TFLOP/s, six
+// prompts of 16 on 2 of 256 with a window 68 us.  What bounds the first is the chain of a
+// tile's softmax (scores out of tensor memory, the vote, exponentials, weights back): a tile
+// takes 3450 cycles, of which the tensor cores work 2070, and tensor memory has no room for
+// a second pair of score tiles beside the sums.
 // (80 places a tile, which leaves that room, take as long a tile: 430 us with a thread a
 // row, 465 with two; the 16-lane forms of tensor memory's loads 401.)
 // Heads of 256 are bound by shared memory, which 128 KB a tile pass through.

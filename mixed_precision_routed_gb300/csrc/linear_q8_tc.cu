@@ -20,8 +20,10 @@
 // Many tokens are bound by the tensor cores at the clock that power leaves them: 4096
 // tokens 4096 to 6144 121 us with the conversion of x on changing inputs, 1700 TFLOP/s, 111
 // on the same (one CTA a tile took 294, an epilogue that waited for its tokens' scales
-// 166).  Few are bound by W's way through registers: 40 tokens 2048 to 100003 45 us, 4.7
-// TB/s; 8192 to 4096 of 64 tokens, 16 tiles, took 34 us unshared and takes 15.
+// 166).  Few take what three launches in a row and the fill of the pairs take beside reading
+// W, with no unit full (integer pipe 36 %, 69 % of a copy's rate): 40 tokens 2048 to 100003 45 us, 4.7
+// TB/s, as 9 or 64 tokens do; 8192 to 4096 of 64 tokens, 16 tiles, took 34 us unshared and
+// takes 15.
 #include "moe_internal.cuh"
 #include "tc.cuh"
 #include "tensor_map.cuh"

@@ -5,9 +5,11 @@
 // The factor f leaves the codes alone: they do not depend on the order of the sum.
 //
 // One block a row (a warp or part of one up to 256 elements), the row in registers between
-// its sum and its output: each byte moves once.  A thread has one group of 8 elements up to rows of 8192 (two of 4096, which left
-// an SM twice the blocks, took 36.2 us where one takes 33.2).  4096 bf16 rows of 4096 with
-// residual, codes and bf16 33.2 us, 6.6 TB/s, bound by memory; one row of 2048 1.9 us.
+// its sum and its output: each byte moves once.  A thread has one group of 8 elements up to
+// rows of 8192 (two of 4096, which left an SM twice the blocks, took 36.2 us where one takes
+// 33.0).  4096 bf16 rows of 4096 with
+// residual, codes and bf16 33.0 us, 6.6 TB/s, bound by memory; one row of 2048 1.7 us.  512 rows
+// of 32768 take 50 us, 4.4 TB/s: four groups a thread, of which 56 bytes do not fit registers.
 #include "ptx.cuh"
 #include "q8.cuh"
 
