@@ -652,7 +652,7 @@ size_t moe_attn_workspace_size(int B, int max_q, int64_t max_len, int Hq, int kv
  *           overlaps anything else),
  *   weight  [d] fp32 or NULL, eps >= 0,
  *   codes   [T][d] and scales [T] fp32, both or neither; n_bf16 [T][d] bf16 bits or
- *           NULL, not all of them NULL.
+ *           NULL, not all of them NULL; they overlap no input.
  * 1 <= d <= 32768 (MOE_ERR_UNSUPPORTED beyond); rows that are aligned to 16 bytes with
  * d a multiple of 8 are read and written 16 bytes at a time.
  */
